@@ -37,7 +37,9 @@ EXPORTS = ("ar_allreduce", "ar_reduce_scatter", "ar_all_gather", "ar_reduce", "a
            "ar_bucketed_allreduce_noalloc", "ar_chunk_range", "ar_device_status", "ar_set_barrier_timeout_ns", "ar_debug_skip_barrier",
            "ar_last_cuda_error", "ar_strerror", "ar_version", "ar_kernel_launches", "ar_reducer_create",
            "ar_reducer_mark_ready", "ar_reducer_finish", "ar_reducer_destroy", "ar_reducer_buckets",
-           "ar_reducer_set_max_blocks", "ar_plan_create", "ar_plan_run", "ar_plan_destroy")
+           "ar_reducer_set_max_blocks", "ar_plan_create", "ar_plan_run", "ar_plan_destroy",
+           "ar_layer_norm", "ar_layer_norm_backward", "ar_layer_norm_workspace_bytes", "ar_distill_loss",
+           "ar_distill_loss_backward")
 
 
 class ArError(RuntimeError):
@@ -84,10 +86,18 @@ def _load():
     L.ar_plan_create.argtypes = [cint, pp, cint, i64, cint, cint, cint, cint, ctypes.POINTER(vp)]
     L.ar_plan_run.argtypes = [vp, vp]
     L.ar_plan_destroy.argtypes = [vp]
+    flt = ctypes.c_float
+    L.ar_layer_norm.argtypes = [vp, i64, vp, vp, vp, i64, vp, vp, i64, i64, flt, cint, cint, vp]
+    L.ar_layer_norm_backward.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, vp, i64, i64, cint, cint, vp, i64,
+                                         vp]
+    L.ar_layer_norm_workspace_bytes.argtypes = [i64, i64]
+    L.ar_distill_loss.argtypes = [vp, i64, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, flt, cint, cint, vp]
+    L.ar_distill_loss_backward.argtypes = [vp, i64, vp, vp, vp, vp, vp, i64, i64, i64, i64, flt, cint, cint, vp]
     for name in EXPORTS:
         if name != "ar_strerror":
             getattr(L, name).restype = cint
-    L.ar_kernel_launches.restype = i64
+    for name in ("ar_kernel_launches", "ar_layer_norm_workspace_bytes"):
+        getattr(L, name).restype = i64
     return L
 
 
@@ -316,6 +326,115 @@ class Plan:
             self.close()
         except Exception:
             pass
+
+
+# ---- training-step operators ----------------------------------------------------------
+#
+# These take torch CUDA tensors and read sizes, strides and element types from
+# them.  Operands whose shapes, types or inner strides do not belong together
+# are refused (AR_ERR_INVALID_ARG, or AR_ERR_UNSUPPORTED for an element type
+# the library does not have) before the library is called.
+
+_TORCH_DTYPE = {"torch.float32": 0, "torch.bfloat16": 1, "torch.int32": 2, "torch.float16": 3}
+
+
+def _dtype_of(t):
+    return _TORCH_DTYPE.get(str(t.dtype))
+
+
+def _is(t, shape, dtype):
+    """t is a contiguous tensor of this shape and element type."""
+    return tuple(t.shape) == tuple(shape) and _dtype_of(t) == dtype and t.is_contiguous()
+
+
+def _is_rows(t, like):
+    """t is a matrix of like's shape and type whose rows are contiguous."""
+    return t.shape == like.shape and t.dtype == like.dtype and (t.shape[1] <= 1 or t.stride(1) == 1)
+
+
+def _params(weight, others, cols):
+    """The parameters' element type, or None if they do not belong together."""
+    dt = _dtype_of(weight)
+    ok = dt is not None and all(_is(p, (cols,), dt) for p in (weight, *others) if p is not None)
+    return dt if ok else None
+
+
+def ar_layer_norm(x, weight, bias, y, mean=None, rstd=None, eps=1e-5, stream=None) -> int:
+    """y = layer norm of the rows of the matrix x.  bias, mean and rstd may be
+    None; weight and bias have x's type or f32; y may be x."""
+    if x.dim() != 2 or not _is_rows(x, x) or not _is_rows(y, x):
+        return AR_ERR_INVALID_ARG
+    rows, cols = x.shape
+    dt, pt = _dtype_of(x), _params(weight, (bias,), cols)
+    if dt is None:
+        return AR_ERR_UNSUPPORTED
+    if pt is None or any(s is not None and not _is(s, (rows,), 0) for s in (mean, rstd)):
+        return AR_ERR_INVALID_ARG
+    return lib.ar_layer_norm(x.data_ptr(), x.stride(0), weight.data_ptr(), _ptr(bias), y.data_ptr(), y.stride(0),
+                             _ptr(mean), _ptr(rstd), rows, cols, eps, dt, pt, _stream(stream))
+
+
+def ar_layer_norm_workspace_bytes(rows, cols) -> int:
+    return lib.ar_layer_norm_workspace_bytes(int(rows), int(cols))
+
+
+def ar_layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, workspace, stream=None) -> int:
+    """dx (may be dy or x), dweight and dbias (may be None) for an upstream
+    dy, from the forward call's mean and rstd.  workspace: a tensor of at least
+    ar_layer_norm_workspace_bytes(rows, cols) bytes."""
+    if x.dim() != 2 or not _is_rows(x, x) or not _is_rows(dy, x) or not _is_rows(dx, x):
+        return AR_ERR_INVALID_ARG
+    rows, cols = x.shape
+    dt, pt = _dtype_of(x), _params(weight, (dweight, dbias), cols)
+    if dt is None:
+        return AR_ERR_UNSUPPORTED
+    if pt is None or not _is(mean, (rows,), 0) or not _is(rstd, (rows,), 0) or not workspace.is_contiguous():
+        return AR_ERR_INVALID_ARG
+    return lib.ar_layer_norm_backward(dy.data_ptr(), dy.stride(0), x.data_ptr(), x.stride(0), weight.data_ptr(),
+                                      mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(), dx.stride(0),
+                                      dweight.data_ptr(), _ptr(dbias), rows, cols, dt, pt, workspace.data_ptr(),
+                                      workspace.numel() * workspace.element_size(), _stream(stream))
+
+
+def _distill_types(logits, teacher_index, teacher_logits, rows_f32, dlogits):
+    """(status, element types of the logits and of the teacher's)."""
+    if logits.dim() != 2 or not _is_rows(logits, logits) or (dlogits is not None and not _is_rows(dlogits, logits)):
+        return AR_ERR_INVALID_ARG, 0, 0
+    rows = logits.shape[0]
+    dt, vt = _dtype_of(logits), _dtype_of(teacher_logits)
+    if dt is None or vt is None:
+        return AR_ERR_UNSUPPORTED, 0, 0
+    if (teacher_index.dim() != 2 or not _is(teacher_index, (rows, teacher_index.shape[1]), 2)
+            or not _is(teacher_logits, teacher_index.shape, vt)
+            or any(r is not None and not _is(r, (rows,), 0) for r in rows_f32)):
+        return AR_ERR_INVALID_ARG, 0, 0
+    return AR_OK, dt, vt
+
+
+def ar_distill_loss(logits, teacher_index, teacher_logits, loss, lse, scale=None, dlogits=None, temperature=1.0,
+                    stream=None) -> int:
+    """loss and lse of each row of logits against the teacher's lists and, with
+    dlogits (which may be logits), the gradient of sum(scale * loss)."""
+    rc, dt, vt = _distill_types(logits, teacher_index, teacher_logits, (loss, lse, scale), dlogits)
+    if rc:
+        return rc
+    return lib.ar_distill_loss(logits.data_ptr(), logits.stride(0), teacher_index.data_ptr(),
+                               teacher_logits.data_ptr(), _ptr(scale), loss.data_ptr(), lse.data_ptr(), _ptr(dlogits),
+                               0 if dlogits is None else dlogits.stride(0), logits.shape[0], logits.shape[1],
+                               teacher_index.shape[1], temperature, dt, vt, _stream(stream))
+
+
+def ar_distill_loss_backward(logits, teacher_index, teacher_logits, lse, dloss, dlogits, temperature=1.0,
+                             stream=None) -> int:
+    """dlogits (which may be logits) for an upstream dloss, from the forward
+    call's lse."""
+    rc, dt, vt = _distill_types(logits, teacher_index, teacher_logits, (lse, dloss), dlogits)
+    if rc:
+        return rc
+    return lib.ar_distill_loss_backward(logits.data_ptr(), logits.stride(0), teacher_index.data_ptr(),
+                                        teacher_logits.data_ptr(), lse.data_ptr(), dloss.data_ptr(),
+                                        dlogits.data_ptr(), dlogits.stride(0), logits.shape[0], logits.shape[1],
+                                        teacher_index.shape[1], temperature, dt, vt, _stream(stream))
 
 
 def ar_chunk_range(count, nranks, c):

@@ -71,16 +71,15 @@ int check_disjoint(std::vector<Range>& rs, int esize) {
   return AR_OK;
 }
 
-// ... and lie inside device memory of the current device.
-int check_ranges(std::vector<Range>& rs, int esize) {
-  int rc = check_disjoint(rs, esize);
-  if (rc) return rc;
+// Every range lies inside device memory of the current device.  Fewest
+// queries when the ranges are sorted.
+int check_resident(const std::vector<Range>& rs) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e);
   PointerGetAttributesFn attrs = pointer_attrs_fn();
   if (!attrs) return cuda_fail(cudaErrorNotSupported);
-  // ranges are sorted: one driver query (four attributes) per allocation they fall into
+  // one driver query (four attributes) per allocation the ranges fall into
   uintptr_t alloc_lo = 0, alloc_hi = 0;
   for (const Range& r : rs) {
     if (r.lo >= alloc_lo && r.hi <= alloc_hi && alloc_hi > alloc_lo) continue;
@@ -98,6 +97,13 @@ int check_ranges(std::vector<Range>& rs, int esize) {
     if (r.lo < alloc_lo || r.hi > alloc_hi) return AR_ERR_INVALID_ARG;
   }
   return AR_OK;
+}
+
+// Every range must be non-null, element aligned, pairwise disjoint, and lie
+// inside device memory of the current device.
+int check_ranges(std::vector<Range>& rs, int esize) {
+  const int rc = check_disjoint(rs, esize);
+  return rc ? rc : check_resident(rs);
 }
 
 // Every range must be non-null, element aligned, pairwise disjoint, and lie
@@ -553,6 +559,11 @@ int check_common(int nranks, int64_t count, int dtype, int op, int algo) {
   return ::check_common(nranks, count, dtype, op, algo);
 }
 int current_context_id(unsigned long long* id) { return context_id(id); }
+int check_device_ranges(const std::vector<AddressRange>& ranges) {
+  std::vector<Range> rs;
+  for (const AddressRange& r : ranges) rs.push_back({r.lo, r.hi});
+  return check_resident(rs);
+}
 
 cudaError_t open_kernel(const void* kernel, int smem_bytes, bool big_clusters,
                         std::atomic<unsigned long long>* tag) {

@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <vector>
 
 namespace ar {
 
@@ -180,6 +181,12 @@ int sm_count();
 // count, dtype, op and algo; AVG on i32 and trees of other than 2^k ranks are
 // AR_ERR_UNSUPPORTED).
 int check_common(int nranks, int64_t count, int dtype, int op, int algo);
+// Addresses [lo, hi) of one operand.
+struct AddressRange {
+  uintptr_t lo, hi;
+};
+// AR_OK if every range lies inside device memory of the current device.
+int check_device_ranges(const std::vector<AddressRange>& ranges);
 // Records a CUDA failure for ar_last_cuda_error and maps it to a status.
 int note_cuda_failure(cudaError_t e);
 // Unique id of the context current on this thread (0 if none is current).

@@ -415,6 +415,100 @@ int ar_plan_create(int kind, void* const* bufs, int nranks, int64_t count, ar_dt
 int ar_plan_run(const ar_plan* plan, ar_stream_t stream);
 int ar_plan_destroy(ar_plan* plan);
 
+/* ---- training-step operators ------------------------------------------------
+ *
+ * The operators of a language model's training step that stand beside its
+ * library matrix products and whose gradients the collectives above combine:
+ * layer norm and distillation from a teacher's top logits, each with its
+ * gradient (additions with no counterpart on the pages).
+ *
+ * Conventions they share, beyond the common ones above:
+ *   - Sums, softmax statistics and norms are held in binary32, and each
+ *     result is rounded once to its type (nearest even).  The same call on
+ *     the same inputs gives the same bits: nothing is summed in an order that
+ *     depends on timing.
+ *   - Matrices are rows of contiguous elements; a row stride counts elements
+ *     and is at least the row's length (not looked at for a single row).
+ *   - What a call writes may overlap nothing that it reads or writes
+ *     (AR_ERR_INVALID_ARG), except where "in place" is stated.  Column ranges
+ *     of one wider buffer with the same stride do not overlap.
+ *   - i32 is AR_ERR_UNSUPPORTED; sizes beyond a kernel's 32-bit counters
+ *     (2^31 - 1 rows, 2^30 columns) are AR_ERR_TOO_LARGE.
+ *   - No call allocates or synchronises, so all of them can be captured into
+ *     a CUDA graph.
+ */
+
+/*
+ * Layer norm: for each row of x,
+ *   mean = sum(x) / cols, rstd = (sum((x - mean)^2) / cols + eps)^-1/2,
+ *   y = (x - mean) rstd weight + bias.
+ *   x, y        [rows][cols] of dtype (f32, bf16 or f16); y may be x in place
+ *   weight, bias  [cols] of param_dtype (dtype or f32); bias may be NULL
+ *   mean, rstd  [rows] f32, what the backward call needs; either may be NULL
+ *   eps         finite, >= 0
+ * Rows whose addresses and parameters lie on 16-byte boundaries move in
+ * 16-byte vectors, others one element at a time.
+ */
+int ar_layer_norm(const void* x, int64_t x_stride, const void* weight, const void* bias, void* y, int64_t y_stride,
+                  float* mean, float* rstd, int64_t rows, int64_t cols, float eps, ar_dtype dtype,
+                  ar_dtype param_dtype, ar_stream_t stream);
+
+/*
+ * Its gradient: with xh = (x - mean) rstd and g = dy weight,
+ *   dx = rstd (g - sum(g)/cols - xh sum(g xh)/cols),
+ *   dweight = sum over rows of dy xh, dbias = sum over rows of dy.
+ *   dx          [rows][cols]; may be dy or x in place
+ *   dweight, dbias  [cols] of param_dtype, overwritten (zeros if rows is 0);
+ *               dbias may be NULL
+ *   workspace   device memory of at least ar_layer_norm_workspace_bytes(rows,
+ *               cols) bytes, 4-byte aligned; its contents do not matter before
+ *               or after the call
+ */
+int ar_layer_norm_backward(const void* dy, int64_t dy_stride, const void* x, int64_t x_stride, const void* weight,
+                           const float* mean, const float* rstd, void* dx, int64_t dx_stride, void* dweight,
+                           void* dbias, int64_t rows, int64_t cols, ar_dtype dtype, ar_dtype param_dtype,
+                           void* workspace, int64_t workspace_bytes, ar_stream_t stream);
+/* Host-only; a negative ar_status for sizes the call would refuse. */
+int64_t ar_layer_norm_workspace_bytes(int64_t rows, int64_t cols);
+
+/*
+ * Distillation from a teacher's top logits.  For each row, with
+ *   p = softmax(teacher_logits / temperature) over the row's listed words,
+ *   q = softmax(logits / temperature) over the whole vocabulary:
+ *   loss = temperature^2 sum_k p_k (log p_k - log q[teacher_index_k]),
+ *   lse  = log sum_v exp(logits_v / temperature),
+ *   dlogits = scale temperature (q - sum_k p_k onehot(teacher_index_k)),
+ * the gradient of sum(scale * loss).
+ *   logits, dlogits  [rows][vocab] of dtype (f32, bf16 or f16); dlogits may be
+ *               logits in place; dlogits NULL: no gradient.  With both, each
+ *               is moved once through HBM (the row is re-read from L2).
+ *   teacher_index   [rows][top] i32.  An entry outside [0, vocab) is no entry
+ *               (lists shorter than top are padded with -1).  A word listed
+ *               more than once counts with the sum of its probabilities.
+ *   teacher_logits  [rows][top] of teacher_dtype (dtype or f32); -inf: p = 0
+ *   scale       [rows] f32, NULL: ones
+ *   loss, lse   [rows] f32
+ *   temperature finite, > 0
+ * A row without entries (or with teacher logits of -inf alone) has loss 0
+ * and a zero gradient; so has a row with scale 0 a zero gradient, whatever
+ * its logits hold.  Student logits of -inf have q = 0.
+ * top may be 0 and is at most 1024 (AR_ERR_TOO_LARGE beyond).
+ */
+int ar_distill_loss(const void* logits, int64_t logits_stride, const int32_t* teacher_index,
+                    const void* teacher_logits, const float* scale, float* loss, float* lse, void* dlogits,
+                    int64_t dlogits_stride, int64_t rows, int64_t vocab, int64_t top, float temperature,
+                    ar_dtype dtype, ar_dtype teacher_dtype, ar_stream_t stream);
+
+/*
+ * The gradient for an upstream dloss ([rows] f32, in the place of scale)
+ * that is known only after the loss: dlogits as above, from the lse that the
+ * forward call wrote for the same logits and temperature.
+ */
+int ar_distill_loss_backward(const void* logits, int64_t logits_stride, const int32_t* teacher_index,
+                             const void* teacher_logits, const float* lse, const float* dloss, void* dlogits,
+                             int64_t dlogits_stride, int64_t rows, int64_t vocab, int64_t top, float temperature,
+                             ar_dtype dtype, ar_dtype teacher_dtype, ar_stream_t stream);
+
 /* Chunk c of a rank buffer of `count` elements split N ways: [*lo, *hi).
  * Host-only; errors: AR_ERR_INVALID_ARG. */
 int ar_chunk_range(int64_t count, int nranks, int c, int64_t* lo, int64_t* hi);
