@@ -39,7 +39,12 @@ EXPORTS = ("ar_allreduce", "ar_reduce_scatter", "ar_all_gather", "ar_reduce", "a
            "ar_reducer_mark_ready", "ar_reducer_finish", "ar_reducer_destroy", "ar_reducer_buckets",
            "ar_reducer_set_max_blocks", "ar_plan_create", "ar_plan_run", "ar_plan_destroy",
            "ar_layer_norm", "ar_layer_norm_backward", "ar_layer_norm_workspace_bytes", "ar_distill_loss",
-           "ar_distill_loss_backward")
+           "ar_distill_loss_backward", "ar_attention", "ar_attention_backward", "ar_attention_workspace_bytes")
+
+
+class AttentionTensor(ctypes.Structure):
+    """ar_attention_tensor: an operand of the attention calls."""
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
 class ArError(RuntimeError):
@@ -86,17 +91,21 @@ def _load():
     L.ar_plan_create.argtypes = [cint, pp, cint, i64, cint, cint, cint, cint, ctypes.POINTER(vp)]
     L.ar_plan_run.argtypes = [vp, vp]
     L.ar_plan_destroy.argtypes = [vp]
-    flt = ctypes.c_float
+    flt, at = ctypes.c_float, ctypes.POINTER(AttentionTensor)
     L.ar_layer_norm.argtypes = [vp, i64, vp, vp, vp, i64, vp, vp, i64, i64, flt, cint, cint, vp]
     L.ar_layer_norm_backward.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, vp, i64, i64, cint, cint, vp, i64,
                                          vp]
     L.ar_layer_norm_workspace_bytes.argtypes = [i64, i64]
     L.ar_distill_loss.argtypes = [vp, i64, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, flt, cint, cint, vp]
     L.ar_distill_loss_backward.argtypes = [vp, i64, vp, vp, vp, vp, vp, i64, i64, i64, i64, flt, cint, cint, vp]
+    L.ar_attention.argtypes = [at, at, at, vp, at, vp, i64, i64, i64, i64, i64, flt, cint, vp]
+    L.ar_attention_backward.argtypes = [at, at, at, at, at, vp, vp, at, at, at, i64, i64, i64, i64, i64, flt, cint, vp,
+                                        i64, vp]
+    L.ar_attention_workspace_bytes.argtypes = [i64, i64, i64, i64]
     for name in EXPORTS:
         if name != "ar_strerror":
             getattr(L, name).restype = cint
-    for name in ("ar_kernel_launches", "ar_layer_norm_workspace_bytes"):
+    for name in ("ar_kernel_launches", "ar_layer_norm_workspace_bytes", "ar_attention_workspace_bytes"):
         getattr(L, name).restype = i64
     return L
 
@@ -435,6 +444,62 @@ def ar_distill_loss_backward(logits, teacher_index, teacher_logits, lse, dloss, 
                                         teacher_logits.data_ptr(), lse.data_ptr(), dloss.data_ptr(),
                                         dlogits.data_ptr(), dlogits.stride(0), logits.shape[0], logits.shape[1],
                                         teacher_index.shape[1], temperature, dt, vt, _stream(stream))
+
+
+def _heads(t):
+    return AttentionTensor(t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def _attention_shapes(q, k, queries, keys, cu_seqlens, lse):
+    """(status, element type): q and `queries` are [tokens, heads, dim], k and
+    `keys` [tokens, kv_heads, dim], all of one type."""
+    if q.dim() != 3 or k.dim() != 3 or q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2]:
+        return AR_ERR_INVALID_ARG, 0
+    for like, ts in ((q, (q, *queries)), (k, (k, *keys))):
+        if any(t.shape != like.shape or t.dtype != q.dtype or (t.shape[2] > 1 and t.stride(2) != 1) for t in ts):
+            return AR_ERR_INVALID_ARG, 0
+    dt = _dtype_of(q)
+    if dt is None:
+        return AR_ERR_UNSUPPORTED, 0
+    if (cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1 or not _is(cu_seqlens, cu_seqlens.shape, 2)
+            or (lse is not None and not _is(lse, (q.shape[1], q.shape[0]), 0))):
+        return AR_ERR_INVALID_ARG, 0
+    return AR_OK, dt
+
+
+def ar_attention(q, k, v, cu_seqlens, out, lse=None, scale=None, stream=None) -> int:
+    """Causal attention of q [tokens, heads, dim] over k and v [tokens,
+    kv_heads, dim], tokens packed by cu_seqlens [seqs + 1] (i32, on the
+    device).  scale None: dim ** -0.5.  lse [heads, tokens] is what the
+    backward call needs."""
+    rc, dt = _attention_shapes(q, k, (out,), (v,), cu_seqlens, lse)
+    if rc:
+        return rc
+    tokens, heads, dim = q.shape
+    return lib.ar_attention(_heads(q), _heads(k), _heads(v), cu_seqlens.data_ptr(), _heads(out), _ptr(lse), tokens,
+                            cu_seqlens.numel() - 1, heads, k.shape[1], dim, dim ** -0.5 if scale is None else scale,
+                            dt, _stream(stream))
+
+
+def ar_attention_workspace_bytes(tokens, heads, kv_heads, dim) -> int:
+    return lib.ar_attention_workspace_bytes(int(tokens), int(heads), int(kv_heads), int(dim))
+
+
+def ar_attention_backward(dout, q, k, v, out, lse, cu_seqlens, dq, dk, dv, workspace, scale=None, stream=None) -> int:
+    """dq, dk and dv for an upstream dout, from the forward call's out and
+    lse.  workspace: a tensor of at least ar_attention_workspace_bytes(tokens,
+    heads, kv_heads, dim) bytes."""
+    rc, dt = _attention_shapes(q, k, (out, dout, dq), (v, dk, dv), cu_seqlens, lse)
+    if rc:
+        return rc
+    if lse is None or not workspace.is_contiguous():
+        return AR_ERR_INVALID_ARG
+    tokens, heads, dim = q.shape
+    return lib.ar_attention_backward(_heads(dout), _heads(q), _heads(k), _heads(v), _heads(out), lse.data_ptr(),
+                                     cu_seqlens.data_ptr(), _heads(dq), _heads(dk), _heads(dv), tokens,
+                                     cu_seqlens.numel() - 1, heads, k.shape[1], dim,
+                                     dim ** -0.5 if scale is None else scale, dt, workspace.data_ptr(),
+                                     workspace.numel() * workspace.element_size(), _stream(stream))
 
 
 def ar_chunk_range(count, nranks, c):

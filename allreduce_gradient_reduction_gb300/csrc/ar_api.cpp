@@ -13,6 +13,7 @@
 #include <vector>
 
 #include "ar_internal.h"
+#include "ar_ops.h"
 
 namespace {
 
@@ -1127,6 +1128,9 @@ int ar_device_status(ar_stream_t stream, int* status) {
     int dev = 0;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return cuda_fail(e);
     *status = AR_OK;
+    // a wait inside an attention kernel that ran out is reported first
+    if ((e = ar::attention_take_status(status)) != cudaSuccess) return cuda_fail(e);
+    if (*status != AR_OK) return AR_OK;
     ar::SyncBlock* sb = nullptr;
     unsigned long long ctx = 0;
     int rc = context_id(&ctx);
@@ -1163,7 +1167,7 @@ const char* ar_strerror(int status) {
     case AR_ERR_INVALID_ARG: return "AR_ERR_INVALID_ARG: invalid argument";
     case AR_ERR_UNSUPPORTED: return "AR_ERR_UNSUPPORTED: unsupported combination";
     case AR_ERR_CUDA: return "AR_ERR_CUDA: a CUDA call failed";
-    case AR_ERR_TIMEOUT: return "AR_ERR_TIMEOUT: a step-wise barrier wait ran out";
+    case AR_ERR_TIMEOUT: return "AR_ERR_TIMEOUT: a wait inside a kernel ran out";
     case AR_ERR_NO_DEVICE: return "AR_ERR_NO_DEVICE: no usable CUDA device";
     case AR_ERR_HOST: return "AR_ERR_HOST: host-side failure (out of host memory)";
     case AR_ERR_TOO_LARGE: return "AR_ERR_TOO_LARGE: descriptor tables too large";

@@ -1,0 +1,315 @@
+// Causal attention over packed sequences, forward.
+//
+//   a_ij = scale q_i . k_j (j <= i, same sequence), out_i = sum_j p_ij v_j with
+//   p = softmax(a_i), lse_i = log sum_j exp(a_ij).
+//
+// Bound by the tensor cores at head sizes near 128 (4 dim operations a pair,
+// every operand read once per 256 queries), by the exponentials at 64 and
+// below.  One pass over the keys with a running maximum and sum: a block takes
+// 256 queries of one head as two tiles of 128, each with its scores and its
+// output in tensor memory, so that one tile's products run while the other's
+// exponentials are taken.  Ten warps: four for each tile's softmax (a thread
+// has one query's whole row of 128 scores), one that issues the products, one
+// that loads.  The probabilities take the scores' place in tensor memory as
+// 16-bit pairs and are the second product's left operand there.
+//
+// The running maximum that scales the output is moved only when a row's true
+// maximum has grown by more than 8 in the exponent of two: until then the
+// probabilities stay below 2^8, exact enough in either 16-bit type, and the
+// output need not be touched.
+#include "ar_tcgen05.cuh"
+
+#include <algorithm>
+
+#include "../../include/ar.h"
+
+namespace ar {
+namespace {
+
+__device__ int g_status;  // AR_ERR_TIMEOUT once a wait has run out
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kSlack = 8.f;  // powers of two that a row's maximum may grow by before the output is rescaled
+constexpr int kStages = 4;     // tiles of K or V in flight
+constexpr int kThreads = 320;
+constexpr int kPair = 2 * kTile;
+
+struct Shared {
+  alignas(8) uint64_t q_full[2], kv_full[kStages], kv_empty[kStages], s_full[2], p_full[2], o_done[2], own;
+  uint32_t tmem;
+  int gave_up;
+  SeqUnit unit;
+};
+
+template <class T, int PANELS>
+__global__ void __launch_bounds__(kThreads, 1)
+    attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
+                     const __grid_constant__ CUtensorMap v_map, const AttnArgs a) {
+  extern __shared__ __align__(1024) uint8_t tiles[];
+  __shared__ Shared sh;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int head = blockIdx.x % a.heads;
+
+  if (warp == 0) {
+    const SeqUnit u = find_unit(a.cu_seqlens, a.seqs, (int)a.tokens, kPair, blockIdx.x / a.heads);
+    if (lane == 0) {
+      sh.unit = u;
+      sh.gave_up = 0;
+    }
+  }
+  __syncthreads();
+  if (sh.unit.count == 0) return;
+  const SeqUnit unit = sh.unit;
+
+  constexpr uint32_t kTileBytes = PANELS * kPanelBytes;
+  const uint32_t q_tile = smem_addr(tiles), kv_tile = q_tile + 2 * kTileBytes;
+  volatile int* gave_up = &sh.gave_up;
+  if (warp == 8) tmem_alloc(smem_addr(&sh.tmem), 512);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&sh.q_full[i]), 1);
+      mbar_init(smem_addr(&sh.s_full[i]), 1);
+      mbar_init(smem_addr(&sh.p_full[i]), kTile);
+      mbar_init(smem_addr(&sh.o_done[i]), 1);
+    }
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(smem_addr(&sh.kv_full[i]), 1);
+      mbar_init(smem_addr(&sh.kv_empty[i]), 1);
+    }
+    mbar_init(smem_addr(&sh.own), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+
+  // the longest rows of a sequence first
+  const int first = (unit.count - 1 - unit.index) * kPair;  // first query of the pair, within the sequence
+  int blocks[2];                                            // tiles of keys that each tile of queries sees
+  blocks[0] = first / kTile + 1;
+  blocks[1] = first + kTile < unit.length ? blocks[0] + 1 : 0;
+  const int most = max(blocks[0], blocks[1]);
+  const int dim16 = (a.dim + 15) / 16;
+
+  if (warp == 9) {
+    // ---- loads: Q tiles, then K 0, V 0, K 1, V 1, ...
+    const int kv_head = head / (a.heads / a.kv_heads);
+    if (lane == 0) {
+      for (int i = 0; i < 2; ++i) {
+        if (!blocks[i]) continue;
+        const uint32_t bar = smem_addr(&sh.q_full[i]);
+        mbar_expect(bar, kTileBytes);
+        for (int p = 0; p < PANELS; ++p)
+          tma_load(q_tile + i * kTileBytes + p * kPanelBytes, &q_map, p * 64, head, unit.begin + first + i * kTile, bar);
+      }
+    }
+    uint32_t own_parity = 0;
+    for (int n = 0; n < 2 * most; ++n) {
+      const int stage = n % kStages;
+      if (n >= kStages && !mbar_wait(smem_addr(&sh.kv_empty[stage]), (n / kStages - 1) & 1, gave_up)) break;
+      const int key = (n >> 1) * kTile;
+      if (!load_tile(n & 1 ? &v_map : &k_map, kv_tile + stage * kTileBytes, PANELS, kv_head, unit.begin + key,
+                     n & 1 ? unit.length - key : kTile, smem_addr(&sh.kv_full[stage]), smem_addr(&sh.own), &own_parity,
+                     gave_up))
+        break;
+    }
+  } else if (warp == 8) {
+    // ---- products, all issued by one thread
+    if (lane == 0) {
+      const uint32_t qk = mma_shape<T>(kTile, false), pv = mma_shape<T>(dim16 * 16, true);
+      auto full = [&](int n) {
+        return mbar_wait(smem_addr(&sh.kv_full[n % kStages]), (n / kStages) & 1, gave_up);
+      };
+      auto scores = [&](int i, int j) {
+        const uint32_t k = kv_tile + (2 * j % kStages) * kTileBytes;
+        for (int s = 0; s < dim16; ++s)
+          mma_ss(tmem + i * 128, k_major(q_tile + i * kTileBytes, s), k_major(k, s), qk, s > 0);
+        mma_commit(smem_addr(&sh.s_full[i]));
+      };
+      bool ok = full(0);
+      for (int i = 0; i < 2 && ok; ++i)
+        if (blocks[i] && (ok = mbar_wait(smem_addr(&sh.q_full[i]), 0, gave_up))) scores(i, 0);
+      if (ok) mma_commit(smem_addr(&sh.kv_empty[0]));
+      for (int j = 0; j < most && ok; ++j) {
+        const int vn = 2 * j + 1, kn = vn + 1;
+        const uint32_t v = kv_tile + (vn % kStages) * kTileBytes;
+        ok = full(vn) && (j + 1 >= most || full(kn));
+        for (int i = 0; i < 2 && ok; ++i) {
+          if (j >= blocks[i]) continue;
+          if (!(ok = mbar_wait(smem_addr(&sh.p_full[i]), j & 1, gave_up))) break;
+          tc_fence_after();
+          for (int s = 0; s < kTile / 16; ++s)
+            mma_ts(tmem + 256 + i * 128, tmem + i * 128 + s * 8, mn_major(v, s), pv, j > 0 || s > 0);
+          mma_commit(smem_addr(&sh.o_done[i]));
+          if (j + 1 < blocks[i]) scores(i, j + 1);
+        }
+        if (!ok) break;
+        mma_commit(smem_addr(&sh.kv_empty[vn % kStages]));
+        if (j + 1 < most) mma_commit(smem_addr(&sh.kv_empty[kn % kStages]));
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---- softmax of tile i: thread t has query t's row
+    const int i = warp >> 2, n = blocks[i];
+    const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
+    const uint32_t s_at = lanes + i * 128, o_at = lanes + 256 + i * 128;
+    const int row = (warp & 3) * 32 + lane;
+    const float c = a.scale * kLog2e;
+    float m = -INFINITY, sum = 0.f;
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+      if (!(ok = mbar_wait(smem_addr(&sh.s_full[i]), j & 1, gave_up))) break;
+      tc_fence_after();
+      float s[4][32];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) tmem_load32(s_at + b * 32, s[b]);
+      tmem_wait_load();
+#pragma unroll
+      for (int b = 0; b < 4; ++b) tmem_loaded(s[b]);
+      if (j == n - 1) {
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+          for (int x = 0; x < 32; ++x)
+            if (b * 32 + x > row) s[b][x] = -INFINITY;
+      }
+      float top[4] = {s[0][0], s[1][0], s[2][0], s[3][0]};
+#pragma unroll
+      for (int x = 1; x < 32; ++x)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) top[b] = fmaxf(top[b], s[b][x]);
+      const float most_s = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+      if (j == 0) {
+        m = most_s;
+      } else if (__any_sync(0xFFFFFFFFu, (most_s - m) * c > kSlack)) {
+        const float moved = fmaxf(m, most_s);
+        const float by = m == moved ? 1.f : exp2_approx((m - moved) * c);
+        m = moved;
+        sum *= by;
+        if (!(ok = mbar_wait(smem_addr(&sh.o_done[i]), (j - 1) & 1, gave_up))) break;
+        tc_fence_after();
+        for (int d = 0; d < dim16; ++d) {
+          float o[16];
+          tmem_load16(o_at + d * 16, o);
+          tmem_wait_load();
+          tmem_loaded(o);
+#pragma unroll
+          for (int x = 0; x < 16; ++x) o[x] *= by;
+          tmem_store16(o_at + d * 16, o);
+        }
+      }
+      const float base = m == -INFINITY ? 0.f : m * c;
+      float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t p[32];
+#pragma unroll
+        for (int x = 0; x < 32; ++x) {
+          const int b = 2 * h + (x >> 4), e = 2 * (x & 15);
+          const float lo = exp2_approx(fmaf(s[b][e], c, -base)), hi = exp2_approx(fmaf(s[b][e + 1], c, -base));
+          part[x & 3] += lo + hi;
+          p[x] = pack2<T>(lo, hi);
+        }
+        tmem_store32(s_at + h * 32, p);
+      }
+      sum += (part[0] + part[1]) + (part[2] + part[3]);
+      tmem_wait_store();
+      tc_fence_before();
+      mbar_arrive(smem_addr(&sh.p_full[i]));
+    }
+    if (n && ok && mbar_wait(smem_addr(&sh.o_done[i]), (n - 1) & 1, gave_up)) {
+      tc_fence_after();
+      const int at = first + i * kTile + row;  // within the sequence
+      const int64_t token = unit.begin + at;
+      const float inv = 1.f / sum;
+      T* out = static_cast<T*>(const_cast<void*>(a.out.ptr)) + token * a.out.token_stride + head * a.out.head_stride;
+      for (int d = 0; d < dim16; ++d) {
+        float o[16];
+        tmem_load16(o_at + d * 16, o);
+        tmem_wait_load();
+        tmem_loaded(o);
+        if (at < unit.length) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (d * 16 + h * 8 >= a.dim) break;
+            *reinterpret_cast<uint4*>(out + d * 16 + h * 8) =
+                make_uint4(pack2<T>(o[h * 8] * inv, o[h * 8 + 1] * inv), pack2<T>(o[h * 8 + 2] * inv, o[h * 8 + 3] * inv),
+                           pack2<T>(o[h * 8 + 4] * inv, o[h * 8 + 5] * inv), pack2<T>(o[h * 8 + 6] * inv, o[h * 8 + 7] * inv));
+          }
+        }
+      }
+      if (a.lse && at < unit.length) a.lse[(int64_t)head * a.tokens + token] = (m * c + log2f(sum)) * kLn2;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (sh.gave_up) {
+    // copies and products in flight end by themselves: give them time
+    for (int i = 0; i < 100; ++i) __nanosleep(100000);
+    if (threadIdx.x == 0) g_status = AR_ERR_TIMEOUT;
+    __syncthreads();
+  }
+  if (warp == 8) tmem_free(tmem, 512);
+}
+
+template <class T, int PANELS>
+cudaError_t run(int dtype, const AttnArgs& a, cudaStream_t s) {
+  static std::atomic<unsigned long long> opened[256];
+  constexpr int smem = (2 + kStages) * PANELS * (int)kPanelBytes;
+  cudaError_t e = open_kernel((const void*)attention_kernel<T, PANELS>, smem, false, opened);
+  if (e != cudaSuccess) return e;
+  CUtensorMap q, k, v;
+  if (!make_tensor_map(&q, dtype, a.q, a.tokens, a.heads, a.dim) ||
+      !make_tensor_map(&k, dtype, a.k, a.tokens, a.kv_heads, a.dim) ||
+      !make_tensor_map(&v, dtype, a.v, a.tokens, a.kv_heads, a.dim))
+    return cudaErrorInvalidValue;
+  // at most this many pairs of tiles, however the tokens are split
+  const int64_t pairs = a.tokens / kPair + std::min<int64_t>(a.seqs, a.tokens);
+  attention_kernel<T, PANELS><<<(unsigned)(pairs * a.heads), kThreads, smem, s>>>(q, k, v, a);
+  count_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+bool make_tensor_map(CUtensorMap* map, int dtype, const AttnTensor& t, int64_t tokens, int heads, int dim) {
+  typedef CUresult (*Encode)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static const Encode encode = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<Encode>(p);
+  }();
+  if (!encode) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)tokens};
+  const cuuint64_t strides[2] = {(cuuint64_t)t.head_stride * 2, (cuuint64_t)t.token_stride * 2};
+  const cuuint32_t box[3] = {64, 1, kTile}, unit[3] = {1, 1, 1};
+  return encode(map, dtype == BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                const_cast<void*>(t.ptr), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaError_t launch_attention(int dtype, const AttnArgs& a, cudaStream_t s) {
+  if (dtype == BF16) return a.dim <= 64 ? run<__nv_bfloat16, 1>(dtype, a, s) : run<__nv_bfloat16, 2>(dtype, a, s);
+  return a.dim <= 64 ? run<__half, 1>(dtype, a, s) : run<__half, 2>(dtype, a, s);
+}
+
+cudaError_t attention_forward_take_status(int* status) {
+  int v = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_status, sizeof(int));
+  if (e != cudaSuccess || !v) return e;
+  *status = v;
+  v = 0;
+  return cudaMemcpyToSymbol(g_status, &v, sizeof(int));
+}
+
+}  // namespace ar

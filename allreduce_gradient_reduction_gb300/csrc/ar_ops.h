@@ -66,4 +66,28 @@ constexpr int kDistillMaxTop = 1024;
 
 cudaError_t launch_distill(int dtype, int vdtype, bool backward, const DistillArgs& a, cudaStream_t stream);
 
+// ---- attention -----------------------------------------------------------------------
+
+struct AttnTensor {
+  const void* ptr;
+  int64_t token_stride, head_stride;  // elements
+};
+
+struct AttnArgs {
+  AttnTensor q, k, v, out;
+  AttnTensor dout, dq, dk, dv;  // backward
+  float* lse;                   // [heads][tokens]
+  float* delta;                 // backward: [heads][tokens], workspace
+  const int32_t* cu_seqlens;    // [seqs + 1]
+  int64_t tokens;
+  int32_t seqs, heads, kv_heads, dim;
+  float scale;
+};
+
+cudaError_t launch_attention(int dtype, const AttnArgs& a, cudaStream_t stream);
+cudaError_t launch_attention_backward(int dtype, const AttnArgs& a, cudaStream_t stream);
+// Reads and clears what a kernel of the current device left when one of its
+// waits ran out: AR_ERR_TIMEOUT, or AR_OK.  The caller has synchronised.
+cudaError_t attention_take_status(int* status);
+
 }  // namespace ar

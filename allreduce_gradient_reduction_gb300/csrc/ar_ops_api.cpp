@@ -150,6 +150,36 @@ int distill(bool backward, const void* logits, int64_t logits_stride, const int3
   return status_of(ar::launch_distill(dtype, vdtype, backward, a, s));
 }
 
+int check_attention(int64_t tokens, int64_t seqs, int64_t heads, int64_t kv_heads, int64_t dim, float scale, int dtype) {
+  if (tokens < 0 || seqs < 0 || heads < 1 || kv_heads < 1 || dim < 1 || heads % kv_heads) return AR_ERR_INVALID_ARG;
+  if (dtype < AR_F32 || dtype > AR_F16 || !(scale > 0.f) || !std::isfinite(scale)) return AR_ERR_INVALID_ARG;
+  if ((dtype != AR_BF16 && dtype != AR_F16) || dim % 8 || dim > AR_ATTENTION_MAX_DIM) return AR_ERR_UNSUPPORTED;
+  if (tokens > (1 << 30) || seqs > (1 << 24) || heads > 4096 || (tokens / 128 + seqs) * heads > INT32_MAX) return AR_ERR_TOO_LARGE;
+  return AR_OK;
+}
+
+// A [tokens][heads][dim] operand: tokens outside heads or heads outside
+// tokens, every row of `dim` elements on a 16-byte boundary.  Strides of
+// an axis of length one are not looked at.
+bool add_tensor(Operands& o, ar::AttnTensor& t, const ar_attention_tensor& p, int64_t tokens, int64_t heads,
+                int64_t dim, bool written) {
+  int64_t ts = p.token_stride, hs = p.head_stride;
+  if (heads == 1) hs = dim;
+  if (tokens == 1) ts = heads * (hs > dim ? hs : dim);
+  if (ts < dim || hs < dim || ts > AR_MAX_COUNT || hs > AR_MAX_COUNT || ts % 8 || hs % 8) return false;
+  if ((uintptr_t)p.data % 16) return false;
+  const bool token_major = ts >= (__int128)(heads - 1) * hs + dim;
+  const bool head_major = hs >= (__int128)(tokens - 1) * ts + dim;
+  if (!token_major && !head_major) return false;
+  std::vector<Rows>* to = written ? &o.out : &o.in;
+  if (token_major) o.add(p.data, tokens, (heads - 1) * hs + dim, ts, 2, to);
+  else o.add(p.data, heads, (tokens - 1) * ts + dim, hs, 2, to);
+  t = ar::AttnTensor{p.data, ts, hs};
+  return true;
+}
+
+int64_t attention_workspace(int64_t tokens, int64_t heads) { return (tokens * heads * 4 + 15) / 16 * 16; }
+
 }  // namespace
 
 extern "C" {
@@ -237,6 +267,76 @@ int ar_distill_loss_backward(const void* logits, int64_t logits_stride, const in
     return distill(true, logits, logits_stride, teacher_index, teacher_logits, dloss, nullptr,
                    const_cast<float*>(lse), dlogits, dlogits_stride, rows, vocab, top, temperature, dtype,
                    teacher_dtype, (cudaStream_t)stream);
+  });
+}
+
+int ar_attention(const ar_attention_tensor* q, const ar_attention_tensor* k, const ar_attention_tensor* v,
+                 const int32_t* cu_seqlens, const ar_attention_tensor* out, float* lse, int64_t tokens, int64_t seqs,
+                 int64_t heads, int64_t kv_heads, int64_t dim, float scale, ar_dtype dtype, ar_stream_t stream) {
+  return guarded([&]() -> int {
+    int rc = check_attention(tokens, seqs, heads, kv_heads, dim, scale, dtype);
+    if (rc) return rc;
+    if (!q || !k || !v || !out) return AR_ERR_INVALID_ARG;
+    if (tokens == 0 || seqs == 0) return AR_OK;
+    ar::AttnArgs a{};
+    Operands o;
+    if (!add_tensor(o, a.q, *q, tokens, heads, dim, false) || !add_tensor(o, a.k, *k, tokens, kv_heads, dim, false) ||
+        !add_tensor(o, a.v, *v, tokens, kv_heads, dim, false) || !add_tensor(o, a.out, *out, tokens, heads, dim, true))
+      return AR_ERR_INVALID_ARG;
+    o.read(cu_seqlens, 1, seqs + 1, 0, 4);
+    if (lse) o.write(lse, 1, tokens * heads, 0, 4);
+    if ((rc = o.check(0))) return rc;
+    a.lse = lse;
+    a.cu_seqlens = cu_seqlens;
+    a.tokens = tokens;
+    a.seqs = (int32_t)seqs;
+    a.heads = (int32_t)heads;
+    a.kv_heads = (int32_t)kv_heads;
+    a.dim = (int32_t)dim;
+    a.scale = scale;
+    return status_of(ar::launch_attention(dtype, a, (cudaStream_t)stream));
+  });
+}
+
+int64_t ar_attention_workspace_bytes(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t dim) {
+  const int rc = check_attention(tokens, 1, heads, kv_heads, dim, 1.f, AR_BF16);
+  return rc ? rc : attention_workspace(tokens, heads);
+}
+
+int ar_attention_backward(const ar_attention_tensor* dout, const ar_attention_tensor* q, const ar_attention_tensor* k,
+                          const ar_attention_tensor* v, const ar_attention_tensor* out, const float* lse,
+                          const int32_t* cu_seqlens, const ar_attention_tensor* dq, const ar_attention_tensor* dk,
+                          const ar_attention_tensor* dv, int64_t tokens, int64_t seqs, int64_t heads,
+                          int64_t kv_heads, int64_t dim, float scale, ar_dtype dtype, void* workspace,
+                          int64_t workspace_bytes, ar_stream_t stream) {
+  return guarded([&]() -> int {
+    int rc = check_attention(tokens, seqs, heads, kv_heads, dim, scale, dtype);
+    if (rc) return rc;
+    if (!dout || !q || !k || !v || !out || !dq || !dk || !dv) return AR_ERR_INVALID_ARG;
+    if (tokens == 0 || seqs == 0) return AR_OK;
+    const int64_t need = attention_workspace(tokens, heads);
+    if (workspace_bytes < need || (uintptr_t)workspace % 16) return AR_ERR_INVALID_ARG;
+    ar::AttnArgs a{};
+    Operands o;
+    if (!add_tensor(o, a.q, *q, tokens, heads, dim, false) || !add_tensor(o, a.k, *k, tokens, kv_heads, dim, false) ||
+        !add_tensor(o, a.v, *v, tokens, kv_heads, dim, false) || !add_tensor(o, a.out, *out, tokens, heads, dim, false) ||
+        !add_tensor(o, a.dout, *dout, tokens, heads, dim, false) || !add_tensor(o, a.dq, *dq, tokens, heads, dim, true) ||
+        !add_tensor(o, a.dk, *dk, tokens, kv_heads, dim, true) || !add_tensor(o, a.dv, *dv, tokens, kv_heads, dim, true))
+      return AR_ERR_INVALID_ARG;
+    o.read(cu_seqlens, 1, seqs + 1, 0, 4);
+    o.read(lse, 1, tokens * heads, 0, 4);
+    o.write(workspace, 1, need / 4, 0, 4);
+    if ((rc = o.check(0))) return rc;
+    a.lse = const_cast<float*>(lse);
+    a.delta = static_cast<float*>(workspace);
+    a.cu_seqlens = cu_seqlens;
+    a.tokens = tokens;
+    a.seqs = (int32_t)seqs;
+    a.heads = (int32_t)heads;
+    a.kv_heads = (int32_t)kv_heads;
+    a.dim = (int32_t)dim;
+    a.scale = scale;
+    return status_of(ar::launch_attention_backward(dtype, a, (cudaStream_t)stream));
   });
 }
 

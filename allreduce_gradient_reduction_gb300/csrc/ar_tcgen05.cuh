@@ -1,0 +1,282 @@
+// Blackwell's asynchronous units, as the attention kernels use them: mbarriers
+// with bounded waits, tiled TMA loads, and the tensor cores' products from
+// shared and tensor memory (tcgen05) with their descriptors.
+//
+// Tiles in shared memory are 128 rows of 64 16-bit elements ("panels" of 16
+// KB), in the 128-byte swizzle: row r is the 128 bytes at r * 128, its 16-byte
+// pieces permuted within the row by r mod 8.  A row-major matrix of 128
+// columns is two panels.  The same panel serves a product in both readings:
+// rows as the M or N axis and columns as K ("K-major"), or rows as K and
+// columns as the N axis ("MN-major").
+#pragma once
+
+#include <cuda.h>
+#include <stdint.h>
+
+#include "ar_ops.cuh"
+
+namespace ar {
+
+constexpr int kTile = 128;                        // rows of a tile
+constexpr uint32_t kPanelBytes = kTile * 64 * 2;  // 128 rows of 128 bytes
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+
+// ---- mbarriers -------------------------------------------------------------------
+
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ uint64_t global_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+  return t;
+}
+
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+
+// Waits for the phase of the given parity to end.  Every wait is bounded: one
+// that runs out (no correct launch does) sets the block's `gave_up`, which
+// ends the other threads' waits too, and the caller returns.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
+  if (mbar_try(bar, parity)) return true;
+  const uint64_t until = global_ns() + kWaitLimitNs;
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try(bar, parity)) return true;
+    if ((i & 63) == 0) {
+      if (*gave_up) return false;
+      if (global_ns() > until) {
+        *gave_up = 1;
+        return false;
+      }
+    }
+  }
+}
+
+// ---- TMA ----------------------------------------------------------------------------
+
+// The box of one panel at (column, head, token); columns are a multiple of 64
+// elements, so every copy starts on a 16-byte boundary.
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int column, int head, int token,
+                                         uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+      ::"r"(dst), "l"(map), "r"(column), "r"(head), "r"(token), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_prefetch(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// One warp loads `panels` panels of a tile whose first `rows` rows belong to
+// the sequence.  The rows after them are another sequence's: they are
+// overwritten with zeros before the tile is announced on `full`, so that what
+// they hold (an infinity, a NaN) cannot reach a sum through a zero weight.
+// `own` is a barrier of this warp's alone for that case.
+__device__ __forceinline__ bool load_tile(const CUtensorMap* map, uint32_t dst, int panels, int head, int token,
+                                          int rows, uint32_t full, uint32_t own, uint32_t* own_parity,
+                                          volatile int* gave_up) {
+  const int lane = threadIdx.x & 31;
+  const bool cut = rows < kTile;
+  if (lane == 0) {
+    const uint32_t bar = cut ? own : full;
+    mbar_expect(bar, panels * kPanelBytes);
+    for (int p = 0; p < panels; ++p) tma_load(dst + p * kPanelBytes, map, p * 64, head, token, bar);
+  }
+  if (!cut) return true;
+  if (!mbar_wait(own, *own_parity, gave_up)) return false;
+  *own_parity ^= 1;
+  for (int p = 0; p < panels; ++p)
+    for (uint32_t b = rows * 128 + lane * 16; b < kPanelBytes; b += 512)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + p * kPanelBytes + b), "r"(0) : "memory");
+  fence_async_shared();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(full);
+  return true;
+}
+
+// ---- tensor memory -----------------------------------------------------------------
+
+// 128 lanes x 512 columns of 32 bits; an address is lane << 16 | column.  Warp
+// w reaches lanes 32 (w mod 4) ... + 31.
+__device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t columns) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(columns) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free(uint32_t base, uint32_t columns) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(columns) : "memory");
+}
+__device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// 32 or 16 columns of the thread's lane.  The registers hold the values after
+// tmem_wait_load; the empty statement there keeps uses behind it.
+__device__ __forceinline__ void tmem_load32(uint32_t at, float (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
+        "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
+        "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+      : "r"(at)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_load16(uint32_t at, float (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+      : "r"(at)
+      : "memory");
+}
+// Ties the registers to the wait before them.
+template <int N>
+__device__ __forceinline__ void tmem_loaded(float (&r)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+f"(r[i])::"memory");
+}
+__device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_store16(uint32_t at, const float (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16};" ::"r"(at),
+      "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]), "f"(r[8]), "f"(r[9]),
+      "f"(r[10]), "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]), "f"(r[15])
+      : "memory");
+}
+
+// ---- products -------------------------------------------------------------------------
+
+// Instruction descriptor: f32 sums, A and B of the same 16-bit type, M = 128.
+template <class T>
+__device__ __forceinline__ uint32_t mma_shape(int n, bool b_mn_major) {
+  const uint32_t type = sizeof(T) == 2 && __is_same(T, __nv_bfloat16) ? 1 : 0;
+  return 1u << 4 | type << 7 | type << 10 | (b_mn_major ? 1u << 16 : 0) | (uint32_t)(n >> 3) << 17 | (kTile >> 4) << 24;
+}
+
+// Shared-memory descriptors of a panel (128-byte swizzle): groups of eight
+// rows are 1024 bytes apart; MN-major operands wider than a panel find the
+// next one kPanelBytes on.
+__device__ __forceinline__ uint64_t panel_desc(uint32_t at, bool mn_major) {
+  const uint64_t lead = mn_major ? kPanelBytes >> 4 : 1;
+  return (uint64_t)((at & 0x3FFFF) >> 4) | lead << 16 | (uint64_t)(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
+// ... advanced to the k-th 16 elements along K
+__device__ __forceinline__ uint64_t k_major(uint32_t tile, int k) {
+  return panel_desc(tile + (k >> 2) * kPanelBytes + (k & 3) * 32, false);
+}
+__device__ __forceinline__ uint64_t mn_major(uint32_t tile, int k) { return panel_desc(tile + k * 16 * 128, true); }
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t shape, bool add) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\ntcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(shape), "r"((uint32_t)add)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t shape, bool add) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\ntcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+      "r"(a), "l"(b), "r"(shape), "r"((uint32_t)add)
+      : "memory");
+}
+// Arrives on the barrier when every product issued by this thread so far is done.
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// ---- 16-bit pairs ----------------------------------------------------------------------
+
+template <class T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+  const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+  const __half2 r = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// ---- packed sequences ------------------------------------------------------------------
+
+// Unit `unit` of the work that splits every sequence into ceil(length / size)
+// units, sequences in order.  `index` is its place in its sequence.
+struct SeqUnit {
+  int begin, length, index, count;
+};
+
+// By one warp; count 0 when there is no such unit.  Entries are clamped, so
+// that no value in cu_seqlens leads outside the tensors.
+__device__ __forceinline__ SeqUnit find_unit(const int32_t* cu_seqlens, int seqs, int tokens, int size, int unit) {
+  const int lane = threadIdx.x & 31;
+  int before = 0;
+  for (int s0 = 0; s0 < seqs; s0 += 32) {
+    const int s = s0 + lane;
+    int begin = 0, length = 0;
+    if (s < seqs) {
+      begin = min(max(cu_seqlens[s], 0), tokens);
+      length = min(max(cu_seqlens[s + 1], begin), tokens) - begin;
+    }
+    const int units = (length + size - 1) / size;
+    int upto = units;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+      if (lane >= d) upto += v;
+    }
+    const int place = unit - before - (upto - units);
+    const uint32_t mine = __ballot_sync(0xFFFFFFFFu, place >= 0 && place < units);
+    if (mine) {
+      const int from = __ffs(mine) - 1;
+      return SeqUnit{__shfl_sync(0xFFFFFFFFu, begin, from), __shfl_sync(0xFFFFFFFFu, length, from),
+                     __shfl_sync(0xFFFFFFFFu, place, from), __shfl_sync(0xFFFFFFFFu, units, from)};
+    }
+    before += __shfl_sync(0xFFFFFFFFu, upto, 31);
+  }
+  return SeqUnit{0, 0, 0, 0};
+}
+
+// Host: the tensor map of a [tokens][heads][dim] operand, one panel to a box.
+// False if the driver refuses it.
+bool make_tensor_map(CUtensorMap* map, int dtype, const AttnTensor& t, int64_t tokens, int heads, int dim);
+
+}  // namespace ar

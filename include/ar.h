@@ -419,8 +419,9 @@ int ar_plan_destroy(ar_plan* plan);
  *
  * The operators of a language model's training step that stand beside its
  * library matrix products and whose gradients the collectives above combine:
- * layer norm and distillation from a teacher's top logits, each with its
- * gradient (additions with no counterpart on the pages).
+ * layer norm, causal attention over packed sequences and distillation from a
+ * teacher's top logits, each with its gradient (additions with no counterpart
+ * on the pages).
  *
  * Conventions they share, beyond the common ones above:
  *   - Sums, softmax statistics and norms are held in binary32, and each
@@ -509,6 +510,66 @@ int ar_distill_loss_backward(const void* logits, int64_t logits_stride, const in
                              int64_t dlogits_stride, int64_t rows, int64_t vocab, int64_t top, float temperature,
                              ar_dtype dtype, ar_dtype teacher_dtype, ar_stream_t stream);
 
+#define AR_ATTENTION_MAX_DIM 128
+
+/* Operand of the attention calls: element (token, head, i) is at
+ * data + token * token_stride + head * head_stride + i (strides in elements).
+ * data is 16-byte aligned, the strides are multiples of 8 (a stride along an
+ * axis of length one is not looked at), and either tokens or heads are the
+ * outer axis.  The three parts of one projection's output fit, and so do
+ * [heads][tokens][dim] buffers. */
+typedef struct {
+  void* data;
+  int64_t token_stride, head_stride;
+} ar_attention_tensor;
+
+/*
+ * Causal attention over whole prompts packed one after another, with grouped
+ * heads.  Sequence s holds tokens [cu_seqlens[s], cu_seqlens[s+1]); for token
+ * i of it and head h, over the tokens j <= i of the same sequence,
+ *   a_j = scale q[i,h] . k[j, h / (heads / kv_heads)],
+ *   out[i,h] = sum_j softmax(a)_j v[j, h / (heads / kv_heads)],
+ *   lse[h][i] = log sum_j exp(a_j).
+ *   q, out      [tokens][heads][dim], k, v [tokens][kv_heads][dim] of dtype:
+ *               bf16 or f16 (f32 is AR_ERR_UNSUPPORTED: the products run on
+ *               the tensor cores); heads a multiple of kv_heads; dim a
+ *               multiple of 8 up to 128
+ *   cu_seqlens  [seqs + 1] i32 on the device, not decreasing, within [0,
+ *               tokens]; sequences may be empty.  Entries are clamped to
+ *               [0, tokens]; what lies outside every sequence is neither used
+ *               nor written.
+ *   lse         [heads][tokens] f32, what the backward call needs; may be NULL
+ *   scale       finite, > 0
+ * Infinities and NaN in tokens of another sequence, or outside all of them,
+ * do not reach a sequence's results.  Within a sequence a value of v that is
+ * not finite reaches its own token's result and later ones, and may reach
+ * those of up to 127 earlier tokens.
+ * The unnormalised probabilities are rounded to dtype for their product with v.
+ */
+int ar_attention(const ar_attention_tensor* q, const ar_attention_tensor* k, const ar_attention_tensor* v,
+                 const int32_t* cu_seqlens, const ar_attention_tensor* out, float* lse, int64_t tokens, int64_t seqs,
+                 int64_t heads, int64_t kv_heads, int64_t dim, float scale, ar_dtype dtype, ar_stream_t stream);
+
+/*
+ * Its gradient for an upstream dout: with p = exp(a - lse),
+ *   delta[i,h] = dout[i,h] . out[i,h],
+ *   da_ij = p_ij (dout[i,h] . v[j] - delta[i,h]),
+ *   dq = scale sum_j da_ij k[j], dk = scale sum_i da_ij q[i],
+ *   dv = sum_i p_ij dout[i], dk and dv summed over the heads of a group.
+ *   out, lse    of the forward call on the same q, k, v and cu_seqlens
+ *   workspace   16-byte aligned device memory of at least
+ *               ar_attention_workspace_bytes bytes
+ * p and da are rounded to dtype for their products.
+ */
+int ar_attention_backward(const ar_attention_tensor* dout, const ar_attention_tensor* q, const ar_attention_tensor* k,
+                          const ar_attention_tensor* v, const ar_attention_tensor* out, const float* lse,
+                          const int32_t* cu_seqlens, const ar_attention_tensor* dq, const ar_attention_tensor* dk,
+                          const ar_attention_tensor* dv, int64_t tokens, int64_t seqs, int64_t heads,
+                          int64_t kv_heads, int64_t dim, float scale, ar_dtype dtype, void* workspace,
+                          int64_t workspace_bytes, ar_stream_t stream);
+/* Host-only; a negative ar_status for sizes the calls would refuse. */
+int64_t ar_attention_workspace_bytes(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t dim);
+
 /* Chunk c of a rank buffer of `count` elements split N ways: [*lo, *hi).
  * Host-only; errors: AR_ERR_INVALID_ARG. */
 int ar_chunk_range(int64_t count, int nranks, int c, int64_t* lo, int64_t* hi);
@@ -516,8 +577,9 @@ int ar_chunk_range(int64_t count, int nranks, int c, int64_t* lo, int64_t* hi);
 /*
  * Synchronises `stream`, then reads and clears the current device's
  * asynchronous status word: *status = AR_OK, or AR_ERR_TIMEOUT when a
- * step-wise barrier gave up waiting since the last read (the kernel then
- * stopped early and its buffers hold partial results).
+ * step-wise barrier, or a wait inside an attention kernel, gave up waiting
+ * since the last read (the kernel then stopped early and its buffers hold
+ * partial results).
  * Errors: AR_ERR_INVALID_ARG (status NULL), AR_ERR_CUDA.
  */
 int ar_device_status(ar_stream_t stream, int* status);

@@ -1,6 +1,6 @@
 """ar_distill_loss and ar_distill_loss_backward against the formula in 64 bits.
 
-Tolerances.  u is the relative spacing of the result's type, and the arithmetic
+Tolerances.  u is the unit roundoff of the result's type, and the arithmetic
 before the one rounding to it is binary32 (unit 2^-24).  An exponent z/tau -
 lse is off by a few units of |z|/tau + |lse| (below 64 in these tests, but for
 the rows that are made extreme), so a probability by at most 2^-16 of itself; a

@@ -1,7 +1,7 @@
 """ar_layer_norm and ar_layer_norm_backward against the formula in 64 bits.
 
-Tolerances.  u is the relative spacing of the result's type (2^-24 f32, 2^-8
-bf16, 2^-11 f16): one rounding of the result costs at most u/2 of it.  The
+Tolerances.  u is the unit roundoff of the result's type (2^-24 f32, 2^-8
+bf16, 2^-11 f16): one rounding of the result costs at most u of it.  The
 arithmetic before it is binary32 (unit 2^-24); a row's sums add at most 32
 elements in a thread, then five levels in a warp and five across warps, so a
 sum is off by at most 42 units of the sum of magnitudes, and the few products
