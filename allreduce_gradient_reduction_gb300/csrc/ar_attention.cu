@@ -8,10 +8,11 @@
 // below.  One pass over the keys with a running maximum and sum: a block takes
 // 256 queries of one head as two tiles of 128, each with its scores and its
 // output in tensor memory, so that one tile's products run while the other's
-// exponentials are taken.  Ten warps: four for each tile's softmax (a thread
-// has one query's whole row of 128 scores), one that issues the products, one
-// that loads.  The probabilities take the scores' place in tensor memory as
-// 16-bit pairs and are the second product's left operand there.
+// exponentials are taken.  Four warps for each tile's softmax (a thread has one
+// query's whole row of 128 scores), one that issues the products, one that
+// loads, two that only give their registers.  The probabilities go back to
+// tensor memory as 16-bit pairs and are the second product's left operand
+// there.
 //
 // The running maximum that scales the output is moved only when a row's true
 // maximum has grown by more than 8 in the exponent of two: until then the
@@ -32,11 +33,12 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.f;  // powers of two that a row's maximum may grow by before the output is rescaled
 constexpr int kStages = 4;     // tiles of K or V in flight
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
 constexpr int kPair = 2 * kTile;
 
 struct Shared {
-  alignas(8) uint64_t q_full[2], kv_full[kStages], kv_empty[kStages], s_full[2], p_full[2], o_done[2], own;
+  alignas(8) uint64_t q_full[2], kv_full[kStages], kv_empty[kStages], s_full[2], s_read[2], p_full[2][2], o_done[2],
+      own;
   uint32_t tmem;
   int gave_up;
   SeqUnit unit;
@@ -70,7 +72,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&sh.q_full[i]), 1);
       mbar_init(smem_addr(&sh.s_full[i]), 1);
-      mbar_init(smem_addr(&sh.p_full[i]), kTile);
+      mbar_init(smem_addr(&sh.s_read[i]), 4);
+      mbar_init(smem_addr(&sh.p_full[i][0]), 4);
+      mbar_init(smem_addr(&sh.p_full[i][1]), 4);
       mbar_init(smem_addr(&sh.o_done[i]), 1);
     }
     for (int i = 0; i < kStages; ++i) {
@@ -84,6 +88,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
+  // Tensor memory, for tile i: scores at 128 i, output behind both tiles'
+  // scores.  Outputs of up to 64 columns leave room for the probabilities
+  // beside the scores, so that the next scores are computed as soon as the
+  // current ones have been read; wider ones do not, and the probabilities
+  // take the scores' first 64 columns.
+  constexpr bool kApart = PANELS == 1;
+  auto p_at = [&](int i) { return tmem + (kApart ? 256 + i * 64 : i * 128); };
+  auto out_at = [&](int i) { return tmem + (kApart ? 384 + i * 64 : 256 + i * 128); };
 
   // the longest rows of a sequence first
   const int first = (unit.count - 1 - unit.index) * kPair;  // first query of the pair, within the sequence
@@ -93,7 +105,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int most = max(blocks[0], blocks[1]);
   const int dim16 = (a.dim + 15) / 16;
 
-  if (warp == 9) {
+  if (warp >= 8) {
+    give_registers();
+    if (warp == 9) {
     // ---- loads: Q tiles, then K 0, V 0, K 1, V 1, ...
     const int kv_head = head / (a.heads / a.kv_heads);
     if (lane == 0) {
@@ -117,16 +131,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 8) {
     // ---- products, all issued by one thread
-    if (lane == 0) {
+    if (elect_one()) {
       const uint32_t qk = mma_shape<T>(kTile, false), pv = mma_shape<T>(dim16 * 16, true);
       auto full = [&](int n) {
         return mbar_wait(smem_addr(&sh.kv_full[n % kStages]), (n / kStages) & 1, gave_up);
       };
       auto scores = [&](int i, int j) {
-        const uint32_t k = kv_tile + (2 * j % kStages) * kTileBytes;
-        for (int s = 0; s < dim16; ++s)
-          mma_ss(tmem + i * 128, k_major(q_tile + i * kTileBytes, s), k_major(k, s), qk, s > 0);
+        product_ss<4 * PANELS>(tmem + i * 128, q_tile + i * kTileBytes, kv_tile + (2 * j % kStages) * kTileBytes, qk, dim16);
         mma_commit(smem_addr(&sh.s_full[i]));
+      };
+      auto output = [&](int i, int j) {
+        const uint32_t v = kv_tile + ((2 * j + 1) % kStages) * kTileBytes;
+        for (int h = 0; h < 2; ++h) {
+          if (!mbar_wait(smem_addr(&sh.p_full[i][h]), j & 1, gave_up)) return false;
+          tc_fence_after();
+          product_ts<4>(out_at(i), p_at(i) + h * 32, v, h, pv, j > 0 || h > 0);
+        }
+        mma_commit(smem_addr(&sh.o_done[i]));
+        return true;
       };
       bool ok = full(0);
       for (int i = 0; i < 2 && ok; ++i)
@@ -134,28 +156,43 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok) mma_commit(smem_addr(&sh.kv_empty[0]));
       for (int j = 0; j < most && ok; ++j) {
         const int vn = 2 * j + 1, kn = vn + 1;
-        const uint32_t v = kv_tile + (vn % kStages) * kTileBytes;
-        ok = full(vn) && (j + 1 >= most || full(kn));
-        for (int i = 0; i < 2 && ok; ++i) {
-          if (j >= blocks[i]) continue;
-          if (!(ok = mbar_wait(smem_addr(&sh.p_full[i]), j & 1, gave_up))) break;
-          tc_fence_after();
-          for (int s = 0; s < kTile / 16; ++s)
-            mma_ts(tmem + 256 + i * 128, tmem + i * 128 + s * 8, mn_major(v, s), pv, j > 0 || s > 0);
-          mma_commit(smem_addr(&sh.o_done[i]));
-          if (j + 1 < blocks[i]) scores(i, j + 1);
+        if constexpr (kApart) {
+          if (j + 1 < most) {
+            if (!(ok = full(kn))) break;
+            for (int i = 0; i < 2 && ok; ++i) {
+              if (j + 1 >= blocks[i]) continue;
+              if (!(ok = mbar_wait(smem_addr(&sh.s_read[i]), j & 1, gave_up))) break;
+              tc_fence_after();
+              scores(i, j + 1);
+            }
+            if (!ok) break;
+            mma_commit(smem_addr(&sh.kv_empty[kn % kStages]));
+          }
+          ok = full(vn);
+          for (int i = 0; i < 2 && ok; ++i)
+            if (j < blocks[i]) ok = output(i, j);
+          if (!ok) break;
+          mma_commit(smem_addr(&sh.kv_empty[vn % kStages]));
+        } else {
+          ok = full(vn) && (j + 1 >= most || full(kn));
+          for (int i = 0; i < 2 && ok; ++i) {
+            if (j >= blocks[i]) continue;
+            if ((ok = output(i, j)) && j + 1 < blocks[i]) scores(i, j + 1);
+          }
+          if (!ok) break;
+          mma_commit(smem_addr(&sh.kv_empty[vn % kStages]));
+          if (j + 1 < most) mma_commit(smem_addr(&sh.kv_empty[kn % kStages]));
         }
-        if (!ok) break;
-        mma_commit(smem_addr(&sh.kv_empty[vn % kStages]));
-        if (j + 1 < most) mma_commit(smem_addr(&sh.kv_empty[kn % kStages]));
       }
     }
     __syncwarp();
+    }
   } else {
+    take_registers();
     // ---- softmax of tile i: thread t has query t's row
     const int i = warp >> 2, n = blocks[i];
-    const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
-    const uint32_t s_at = lanes + i * 128, o_at = lanes + 256 + i * 128;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+    const uint32_t s_at = lanes + tmem + i * 128, o_at = lanes + out_at(i);
     const int row = (warp & 3) * 32 + lane;
     const float c = a.scale * kLog2e;
     float m = -INFINITY, sum = 0.f;
@@ -163,25 +200,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int j = 0; j < n; ++j) {
       if (!(ok = mbar_wait(smem_addr(&sh.s_full[i]), j & 1, gave_up))) break;
       tc_fence_after();
-      float s[4][32];
+      float s[4][32], top[4];
+      tmem_load32(s_at, s[0]);
 #pragma unroll
-      for (int b = 0; b < 4; ++b) tmem_load32(s_at + b * 32, s[b]);
-      tmem_wait_load();
-#pragma unroll
-      for (int b = 0; b < 4; ++b) tmem_loaded(s[b]);
-      if (j == n - 1) {
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
+      for (int b = 0; b < 4; ++b) {
+        tmem_wait_load();
+        tmem_loaded(s[b]);
+        if (b < 3) tmem_load32(s_at + (b + 1) * 32, s[b + 1]);  // on its way while these are looked at
+        if (j == n - 1) {
 #pragma unroll
           for (int x = 0; x < 32; ++x)
             if (b * 32 + x > row) s[b][x] = -INFINITY;
+        }
+        float even = fmaxf(s[b][0], s[b][1]), odd = fmaxf(s[b][2], s[b][3]);
+#pragma unroll
+        for (int x = 4; x < 32; x += 4) {
+          even = max3(even, s[b][x], s[b][x + 1]);
+          odd = max3(odd, s[b][x + 2], s[b][x + 3]);
+        }
+        top[b] = fmaxf(even, odd);
       }
-      float top[4] = {s[0][0], s[1][0], s[2][0], s[3][0]};
-#pragma unroll
-      for (int x = 1; x < 32; ++x)
-#pragma unroll
-        for (int b = 0; b < 4; ++b) top[b] = fmaxf(top[b], s[b][x]);
-      const float most_s = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+      if constexpr (kApart) {
+        warp_arrive(smem_addr(&sh.s_read[i]));
+      }
+      const float most_s = max3(fmaxf(top[0], top[1]), top[2], top[3]);
       if (j == 0) {
         m = most_s;
       } else if (__any_sync(0xFFFFFFFFu, (most_s - m) * c > kSlack)) {
@@ -202,23 +244,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       const float base = m == -INFINITY ? 0.f : m * c;
-      float part[4] = {0.f, 0.f, 0.f, 0.f};
+      const Two c2 = two(c, c), base2 = two(-base, -base);
+      Two part[2] = {two(0.f, 0.f), two(0.f, 0.f)};
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t p[32];
 #pragma unroll
         for (int x = 0; x < 32; ++x) {
           const int b = 2 * h + (x >> 4), e = 2 * (x & 15);
-          const float lo = exp2_approx(fmaf(s[b][e], c, -base)), hi = exp2_approx(fmaf(s[b][e + 1], c, -base));
-          part[x & 3] += lo + hi;
+          float lo, hi;
+          split(fma2(two(s[b][e], s[b][e + 1]), c2, base2), lo, hi);
+          lo = exp2_approx(lo);
+          hi = exp2_approx(hi);
+          part[x & 1] = add2(part[x & 1], two(lo, hi));
           p[x] = pack2<T>(lo, hi);
         }
-        tmem_store32(s_at + h * 32, p);
+        if (kApart && h == 0 && j > 0) {
+          // the last product has read the probabilities that these replace
+          if (!(ok = mbar_wait(smem_addr(&sh.o_done[i]), (j - 1) & 1, gave_up))) break;
+          tc_fence_after();
+        }
+        tmem_store32(lanes + p_at(i) + h * 32, p);
+        tmem_wait_store();
+        warp_arrive(smem_addr(&sh.p_full[i][h]));
       }
-      sum += (part[0] + part[1]) + (part[2] + part[3]);
-      tmem_wait_store();
-      tc_fence_before();
-      mbar_arrive(smem_addr(&sh.p_full[i]));
+      if (!ok) break;
+      float sum_lo, sum_hi;
+      split(add2(part[0], part[1]), sum_lo, sum_hi);
+      sum += sum_lo + sum_hi;
     }
     if (n && ok && mbar_wait(smem_addr(&sh.o_done[i]), (n - 1) & 1, gave_up)) {
       tc_fence_after();
@@ -262,6 +315,12 @@ cudaError_t run(int dtype, const AttnArgs& a, cudaStream_t s) {
   constexpr int smem = (2 + kStages) * PANELS * (int)kPanelBytes;
   cudaError_t e = open_kernel((const void*)attention_kernel<T, PANELS>, smem, false, opened);
   if (e != cudaSuccess) return e;
+  // the warpgroups' shares are sound only if the launch brings them
+  static const int registers = [] {
+    cudaFuncAttributes f;
+    return cudaFuncGetAttributes(&f, (const void*)attention_kernel<T, PANELS>) == cudaSuccess ? f.numRegs : 0;
+  }();
+  if (registers != kLaunchRegisters) return cudaErrorInvalidConfiguration;
   CUtensorMap q, k, v;
   if (!make_tensor_map(&q, dtype, a.q, a.tokens, a.heads, a.dim) ||
       !make_tensor_map(&k, dtype, a.k, a.tokens, a.kv_heads, a.dim) ||

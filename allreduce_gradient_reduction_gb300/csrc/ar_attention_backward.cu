@@ -12,8 +12,8 @@
 // products where five are the least; a single kernel would have to add dq from
 // many blocks to memory, in an order that changes.
 //
-// In both, eight warps take the exponentials: two threads share a row of the
-// tile, 64 columns each.  p and ds take the places of the scores and of
+// In both, sixteen warps take the exponentials: four threads share a row of
+// the tile, 32 columns each.  p and ds take the places of the scores and of
 // dout v^T in tensor memory, as 16-bit pairs, and are the left operands of the
 // sums' products there.  The next tiles' products are issued between the
 // current one's sums, so the tensor cores work while exponentials are taken.
@@ -29,7 +29,9 @@ namespace {
 __device__ int g_status;  // AR_ERR_TIMEOUT once a wait has run out
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kThreads = 320;
+constexpr int kThreads = 576;
+constexpr int kIssuer = 16, kLoader = 17;  // warps
+constexpr int kWorkers = 512;              // threads of the others
 
 // delta[head][token] = dout . out: 16 threads to a row, 16 bytes each.
 template <class T>
@@ -78,17 +80,59 @@ __device__ __forceinline__ void leave(int* gave_up, int warp, uint32_t tmem) {
     if (threadIdx.x == 0) g_status = AR_ERR_TIMEOUT;
     __syncthreads();
   }
-  if (warp == 8) tmem_free(tmem, 512);
+  if (warp == kIssuer) tmem_free(tmem, 512);
+}
+
+// 32 scores of a thread become probabilities 2^(c s - lse) in place, and pairs
+// of them in `packed`; `seen` is asked in the tile on the diagonal alone.
+template <class T, class L, class S>
+__device__ __forceinline__ void probabilities(float (&p)[32], uint32_t (&packed)[16], float c, L lse, bool diagonal,
+                                              S seen) {
+  const Two c2 = two(c, c);
+#pragma unroll
+  for (int x = 0; x < 32; x += 2) {
+    split(fma2(two(p[x], p[x + 1]), c2, lse(x)), p[x], p[x + 1]);
+    p[x] = exp2_approx(p[x]);
+    p[x + 1] = exp2_approx(p[x + 1]);
+  }
+  if (diagonal) {
+#pragma unroll
+    for (int x = 0; x < 32; ++x)
+      if (!seen(x)) p[x] = 0.f;
+  }
+#pragma unroll
+  for (int x = 0; x < 32; x += 2) packed[x / 2] = pack2<T>(p[x], p[x + 1]);
+}
+
+// Pairs of ds = p (d - delta).  What is not seen has p = 0 and no ds, whatever
+// d holds there (tokens of another sequence, in the tile on the diagonal).
+template <class T, class L>
+__device__ __forceinline__ void score_gradients(float (&p)[32], float (&d)[32], uint32_t (&packed)[16], L minus_delta,
+                                                bool diagonal) {
+  if (diagonal) {
+#pragma unroll
+    for (int x = 0; x < 32; ++x)
+      if (p[x] == 0.f) d[x] = 0.f;
+  }
+#pragma unroll
+  for (int x = 0; x < 32; x += 2) {
+    float lo, hi;
+    split(mul2(two(p[x], p[x + 1]), add2(two(d[x], d[x + 1]), minus_delta(x))), lo, hi);
+    packed[x / 2] = pack2<T>(lo, hi);
+  }
 }
 
 // ---- dk and dv ---------------------------------------------------------------------
 
-constexpr int kStages = 2;  // tiles of queries (q and dout) in flight
+constexpr int kMostStages = 4;
+
+// Tiles of queries (q and dout) in flight: as many as fit beside k and v.
+__host__ __device__ constexpr int query_stages(int panels) { return panels == 1 ? kMostStages : 2; }
 
 struct SharedKV {
-  alignas(8) uint64_t kv_full, q_full[kStages], do_full[kStages], empty[kStages], s_full, dp_full, p_ready, ds_ready,
-      done, own;
-  alignas(16) float lse[2][2][64], delta[2][2][64];  // [buffer][half]
+  alignas(8) uint64_t kv_full, q_full[kMostStages], do_full[kMostStages], empty[kMostStages], s_full, s_read, dp_full,
+      dp_read, p_ready, ds_ready, dv_done, dk_done, done, own;
+  alignas(16) float lse[2][4][32], delta[2][4][32];  // [turn][quarter]
   uint32_t tmem;
   int gave_up;
   SeqUnit unit;
@@ -99,6 +143,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     attention_dkv_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                          const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap do_map,
                          const AttnArgs a) {
+  constexpr int kStages = query_stages(PANELS);
   extern __shared__ __align__(1024) uint8_t tiles[];
   __shared__ SharedKV sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -118,25 +163,38 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t k_tile = smem_addr(tiles), v_tile = k_tile + kTileBytes, q_tile = v_tile + kTileBytes,
                  do_tile = q_tile + kStages * kTileBytes;
   volatile int* gave_up = &sh.gave_up;
-  if (warp == 8) tmem_alloc(smem_addr(&sh.tmem), 512);
+  if (warp == kIssuer) tmem_alloc(smem_addr(&sh.tmem), 512);
   if (threadIdx.x == 0) {
-    uint64_t* const one[] = {&sh.kv_full, &sh.q_full[0], &sh.q_full[1], &sh.do_full[0], &sh.do_full[1], &sh.empty[0],
-                             &sh.empty[1], &sh.s_full, &sh.dp_full, &sh.done, &sh.own};
+    uint64_t* const one[] = {&sh.kv_full, &sh.s_full, &sh.dp_full, &sh.dv_done, &sh.dk_done, &sh.done, &sh.own};
     for (uint64_t* b : one) mbar_init(smem_addr(b), 1);
-    mbar_init(smem_addr(&sh.p_ready), 256);
-    mbar_init(smem_addr(&sh.ds_ready), 256);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(smem_addr(&sh.q_full[i]), 1);
+      mbar_init(smem_addr(&sh.do_full[i]), 1);
+      mbar_init(smem_addr(&sh.empty[i]), 1);
+    }
+    uint64_t* const all[] = {&sh.s_read, &sh.dp_read, &sh.p_ready, &sh.ds_ready};
+    for (uint64_t* b : all) mbar_init(smem_addr(b), kWorkers / 32);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sh.tmem;  // columns: scores 0, dout v^T 128, dv 256, dk 384
+  const uint32_t tmem = sh.tmem;
+  // Tensor memory: scores 0, dout v^T 128, dv 256.  Heads of up to 64 leave
+  // room for p and ds beside them, so that the next tile's products run as
+  // soon as the current scores and dout v^T have been read; otherwise they
+  // take those places, each quarter's 16 columns of pairs at the front of the
+  // 32 that it read.
+  constexpr bool kApart = PANELS == 1;
+  const uint32_t dv_at = tmem + 256, dk_at = tmem + (kApart ? 320 : 384);
+  auto p_at = [&](int quarter) { return tmem + (kApart ? 384 + quarter * 16 : quarter * 32); };
+  auto ds_at = [&](int quarter) { return tmem + (kApart ? 448 + quarter * 16 : 128 + quarter * 32); };
 
   // step n: head n / per of the group, tile of queries unit.index + n % per
   const int group = a.heads / a.kv_heads, per = unit.count - unit.index, steps = group * per;
   const int dim16 = (a.dim + 15) / 16;
 
-  if (warp == 9) {
+  if (warp == kLoader) {
     if (lane == 0) {
       const uint32_t bar = smem_addr(&sh.kv_full);
       mbar_expect(bar, 2 * kTileBytes);
@@ -156,57 +214,69 @@ __global__ void __launch_bounds__(kThreads, 1)
                      smem_addr(&sh.do_full[stage]), smem_addr(&sh.own), &own_parity, gave_up))
         break;
     }
-  } else if (warp == 8) {
-    if (lane == 0) {
+  } else if (warp == kIssuer) {
+    if (elect_one()) {
       const uint32_t wide = mma_shape<T>(kTile, false), sums = mma_shape<T>(dim16 * 16, true);
       auto at = [&](uint32_t tile, int n) { return tile + (n % kStages) * kTileBytes; };
       auto scores = [&](int n) {  // K Q^T
         if (!mbar_wait(smem_addr(&sh.q_full[n % kStages]), (n / kStages) & 1, gave_up)) return false;
-        for (int s = 0; s < dim16; ++s) mma_ss(tmem, k_major(k_tile, s), k_major(at(q_tile, n), s), wide, s > 0);
+        product_ss<4 * PANELS>(tmem, k_tile, at(q_tile, n), wide, dim16);
         mma_commit(smem_addr(&sh.s_full));
         return true;
       };
       auto dprob = [&](int n) {  // V dout^T
         if (!mbar_wait(smem_addr(&sh.do_full[n % kStages]), (n / kStages) & 1, gave_up)) return false;
-        for (int s = 0; s < dim16; ++s) mma_ss(tmem + 128, k_major(v_tile, s), k_major(at(do_tile, n), s), wide, s > 0);
+        product_ss<4 * PANELS>(tmem + 128, v_tile, at(do_tile, n), wide, dim16);
         mma_commit(smem_addr(&sh.dp_full));
         return true;
       };
-      // a half's 32 columns of pairs lie at the front of the 64 that it read
-      auto sum = [&](uint32_t to, uint32_t from, uint32_t right, bool add) {
-        for (int s = 0; s < kTile / 16; ++s)
-          mma_ts(to, from + (s >> 2) * 64 + (s & 3) * 8, mn_major(right, s), sums, add || s > 0);
+      auto ready = [&](uint64_t& bar, int n) {
+        if (!mbar_wait(smem_addr(&bar), n & 1, gave_up)) return false;
+        tc_fence_after();
+        return true;
+      };
+      auto sum_dv = [&](int n) {
+        if (!ready(sh.p_ready, n)) return false;
+        for (int h = 0; h < 4; ++h) product_ts<2>(dv_at, p_at(h), at(do_tile, n), h, sums, n > 0 || h > 0);
+        if (kApart) mma_commit(smem_addr(&sh.dv_done));
+        return true;
+      };
+      auto sum_dk = [&](int n) {
+        if (!ready(sh.ds_ready, n)) return false;
+        for (int h = 0; h < 4; ++h) product_ts<2>(dk_at, ds_at(h), at(q_tile, n), h, sums, n > 0 || h > 0);
+        if (kApart) mma_commit(smem_addr(&sh.dk_done));
+        mma_commit(smem_addr(&sh.empty[n % kStages]));
+        return true;
       };
       bool ok = mbar_wait(smem_addr(&sh.kv_full), 0, gave_up) && scores(0) && dprob(0);
       for (int n = 0; n < steps && ok; ++n) {
-        if (!(ok = mbar_wait(smem_addr(&sh.p_ready), n & 1, gave_up))) break;
-        tc_fence_after();
-        sum(tmem + 256, tmem, at(do_tile, n), n > 0);
-        if (n + 1 < steps && !(ok = scores(n + 1))) break;
-        if (!(ok = mbar_wait(smem_addr(&sh.ds_ready), n & 1, gave_up))) break;
-        tc_fence_after();
-        sum(tmem + 384, tmem + 128, at(q_tile, n), n > 0);
-        mma_commit(smem_addr(&sh.empty[n % kStages]));
-        if (n + 1 < steps && !(ok = dprob(n + 1))) break;
+        const bool more = n + 1 < steps;
+        if constexpr (kApart) {
+          ok = (!more || (ready(sh.s_read, n) && scores(n + 1))) && sum_dv(n) &&
+               (!more || (ready(sh.dp_read, n) && dprob(n + 1))) && sum_dk(n);
+        } else {
+          ok = sum_dv(n) && (!more || scores(n + 1)) && sum_dk(n) && (!more || dprob(n + 1));
+        }
       }
       if (ok) mma_commit(smem_addr(&sh.done));
     }
     __syncwarp();
   } else {
-    // thread: key row, queries [64 half, 64 half + 64) of each tile
-    const int half = warp >> 2, row = (warp & 3) * 32 + lane, t = threadIdx.x & 127;
-    const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
+    // thread: key row, queries [32 quarter, 32 quarter + 32) of each tile
+    const int quarter = warp >> 2, row = (warp & 3) * 32 + lane, t = threadIdx.x & 127;
+    const uint32_t lane0 = (uint32_t)(warp & 3) << 21, s_at = tmem + lane0 + quarter * 32;
     const float c = a.scale * kLog2e;
-    // threads 0..63 of a half fetch its queries' lse, the others their delta
+    // threads 0..31 of a quarter fetch its queries' -lse in powers of two, the next 32 their -delta
     auto fetch = [&](int n) {
-      const int query = (unit.index + n % per) * kTile + half * 64 + (t & 63);
-      if (query >= unit.length) return t < 64 ? INFINITY : 0.f;  // p = 0 after the sequence's end
+      const int query = (unit.index + n % per) * kTile + quarter * 32 + (t & 31);
+      if (t >= 64) return 0.f;
+      if (query >= unit.length) return t < 32 ? -INFINITY : 0.f;  // p = 0 after the sequence's end
       const int64_t at = (int64_t)(kv_head * group + n / per) * a.tokens + unit.begin + query;
-      return t < 64 ? a.lse[at] * kLog2e : a.delta[at];
+      return t < 32 ? -a.lse[at] * kLog2e : -a.delta[at];
     };
     auto put = [&](int n, float v) {
-      (t < 64 ? sh.lse : sh.delta)[n & 1][half][t & 63] = v;
-      named_barrier(1 + half, 128);
+      if (t < 64) (t < 32 ? sh.lse : sh.delta)[n & 1][quarter][t & 31] = v;
+      named_barrier(1 + quarter, 128);
     };
     put(0, fetch(0));
     bool ok = true;
@@ -215,65 +285,53 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool diagonal = n % per == 0;
       if (!(ok = mbar_wait(smem_addr(&sh.s_full), n & 1, gave_up))) break;
       tc_fence_after();
-      float p[2][32];
-      tmem_load32(lanes + half * 64, p[0]);
-      tmem_load32(lanes + half * 64 + 32, p[1]);
+      float p[32], d[32];
+      uint32_t packed[16];
+      tmem_load32(s_at, p);
       tmem_wait_load();
-      tmem_loaded(p[0]);
-      tmem_loaded(p[1]);
-      uint32_t packed[32];
-#pragma unroll
-      for (int x = 0; x < 64; x += 4) {
-        const float4 l = *reinterpret_cast<const float4*>(&sh.lse[n & 1][half][x]);
-        const float ls[4] = {l.x, l.y, l.z, l.w};
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          float& e = p[x >> 5][(x & 31) + y];
-          e = exp2_approx(fmaf(e, c, -ls[y]));
-          if (diagonal && half * 64 + x + y < row) e = 0.f;
-        }
-        packed[x / 2] = pack2<T>(p[x >> 5][x & 31], p[x >> 5][(x & 31) + 1]);
-        packed[x / 2 + 1] = pack2<T>(p[x >> 5][(x & 31) + 2], p[x >> 5][(x & 31) + 3]);
+      tmem_loaded(p);
+      if constexpr (kApart) {
+        warp_arrive(smem_addr(&sh.s_read));
       }
-      tmem_store32(lanes + half * 64, packed);
+      const float* lse = sh.lse[n & 1][quarter];
+      probabilities<T>(p, packed, c, [&](int x) { return Two{*reinterpret_cast<const uint64_t*>(lse + x)}; }, diagonal,
+                       [&](int x) { return quarter * 32 + x >= row; });
+      if (kApart && n > 0) {
+        // the last sums have read what these replace
+        if (!(ok = mbar_wait(smem_addr(&sh.dv_done), (n - 1) & 1, gave_up))) break;
+        tc_fence_after();
+      }
+      tmem_store16(lane0 + p_at(quarter), packed);
       tmem_wait_store();
-      tc_fence_before();
-      mbar_arrive(smem_addr(&sh.p_ready));
+      warp_arrive(smem_addr(&sh.p_ready));
       if (!(ok = mbar_wait(smem_addr(&sh.dp_full), n & 1, gave_up))) break;
       tc_fence_after();
-      float d[2][32];
-      tmem_load32(lanes + 128 + half * 64, d[0]);
-      tmem_load32(lanes + 128 + half * 64 + 32, d[1]);
+      tmem_load32(s_at + 128, d);
       tmem_wait_load();
-      tmem_loaded(d[0]);
-      tmem_loaded(d[1]);
-#pragma unroll
-      for (int x = 0; x < 64; x += 4) {
-        const float4 l = *reinterpret_cast<const float4*>(&sh.delta[n & 1][half][x]);
-        const float ls[4] = {l.x, l.y, l.z, l.w};
-        float v[4];
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const float e = p[x >> 5][(x & 31) + y];
-          v[y] = e == 0.f ? 0.f : e * (d[x >> 5][(x & 31) + y] - ls[y]);
-        }
-        packed[x / 2] = pack2<T>(v[0], v[1]);
-        packed[x / 2 + 1] = pack2<T>(v[2], v[3]);
+      tmem_loaded(d);
+      if constexpr (kApart) {
+        warp_arrive(smem_addr(&sh.dp_read));
       }
-      tmem_store32(lanes + 128 + half * 64, packed);
+      const float* delta = sh.delta[n & 1][quarter];
+      score_gradients<T>(p, d, packed, [&](int x) { return Two{*reinterpret_cast<const uint64_t*>(delta + x)}; }, diagonal);
+      if (kApart && n > 0) {
+        if (!(ok = mbar_wait(smem_addr(&sh.dk_done), (n - 1) & 1, gave_up))) break;
+        tc_fence_after();
+      }
+      tmem_store16(lane0 + ds_at(quarter), packed);
       tmem_wait_store();
-      tc_fence_before();
-      mbar_arrive(smem_addr(&sh.ds_ready));
+      warp_arrive(smem_addr(&sh.ds_ready));
       put(n + 1, next);
     }
     if (ok && mbar_wait(smem_addr(&sh.done), 0, gave_up)) {
       tc_fence_after();
       const int key = unit.index * kTile + row;
-      const AttnTensor& to = half ? a.dk : a.dv;
+      const bool is_dk = quarter & 1;
+      const AttnTensor& to = is_dk ? a.dk : a.dv;
       T* out = static_cast<T*>(const_cast<void*>(to.ptr)) + (int64_t)(unit.begin + key) * to.token_stride +
                kv_head * to.head_stride;
-      for (int d = 0; d < dim16; ++d)
-        write16<T>(lanes + (half ? 384 : 256), out, d * 16, a.dim, half ? a.scale : 1.f, key < unit.length);
+      for (int x = quarter >> 1; x < dim16; x += 2)
+        write16<T>(lane0 + (is_dk ? dk_at : dv_at), out, x * 16, a.dim, is_dk ? a.scale : 1.f, key < unit.length);
     }
   }
   leave(&sh.gave_up, warp, tmem);
@@ -284,8 +342,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 constexpr int kKStages = 3, kVStages = 2;
 
 struct SharedQ {
-  alignas(8) uint64_t q_full, k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages], s_full[2],
-      dp_full, ds_ready, done, own;
+  alignas(8) uint64_t q_full, k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages], s_full, s_read,
+      dp_full[2], ds_ready, done, own;
   uint32_t tmem;
   int gave_up;
   SeqUnit unit;
@@ -315,9 +373,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t q_tile = smem_addr(tiles), do_tile = q_tile + kTileBytes, k_tile = do_tile + kTileBytes,
                  v_tile = k_tile + kKStages * kTileBytes;
   volatile int* gave_up = &sh.gave_up;
-  if (warp == 8) tmem_alloc(smem_addr(&sh.tmem), 512);
+  if (warp == kIssuer) tmem_alloc(smem_addr(&sh.tmem), 512);
   if (threadIdx.x == 0) {
-    uint64_t* const one[] = {&sh.q_full, &sh.s_full[0], &sh.s_full[1], &sh.dp_full, &sh.done, &sh.own};
+    uint64_t* const one[] = {&sh.q_full, &sh.s_full, &sh.dp_full[0], &sh.dp_full[1], &sh.done, &sh.own};
     for (uint64_t* b : one) mbar_init(smem_addr(b), 1);
     for (int i = 0; i < kKStages; ++i) {
       mbar_init(smem_addr(&sh.k_full[i]), 1);
@@ -327,19 +385,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_addr(&sh.v_full[i]), 1);
       mbar_init(smem_addr(&sh.v_empty[i]), 1);
     }
-    mbar_init(smem_addr(&sh.ds_ready), 256);
+    mbar_init(smem_addr(&sh.s_read), kWorkers / 32);
+    mbar_init(smem_addr(&sh.ds_ready), kWorkers / 32);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sh.tmem;  // columns: scores 0 and 128, dout v^T 256, dq 384
+  // Tensor memory: scores 0, dout v^T 128 and 256 (by turns), dq 384.  The
+  // next tile's scores and dout v^T are under way while this one's ds is made.
+  const uint32_t tmem = sh.tmem;
 
   const int tile = unit.count - 1 - unit.index;  // the longest rows of a sequence first
   const int steps = tile + 1, query = tile * kTile;
   const int dim16 = (a.dim + 15) / 16;
 
-  if (warp == 9) {
+  if (warp == kLoader) {
     const int kv_head = head / (a.heads / a.kv_heads);
     if (lane == 0) {
       const uint32_t bar = smem_addr(&sh.q_full);
@@ -362,86 +423,76 @@ __global__ void __launch_bounds__(kThreads, 1)
                      smem_addr(&sh.v_full[vs]), smem_addr(&sh.own), &own_parity, gave_up))
         break;
     }
-  } else if (warp == 8) {
-    if (lane == 0) {
+  } else if (warp == kIssuer) {
+    if (elect_one()) {
       const uint32_t wide = mma_shape<T>(kTile, false), sums = mma_shape<T>(dim16 * 16, true);
       auto scores = [&](int n) {  // Q K^T
         if (!mbar_wait(smem_addr(&sh.k_full[n % kKStages]), (n / kKStages) & 1, gave_up)) return false;
-        for (int s = 0; s < dim16; ++s)
-          mma_ss(tmem + (n & 1) * 128, k_major(q_tile, s), k_major(k_tile + (n % kKStages) * kTileBytes, s), wide, s > 0);
-        mma_commit(smem_addr(&sh.s_full[n & 1]));
+        product_ss<4 * PANELS>(tmem, q_tile, k_tile + (n % kKStages) * kTileBytes, wide, dim16);
+        mma_commit(smem_addr(&sh.s_full));
         return true;
       };
       auto dprob = [&](int n) {  // dout V^T
         if (!mbar_wait(smem_addr(&sh.v_full[n % kVStages]), (n / kVStages) & 1, gave_up)) return false;
-        for (int s = 0; s < dim16; ++s)
-          mma_ss(tmem + 256, k_major(do_tile, s), k_major(v_tile + (n % kVStages) * kTileBytes, s), wide, s > 0);
-        mma_commit(smem_addr(&sh.dp_full));
+        product_ss<4 * PANELS>(tmem + 128 + (n & 1) * 128, do_tile, v_tile + (n % kVStages) * kTileBytes, wide, dim16);
+        mma_commit(smem_addr(&sh.dp_full[n & 1]));
         mma_commit(smem_addr(&sh.v_empty[n % kVStages]));
         return true;
       };
-      bool ok = mbar_wait(smem_addr(&sh.q_full), 0, gave_up) && scores(0) && dprob(0) && (steps < 2 || scores(1));
+      bool ok = mbar_wait(smem_addr(&sh.q_full), 0, gave_up) && scores(0) && dprob(0);
       for (int n = 0; n < steps && ok; ++n) {
+        if (n + 1 < steps) {
+          if (!(ok = mbar_wait(smem_addr(&sh.s_read), n & 1, gave_up))) break;
+          tc_fence_after();
+          if (!(ok = scores(n + 1) && dprob(n + 1))) break;
+        }
         if (!(ok = mbar_wait(smem_addr(&sh.ds_ready), n & 1, gave_up))) break;
         tc_fence_after();
-        const uint32_t k = k_tile + (n % kKStages) * kTileBytes;
-        for (int s = 0; s < kTile / 16; ++s)
-          mma_ts(tmem + 384, tmem + 256 + (s >> 2) * 64 + (s & 3) * 8, mn_major(k, s), sums, n > 0 || s > 0);
+        for (int h = 0; h < 4; ++h)
+          product_ts<2>(tmem + 384, tmem + 128 + (n & 1) * 128 + h * 32, k_tile + (n % kKStages) * kTileBytes, h, sums,
+                        n > 0 || h > 0);
         mma_commit(smem_addr(&sh.k_empty[n % kKStages]));
-        if (n + 1 < steps && !(ok = dprob(n + 1))) break;
-        if (n + 2 < steps && !(ok = scores(n + 2))) break;
       }
       if (ok) mma_commit(smem_addr(&sh.done));
     }
     __syncwarp();
   } else {
-    // thread: query row, keys [64 half, 64 half + 64) of each tile
-    const int half = warp >> 2, row = (warp & 3) * 32 + lane;
+    // thread: query row, keys [32 quarter, 32 quarter + 32) of each tile
+    const int quarter = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
     const float c = a.scale * kLog2e;
     const bool valid = query + row < unit.length;
     const int64_t at = (int64_t)head * a.tokens + unit.begin + query + row;
-    const float lse = valid ? a.lse[at] * kLog2e : INFINITY, delta = valid ? a.delta[at] : 0.f;
+    const float l = valid ? -a.lse[at] * kLog2e : -INFINITY, dl = valid ? -a.delta[at] : 0.f;
+    const Two lse = two(l, l), delta = two(dl, dl);
     bool ok = true;
     for (int n = 0; n < steps; ++n) {
-      if (!(ok = mbar_wait(smem_addr(&sh.s_full[n & 1]), (n >> 1) & 1, gave_up))) break;
+      const bool diagonal = n == steps - 1;
+      if (!(ok = mbar_wait(smem_addr(&sh.s_full), n & 1, gave_up))) break;
       tc_fence_after();
-      float p[2][32], d[2][32];
-      tmem_load32(lanes + (n & 1) * 128 + half * 64, p[0]);
-      tmem_load32(lanes + (n & 1) * 128 + half * 64 + 32, p[1]);
+      float p[32], d[32];
+      uint32_t packed[16];
+      tmem_load32(lanes + quarter * 32, p);
       tmem_wait_load();
-      tmem_loaded(p[0]);
-      tmem_loaded(p[1]);
-#pragma unroll
-      for (int x = 0; x < 64; ++x) {
-        float& e = p[x >> 5][x & 31];
-        e = exp2_approx(fmaf(e, c, -lse));
-        if (n == steps - 1 && half * 64 + x > row) e = 0.f;
-      }
-      if (!(ok = mbar_wait(smem_addr(&sh.dp_full), n & 1, gave_up))) break;
+      tmem_loaded(p);
+      warp_arrive(smem_addr(&sh.s_read));
+      probabilities<T>(p, packed, c, [&](int) { return lse; }, diagonal, [&](int x) { return quarter * 32 + x <= row; });
+      const uint32_t dp_at = lanes + 128 + (n & 1) * 128 + quarter * 32;
+      if (!(ok = mbar_wait(smem_addr(&sh.dp_full[n & 1]), (n >> 1) & 1, gave_up))) break;
       tc_fence_after();
-      tmem_load32(lanes + 256 + half * 64, d[0]);
-      tmem_load32(lanes + 256 + half * 64 + 32, d[1]);
+      tmem_load32(dp_at, d);
       tmem_wait_load();
-      tmem_loaded(d[0]);
-      tmem_loaded(d[1]);
-      uint32_t packed[32];
-#pragma unroll
-      for (int x = 0; x < 64; x += 2) {
-        const float e = p[x >> 5][x & 31], f = p[x >> 5][(x & 31) + 1];
-        packed[x / 2] = pack2<T>(e == 0.f ? 0.f : e * (d[x >> 5][x & 31] - delta),
-                                 f == 0.f ? 0.f : f * (d[x >> 5][(x & 31) + 1] - delta));
-      }
-      tmem_store32(lanes + 256 + half * 64, packed);
+      tmem_loaded(d);
+      score_gradients<T>(p, d, packed, [&](int) { return delta; }, diagonal);
+      tmem_store16(dp_at, packed);
       tmem_wait_store();
-      tc_fence_before();
-      mbar_arrive(smem_addr(&sh.ds_ready));
+      warp_arrive(smem_addr(&sh.ds_ready));
     }
     if (ok && mbar_wait(smem_addr(&sh.done), 0, gave_up)) {
       tc_fence_after();
       T* out = static_cast<T*>(const_cast<void*>(a.dq.ptr)) + (int64_t)(unit.begin + query + row) * a.dq.token_stride +
                head * a.dq.head_stride;
-      for (int d = half; d < dim16; d += 2) write16<T>(lanes + 384, out, d * 16, a.dim, a.scale, valid);
+      for (int x = quarter; x < dim16; x += 4) write16<T>(lanes + 384, out, x * 16, a.dim, a.scale, valid);
     }
   }
   leave(&sh.gave_up, warp, tmem);
@@ -450,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <class T, int PANELS>
 cudaError_t run(int dtype, const AttnArgs& a, cudaStream_t s) {
   static std::atomic<unsigned long long> opened_kv[256], opened_q[256];
-  constexpr int smem_kv = (2 + 2 * kStages) * PANELS * (int)kPanelBytes;
+  constexpr int smem_kv = (2 + 2 * query_stages(PANELS)) * PANELS * (int)kPanelBytes;
   constexpr int smem_q = (2 + kKStages + kVStages) * PANELS * (int)kPanelBytes;
   cudaError_t e = open_kernel((const void*)attention_dkv_kernel<T, PANELS>, smem_kv, false, opened_kv);
   if (e != cudaSuccess) return e;

@@ -32,15 +32,28 @@ __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// For a whole warp, after tensor memory accesses that must come before: one
+// arrival.  (A barrier takes arrivals one by one, some five cycles each: 128
+// threads' own arrivals took 600 cycles.)
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
 __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+// Waits up to `ns` for the phase of the given parity to end, the thread asleep
+// meanwhile.  (Without a time the instruction returns at once, and a warp that
+// looks again and again takes every fourth issue slot from the others on its
+// quarter of the multiprocessor; it wakes no sooner, 90 cycles after the
+// arrival.)
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity, uint32_t ns) {
   uint32_t ok;
   asm volatile(
-      "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+      "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\nselp.u32 %0, 1, 0, p;\n}"
       : "=r"(ok)
-      : "r"(bar), "r"(parity)
+      : "r"(bar), "r"(parity), "r"(ns)
       : "memory");
   return ok != 0;
 }
@@ -50,22 +63,21 @@ __device__ __forceinline__ uint64_t global_ns() {
   return t;
 }
 
-constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr uint32_t kSleepNs = 10000000;           // one look
+constexpr uint64_t kWaitLimitNs = 2000000000ull;  // one wait
 
 // Waits for the phase of the given parity to end.  Every wait is bounded: one
 // that runs out (no correct launch does) sets the block's `gave_up`, which
 // ends the other threads' waits too, and the caller returns.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
-  if (mbar_try(bar, parity)) return true;
+  if (mbar_try(bar, parity, kSleepNs)) return true;
   const uint64_t until = global_ns() + kWaitLimitNs;
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try(bar, parity)) return true;
-    if ((i & 63) == 0) {
-      if (*gave_up) return false;
-      if (global_ns() > until) {
-        *gave_up = 1;
-        return false;
-      }
+  for (;;) {
+    if (mbar_try(bar, parity, kSleepNs)) return true;
+    if (*gave_up) return false;
+    if (global_ns() > until) {
+      *gave_up = 1;
+      return false;
     }
   }
 }
@@ -157,6 +169,15 @@ __device__ __forceinline__ void tmem_loaded(float (&r)[N]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) asm volatile("" : "+f"(r[i])::"memory");
 }
+__device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
 __device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -168,12 +189,10 @@ __device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t (&r)[32
       : "memory");
 }
 __device__ __forceinline__ void tmem_store16(uint32_t at, const float (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16};" ::"r"(at),
-      "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]), "f"(r[8]), "f"(r[9]),
-      "f"(r[10]), "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]), "f"(r[15])
-      : "memory");
+  uint32_t bits[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) bits[i] = __float_as_uint(r[i]);
+  tmem_store16(at, bits);
 }
 
 // ---- products -------------------------------------------------------------------------
@@ -192,11 +211,16 @@ __device__ __forceinline__ uint64_t panel_desc(uint32_t at, bool mn_major) {
   const uint64_t lead = mn_major ? kPanelBytes >> 4 : 1;
   return (uint64_t)((at & 0x3FFFF) >> 4) | lead << 16 | (uint64_t)(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
 }
-// ... advanced to the k-th 16 elements along K
-__device__ __forceinline__ uint64_t k_major(uint32_t tile, int k) {
-  return panel_desc(tile + (k >> 2) * kPanelBytes + (k & 3) * 32, false);
+// What the k-th 16 elements along K add to it.
+__host__ __device__ constexpr uint32_t k_major_step(int k) { return ((k >> 2) * kPanelBytes + (k & 3) * 32) >> 4; }
+__host__ __device__ constexpr uint32_t mn_major_step(int k) { return k * 16 * 128 >> 4; }
+
+// One thread of the warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+  return r != 0;
 }
-__device__ __forceinline__ uint64_t mn_major(uint32_t tile, int k) { return panel_desc(tile + k * 16 * 128, true); }
 
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t shape, bool add) {
   asm volatile(
@@ -210,10 +234,39 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       "r"(a), "l"(b), "r"(shape), "r"((uint32_t)add)
       : "memory");
 }
+// D = A B^T over `steps` times 16 columns of two K-major tiles.  Issuing is
+// one thread's work and has to stay ahead of the tensor cores (64 cycles a
+// product of 128 x 128 x 16), so the loop is unrolled and a step's
+// descriptors are one addition each.
+template <int MAX>
+__device__ __forceinline__ void product_ss(uint32_t d, uint32_t a_tile, uint32_t b_tile, uint32_t shape, int steps) {
+  const uint64_t a = panel_desc(a_tile, false), b = panel_desc(b_tile, false);
+#pragma unroll
+  for (int k = 0; k < MAX; ++k)
+    if (k < steps) mma_ss(d, a + k_major_step(k), b + k_major_step(k), shape, k > 0);
+}
+// D (+)= P B over STEPS times 16 rows of B, the `part`-th such part of its
+// rows; P's pairs of that part, eight columns a step, in tensor memory.
+template <int STEPS>
+__device__ __forceinline__ void product_ts(uint32_t d, uint32_t p, uint32_t b_tile, int part, uint32_t shape, bool add) {
+  const uint64_t b = panel_desc(b_tile, true) + part * mn_major_step(STEPS);
+#pragma unroll
+  for (int k = 0; k < STEPS; ++k) mma_ts(d, p + k * 8, b + mn_major_step(k), shape, k > 0 || add);
+}
 // Arrives on the barrier when every product issued by this thread so far is done.
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
+
+// ---- registers ---------------------------------------------------------------------------
+
+// Blocks of 384 threads are launched with 168 registers each, 64512 in all;
+// two warpgroups that hold rows of scores take 208 and the third, which
+// issues and loads, keeps 88: 256 * 208 + 128 * 88 = 64512.  Every warp of a
+// warpgroup has to say so.
+constexpr int kLaunchRegisters = 168;
+__device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 208;"); }
+__device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 88;"); }
 
 // ---- 16-bit pairs ----------------------------------------------------------------------
 
@@ -228,6 +281,39 @@ template <>
 __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
   const __half2 r = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// Two binary32 values in one register pair, and the operations that take pairs.
+struct Two {
+  uint64_t v;
+};
+__device__ __forceinline__ Two two(float lo, float hi) {
+  Two r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void split(Two t, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(t.v));
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+  Two r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ Two add2(Two a, Two b) {
+  Two r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ Two mul2(Two a, Two b) {
+  Two r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
 __device__ __forceinline__ float exp2_approx(float x) {
