@@ -91,7 +91,7 @@ def _load():
     L.ar_plan_create.argtypes = [cint, pp, cint, i64, cint, cint, cint, cint, ctypes.POINTER(vp)]
     L.ar_plan_run.argtypes = [vp, vp]
     L.ar_plan_destroy.argtypes = [vp]
-    flt, at = ctypes.c_float, ctypes.POINTER(AttentionTensor)
+    flt, at = ctypes.c_float, vp  # vp: the address of an AttentionTensor
     L.ar_layer_norm.argtypes = [vp, i64, vp, vp, vp, i64, vp, vp, i64, i64, flt, cint, cint, vp]
     L.ar_layer_norm_backward.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, vp, i64, i64, cint, cint, vp, i64,
                                          vp]
@@ -342,45 +342,67 @@ class Plan:
 # These take torch CUDA tensors and read sizes, strides and element types from
 # them.  Operands whose shapes, types or inner strides do not belong together
 # are refused (AR_ERR_INVALID_ARG, or AR_ERR_UNSUPPORTED for an element type
-# the library does not have) before the library is called.
+# the library does not have) before the library is called.  A small call costs
+# as much here as on the device, so the checks read each property once.
 
-_TORCH_DTYPE = {"torch.float32": 0, "torch.bfloat16": 1, "torch.int32": 2, "torch.float16": 3}
-
-
-def _dtype_of(t):
-    return _TORCH_DTYPE.get(str(t.dtype))
+_TORCH_DTYPE = {}  # torch dtype: the library's; filled on first use, as torch may not be there before
+_F32 = []          # torch.float32
 
 
-def _is(t, shape, dtype):
-    """t is a contiguous tensor of this shape and element type."""
-    return tuple(t.shape) == tuple(shape) and _dtype_of(t) == dtype and t.is_contiguous()
+def _dtypes():
+    if not _TORCH_DTYPE:
+        import torch
+        _F32.append(torch.float32)
+        _TORCH_DTYPE.update({torch.float32: 0, torch.bfloat16: 1, torch.int32: 2, torch.float16: 3})
+    return _TORCH_DTYPE
 
 
-def _is_rows(t, like):
-    """t is a matrix of like's shape and type whose rows are contiguous."""
-    return t.shape == like.shape and t.dtype == like.dtype and (t.shape[1] <= 1 or t.stride(1) == 1)
+def _stream_of(stream, tensor) -> int:
+    """As _stream; None is the current stream of the tensor's device."""
+    if stream is not None:
+        return _stream(stream)
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None or not tensor.is_cuda:
+        return _stream(None)
+    return raw(tensor.get_device())
 
 
-def _params(weight, others, cols):
-    """The parameters' element type, or None if they do not belong together."""
-    dt = _dtype_of(weight)
-    ok = dt is not None and all(_is(p, (cols,), dt) for p in (weight, *others) if p is not None)
-    return dt if ok else None
+def _vector(t, n, dtype):
+    """t is a contiguous vector of n elements of a torch dtype."""
+    return t.dtype is dtype and t.dim() == 1 and t.numel() == n and t.is_contiguous()
+
+
+def _row_stride(t, shape, dtype):
+    """The row stride of a matrix of this shape and torch dtype with contiguous rows; else None."""
+    if t.dtype is not dtype or t.shape != shape:
+        return None
+    row, inner = t.stride()
+    return row if inner == 1 or shape[1] <= 1 else None
 
 
 def ar_layer_norm(x, weight, bias, y, mean=None, rstd=None, eps=1e-5, stream=None) -> int:
     """y = layer norm of the rows of the matrix x.  bias, mean and rstd may be
     None; weight and bias have x's type or f32; y may be x."""
-    if x.dim() != 2 or not _is_rows(x, x) or not _is_rows(y, x):
+    types = _TORCH_DTYPE or _dtypes()
+    shape, dtype, pdtype = x.shape, x.dtype, weight.dtype
+    if len(shape) != 2:
         return AR_ERR_INVALID_ARG
-    rows, cols = x.shape
-    dt, pt = _dtype_of(x), _params(weight, (bias,), cols)
-    if dt is None:
+    dt, pt = types.get(dtype), types.get(pdtype)
+    if dt is None or pt is None:
         return AR_ERR_UNSUPPORTED
-    if pt is None or any(s is not None and not _is(s, (rows,), 0) for s in (mean, rstd)):
+    rows, cols = shape
+    xs, ys = _row_stride(x, shape, dtype), _row_stride(y, shape, dtype)
+    if xs is None or ys is None or not _vector(weight, cols, pdtype) or (
+            bias is not None and not _vector(bias, cols, pdtype)):
         return AR_ERR_INVALID_ARG
-    return lib.ar_layer_norm(x.data_ptr(), x.stride(0), weight.data_ptr(), _ptr(bias), y.data_ptr(), y.stride(0),
-                             _ptr(mean), _ptr(rstd), rows, cols, eps, dt, pt, _stream(stream))
+    f32 = _F32[0]
+    if (mean is not None and not _vector(mean, rows, f32)) or (rstd is not None and not _vector(rstd, rows, f32)):
+        return AR_ERR_INVALID_ARG
+    return lib.ar_layer_norm(x.data_ptr(), xs, weight.data_ptr(), None if bias is None else bias.data_ptr(),
+                             y.data_ptr(), ys, None if mean is None else mean.data_ptr(),
+                             None if rstd is None else rstd.data_ptr(), rows, cols, eps, dt, pt,
+                             _stream_of(stream, x))
 
 
 def ar_layer_norm_workspace_bytes(rows, cols) -> int:
@@ -391,80 +413,99 @@ def ar_layer_norm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, worksp
     """dx (may be dy or x), dweight and dbias (may be None) for an upstream
     dy, from the forward call's mean and rstd.  workspace: a tensor of at least
     ar_layer_norm_workspace_bytes(rows, cols) bytes."""
-    if x.dim() != 2 or not _is_rows(x, x) or not _is_rows(dy, x) or not _is_rows(dx, x):
+    types = _TORCH_DTYPE or _dtypes()
+    shape, dtype, pdtype = x.shape, x.dtype, weight.dtype
+    if len(shape) != 2:
         return AR_ERR_INVALID_ARG
-    rows, cols = x.shape
-    dt, pt = _dtype_of(x), _params(weight, (dweight, dbias), cols)
-    if dt is None:
+    dt, pt = types.get(dtype), types.get(pdtype)
+    if dt is None or pt is None:
         return AR_ERR_UNSUPPORTED
-    if pt is None or not _is(mean, (rows,), 0) or not _is(rstd, (rows,), 0) or not workspace.is_contiguous():
+    rows, cols = shape
+    xs, dys, dxs = _row_stride(x, shape, dtype), _row_stride(dy, shape, dtype), _row_stride(dx, shape, dtype)
+    f32 = _F32[0]
+    if (xs is None or dys is None or dxs is None or not _vector(weight, cols, pdtype)
+            or not _vector(dweight, cols, pdtype) or (dbias is not None and not _vector(dbias, cols, pdtype))
+            or not _vector(mean, rows, f32) or not _vector(rstd, rows, f32) or not workspace.is_contiguous()):
         return AR_ERR_INVALID_ARG
-    return lib.ar_layer_norm_backward(dy.data_ptr(), dy.stride(0), x.data_ptr(), x.stride(0), weight.data_ptr(),
-                                      mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(), dx.stride(0),
-                                      dweight.data_ptr(), _ptr(dbias), rows, cols, dt, pt, workspace.data_ptr(),
-                                      workspace.numel() * workspace.element_size(), _stream(stream))
+    return lib.ar_layer_norm_backward(dy.data_ptr(), dys, x.data_ptr(), xs, weight.data_ptr(), mean.data_ptr(),
+                                      rstd.data_ptr(), dx.data_ptr(), dxs, dweight.data_ptr(),
+                                      None if dbias is None else dbias.data_ptr(), rows, cols, dt, pt,
+                                      workspace.data_ptr(), workspace.nbytes, _stream_of(stream, x))
 
 
-def _distill_types(logits, teacher_index, teacher_logits, rows_f32, dlogits):
-    """(status, element types of the logits and of the teacher's)."""
-    if logits.dim() != 2 or not _is_rows(logits, logits) or (dlogits is not None and not _is_rows(dlogits, logits)):
-        return AR_ERR_INVALID_ARG, 0, 0
-    rows = logits.shape[0]
-    dt, vt = _dtype_of(logits), _dtype_of(teacher_logits)
+def _distill_operands(logits, teacher_index, teacher_logits, rows_f32, dlogits):
+    """(status, element types of the logits and of the teacher's, row strides of logits and dlogits)."""
+    types = _TORCH_DTYPE or _dtypes()
+    shape, lists, dtype, vdtype = logits.shape, teacher_index.shape, logits.dtype, teacher_logits.dtype
+    dt, vt = types.get(dtype), types.get(vdtype)
     if dt is None or vt is None:
-        return AR_ERR_UNSUPPORTED, 0, 0
-    if (teacher_index.dim() != 2 or not _is(teacher_index, (rows, teacher_index.shape[1]), 2)
-            or not _is(teacher_logits, teacher_index.shape, vt)
-            or any(r is not None and not _is(r, (rows,), 0) for r in rows_f32)):
-        return AR_ERR_INVALID_ARG, 0, 0
-    return AR_OK, dt, vt
+        return AR_ERR_UNSUPPORTED, 0, 0, 0, 0
+    zs = _row_stride(logits, shape, dtype) if len(shape) == 2 else None
+    ds = 0 if dlogits is None else _row_stride(dlogits, shape, dtype)
+    if (zs is None or ds is None or len(lists) != 2 or lists[0] != shape[0] or teacher_logits.shape != lists
+            or types.get(teacher_index.dtype) != 2 or not teacher_index.is_contiguous()
+            or not teacher_logits.is_contiguous()):
+        return AR_ERR_INVALID_ARG, 0, 0, 0, 0
+    f32, rows = _F32[0], shape[0]
+    for r in rows_f32:
+        if r is not None and not _vector(r, rows, f32):
+            return AR_ERR_INVALID_ARG, 0, 0, 0, 0
+    return AR_OK, dt, vt, zs, ds
 
 
 def ar_distill_loss(logits, teacher_index, teacher_logits, loss, lse, scale=None, dlogits=None, temperature=1.0,
                     stream=None) -> int:
     """loss and lse of each row of logits against the teacher's lists and, with
     dlogits (which may be logits), the gradient of sum(scale * loss)."""
-    rc, dt, vt = _distill_types(logits, teacher_index, teacher_logits, (loss, lse, scale), dlogits)
+    rc, dt, vt, zs, ds = _distill_operands(logits, teacher_index, teacher_logits, (loss, lse, scale), dlogits)
     if rc:
         return rc
-    return lib.ar_distill_loss(logits.data_ptr(), logits.stride(0), teacher_index.data_ptr(),
-                               teacher_logits.data_ptr(), _ptr(scale), loss.data_ptr(), lse.data_ptr(), _ptr(dlogits),
-                               0 if dlogits is None else dlogits.stride(0), logits.shape[0], logits.shape[1],
-                               teacher_index.shape[1], temperature, dt, vt, _stream(stream))
+    rows, vocab = logits.shape
+    return lib.ar_distill_loss(logits.data_ptr(), zs, teacher_index.data_ptr(), teacher_logits.data_ptr(),
+                               None if scale is None else scale.data_ptr(), loss.data_ptr(), lse.data_ptr(),
+                               None if dlogits is None else dlogits.data_ptr(), ds, rows, vocab,
+                               teacher_index.shape[1], temperature, dt, vt, _stream_of(stream, logits))
 
 
 def ar_distill_loss_backward(logits, teacher_index, teacher_logits, lse, dloss, dlogits, temperature=1.0,
                              stream=None) -> int:
     """dlogits (which may be logits) for an upstream dloss, from the forward
     call's lse."""
-    rc, dt, vt = _distill_types(logits, teacher_index, teacher_logits, (lse, dloss), dlogits)
+    rc, dt, vt, zs, ds = _distill_operands(logits, teacher_index, teacher_logits, (lse, dloss), dlogits)
     if rc:
         return rc
-    return lib.ar_distill_loss_backward(logits.data_ptr(), logits.stride(0), teacher_index.data_ptr(),
-                                        teacher_logits.data_ptr(), lse.data_ptr(), dloss.data_ptr(),
-                                        dlogits.data_ptr(), dlogits.stride(0), logits.shape[0], logits.shape[1],
-                                        teacher_index.shape[1], temperature, dt, vt, _stream(stream))
+    rows, vocab = logits.shape
+    return lib.ar_distill_loss_backward(logits.data_ptr(), zs, teacher_index.data_ptr(), teacher_logits.data_ptr(),
+                                        lse.data_ptr(), dloss.data_ptr(), dlogits.data_ptr(), ds, rows, vocab,
+                                        teacher_index.shape[1], temperature, dt, vt, _stream_of(stream, logits))
 
 
-def _heads(t):
-    return AttentionTensor(t.data_ptr(), t.stride(0), t.stride(1))
+_TENSOR_BYTES = ctypes.sizeof(AttentionTensor)
 
 
-def _attention_shapes(q, k, queries, keys, cu_seqlens, lse):
-    """(status, element type): q and `queries` are [tokens, heads, dim], k and
-    `keys` [tokens, kv_heads, dim], all of one type."""
-    if q.dim() != 3 or k.dim() != 3 or q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2]:
-        return AR_ERR_INVALID_ARG, 0
-    for like, ts in ((q, (q, *queries)), (k, (k, *keys))):
-        if any(t.shape != like.shape or t.dtype != q.dtype or (t.shape[2] > 1 and t.stride(2) != 1) for t in ts):
-            return AR_ERR_INVALID_ARG, 0
-    dt = _dtype_of(q)
+def _attention_operands(q, k, queries, keys, cu_seqlens, lse):
+    """(status, element type, the operands as an array of ar_attention_tensor):
+    q and `queries` are [tokens, heads, dim], k and `keys` [tokens, kv_heads,
+    dim], all of one type."""
+    types = _TORCH_DTYPE or _dtypes()
+    qshape, kshape, dtype = q.shape, k.shape, q.dtype
+    if len(qshape) != 3 or len(kshape) != 3 or qshape[0] != kshape[0] or qshape[2] != kshape[2]:
+        return AR_ERR_INVALID_ARG, 0, None
+    dt = types.get(dtype)
     if dt is None:
-        return AR_ERR_UNSUPPORTED, 0
-    if (cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1 or not _is(cu_seqlens, cu_seqlens.shape, 2)
-            or (lse is not None and not _is(lse, (q.shape[1], q.shape[0]), 0))):
-        return AR_ERR_INVALID_ARG, 0
-    return AR_OK, dt
+        return AR_ERR_UNSUPPORTED, 0, None
+    flat = []
+    for t, shape in ((q, qshape), (k, kshape), *((t, kshape) for t in keys), *((t, qshape) for t in queries)):
+        token, head, inner = t.stride()
+        if t.dtype is not dtype or t.shape != shape or (inner != 1 and shape[2] > 1):
+            return AR_ERR_INVALID_ARG, 0, None
+        flat += (t.data_ptr(), token, head)
+    if (types.get(cu_seqlens.dtype) != 2 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1
+            or not cu_seqlens.is_contiguous()):
+        return AR_ERR_INVALID_ARG, 0, None
+    if lse is not None and (lse.dtype is not _F32[0] or lse.shape != (qshape[1], qshape[0]) or not lse.is_contiguous()):
+        return AR_ERR_INVALID_ARG, 0, None
+    return AR_OK, dt, array.array("q", flat)
 
 
 def ar_attention(q, k, v, cu_seqlens, out, lse=None, scale=None, stream=None) -> int:
@@ -472,13 +513,14 @@ def ar_attention(q, k, v, cu_seqlens, out, lse=None, scale=None, stream=None) ->
     kv_heads, dim], tokens packed by cu_seqlens [seqs + 1] (i32, on the
     device).  scale None: dim ** -0.5.  lse [heads, tokens] is what the
     backward call needs."""
-    rc, dt = _attention_shapes(q, k, (out,), (v,), cu_seqlens, lse)
+    rc, dt, operands = _attention_operands(q, k, (out,), (v,), cu_seqlens, lse)
     if rc:
         return rc
     tokens, heads, dim = q.shape
-    return lib.ar_attention(_heads(q), _heads(k), _heads(v), cu_seqlens.data_ptr(), _heads(out), _ptr(lse), tokens,
-                            cu_seqlens.numel() - 1, heads, k.shape[1], dim, dim ** -0.5 if scale is None else scale,
-                            dt, _stream(stream))
+    at, n = operands.buffer_info()[0], _TENSOR_BYTES
+    return lib.ar_attention(at, at + n, at + 2 * n, cu_seqlens.data_ptr(), at + 3 * n,
+                            None if lse is None else lse.data_ptr(), tokens, cu_seqlens.numel() - 1, heads,
+                            k.shape[1], dim, dim ** -0.5 if scale is None else scale, dt, _stream_of(stream, q))
 
 
 def ar_attention_workspace_bytes(tokens, heads, kv_heads, dim) -> int:
@@ -489,17 +531,18 @@ def ar_attention_backward(dout, q, k, v, out, lse, cu_seqlens, dq, dk, dv, works
     """dq, dk and dv for an upstream dout, from the forward call's out and
     lse.  workspace: a tensor of at least ar_attention_workspace_bytes(tokens,
     heads, kv_heads, dim) bytes."""
-    rc, dt = _attention_shapes(q, k, (out, dout, dq), (v, dk, dv), cu_seqlens, lse)
+    rc, dt, operands = _attention_operands(q, k, (out, dout, dq), (v, dk, dv), cu_seqlens, lse)
     if rc:
         return rc
     if lse is None or not workspace.is_contiguous():
         return AR_ERR_INVALID_ARG
     tokens, heads, dim = q.shape
-    return lib.ar_attention_backward(_heads(dout), _heads(q), _heads(k), _heads(v), _heads(out), lse.data_ptr(),
-                                     cu_seqlens.data_ptr(), _heads(dq), _heads(dk), _heads(dv), tokens,
+    at, n = operands.buffer_info()[0], _TENSOR_BYTES  # q, k, v, dk, dv, out, dout, dq
+    return lib.ar_attention_backward(at + 6 * n, at, at + n, at + 2 * n, at + 5 * n, lse.data_ptr(),
+                                     cu_seqlens.data_ptr(), at + 7 * n, at + 3 * n, at + 4 * n, tokens,
                                      cu_seqlens.numel() - 1, heads, k.shape[1], dim,
                                      dim ** -0.5 if scale is None else scale, dt, workspace.data_ptr(),
-                                     workspace.numel() * workspace.element_size(), _stream(stream))
+                                     workspace.nbytes, _stream_of(stream, q))
 
 
 def ar_chunk_range(count, nranks, c):

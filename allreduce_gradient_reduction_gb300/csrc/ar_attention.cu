@@ -3,16 +3,12 @@
 //   a_ij = scale q_i . k_j (j <= i, same sequence), out_i = sum_j p_ij v_j with
 //   p = softmax(a_i), lse_i = log sum_j exp(a_ij).
 //
-// Bound by the tensor cores at head sizes near 128 (4 dim operations a pair,
-// every operand read once per 256 queries), by the exponentials at 64 and
-// below.  One pass over the keys with a running maximum and sum: a block takes
-// 256 queries of one head as two tiles of 128, each with its scores and its
-// output in tensor memory, so that one tile's products run while the other's
-// exponentials are taken.  Four warps for each tile's softmax (a thread has one
-// query's whole row of 128 scores), one that issues the products, one that
-// loads, two that only give their registers.  The probabilities go back to
-// tensor memory as 16-bit pairs and are the second product's left operand
-// there.
+// Bound by the tensor cores at head sizes near 128 (4 dim operations a pair of
+// tokens), by the exponentials at 64 and below.  One pass over the keys with a
+// running maximum and sum, the scores and the output in tensor memory.  Eight
+// warps take the exponentials, one issues the products, one loads.  The
+// probabilities go back to tensor memory as 16-bit pairs and are the second
+// product's left operand there.
 //
 // The running maximum that scales the output is moved only when a row's true
 // maximum has grown by more than 8 in the exponent of two: until then the
@@ -33,46 +29,64 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.f;  // powers of two that a row's maximum may grow by before the output is rescaled
 constexpr int kStages = 4;     // tiles of K or V in flight
-constexpr int kThreads = 384;
-constexpr int kPair = 2 * kTile;
+
+// What differs with the head size.  A tensor core product of 128 x 128 scores
+// takes 4 cycles for each element of the head, the exponentials of a tile at
+// least 512 cycles whatever the head.
+//
+// Up to 64 elements (one panel) the exponentials bound it, and what counts is
+// that they never wait: a block takes one tile of 128 queries, two threads to
+// a row, and two blocks share a multiprocessor.  Tensor memory has room for
+// the probabilities beside the scores, so the next scores are computed as
+// soon as the current ones have been read.
+//
+// Beyond, the products bound it: a block takes two tiles, one thread to a row,
+// so that K and V are fetched once for 256 queries and one tile's products run
+// while the other's exponentials are taken.  The outputs fill tensor memory
+// and the probabilities take the scores' place.
+template <int PANELS>
+struct Form {
+  static constexpr int kTiles = PANELS == 1 ? 1 : 2;
+  static constexpr int kShare = 1;  // threads to a row of scores
+  static constexpr bool kApart = PANELS == 1;
+  static constexpr int kThreads = PANELS == 1 ? 192 : 384;
+  static constexpr int kIssuer = 4 * kTiles * kShare, kLoader = kIssuer + 1;  // warps; those before them take exponentials
+  static constexpr int kBlocks = PANELS == 1 ? 2 : 1;  // on a multiprocessor
+  static constexpr int kColumns = PANELS == 1 ? 256 : 512;
+  static constexpr int kQueries = kTiles * kTile;
+};
 
 struct Shared {
-  alignas(8) uint64_t q_full[2], kv_full[kStages], kv_empty[kStages], s_full[2], s_read[2], p_full[2][2], o_done[2],
-      own;
+  alignas(8) uint64_t q_full[2], kv_full[kStages], kv_empty[kStages], s_full[2], s_read[2], p_full[2][2], o_done[2], own;
+  float top[2][2][kTile];  // [turn][half][row]: the halves' row maxima, where two threads share a row
+  float sum[kTile];
   uint32_t tmem;
   int gave_up;
   SeqUnit unit;
 };
 
 template <class T, int PANELS>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Form<PANELS>::kThreads, Form<PANELS>::kBlocks)
     attention_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                      const __grid_constant__ CUtensorMap v_map, const AttnArgs a) {
+  using F = Form<PANELS>;
+  constexpr int kTiles = F::kTiles, kShare = F::kShare;
   extern __shared__ __align__(1024) uint8_t tiles[];
   __shared__ Shared sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int head = blockIdx.x % a.heads;
 
   if (warp == 0) {
-    const SeqUnit u = find_unit(a.cu_seqlens, a.seqs, (int)a.tokens, kPair, blockIdx.x / a.heads);
+    const SeqUnit u = find_unit(a.cu_seqlens, a.seqs, (int)a.tokens, F::kQueries, blockIdx.x / a.heads);
     if (lane == 0) {
       sh.unit = u;
       sh.gave_up = 0;
     }
-  }
-  __syncthreads();
-  if (sh.unit.count == 0) return;
-  const SeqUnit unit = sh.unit;
-
-  constexpr uint32_t kTileBytes = PANELS * kPanelBytes;
-  const uint32_t q_tile = smem_addr(tiles), kv_tile = q_tile + 2 * kTileBytes;
-  volatile int* gave_up = &sh.gave_up;
-  if (warp == 8) tmem_alloc(smem_addr(&sh.tmem), 512);
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) {
+  } else if (warp == F::kLoader && lane == 0) {
+    for (int i = 0; i < kTiles; ++i) {
       mbar_init(smem_addr(&sh.q_full[i]), 1);
       mbar_init(smem_addr(&sh.s_full[i]), 1);
-      mbar_init(smem_addr(&sh.s_read[i]), 4);
+      mbar_init(smem_addr(&sh.s_read[i]), 4 * kShare);
       mbar_init(smem_addr(&sh.p_full[i][0]), 4);
       mbar_init(smem_addr(&sh.p_full[i][1]), 4);
       mbar_init(smem_addr(&sh.o_done[i]), 1);
@@ -84,34 +98,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_addr(&sh.own), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  tc_fence_before();
   __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = sh.tmem;
-  // Tensor memory, for tile i: scores at 128 i, output behind both tiles'
-  // scores.  Outputs of up to 64 columns leave room for the probabilities
-  // beside the scores, so that the next scores are computed as soon as the
-  // current ones have been read; wider ones do not, and the probabilities
-  // take the scores' first 64 columns.
-  constexpr bool kApart = PANELS == 1;
-  auto p_at = [&](int i) { return tmem + (kApart ? 256 + i * 64 : i * 128); };
-  auto out_at = [&](int i) { return tmem + (kApart ? 384 + i * 64 : 256 + i * 128); };
+  if (sh.unit.count == 0) return;
+  const SeqUnit unit = sh.unit;
+  if (warp == F::kIssuer) tmem_alloc(smem_addr(&sh.tmem), F::kColumns);
 
-  // the longest rows of a sequence first
-  const int first = (unit.count - 1 - unit.index) * kPair;  // first query of the pair, within the sequence
-  int blocks[2];                                            // tiles of keys that each tile of queries sees
-  blocks[0] = first / kTile + 1;
-  blocks[1] = first + kTile < unit.length ? blocks[0] + 1 : 0;
-  const int most = max(blocks[0], blocks[1]);
+  constexpr uint32_t kTileBytes = PANELS * kPanelBytes;
+  const uint32_t q_tile = smem_addr(tiles), kv_tile = q_tile + kTiles * kTileBytes;
+  volatile int* gave_up = &sh.gave_up;
+
+  const int first = unit.index * F::kQueries;  // first query, within the sequence
+  int blocks[kTiles];                          // tiles of keys that each tile of queries sees
+  for (int i = 0; i < kTiles; ++i) blocks[i] = first + i * kTile < unit.length ? first / kTile + 1 + i : 0;
+  const int most = max(blocks[0], blocks[kTiles - 1]);
   const int dim16 = (a.dim + 15) / 16;
 
-  if (warp >= 8) {
-    give_registers();
-    if (warp == 9) {
-    // ---- loads: Q tiles, then K 0, V 0, K 1, V 1, ...
-    const int kv_head = head / (a.heads / a.kv_heads);
+  // The loads need no tensor memory: they begin before it has been given.
+  // Q tiles first, then K 0, V 0, K 1, V 1, ...
+  const int kv_head = head / (a.heads / a.kv_heads);
+  uint32_t own_parity = 0;
+  auto load = [&](int n) {
+    const int stage = n % kStages, key = (n >> 1) * kTile;
+    return load_tile(n & 1 ? &v_map : &k_map, kv_tile + stage * kTileBytes, PANELS, kv_head, unit.begin + key,
+                     n & 1 ? unit.length - key : kTile, smem_addr(&sh.kv_full[stage]), smem_addr(&sh.own), &own_parity,
+                     gave_up);
+  };
+  if (warp == F::kLoader) {
     if (lane == 0) {
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < kTiles; ++i) {
         if (!blocks[i]) continue;
         const uint32_t bar = smem_addr(&sh.q_full[i]);
         mbar_expect(bar, kTileBytes);
@@ -119,98 +133,97 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load(q_tile + i * kTileBytes + p * kPanelBytes, &q_map, p * 64, head, unit.begin + first + i * kTile, bar);
       }
     }
-    uint32_t own_parity = 0;
-    for (int n = 0; n < 2 * most; ++n) {
-      const int stage = n % kStages;
-      if (n >= kStages && !mbar_wait(smem_addr(&sh.kv_empty[stage]), (n / kStages - 1) & 1, gave_up)) break;
-      const int key = (n >> 1) * kTile;
-      if (!load_tile(n & 1 ? &v_map : &k_map, kv_tile + stage * kTileBytes, PANELS, kv_head, unit.begin + key,
-                     n & 1 ? unit.length - key : kTile, smem_addr(&sh.kv_full[stage]), smem_addr(&sh.own), &own_parity,
-                     gave_up))
-        break;
-    }
-  } else if (warp == 8) {
-    // ---- products, all issued by one thread
-    if (elect_one()) {
-      const uint32_t qk = mma_shape<T>(kTile, false), pv = mma_shape<T>(dim16 * 16, true);
-      auto full = [&](int n) {
-        return mbar_wait(smem_addr(&sh.kv_full[n % kStages]), (n / kStages) & 1, gave_up);
-      };
-      auto scores = [&](int i, int j) {
-        product_ss<4 * PANELS>(tmem + i * 128, q_tile + i * kTileBytes, kv_tile + (2 * j % kStages) * kTileBytes, qk, dim16);
-        mma_commit(smem_addr(&sh.s_full[i]));
-      };
-      auto output = [&](int i, int j) {
-        const uint32_t v = kv_tile + ((2 * j + 1) % kStages) * kTileBytes;
-        for (int h = 0; h < 2; ++h) {
-          if (!mbar_wait(smem_addr(&sh.p_full[i][h]), j & 1, gave_up)) return false;
-          tc_fence_after();
-          product_ts<4>(out_at(i), p_at(i) + h * 32, v, h, pv, j > 0 || h > 0);
-        }
-        mma_commit(smem_addr(&sh.o_done[i]));
-        return true;
-      };
-      bool ok = full(0);
-      for (int i = 0; i < 2 && ok; ++i)
-        if (blocks[i] && (ok = mbar_wait(smem_addr(&sh.q_full[i]), 0, gave_up))) scores(i, 0);
-      if (ok) mma_commit(smem_addr(&sh.kv_empty[0]));
-      for (int j = 0; j < most && ok; ++j) {
-        const int vn = 2 * j + 1, kn = vn + 1;
-        if constexpr (kApart) {
-          if (j + 1 < most) {
-            if (!(ok = full(kn))) break;
-            for (int i = 0; i < 2 && ok; ++i) {
-              if (j + 1 >= blocks[i]) continue;
-              if (!(ok = mbar_wait(smem_addr(&sh.s_read[i]), j & 1, gave_up))) break;
+    load(0);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  // tensor memory: each tile's scores, then probabilities where they are apart, then outputs
+  const uint32_t tmem = sh.tmem;
+  auto p_at = [&](int i, int half) { return tmem + (F::kApart ? 128 + half * 32 : i * 128 + half * 32); };
+  auto out_at = [&](int i) { return tmem + (F::kApart ? 192 : 256 + i * 128); };
+
+  if (warp >= F::kIssuer) {
+    if constexpr (F::kThreads == 384) give_registers();
+    if (warp == F::kLoader) {
+      for (int n = 1; n < 2 * most; ++n) {
+        if (n >= kStages && !mbar_wait(smem_addr(&sh.kv_empty[n % kStages]), (n / kStages - 1) & 1, gave_up)) break;
+        if (!load(n)) break;
+      }
+    } else if (warp == F::kIssuer) {
+      // ---- products, all issued by one thread
+      if (elect_one()) {
+        const uint32_t qk = mma_shape<T>(kTile, false), pv = mma_shape<T>(dim16 * 16, true);
+        auto full = [&](int n) {
+          return mbar_wait(smem_addr(&sh.kv_full[n % kStages]), (n / kStages) & 1, gave_up);
+        };
+        auto scores = [&](int i, int j) {
+          product_ss<4 * PANELS>(tmem + i * 128, q_tile + i * kTileBytes, kv_tile + (2 * j % kStages) * kTileBytes, qk, dim16);
+          mma_commit(smem_addr(&sh.s_full[i]));
+        };
+        auto output = [&](int i, int j) {
+          const uint32_t v = kv_tile + ((2 * j + 1) % kStages) * kTileBytes;
+          for (int h = 0; h < 2; ++h) {
+            if (!mbar_wait(smem_addr(&sh.p_full[i][h]), j & 1, gave_up)) return false;
+            tc_fence_after();
+            product_ts<4>(out_at(i), p_at(i, h), v, h, pv, j > 0 || h > 0);
+          }
+          mma_commit(smem_addr(&sh.o_done[i]));
+          return true;
+        };
+        bool ok = full(0);
+        for (int i = 0; i < kTiles && ok; ++i)
+          if (blocks[i] && (ok = mbar_wait(smem_addr(&sh.q_full[i]), 0, gave_up))) scores(i, 0);
+        if (ok) mma_commit(smem_addr(&sh.kv_empty[0]));
+        for (int j = 0; j < most && ok; ++j) {
+          const int vn = 2 * j + 1, kn = vn + 1;
+          const bool more = j + 1 < most;
+          if constexpr (F::kApart) {
+            if (more) {
+              if (!(ok = full(kn) && mbar_wait(smem_addr(&sh.s_read[0]), j & 1, gave_up))) break;
               tc_fence_after();
-              scores(i, j + 1);
+              scores(0, j + 1);
+              mma_commit(smem_addr(&sh.kv_empty[kn % kStages]));
             }
+            if (!(ok = full(vn) && output(0, j))) break;
+          } else {
+            ok = full(vn) && (!more || full(kn));
+            for (int i = 0; i < kTiles && ok; ++i)
+              if (j < blocks[i] && (ok = output(i, j)) && j + 1 < blocks[i]) scores(i, j + 1);
             if (!ok) break;
-            mma_commit(smem_addr(&sh.kv_empty[kn % kStages]));
+            if (more) mma_commit(smem_addr(&sh.kv_empty[kn % kStages]));
           }
-          ok = full(vn);
-          for (int i = 0; i < 2 && ok; ++i)
-            if (j < blocks[i]) ok = output(i, j);
-          if (!ok) break;
           mma_commit(smem_addr(&sh.kv_empty[vn % kStages]));
-        } else {
-          ok = full(vn) && (j + 1 >= most || full(kn));
-          for (int i = 0; i < 2 && ok; ++i) {
-            if (j >= blocks[i]) continue;
-            if ((ok = output(i, j)) && j + 1 < blocks[i]) scores(i, j + 1);
-          }
-          if (!ok) break;
-          mma_commit(smem_addr(&sh.kv_empty[vn % kStages]));
-          if (j + 1 < most) mma_commit(smem_addr(&sh.kv_empty[kn % kStages]));
         }
       }
-    }
-    __syncwarp();
+      __syncwarp();
     }
   } else {
-    take_registers();
-    // ---- softmax of tile i: thread t has query t's row
-    const int i = warp >> 2, n = blocks[i];
+    if constexpr (F::kThreads == 384) take_registers();
+    // ---- softmax: a thread has one query of tile i and 128 / kShare of its keys
+    constexpr int kKeys = kTile / kShare, kChunks = kKeys / 32;
+    const int i = kShare == 1 ? warp >> 2 : 0, half = kShare == 1 ? 0 : warp >> 2, n = blocks[i];
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
-    const uint32_t s_at = lanes + tmem + i * 128, o_at = lanes + out_at(i);
-    const int row = (warp & 3) * 32 + lane;
+    const uint32_t s_at = lanes + tmem + i * 128 + half * kKeys, o_at = lanes + out_at(i);
+    const int row = (warp & 3) * 32 + lane, pair = 1 + (warp & 3);
     const float c = a.scale * kLog2e;
+    const Two c2 = two(c, c);
     float m = -INFINITY, sum = 0.f;
     bool ok = true;
     for (int j = 0; j < n; ++j) {
       if (!(ok = mbar_wait(smem_addr(&sh.s_full[i]), j & 1, gave_up))) break;
       tc_fence_after();
-      float s[4][32], top[4];
+      float s[kChunks][32], top[kChunks];
       tmem_load32(s_at, s[0]);
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
+      for (int b = 0; b < kChunks; ++b) {
         tmem_wait_load();
         tmem_loaded(s[b]);
-        if (b < 3) tmem_load32(s_at + (b + 1) * 32, s[b + 1]);  // on its way while these are looked at
+        if (b + 1 < kChunks) tmem_load32(s_at + (b + 1) * 32, s[b + 1]);  // on its way while these are looked at
         if (j == n - 1) {
 #pragma unroll
           for (int x = 0; x < 32; ++x)
-            if (b * 32 + x > row) s[b][x] = -INFINITY;
+            if (half * kKeys + b * 32 + x > row) s[b][x] = -INFINITY;
         }
         float even = fmaxf(s[b][0], s[b][1]), odd = fmaxf(s[b][2], s[b][3]);
 #pragma unroll
@@ -220,10 +233,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         top[b] = fmaxf(even, odd);
       }
-      if constexpr (kApart) {
-        warp_arrive(smem_addr(&sh.s_read[i]));
+      if constexpr (F::kApart) warp_arrive(smem_addr(&sh.s_read[i]));
+      float most_s = fmaxf(top[0], top[1]);
+      if constexpr (kShare == 1) {
+        most_s = max3(most_s, top[kChunks - 2], top[kChunks - 1]);
+      } else {
+        // the other half's; this one's next goes elsewhere, and the one after
+        // that is written after both have met again
+        sh.top[j & 1][half][row] = most_s;
+        named_barrier(pair, 64);
+        most_s = fmaxf(most_s, sh.top[j & 1][half ^ 1][row]);
       }
-      const float most_s = max3(fmaxf(top[0], top[1]), top[2], top[3]);
       if (j == 0) {
         m = most_s;
       } else if (__any_sync(0xFFFFFFFFu, (most_s - m) * c > kSlack)) {
@@ -233,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         sum *= by;
         if (!(ok = mbar_wait(smem_addr(&sh.o_done[i]), (j - 1) & 1, gave_up))) break;
         tc_fence_after();
-        for (int d = 0; d < dim16; ++d) {
+        for (int d = half; d < dim16; d += kShare) {
           float o[16];
           tmem_load16(o_at + d * 16, o);
           tmem_wait_load();
@@ -242,44 +262,60 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int x = 0; x < 16; ++x) o[x] *= by;
           tmem_store16(o_at + d * 16, o);
         }
+        if constexpr (kShare == 2) {
+          // the product may begin once one half's probabilities are there: by then both have rescaled
+          tmem_wait_store();
+          tc_fence_before();
+          named_barrier(pair, 64);
+        }
       }
       const float base = m == -INFINITY ? 0.f : m * c;
-      const Two c2 = two(c, c), base2 = two(-base, -base);
+      const Two base2 = two(-base, -base);
+      if (F::kApart && j > 0) {
+        // the last product has read the probabilities that these replace
+        if (!(ok = mbar_wait(smem_addr(&sh.o_done[i]), (j - 1) & 1, gave_up))) break;
+        tc_fence_after();
+      }
       Two part[2] = {two(0.f, 0.f), two(0.f, 0.f)};
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t p[32];
+      for (int b = 0; b < kChunks; ++b) {
+        uint32_t p[16];
 #pragma unroll
-        for (int x = 0; x < 32; ++x) {
-          const int b = 2 * h + (x >> 4), e = 2 * (x & 15);
+        for (int x = 0; x < 16; ++x) {
           float lo, hi;
-          split(fma2(two(s[b][e], s[b][e + 1]), c2, base2), lo, hi);
+          split(fma2(two(s[b][2 * x], s[b][2 * x + 1]), c2, base2), lo, hi);
           lo = exp2_approx(lo);
           hi = exp2_approx(hi);
           part[x & 1] = add2(part[x & 1], two(lo, hi));
           p[x] = pack2<T>(lo, hi);
         }
-        if (kApart && h == 0 && j > 0) {
-          // the last product has read the probabilities that these replace
-          if (!(ok = mbar_wait(smem_addr(&sh.o_done[i]), (j - 1) & 1, gave_up))) break;
-          tc_fence_after();
+        tmem_store16(lanes + p_at(i, half) + b * 16, p);
+        if (kShare == 1 && b == 1) {
+          tmem_wait_store();
+          warp_arrive(smem_addr(&sh.p_full[i][0]));
         }
-        tmem_store32(lanes + p_at(i) + h * 32, p);
-        tmem_wait_store();
-        warp_arrive(smem_addr(&sh.p_full[i][h]));
       }
-      if (!ok) break;
+      tmem_wait_store();
+      warp_arrive(smem_addr(&sh.p_full[i][kShare == 1 ? 1 : half]));
       float sum_lo, sum_hi;
       split(add2(part[0], part[1]), sum_lo, sum_hi);
       sum += sum_lo + sum_hi;
     }
     if (n && ok && mbar_wait(smem_addr(&sh.o_done[i]), (n - 1) & 1, gave_up)) {
       tc_fence_after();
+      if constexpr (kShare == 2) {
+        // both halves go on with the same sum, added in the same order
+        if (half) sh.sum[row] = sum;
+        named_barrier(pair, 64);
+        if (!half) sh.sum[row] = sum += sh.sum[row];
+        named_barrier(pair, 64);
+        sum = sh.sum[row];
+      }
       const int at = first + i * kTile + row;  // within the sequence
       const int64_t token = unit.begin + at;
       const float inv = 1.f / sum;
       T* out = static_cast<T*>(const_cast<void*>(a.out.ptr)) + token * a.out.token_stride + head * a.out.head_stride;
-      for (int d = 0; d < dim16; ++d) {
+      for (int d = half; d < dim16; d += kShare) {
         float o[16];
         tmem_load16(o_at + d * 16, o);
         tmem_wait_load();
@@ -294,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (a.lse && at < unit.length) a.lse[(int64_t)head * a.tokens + token] = (m * c + log2f(sum)) * kLn2;
+      if (a.lse && !half && at < unit.length) a.lse[(int64_t)head * a.tokens + token] = (m * c + log2f(sum)) * kLn2;
     }
   }
 
@@ -306,13 +342,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) g_status = AR_ERR_TIMEOUT;
     __syncthreads();
   }
-  if (warp == 8) tmem_free(tmem, 512);
+  if (warp == F::kIssuer) tmem_free(tmem, F::kColumns);
 }
 
 template <class T, int PANELS>
 cudaError_t run(int dtype, const AttnArgs& a, cudaStream_t s) {
   static std::atomic<unsigned long long> opened[256];
-  constexpr int smem = (2 + kStages) * PANELS * (int)kPanelBytes;
+  using F = Form<PANELS>;
+  constexpr int smem = (F::kTiles + kStages) * PANELS * (int)kPanelBytes;
   cudaError_t e = open_kernel((const void*)attention_kernel<T, PANELS>, smem, false, opened);
   if (e != cudaSuccess) return e;
   // the warpgroups' shares are sound only if the launch brings them
@@ -320,15 +357,15 @@ cudaError_t run(int dtype, const AttnArgs& a, cudaStream_t s) {
     cudaFuncAttributes f;
     return cudaFuncGetAttributes(&f, (const void*)attention_kernel<T, PANELS>) == cudaSuccess ? f.numRegs : 0;
   }();
-  if (registers != kLaunchRegisters) return cudaErrorInvalidConfiguration;
+  if (F::kThreads == 384 && registers != kLaunchRegisters) return cudaErrorInvalidConfiguration;
   CUtensorMap q, k, v;
   if (!make_tensor_map(&q, dtype, a.q, a.tokens, a.heads, a.dim) ||
       !make_tensor_map(&k, dtype, a.k, a.tokens, a.kv_heads, a.dim) ||
       !make_tensor_map(&v, dtype, a.v, a.tokens, a.kv_heads, a.dim))
     return cudaErrorInvalidValue;
-  // at most this many pairs of tiles, however the tokens are split
-  const int64_t pairs = a.tokens / kPair + std::min<int64_t>(a.seqs, a.tokens);
-  attention_kernel<T, PANELS><<<(unsigned)(pairs * a.heads), kThreads, smem, s>>>(q, k, v, a);
+  // at most this many units, however the tokens are split
+  const int64_t units = a.tokens / F::kQueries + std::min<int64_t>(a.seqs, a.tokens);
+  attention_kernel<T, PANELS><<<(unsigned)(units * a.heads), F::kThreads, smem, s>>>(q, k, v, a);
   count_launch();
   return cudaGetLastError();
 }

@@ -154,17 +154,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       sh.unit = u;
       sh.gave_up = 0;
     }
-  }
-  __syncthreads();
-  if (sh.unit.count == 0) return;
-  const SeqUnit unit = sh.unit;
-
-  constexpr uint32_t kTileBytes = PANELS * kPanelBytes;
-  const uint32_t k_tile = smem_addr(tiles), v_tile = k_tile + kTileBytes, q_tile = v_tile + kTileBytes,
-                 do_tile = q_tile + kStages * kTileBytes;
-  volatile int* gave_up = &sh.gave_up;
-  if (warp == kIssuer) tmem_alloc(smem_addr(&sh.tmem), 512);
-  if (threadIdx.x == 0) {
+  } else if (warp == kLoader && lane == 0) {
     uint64_t* const one[] = {&sh.kv_full, &sh.s_full, &sh.dp_full, &sh.dv_done, &sh.dk_done, &sh.done, &sh.own};
     for (uint64_t* b : one) mbar_init(smem_addr(b), 1);
     for (int i = 0; i < kStages; ++i) {
@@ -176,6 +166,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (uint64_t* b : all) mbar_init(smem_addr(b), kWorkers / 32);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  __syncthreads();
+  if (sh.unit.count == 0) return;
+  SeqUnit unit = sh.unit;
+  unit.index = unit.count - 1 - unit.index;  // the first keys are seen by the most queries
+
+  constexpr uint32_t kTileBytes = PANELS * kPanelBytes;
+  const uint32_t k_tile = smem_addr(tiles), v_tile = k_tile + kTileBytes, q_tile = v_tile + kTileBytes,
+                 do_tile = q_tile + kStages * kTileBytes;
+  volatile int* gave_up = &sh.gave_up;
+  if (warp == kIssuer) tmem_alloc(smem_addr(&sh.tmem), 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -364,17 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       sh.unit = u;
       sh.gave_up = 0;
     }
-  }
-  __syncthreads();
-  if (sh.unit.count == 0) return;
-  const SeqUnit unit = sh.unit;
-
-  constexpr uint32_t kTileBytes = PANELS * kPanelBytes;
-  const uint32_t q_tile = smem_addr(tiles), do_tile = q_tile + kTileBytes, k_tile = do_tile + kTileBytes,
-                 v_tile = k_tile + kKStages * kTileBytes;
-  volatile int* gave_up = &sh.gave_up;
-  if (warp == kIssuer) tmem_alloc(smem_addr(&sh.tmem), 512);
-  if (threadIdx.x == 0) {
+  } else if (warp == kLoader && lane == 0) {
     uint64_t* const one[] = {&sh.q_full, &sh.s_full, &sh.dp_full[0], &sh.dp_full[1], &sh.done, &sh.own};
     for (uint64_t* b : one) mbar_init(smem_addr(b), 1);
     for (int i = 0; i < kKStages; ++i) {
@@ -389,6 +379,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_addr(&sh.ds_ready), kWorkers / 32);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  __syncthreads();
+  if (sh.unit.count == 0) return;
+  const SeqUnit unit = sh.unit;
+
+  constexpr uint32_t kTileBytes = PANELS * kPanelBytes;
+  const uint32_t q_tile = smem_addr(tiles), do_tile = q_tile + kTileBytes, k_tile = do_tile + kTileBytes,
+                 v_tile = k_tile + kKStages * kTileBytes;
+  volatile int* gave_up = &sh.gave_up;
+  if (warp == kIssuer) tmem_alloc(smem_addr(&sh.tmem), 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -396,8 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // next tile's scores and dout v^T are under way while this one's ds is made.
   const uint32_t tmem = sh.tmem;
 
-  const int tile = unit.count - 1 - unit.index;  // the longest rows of a sequence first
-  const int steps = tile + 1, query = tile * kTile;
+  const int steps = unit.index + 1, query = unit.index * kTile;
   const int dim16 = (a.dim + 15) / 16;
 
   if (warp == kLoader) {

@@ -324,39 +324,69 @@ __device__ __forceinline__ float exp2_approx(float x) {
 
 // ---- packed sequences ------------------------------------------------------------------
 
-// Unit `unit` of the work that splits every sequence into ceil(length / size)
-// units, sequences in order.  `index` is its place in its sequence.
+// Every sequence is split into ceil(length / size) units, the i-th of which
+// (from 0) stands for work in proportion to i + 1; where the first unit is the
+// longest, the caller counts from the end.  A launch takes the units of all
+// sequences with the most work first, so that no long one starts last.
 struct SeqUnit {
-  int begin, length, index, count;
+  int begin, length;  // the sequence
+  int index;          // the unit's place in it
+  int count;          // its units; 0: there is no such unit
 };
 
-// By one warp; count 0 when there is no such unit.  Entries are clamped, so
-// that no value in cu_seqlens leads outside the tensors.
+// The `unit`-th unit in that order, by one warp.  There are
+// sum_s max(0, n_s - w) units with more work than w, n_s being the units of
+// sequence s.  The work of the one asked for is found by looking at 32 values
+// of w at a time, one to a lane; then the sequence, which is the next one in
+// order that has a unit of that work.  Entries of cu_seqlens are clamped, so
+// that no value in it leads outside the tensors.
 __device__ __forceinline__ SeqUnit find_unit(const int32_t* cu_seqlens, int seqs, int tokens, int size, int unit) {
+  constexpr uint32_t kAll = 0xFFFFFFFFu;
   const int lane = threadIdx.x & 31;
-  int before = 0;
+  int begin = 0, length = 0, first = -1;
+  auto look = [&](int s0) {  // this lane's sequence of the 32 from s0; its units
+    if (s0 != first) {
+      const int s = s0 + lane;
+      begin = length = 0;
+      if (s < seqs) {
+        begin = min(max(cu_seqlens[s], 0), tokens);
+        length = min(max(cu_seqlens[s + 1], begin), tokens) - begin;
+      }
+      first = s0;
+    }
+    return (length + size - 1) / size;
+  };
+  int w = 0, range = (tokens + size - 1) / size;  // the work less one is in [w, w + range)
+  int after;                                      // units with more work than that and one
+  for (;;) {
+    const int step = (range + 30) / 31;
+    const int mine = w + lane * step;
+    int above = 0;
+    for (int s0 = 0; s0 < seqs; s0 += 32) {
+      const int n = look(s0), here = min(32, seqs - s0);
+      for (int k = 0; k < here; ++k) above += max(__shfl_sync(kAll, n, k) - mine, 0);
+    }
+    const uint32_t more = __ballot_sync(kAll, above > unit);
+    if (!more) return SeqUnit{0, 0, 0, 0};
+    const int last = 31 - __clz(more);
+    w += last * step;
+    if (step == 1) {
+      after = __shfl_sync(kAll, above, min(last + 1, 31));
+      break;
+    }
+    range = step;
+  }
+  int place = unit - after;
   for (int s0 = 0; s0 < seqs; s0 += 32) {
-    const int s = s0 + lane;
-    int begin = 0, length = 0;
-    if (s < seqs) {
-      begin = min(max(cu_seqlens[s], 0), tokens);
-      length = min(max(cu_seqlens[s + 1], begin), tokens) - begin;
+    const int n = look(s0);
+    const uint32_t has = __ballot_sync(kAll, n > w);
+    const int here = __popc(has);
+    if (place < here) {
+      const bool it = n > w && __popc(has & ((1u << lane) - 1)) == place;
+      const int from = __ffs(__ballot_sync(kAll, it)) - 1;
+      return SeqUnit{__shfl_sync(kAll, begin, from), __shfl_sync(kAll, length, from), w, __shfl_sync(kAll, n, from)};
     }
-    const int units = (length + size - 1) / size;
-    int upto = units;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int v = __shfl_up_sync(0xFFFFFFFFu, upto, d);
-      if (lane >= d) upto += v;
-    }
-    const int place = unit - before - (upto - units);
-    const uint32_t mine = __ballot_sync(0xFFFFFFFFu, place >= 0 && place < units);
-    if (mine) {
-      const int from = __ffs(mine) - 1;
-      return SeqUnit{__shfl_sync(0xFFFFFFFFu, begin, from), __shfl_sync(0xFFFFFFFFu, length, from),
-                     __shfl_sync(0xFFFFFFFFu, place, from), __shfl_sync(0xFFFFFFFFu, units, from)};
-    }
-    before += __shfl_sync(0xFFFFFFFFu, upto, 31);
+    place -= here;
   }
   return SeqUnit{0, 0, 0, 0};
 }
