@@ -20,16 +20,11 @@
 namespace ar {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
+constexpr int kStream = kThreads - 32;  // threads that stream the row, while one warp makes the list
+constexpr int kBlocks = 4;    // on a multiprocessor
 constexpr int kMaxParts = 8;  // portable cluster size
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-
-__device__ __forceinline__ float exp2_fast(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
 
 // A softmax's running maximum (of the unscaled logits) and the sum of
 // 2^(c (z - m)), c = log2(e) / tau.
@@ -40,7 +35,7 @@ struct Stat {
 __device__ __forceinline__ Stat join(Stat a, Stat b, float c) {
   const float m = fmaxf(a.m, b.m);
   if (m == -INFINITY) return Stat{m, a.s + b.s};  // nothing but -inf (or NaN) so far
-  return Stat{m, a.s * exp2_fast((a.m - m) * c) + b.s * exp2_fast((b.m - m) * c)};
+  return Stat{m, a.s * exp2_approx((a.m - m) * c) + b.s * exp2_approx((b.m - m) * c)};
 }
 
 __device__ __forceinline__ Stat warp_join(Stat a, float c) {
@@ -50,31 +45,62 @@ __device__ __forceinline__ Stat warp_join(Stat a, float c) {
   return a;
 }
 
+// The largest element of U vectors.
+template <class T, int U>
+__device__ __forceinline__ float largest(const uint4 (&p)[U]) {
+  if constexpr (sizeof(T) == 4) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      m = fmaxf(m, max3(fmaxf(__uint_as_float(p[u].x), __uint_as_float(p[u].y)), __uint_as_float(p[u].z), __uint_as_float(p[u].w)));
+    return m;
+  } else {
+    uint32_t m[2] = {p[0].x, p[0].y};
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      m[0] = max_pairs<T>(m[0], max_pairs<T>(p[u].x, p[u].z));
+      m[1] = max_pairs<T>(m[1], max_pairs<T>(p[u].y, p[u].w));
+    }
+    float lo, hi;
+    split(unpack2<T>(max_pairs<T>(m[0], m[1])), lo, hi);
+    return fmaxf(lo, hi);
+  }
+}
+
 // Takes U vectors in.  With the maximum known first, an element costs one
 // fused multiply-add and one exponential; a maximum so large (a type's lowest
 // value, as masks have) that c m overflows takes differences instead.
-template <class T, int N, int U>
-__device__ __forceinline__ void accumulate(Stat& st, const Pack<T, N> (&p)[U], float c) {
-  float m = st.m;
-#pragma unroll
-  for (int u = 0; u < U; ++u)
-#pragma unroll
-    for (int i = 0; i < N; ++i) m = fmaxf(m, Conv<T>::up(p[u].v[i]));
+template <class T, int U>
+__device__ __forceinline__ void accumulate(Stat& st, const uint4 (&p)[U], float c) {
+  const float m = fmaxf(st.m, largest<T, U>(p));
   const float base = m * c;
+  Two part[2] = {two(0.f, 0.f), two(0.f, 0.f)};
   if (fabsf(base) < INFINITY) {
-    st.s *= exp2_fast(fmaf(st.m, c, -base));
+    st.s *= exp2_approx(fmaf(st.m, c, -base));
+    const Two c2 = two(c, c), base2 = two(-base, -base);
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int i = 0; i < N; ++i) st.s += exp2_fast(fmaf(Conv<T>::up(p[u].v[i]), c, -base));
+      for (int i = 0; i < Pairs<T>::N; ++i) {
+        float lo, hi;
+        split(fma2(Pairs<T>::get(p[u], i), c2, base2), lo, hi);
+        part[i & 1] = add2(part[i & 1], two(exp2_approx(lo), exp2_approx(hi)));
+      }
   } else {
     const float from = m == -INFINITY ? 0.f : m;  // nothing but -inf (or NaN) so far
-    st.s *= exp2_fast((st.m - from) * c);
+    st.s *= exp2_approx((st.m - from) * c);
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int i = 0; i < N; ++i) st.s += exp2_fast((Conv<T>::up(p[u].v[i]) - from) * c);
+      for (int i = 0; i < Pairs<T>::N; ++i) {
+        float lo, hi;
+        split(Pairs<T>::get(p[u], i), lo, hi);
+        part[i & 1] = add2(part[i & 1], two(exp2_approx((lo - from) * c), exp2_approx((hi - from) * c)));
+      }
   }
+  float lo, hi;
+  split(add2(part[0], part[1]), lo, hi);
+  st.s += lo + hi;
   st.m = m;
 }
 
@@ -92,36 +118,21 @@ __device__ __forceinline__ float cluster_read(const float* own, int rank) {
   return v;
 }
 
-__device__ __forceinline__ float block_sum(float v, float* scratch) {
-  v = warp_sum(v);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
-  __syncthreads();
-  return warp_sum((threadIdx.x & 31) < kThreads / 32 ? scratch[threadIdx.x & 31] : 0.f);
-}
-
-__device__ __forceinline__ float block_max(float v, float* scratch) {
-  v = warp_max(v);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
-  __syncthreads();
-  return warp_max((threadIdx.x & 31) < kThreads / 32 ? scratch[threadIdx.x & 31] : -INFINITY);
-}
-
 // A row's elements as the aligned 16-byte vectors they lie in: with `shift`
 // the elements between the vector boundary before the row and its first
 // element, vector v holds elements [v N - shift, v N - shift + N).
-template <class T, int N>
+template <class T>
 struct RowVectors {
+  static constexpr int N = 16 / sizeof(T);
   const T* row;
   int vocab, shift;
   __device__ RowVectors(const T* r, int n) : row(r), vocab(n), shift((int)(((uintptr_t)r & 15) / sizeof(T))) {}
   __device__ int count() const { return (vocab + shift + N - 1) / N; }
   __device__ int first(int v) const { return v * N - shift; }
   __device__ bool whole(int v) const { return first(v) >= 0 && first(v) + N <= vocab; }
-  __device__ Pack<T, N> load(int v) const { return *reinterpret_cast<const Pack<T, N>*>(row + first(v)); }
+  __device__ uint4 load(int v) const { return *reinterpret_cast<const uint4*>(row + first(v)); }
   // any vector: places outside the row as -inf
-  __device__ Pack<T, N> some(int v) const {
+  __device__ uint4 some(int v) const {
     if (whole(v)) return load(v);
     Pack<T, N> p;
 #pragma unroll
@@ -129,161 +140,433 @@ struct RowVectors {
       const int e = first(v) + i;
       p.v[i] = e >= 0 && e < vocab ? row[e] : Conv<T>::down(-INFINITY);
     }
+    return *reinterpret_cast<const uint4*>(&p);
+  }
+};
+
+// What one warp makes of a row's list while the others stream the row.  Arrays
+// of `top` in shared memory:
+//   word   the word, or -1 for an entry outside the vocabulary
+//   logit  the student's logit of the word
+//   prob   the teacher's probability
+//   sum    the word's probability with all of its entries, for the first of
+//          them; -1 for the others
+struct List {
+  int* word;
+  float *logit, *prob, *sum;
+  __device__ List(void* at, int top)
+      : word(static_cast<int*>(at)),
+        logit(reinterpret_cast<float*>(word + top)),
+        prob(logit + top),
+        sum(prob + top) {}
+};
+constexpr int kListBytes = 16;  // for each entry
+
+// sum p (log p - z / tau): the loss is tau^2 times this plus lse.
+struct Divergence {
+  float value;
+  bool some;  // the row has a distribution
+};
+
+template <class T, class V>
+__device__ __forceinline__ Divergence make_list(const DistillArgs& a, int64_t row, const T* z, int vocab, float inv_tau,
+                                                bool gradient, const List& list) {
+  const int lane = threadIdx.x & 31, top = a.top;
+  const int32_t* index = a.index + row * top;
+  const V* value = static_cast<const V*>(a.value) + row * top;
+  float tmax = -INFINITY;
+  for (int k = lane; k < top; k += 32) {
+    const int w = index[k];
+    const bool is = w >= 0 && w < vocab;
+    const float x = is ? Conv<V>::up(value[k]) * inv_tau : -INFINITY;
+    list.word[k] = is ? w : -1;
+    list.logit[k] = is ? Conv<T>::up(z[w]) : 0.f;
+    list.sum[k] = x;
+    tmax = fmaxf(tmax, x);
+  }
+  tmax = warp_max(tmax);
+  if (tmax == -INFINITY) tmax = 0.f;
+  float total = 0.f;
+  for (int k = lane; k < top; k += 32) total += list.prob[k] = expf(list.sum[k] - tmax);
+  total = warp_sum(total);
+  const float log_total = logf(total);
+  float value_sum = 0.f;
+  const bool some = total > 0.f;
+  for (int k = lane; k < top; k += 32) {
+    const float p = list.prob[k] / total;
+    if (some && p > 0.f) value_sum += p * ((list.sum[k] - tmax - log_total) - list.logit[k] * inv_tau);
+    list.prob[k] = p;
+  }
+  value_sum = warp_sum(value_sum);
+  __syncwarp();
+  if (gradient) {
+    for (int k = lane; k < top; k += 32) {
+      const int w = list.word[k];
+      float p = 0.f;
+      bool first = w >= 0;
+#pragma unroll 8
+      for (int j = 0; j < top; ++j)
+        if (list.word[j] == w) {
+          first = first && j >= k;
+          p += list.prob[j];
+        }
+      list.sum[k] = first ? p : -1.f;
+    }
+  }
+  return Divergence{value_sum, some};
+}
+
+// scale tau q for elements of one row.  A 16-bit result hides the rounding of
+// a base-2 exponent, an f32 one would show it (about 7e-7 at a probability of
+// 2^-17).
+template <class T>
+struct Gradient {
+  float coef, lse, c, inv_tau, base;
+  bool plain;
+  __device__ Gradient(float coef_, float lse_, float c_, float inv_tau_)
+      : coef(coef_), lse(lse_), c(c_), inv_tau(inv_tau_), base(lse_ * kLog2e) {
+    plain = fabsf(base) < INFINITY;
+  }
+  __device__ float one(float x) const {
+    if constexpr (sizeof(T) == 4) return coef * expf(fmaf(x, inv_tau, -lse));
+    else return coef * (plain ? exp2_approx(fmaf(x, c, -base)) : exp2_approx(fmaf(x, inv_tau, -lse) * kLog2e));
+  }
+  __device__ uint4 vector(uint4 p) const {
+    const Two c2 = two(c, c), base2 = two(-base, -base), coef2 = two(coef, coef);
+#pragma unroll
+    for (int i = 0; i < Pairs<T>::N; ++i) {
+      float lo, hi;
+      if (sizeof(T) == 4 || !plain) {
+        split(Pairs<T>::get(p, i), lo, hi);
+        Pairs<T>::set(p, i, two(one(lo), one(hi)));
+      } else {
+        split(fma2(Pairs<T>::get(p, i), c2, base2), lo, hi);
+        Pairs<T>::set(p, i, mul2(coef2, two(exp2_approx(lo), exp2_approx(hi))));
+      }
+    }
     return p;
   }
 };
 
+// The listed words in [lo, hi), each once.
+template <class T>
+__device__ __forceinline__ void correct_listed(const List& list, int top, int lo, int hi, int t, int threads,
+                                               const Gradient<T>& gradient, T* dz) {
+  for (int k = t; k < top; k += threads) {
+    const int w = list.word[k];
+    if (w >= lo && w < hi && list.sum[k] >= 0.f)
+      dz[w] = Conv<T>::down(gradient.one(list.logit[k]) - gradient.coef * list.sum[k]);
+  }
+}
+
 // Block b of a row's `parts` blocks takes the b-th share of its vectors.  In
-// the forward direction they are one cluster and join their sums there.
+// the forward direction they are one cluster and join their sums there.  The
+// block's last warp makes the list.
 template <class T, class V, bool BACKWARD>
-__global__ void __launch_bounds__(kThreads) distill_kernel(const DistillArgs a, int parts) {
-  constexpr int N = 16 / sizeof(T);
+__global__ void __launch_bounds__(kThreads, kBlocks) distill_kernel(const DistillArgs a, int parts) {
   constexpr int U = 4;  // vectors in flight in each thread
-  __shared__ float prob[kDistillMaxTop], logit[kDistillMaxTop];
-  __shared__ int word[kDistillMaxTop];
+  extern __shared__ __align__(16) uint8_t lists[];
   __shared__ float scratch[32], scratch2[32];
   __shared__ float shared_stat[2];
+  __shared__ Divergence divergence;
 
   const int64_t row = blockIdx.x / parts;
   const int part = blockIdx.x % parts;
-  const int t = threadIdx.x, vocab = (int)a.vocab, top = a.top;
-  const float tau = a.temperature, c2 = kLog2e / tau;
+  const int t = threadIdx.x, lane = t & 31, vocab = (int)a.vocab, top = a.top;
+  const float tau = a.temperature, c = kLog2e / tau, inv_tau = 1.f / tau;
   const T* z = static_cast<const T*>(a.logits) + row * a.logits_stride;
-  const RowVectors<T, N> rv(z, vocab);
+  const RowVectors<T> rv(z, vocab);
   const int v0 = (int)((int64_t)rv.count() * part / parts), v1 = (int)((int64_t)rv.count() * (part + 1) / parts);
-  const int lo = max(rv.first(v0), 0), hi = min(rv.first(v1), vocab);  // this block's words
+  const List list(lists, top);
+  const bool streams = t < kStream;
 
-  // the teacher's distribution over the list; entries outside the vocabulary are no entries
-  const V* value = static_cast<const V*>(a.value) + row * top;
-  float tmax = -INFINITY;
-  for (int k = t; k < top; k += kThreads) {
-    const int w = a.index[row * top + k];
-    const bool there = w >= 0 && w < vocab;
-    const float x = there ? Conv<V>::up(value[k]) / tau : -INFINITY;
-    word[k] = there ? w : -1;
-    prob[k] = x;
-    logit[k] = there && (!BACKWARD || (w >= lo && w < hi)) ? Conv<T>::up(z[w]) : 0.f;
-    tmax = fmaxf(tmax, x);
+  if (!streams) {
+    // the student's logits of the listed words are read before anything is
+    // written (dlogits may be in the place of the logits)
+    const Divergence d = make_list<T, V>(a, row, z, vocab, inv_tau, a.dlogits != nullptr, list);
+    if (lane == 0) divergence = d;
   }
-  tmax = block_max(tmax, scratch);
-  if (tmax == -INFINITY) tmax = 0.f;
-  float tsum = 0.f;
-  for (int k = t; k < top; k += kThreads) tsum += expf(prob[k] - tmax);
-  tsum = block_sum(tsum, scratch);
-  const bool some = tsum > 0.f;
-  const float log_tsum = logf(tsum);
-
   float lse;
   if constexpr (BACKWARD) {
     lse = a.lse[row];
+    __syncthreads();
   } else {
     Stat st{-INFINITY, 0.f};
-    for (int v = v0 + t; v < v1; v += U * kThreads) {
-      if (v + (U - 1) * kThreads < v1 && rv.whole(v) && rv.whole(v + (U - 1) * kThreads)) {
-        Pack<T, N> p[U];
+    for (int v = v0 + t; v < v1 && streams; v += U * kStream) {
+      if (v + (U - 1) * kStream < v1 && rv.whole(v) && rv.whole(v + (U - 1) * kStream)) {
+        uint4 p[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) p[u] = rv.load(v + u * kThreads);
-        accumulate<T, N, U>(st, p, c2);
+        for (int u = 0; u < U; ++u) p[u] = rv.load(v + u * kStream);
+        accumulate<T, U>(st, p, c);
       } else {
-        for (int u = 0; u < U && v + u * kThreads < v1; ++u) {
-          const Pack<T, N> p[1] = {rv.some(v + u * kThreads)};
-          accumulate<T, N, 1>(st, p, c2);
+        for (int u = 0; u < U && v + u * kStream < v1; ++u) {
+          const uint4 p[1] = {rv.some(v + u * kStream)};
+          accumulate<T, 1>(st, p, c);
         }
       }
     }
-    st = warp_join(st, c2);
-    __syncthreads();  // the last reads of the scratch are done
-    if ((t & 31) == 0) scratch[t >> 5] = st.m, scratch2[t >> 5] = st.s;
+    st = warp_join(st, c);
+    if (lane == 0) scratch[t >> 5] = st.m, scratch2[t >> 5] = st.s;
     __syncthreads();
     st = Stat{-INFINITY, 0.f};
-    if ((t & 31) < kThreads / 32) st = Stat{scratch[t & 31], scratch2[t & 31]};
-    st = warp_join(st, c2);
+    if (lane < kThreads / 32) st = Stat{scratch[lane], scratch2[lane]};
+    st = warp_join(st, c);
     if (parts > 1) {
       if (t == 0) shared_stat[0] = st.m, shared_stat[1] = st.s;
       cluster_barrier();
       st = Stat{cluster_read(&shared_stat[0], 0), cluster_read(&shared_stat[1], 0)};
-      for (int r = 1; r < parts; ++r) st = join(st, Stat{cluster_read(&shared_stat[0], r), cluster_read(&shared_stat[1], r)}, c2);
+      for (int r = 1; r < parts; ++r) st = join(st, Stat{cluster_read(&shared_stat[0], r), cluster_read(&shared_stat[1], r)}, c);
       cluster_barrier();  // a block's shared memory outlives the others' reads of it
     }
     lse = st.m / tau + logf(st.s);
-    if (part == 0) {
-      float l = 0.f;
-      for (int k = t; k < top; k += kThreads) {
-        const float lp = prob[k] - tmax - log_tsum, p = expf(prob[k] - tmax) / tsum;
-        if (some && p > 0.f) l += p * (lp - (logit[k] / tau - lse));
-      }
-      l = block_sum(l, scratch);
-      if (t == 0) {
-        a.loss[row] = l * tau * tau;
-        a.lse[row] = lse;
-      }
+    if (part == 0 && t == 0) {
+      a.loss[row] = divergence.some ? (divergence.value + lse) * tau * tau : 0.f;
+      a.lse[row] = lse;
     }
     if (!a.dlogits) return;
   }
 
   const float scale = a.scale ? a.scale[row] : 1.f;
-  const float coef = scale * tau;
-  const bool live = some && scale != 0.f;
-  const float base = lse * kLog2e, inv_tau = 1.f / tau;
-  // q scaled: a 16-bit result hides the rounding of a base-2 exponent, an f32
-  // one would show it (about 7e-7 at a probability of 2^-17)
-  auto q_of = [&](float x) {
-    if constexpr (sizeof(T) == 4) return expf(fmaf(x, inv_tau, -lse));
-    else return fabsf(base) < INFINITY ? exp2_fast(fmaf(x, c2, -base)) : exp2_fast(fmaf(x, inv_tau, -lse) * kLog2e);
-  };
-  auto gradient = [&](float x) { return coef * q_of(x); };
+  const bool live = divergence.some && scale != 0.f;
+  const Gradient<T> gradient(scale * tau, lse, c, inv_tau);
   T* dz = static_cast<T*>(a.dlogits) + row * a.dlogits_stride;
   const bool same = (((uintptr_t)dz ^ (uintptr_t)z) & 15) == 0;
-  // with dlogits in the place of the logits, every listed logit has been read by now
-  __syncthreads();
+  auto vector = [&](const uint4& p) { return live ? gradient.vector(p) : make_uint4(0, 0, 0, 0); };
   for (int v = v0 + t; v < v1; v += U * kThreads) {
     if (same && v + (U - 1) * kThreads < v1 && rv.whole(v) && rv.whole(v + (U - 1) * kThreads)) {
-      Pack<T, N> p[U];
+      uint4 p[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) p[u] = rv.load(v + u * kThreads);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-          p[u].v[i] = Conv<T>::down(live ? gradient(Conv<T>::up(p[u].v[i])) : 0.f);
-        *reinterpret_cast<Pack<T, N>*>(dz + rv.first(v + u * kThreads)) = p[u];
-      }
+      for (int u = 0; u < U; ++u) *reinterpret_cast<uint4*>(dz + rv.first(v + u * kThreads)) = vector(p[u]);
     } else {
       for (int u = 0; u < U && v + u * kThreads < v1; ++u) {
         const int e = rv.first(v + u * kThreads);
-        Pack<T, N> p = rv.some(v + u * kThreads);
-#pragma unroll
-        for (int i = 0; i < N; ++i) p.v[i] = Conv<T>::down(live ? gradient(Conv<T>::up(p.v[i])) : 0.f);
+        const uint4 p = vector(rv.some(v + u * kThreads));
         if (same && rv.whole(v + u * kThreads)) {
-          *reinterpret_cast<Pack<T, N>*>(dz + e) = p;
+          *reinterpret_cast<uint4*>(dz + e) = p;
         } else {
+          const Pack<T, 16 / sizeof(T)> q = *reinterpret_cast<const Pack<T, 16 / sizeof(T)>*>(&p);
 #pragma unroll
-          for (int i = 0; i < N; ++i)
-            if (e + i >= 0 && e + i < vocab) dz[e + i] = p.v[i];
+          for (int i = 0; i < RowVectors<T>::N; ++i)
+            if (e + i >= 0 && e + i < vocab) dz[e + i] = q.v[i];
         }
       }
     }
   }
   if (!live) return;
   __syncthreads();
-  // the listed words of this block's share: a word listed more than once is
-  // corrected by its first entry, with the sum of all of them in list order
-  for (int k = t; k < top; k += kThreads) {
-    const int w = word[k];
-    if (w < lo || w >= hi) continue;
-    float p = 0.f;
-    bool first = true;
-    for (int j = 0; j < top; ++j)
-      if (word[j] == w) {
-        if (j < k) first = false;
-        p += expf(prob[j] - tmax) / tsum;
+  correct_listed<T>(list, top, max(rv.first(v0), 0), min(rv.first(v1), vocab), t, kThreads, gradient, dz);
+}
+
+// ---- rows through shared memory ----------------------------------------------------
+//
+// With enough rows to keep every multiprocessor busy, a block takes row after
+// row: one warp has pieces of the rows to come copied into shared memory as
+// their places become free, so loads never pause, and three make the lists of
+// the next rows, each of which takes a chain of dependent loads.  Where both
+// the loss and the gradient are wanted and a whole row fits, the second pass
+// reads it there; a longer row is copied in twice, the second time from L2.
+constexpr int kListWarps = 3;
+constexpr int kWorkers = 384;                                  // threads that compute
+constexpr int kRingThreads = kWorkers + 32 * kListWarps + 32;  // the last warp loads
+constexpr int kPieceVectors = 2 * kWorkers;                    // two to a thread
+constexpr int kPieceBytes = kPieceVectors * 16;
+constexpr int kMostPieces = 19;
+constexpr int kStreamPieces = 7;  // places where a row is not kept: 84 KB, two blocks to a multiprocessor
+constexpr int kRingMaxShared = 224 * 1024;
+
+__device__ __forceinline__ void workers_barrier() { named_barrier(1, kWorkers); }
+__device__ __forceinline__ void arrive_on(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_at(bar)) : "memory");
+}
+
+// The place that a sequence of pieces has come to.
+struct Place {
+  int slot = 0, round = 0;
+  __device__ void next(int places) {
+    if (++slot == places) slot = 0, ++round;
+  }
+};
+
+// pieces: to a row; places: of shared memory; keep: a row's pieces stay for a
+// second pass (places == pieces then)
+template <class T, class V, bool BACKWARD>
+__global__ void __launch_bounds__(kRingThreads, 2) distill_ring_kernel(const DistillArgs a, int pieces, int places, bool keep) {
+  constexpr int VN = 16 / sizeof(T);
+  extern __shared__ __align__(16) uint8_t buffer[];  // the places, then the lists
+  __shared__ Stat scratch[2][32];
+  __shared__ Divergence divergence[kListWarps];
+  __shared__ __align__(8) uint64_t filled[kMostPieces], empty[kMostPieces], list_made[kListWarps], list_used[kListWarps];
+
+  const int t = threadIdx.x, lane = t & 31, vocab = (int)a.vocab, top = a.top;
+  const float tau = a.temperature, c = kLog2e / tau, inv_tau = 1.f / tau;
+  const T* logits = static_cast<const T*>(a.logits);
+  const bool twice = !BACKWARD && a.dlogits;
+  auto list_of = [&](int i) { return List(buffer + places * kPieceBytes + i * kListBytes * top, top); };
+  auto init = [](uint64_t* bar, int count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_at(bar)), "r"(count) : "memory");
+  };
+  if (t == 0) {
+    for (int i = 0; i < places; ++i) {
+      init(&filled[i], 1);
+      init(&empty[i], kWorkers / 32);
+    }
+    for (int i = 0; i < kListWarps; ++i) {
+      init(&list_made[i], 1);
+      init(&list_used[i], kWorkers / 32);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+
+  if (t >= kRingThreads - 32) {
+    // ---- loads
+    if (lane == 0) {
+      Place at;
+      for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        const T* z = logits + row * a.logits_stride;
+        const uint8_t* from = reinterpret_cast<const uint8_t*>((uintptr_t)z & ~(uintptr_t)15);
+        const int bytes = (int)covering(z, vocab * (int)sizeof(T));
+        for (int pass = 0; pass < (twice && !keep ? 2 : 1); ++pass)
+          for (int i = 0; i < pieces; ++i, at.next(places)) {
+            if (at.round > 0) ring_wait(smem_at(&empty[at.slot]), (at.round - 1) & 1);
+            // rows that begin at other places in their first word may have a piece less
+            const int n = min(kPieceBytes, bytes - i * kPieceBytes);
+            const uint32_t bar = smem_at(&filled[at.slot]);
+            ring_expect(bar, max(n, 0));
+            if (n > 0) ring_copy(smem_at(buffer + at.slot * kPieceBytes), from + i * kPieceBytes, n, bar);
+          }
       }
-    if (first) dz[w] = Conv<T>::down(coef * (q_of(logit[k]) - p));
+    }
+    return;
+  }
+  if (t >= kWorkers) {
+    // ---- lists: warp i makes those of the block's rows i, i + 3, ...
+    const int i = (t - kWorkers) >> 5;
+    int round = 0;
+    for (int64_t row = blockIdx.x + (int64_t)i * gridDim.x; row < a.rows; row += (int64_t)kListWarps * gridDim.x, ++round) {
+      if (round > 0) ring_wait(smem_at(&list_used[i]), (round - 1) & 1);
+      const Divergence d = make_list<T, V>(a, row, logits + row * a.logits_stride, vocab, inv_tau, a.dlogits != nullptr, list_of(i));
+      if (lane == 0) divergence[i] = d;
+      __syncwarp();
+      if (lane == 0) arrive_on(&list_made[i]);
+    }
+    return;
+  }
+
+  Place at, list_at;
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1, list_at.next(kListWarps)) {
+    const T* z = logits + row * a.logits_stride;
+    const RowVectors<T> rv(z, vocab);
+    const int vecs = rv.count();
+    // vector v of the row, from piece `piece`; places outside the row as -inf
+    auto vector_at = [&](const uint8_t* piece, int v, int in_piece) {
+      uint4 raw = *reinterpret_cast<const uint4*>(piece + in_piece * 16);
+      if (!rv.whole(v)) {
+        Pack<T, VN> p = *reinterpret_cast<const Pack<T, VN>*>(&raw);
+#pragma unroll
+        for (int i = 0; i < VN; ++i)
+          if (rv.first(v) + i < 0 || rv.first(v) + i >= vocab) p.v[i] = Conv<T>::down(-INFINITY);
+        raw = *reinterpret_cast<const uint4*>(&p);
+      }
+      return raw;
+    };
+    auto release = [&](uint64_t* bar) {
+      __syncwarp();
+      if (lane == 0) arrive_on(bar);
+    };
+
+    float lse;
+    if constexpr (BACKWARD) {
+      lse = a.lse[row];
+    } else {
+      Stat st{-INFINITY, 0.f};
+      Place p1 = at;
+      for (int i = 0; i < pieces; ++i, p1.next(places)) {
+        ring_wait(smem_at(&filled[p1.slot]), p1.round & 1);
+        const uint8_t* piece = buffer + p1.slot * kPieceBytes;
+        const int v = i * kPieceVectors + t;
+        if (v + kWorkers < vecs) {
+          const uint4 p[2] = {vector_at(piece, v, t), vector_at(piece, v + kWorkers, t + kWorkers)};
+          accumulate<T, 2>(st, p, c);
+        } else if (v < vecs) {
+          const uint4 p[1] = {vector_at(piece, v, t)};
+          accumulate<T, 1>(st, p, c);
+        }
+        if (!keep) release(&empty[p1.slot]);
+      }
+      if (!keep) at = p1;
+      st = warp_join(st, c);
+      if (lane == 0) scratch[turn][t >> 5] = st;
+      workers_barrier();
+      st = lane < kWorkers / 32 ? scratch[turn][lane] : Stat{-INFINITY, 0.f};
+      st = warp_join(st, c);
+      lse = st.m / tau + logf(st.s);
+    }
+    ring_wait(smem_at(&list_made[list_at.slot]), list_at.round & 1);
+    const Divergence d = divergence[list_at.slot];
+    if (!BACKWARD && t == 0) {
+      a.loss[row] = d.some ? (d.value + lse) * tau * tau : 0.f;
+      a.lse[row] = lse;
+    }
+    if (!BACKWARD && !a.dlogits) {
+      release(&list_used[list_at.slot]);
+      continue;
+    }
+
+    const float scale = a.scale ? a.scale[row] : 1.f;
+    const bool live = d.some && scale != 0.f;
+    const Gradient<T> gradient(scale * tau, lse, c, inv_tau);
+    T* dz = static_cast<T*>(a.dlogits) + row * a.dlogits_stride;
+    const bool same = (((uintptr_t)dz ^ (uintptr_t)z) & 15) == 0;
+    for (int i = 0; i < pieces; ++i, at.next(places)) {
+      if (BACKWARD || !keep) ring_wait(smem_at(&filled[at.slot]), at.round & 1);
+      const uint8_t* piece = buffer + at.slot * kPieceBytes;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int v = i * kPieceVectors + u * kWorkers + t;
+        if (v >= vecs) break;
+        const uint4 p = live ? gradient.vector(vector_at(piece, v, u * kWorkers + t)) : make_uint4(0, 0, 0, 0);
+        const int e = rv.first(v);
+        if (same && rv.whole(v)) {
+          *reinterpret_cast<uint4*>(dz + e) = p;
+        } else {
+          const Pack<T, VN> q = *reinterpret_cast<const Pack<T, VN>*>(&p);
+#pragma unroll
+          for (int x = 0; x < VN; ++x)
+            if (e + x >= 0 && e + x < vocab) dz[e + x] = q.v[x];
+        }
+      }
+      release(&empty[at.slot]);
+    }
+    workers_barrier();
+    if (live) correct_listed<T>(list_of(list_at.slot), top, 0, vocab, t, kWorkers, gradient, dz);
+    release(&list_used[list_at.slot]);
   }
 }
 
 template <class T, class V, bool BACKWARD>
 cudaError_t run(const DistillArgs& a, cudaStream_t s) {
+  if (a.rows >= 2 * sm_count()) {
+    auto* kernel = distill_ring_kernel<T, V, BACKWARD>;
+    static std::atomic<unsigned long long> opened[256];
+    const int64_t row_bytes = (a.vocab * (int64_t)sizeof(T) + 15 + 15) / 16 * 16;
+    const int lists = kListWarps * kListBytes * a.top;
+    const int pieces = (int)((row_bytes + kPieceBytes - 1) / kPieceBytes);
+    const bool keep = !BACKWARD && a.dlogits && pieces <= kMostPieces && pieces * kPieceBytes + lists <= kRingMaxShared;
+    const int places = keep ? pieces : std::min(pieces, kStreamPieces);
+    const int shared = places * kPieceBytes + lists;
+    cudaError_t e = open_kernel((const void*)kernel, kRingMaxShared, false, opened);
+    if (e != cudaSuccess) return e;
+    int per_sm = 0;
+    if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kRingThreads, (size_t)shared)) != cudaSuccess) return e;
+    const int64_t blocks = std::min<int64_t>(a.rows, (int64_t)sm_count() * std::max(per_sm, 1));
+    kernel<<<(unsigned)blocks, kRingThreads, (size_t)shared, s>>>(a, pieces, places, keep);
+    count_launch();
+    return cudaGetLastError();
+  }
   // Few rows: several blocks to a row, until there are about two blocks for
   // each multiprocessor.
   int parts = 1;
@@ -291,6 +574,7 @@ cudaError_t run(const DistillArgs& a, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.rows * parts));
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (size_t)kListBytes * a.top;
   cfg.stream = s;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeClusterDimension;

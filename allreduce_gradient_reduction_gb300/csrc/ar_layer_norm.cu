@@ -43,11 +43,12 @@ __device__ __forceinline__ float group_sum(float v, float (*scratch)[32], int sl
   return warp_sum(lane < warps ? s[lane] : 0.f);
 }
 
-template <class T, class P, int VW, int NV, int MAXT>
-__global__ void __launch_bounds__(MAXT) layer_norm_kernel(const LayerNormArgs a) {
-  __shared__ float scratch[kGroups][2][32];
-  const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-  if (row >= a.rows) return;
+// Rows too wide for a ring (see below): up to 32 elements in each of up to
+// 1024 threads, one row to a block.
+template <class T, class P, int VW, int NV>
+__global__ void __launch_bounds__(1024) layer_norm_kernel(const LayerNormArgs a) {
+  __shared__ float scratch[2][32];
+  const int64_t row = blockIdx.x;
   const int cols = (int)a.cols;
   const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
   T* y = static_cast<T*>(a.y) + row * a.y_stride;
@@ -64,7 +65,7 @@ __global__ void __launch_bounds__(MAXT) layer_norm_kernel(const LayerNormArgs a)
   for (int k = 0; k < NV; ++k)
 #pragma unroll
     for (int i = 0; i < VW; ++i) sum += Conv<T>::up(xr[k].v[i]);
-  const float mean = group_sum(sum, scratch[threadIdx.y], 0) * inv;
+  const float mean = group_sum(sum, scratch, 0) * inv;
   float sq = 0.f;
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
@@ -75,7 +76,7 @@ __global__ void __launch_bounds__(MAXT) layer_norm_kernel(const LayerNormArgs a)
       if (c + i < cols) sq = fmaf(d, d, sq);
     }
   }
-  const float rstd = rsqrtf(group_sum(sq, scratch[threadIdx.y], 1) * inv + a.eps);
+  const float rstd = rsqrtf(group_sum(sq, scratch, 1) * inv + a.eps);
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const int c = (k * g + t) * VW;
@@ -123,11 +124,12 @@ __global__ void __launch_bounds__(1024) layer_norm_wide_kernel(const LayerNormAr
 
 // A block's share of dw and db: its groups' sums added in order (through
 // `joined`, two floats for each of a group's columns) and written as row
-// blockIdx.x of the partial sums.
-template <int VW, int NV>
+// blockIdx.x of the partial sums.  column(k): the first of the VW columns that
+// the thread's k-th sums stand for.
+template <int VW, int NV, class C>
 __device__ __forceinline__ void join_params(const float (&dw)[NV][VW], const float (&db)[NV][VW], float* joined,
-                                            float* partial, int cols) {
-  const int g = blockDim.x, t = threadIdx.x, width = g * NV * VW;
+                                            float* partial, int cols, C column) {
+  const int width = blockDim.x * NV * VW;
   float* out = partial + (int64_t)blockIdx.x * 2 * cols;
   __syncthreads();
   for (int y = 0; y + 1 < (int)blockDim.y; ++y) {
@@ -136,7 +138,7 @@ __device__ __forceinline__ void join_params(const float (&dw)[NV][VW], const flo
       for (int k = 0; k < NV; ++k)
 #pragma unroll
         for (int i = 0; i < VW; ++i) {
-          const int c = (k * g + t) * VW + i;
+          const int c = column(k) + i;
           joined[c] = dw[k][i] + (y ? joined[c] : 0.f);
           joined[width + c] = db[k][i] + (y ? joined[width + c] : 0.f);
         }
@@ -148,7 +150,7 @@ __device__ __forceinline__ void join_params(const float (&dw)[NV][VW], const flo
     for (int k = 0; k < NV; ++k)
 #pragma unroll
       for (int i = 0; i < VW; ++i) {
-        const int c = (k * g + t) * VW + i;
+        const int c = column(k) + i;
         if (c < cols) {
           out[c] = dw[k][i] + (blockDim.y > 1 ? joined[c] : 0.f);
           out[cols + c] = db[k][i] + (blockDim.y > 1 ? joined[width + c] : 0.f);
@@ -157,16 +159,12 @@ __device__ __forceinline__ void join_params(const float (&dw)[NV][VW], const flo
   }
 }
 
-// One block's groups walk over the rows with a stride of all groups; the next
-// row's loads are in flight while the current one is reduced.
-template <class T, class P, int VW, int NV, int MAXT>
-__global__ void __launch_bounds__(MAXT) layer_norm_backward_kernel(const LayerNormBackwardArgs a) {
-  constexpr bool kAhead = MAXT <= 512;  // 1024 threads have 64 registers each: no room for a second row
-  __shared__ float scratch[kGroups][2][32];
-  extern __shared__ float joined[];  // [2][groups' columns] when the block has several groups
-  const int cols = (int)a.cols;
-  const int g = blockDim.x, t = threadIdx.x;
-  const int64_t step = (int64_t)gridDim.x * blockDim.y;
+// Rows too wide for a ring: a block walks over the rows with a stride of all
+// blocks, up to 16 columns in each of up to 1024 threads.
+template <class T, class P, int VW, int NV>
+__global__ void __launch_bounds__(1024) layer_norm_backward_kernel(const LayerNormBackwardArgs a) {
+  __shared__ float scratch[2][2][32];
+  const int cols = (int)a.cols, g = blockDim.x, t = threadIdx.x;
   const P* weight = static_cast<const P*>(a.weight);
   const float inv = 1.0f / (float)cols;
 
@@ -176,33 +174,17 @@ __global__ void __launch_bounds__(MAXT) layer_norm_backward_kernel(const LayerNo
 #pragma unroll
     for (int i = 0; i < VW; ++i) dw[k][i] = db[k][i] = 0.f;
 
-  Pack<T, VW> xr[NV], dr[NV], xn[NV], dn[NV];
-  float mean_n = 0.f, rstd_n = 0.f;
-  auto fetch = [&](int64_t row, Pack<T, VW>* px, Pack<T, VW>* pd, float& m, float& r) {
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
     const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
-    const T* dy = static_cast<const T*>(a.dy) + row * a.dy_stride;
+    const T* d = static_cast<const T*>(a.dy) + row * a.dy_stride;
+    Pack<T, VW> xr[NV], dr[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int c = (k * g + t) * VW;
-      px[k] = load_pack<T, VW>(x, c, cols);
-      pd[k] = load_pack<T, VW>(dy, c, cols);
+      xr[k] = load_pack<T, VW>(x, (k * g + t) * VW, cols);
+      dr[k] = load_pack<T, VW>(d, (k * g + t) * VW, cols);
     }
-    m = a.mean[row];
-    r = a.rstd[row];
-  };
-  int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-  if (kAhead && row < a.rows) fetch(row, xn, dn, mean_n, rstd_n);
-  for (; row < a.rows; row += step) {
-    float mean, rstd;
-    if constexpr (kAhead) {
-#pragma unroll
-      for (int k = 0; k < NV; ++k) xr[k] = xn[k], dr[k] = dn[k];
-      mean = mean_n;
-      rstd = rstd_n;
-      if (row + step < a.rows) fetch(row + step, xn, dn, mean_n, rstd_n);
-    } else {
-      fetch(row, xr, dr, mean, rstd);
-    }
+    const float mean = a.mean[row], rstd = a.rstd[row];
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -220,21 +202,11 @@ __global__ void __launch_bounds__(MAXT) layer_norm_backward_kernel(const LayerNo
     }
     s1 = warp_sum(s1);
     s2 = warp_sum(s2);
-    const int warps = g >> 5;
-    if (warps > 1) {
-      float* s = scratch[threadIdx.y][0];
-      float* u = scratch[threadIdx.y][1];
-      const int w = t >> 5, lane = t & 31;
-      if (blockDim.y == 1) __syncthreads();
-      else named_barrier(1 + threadIdx.y, g);
-      if (lane == 0) s[w] = s1, u[w] = s2;
-      if (blockDim.y == 1) __syncthreads();
-      else named_barrier(1 + threadIdx.y, g);
-      s1 = warp_sum(lane < warps ? s[lane] : 0.f);
-      s2 = warp_sum(lane < warps ? u[lane] : 0.f);
-    }
-    s1 *= inv;
-    s2 *= inv;
+    // by turns, so that one barrier a row is enough
+    if ((t & 31) == 0) scratch[turn][0][t >> 5] = s1, scratch[turn][1][t >> 5] = s2;
+    __syncthreads();
+    s1 = warp_sum((t & 31) < g >> 5 ? scratch[turn][0][t & 31] : 0.f) * inv;
+    s2 = warp_sum((t & 31) < g >> 5 ? scratch[turn][1][t & 31] : 0.f) * inv;
     T* dx = static_cast<T*>(a.dx) + row * a.dx_stride;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -251,133 +223,47 @@ __global__ void __launch_bounds__(MAXT) layer_norm_backward_kernel(const LayerNo
       store_pack<T, VW>(dx, c, cols, o);
     }
   }
-  join_params<VW, NV>(dw, db, joined, a.partial, cols);
+  join_params<VW, NV>(dw, db, nullptr, a.partial, cols, [&](int k) { return (k * g + t) * VW; });
 }
 
 // ---- rows through shared memory -----------------------------------------------------
 //
-// For rows of 1 KB and more: each group keeps a ring of rows in shared memory,
-// filled by bulk copies that its first thread issues several rows ahead, so
-// the bytes in flight do not depend on registers or occupancy.  A copy takes
-// the aligned 16-byte words that hold a row; a row that starts inside a word
-// is put right when it is read (two words and a shift), and so is a result
-// row that starts inside one, on its way through a buffer of the group's.
-// Vectors are therefore counted from the row's first column whatever its
-// address, and the parameters' values for a thread's columns are loaded once.
-
-__device__ __forceinline__ uint32_t smem_at(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
-
-__device__ __forceinline__ void ring_expect(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-
-// The aligned words of `bytes` bytes at `from`.
-__device__ __forceinline__ uint32_t covering(const void* from, int bytes) {
-  return (((uint32_t)(uintptr_t)from & 15) + bytes + 15) & ~15u;
-}
-__device__ __forceinline__ void ring_copy(uint32_t to, const void* from, int bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to),
-               "l"((uintptr_t)from & ~(uintptr_t)15), "r"(covering(from, bytes)), "r"(bar)
-               : "memory");
-}
-
-// A copy ends by itself, so this wait does; the limit is for a launch that
-// has gone wrong, whose results are then wrong too but which ends.
-__device__ __forceinline__ void ring_wait(uint32_t bar, uint32_t parity) {
-  for (int i = 0; i < (1 << 22); ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    if (ok) return;
-  }
-}
-
-// 16 bytes at `at`, `shift` bytes past an aligned word (a multiple of ES).
-template <int ES>
-__device__ __forceinline__ uint4 shifted16(const uint8_t* word, int shift) {
-  const uint4 a = *reinterpret_cast<const uint4*>(word);
-  if (shift == 0) return a;
-  const uint4 b = *reinterpret_cast<const uint4*>(word + 16);
-  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  if (shift & 8) {
-#pragma unroll
-    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
-  }
-  if (shift & 4) {
-#pragma unroll
-    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
-  }
-  if (ES == 2 && (shift & 2)) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// Vector v of a row in its slot, places past the row's end as zeros.
-template <class T>
-__device__ __forceinline__ Pack<T, 16 / sizeof(T)> slot_vector(const uint8_t* slot, int shift, int v, int cols) {
-  constexpr int VW = 16 / sizeof(T);
-  if (v * VW >= cols) return zero_pack<T, VW>();
-  const uint4 raw = shifted16<sizeof(T)>(slot + v * 16, shift);
-  Pack<T, VW> p = *reinterpret_cast<const Pack<T, VW>*>(&raw);
-  if ((v + 1) * VW > cols) {
-#pragma unroll
-    for (int i = 0; i < VW; ++i)
-      if (v * VW + i >= cols) p.v[i] = Conv<T>::down(0.f);
-  }
-  return p;
-}
+// Each group keeps a ring of rows in shared memory, filled by bulk copies that
+// its first thread issues ahead, so the bytes in flight do not depend on
+// registers or occupancy (16384 x 5120 bf16 forward: 116 us with loads into
+// registers, 61 us so).  A copy takes
+// the aligned 16-byte words that hold a row.
 
 __device__ __forceinline__ void group_barrier() {
   if (blockDim.x == 32) __syncwarp();
-  else if (blockDim.y == 1) __syncthreads();
   else named_barrier(1 + threadIdx.y, blockDim.x);
 }
 
-// A thread's parameters, element by element where they are not aligned.
-template <class P, int VW>
-__device__ __forceinline__ Pack<P, VW> param_vector(const P* p, int c, int cols) {
-  if (p && ((uintptr_t)p & (sizeof(Pack<P, VW>) - 1)) == 0) return load_pack<P, VW>(p, c, cols);
-  Pack<P, VW> r = zero_pack<P, VW>();
+// Pairs of a thread's parameters, from the caches: keeping them in registers
+// would cost more in threads than it saves in loads.
+template <class P, int N>
+__device__ __forceinline__ void param_pairs(const P* p, Two (&out)[N]) {
+  if constexpr (sizeof(P) == 4) {
 #pragma unroll
-  for (int i = 0; i < VW; ++i)
-    if (p && c + i < cols) r.v[i] = p[c + i];
-  return r;
-}
-
-// Writes the group's row, vector k * blockDim.x + t of which is o[k].
-template <class T, int NV>
-__device__ __forceinline__ void write_row(T* row, const Pack<T, 16 / sizeof(T)> (&o)[NV], int cols, uint8_t* buffer) {
-  constexpr int VW = 16 / sizeof(T), ES = sizeof(T);
-  const int g = blockDim.x, t = threadIdx.x;
-  const int phase = (int)((uintptr_t)row & 15);
-  if (phase == 0) {
-#pragma unroll
-    for (int k = 0; k < NV; ++k)
-      if ((k * g + t) * VW < cols) store_pack<T, VW>(row, (k * g + t) * VW, cols, o[k]);
-    return;
-  }
-#pragma unroll
-  for (int k = 0; k < NV; ++k)
-    if ((k * g + t) * VW < cols) *reinterpret_cast<Pack<T, VW>*>(buffer + (k * g + t) * 16) = o[k];
-  group_barrier();
-  // aligned word u of the result row holds its bytes [16 u - phase, 16 u - phase + 16)
-  const int bytes = cols * ES, words = (bytes + phase + 15) / 16;
-  for (int u = t; u < words; u += g) {
-    const int b = u * 16 - phase;
-    if (b >= 0 && b + 16 <= bytes) {
-      *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(row) + b) = shifted16<ES>(buffer + (b & ~15), b & 15);
-    } else {
-      for (int c = max(b, 0) / ES; c < min(b + 16, bytes) / ES; ++c) row[c] = reinterpret_cast<const T*>(buffer)[c];
+    for (int i = 0; i < N; i += 2) {
+      const uint4 v = *reinterpret_cast<const uint4*>(p + 2 * i);
+      out[i] = Pairs<float>::get(v, 0);
+      out[i + 1] = Pairs<float>::get(v, 1);
     }
+  } else {
+    uint4 v;
+    if constexpr (N == 4) {
+      v = *reinterpret_cast<const uint4*>(p);
+    } else {
+      const uint2 h = *reinterpret_cast<const uint2*>(p);
+      v = make_uint4(h.x, h.y, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) out[i] = Pairs<P>::get(v, i);
   }
 }
 
-constexpr int kRing = 4;  // rows of a group in flight
+constexpr int kRing = 4;  // most rows of a group in flight
 
 __device__ __forceinline__ void open_ring(uint64_t* full) {
   if (threadIdx.x == 0) {
@@ -388,18 +274,51 @@ __device__ __forceinline__ void open_ring(uint64_t* full) {
   __syncthreads();
 }
 
-// slot: bytes of one row's place in shared memory
-template <class T, class P, int NV, int MAXT>
-__global__ void __launch_bounds__(MAXT) layer_norm_ring_kernel(const LayerNormArgs a, int slot) {
-  constexpr int VW = 16 / sizeof(T);
+// Sums of two values over the group, through one of two halves of its scratch
+// by turns: one barrier a call.
+__device__ __forceinline__ float2 group_sum2(float2 v, float2 (*scratch)[16], int turn) {
+  v.x = warp_sum(v.x);
+  v.y = warp_sum(v.y);
+  const int warps = blockDim.x >> 5;
+  if (warps == 1) {
+    __syncwarp();
+    return v;
+  }
+  float2* s = scratch[turn];
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) s[w] = v;
+  group_barrier();
+  v = lane < warps ? s[lane] : make_float2(0.f, 0.f);
+  return make_float2(warp_sum(v.x), warp_sum(v.y));
+}
+
+
+// Registers of the forward kernel, which holds a thread's columns widened.
+__host__ __device__ constexpr int forward_registers(int columns) { return columns <= 16 ? 64 : columns <= 24 ? 80 : 96; }
+// Registers of the backward kernel: two sums for each of a thread's columns,
+// and xh and dy w of the current row.
+__host__ __device__ constexpr int backward_registers(int columns) { return columns <= 8 ? 72 : 120; }
+
+// slot: bytes of one row's place in shared memory; stages: rows in flight.
+// Every row of every operand and the parameters begin on a vector boundary
+// and rows are whole vectors.
+template <class T, class P, int NV, bool KEEP>
+__global__ void __maxnreg__(KEEP ? 88 : forward_registers(NV * (16 / sizeof(T))))
+    layer_norm_ring_kernel(const LayerNormArgs a, int slot, int stages) {
+  constexpr int VW = 16 / sizeof(T), N = Pairs<T>::N;
   extern __shared__ __align__(16) uint8_t rows[];
   __shared__ float scratch[kGroups][2][32];
-  __shared__ __align__(8) uint64_t full[kGroups][kRing];
+  __shared__ __align__(8) uint64_t filled[kGroups][kRing];
   const int cols = (int)a.cols, g = blockDim.x, t = threadIdx.x;
   const int64_t step = (int64_t)gridDim.x * blockDim.y;
   const T* x = static_cast<const T*>(a.x);
-  uint8_t* mine = rows + (int64_t)threadIdx.y * (kRing + 1) * slot;
-  uint64_t* bars = full[threadIdx.y];
+  // a warp has 32 NV vectors in a row, its lanes every 32nd of them
+  const int vecs = cols / VW, v0 = (t >> 5) * 32 * NV + (t & 31);
+  const bool full = ((t >> 5) + 1) * 32 * NV <= vecs;
+  const P* weight = static_cast<const P*>(a.weight) + v0 * VW;
+  const P* bias = a.bias ? static_cast<const P*>(a.bias) + v0 * VW : nullptr;
+  uint8_t* mine = rows + (int64_t)threadIdx.y * stages * slot;
+  uint64_t* bars = filled[threadIdx.y];
   const float inv = 1.0f / (float)cols;
   auto issue = [&](int64_t row, int stage) {
     const T* from = x + row * a.x_stride;
@@ -410,64 +329,117 @@ __global__ void __launch_bounds__(MAXT) layer_norm_ring_kernel(const LayerNormAr
   open_ring(bars);
   int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   if (t == 0)
-    for (int i = 0; i < kRing && row + i * step < a.rows; ++i) issue(row + i * step, i);
+    for (int i = 0; i < stages && row + i * step < a.rows; ++i) issue(row + i * step, i);
 
-  Pack<P, VW> w[NV], b[NV];
+  Two kept_w[KEEP ? NV : 1][N], kept_b[KEEP ? NV : 1][N];
+  if constexpr (KEEP) {
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    w[k] = param_vector<P, VW>(static_cast<const P*>(a.weight), (k * g + t) * VW, cols);
-    b[k] = param_vector<P, VW>(static_cast<const P*>(a.bias), (k * g + t) * VW, cols);
+    for (int k = 0; k < NV; ++k) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) kept_w[k][i] = kept_b[k][i] = two(0.f, 0.f);
+      if (v0 + k * 32 < vecs) {
+        param_pairs<P, N>(weight + k * 32 * VW, kept_w[k]);
+        if (bias) param_pairs<P, N>(bias + k * 32 * VW, kept_b[k]);
+      }
+    }
   }
   int stage = 0, parity = 0;
   for (; row < a.rows; row += step) {
     ring_wait(smem_at(bars + stage), parity);
-    Pack<T, VW> xr[NV];
-    const int shift = (int)((uintptr_t)(x + row * a.x_stride) & 15);
-    float sum = 0.f;
+    const uint8_t* from = mine + stage * slot + v0 * 16;
+    Two e[NV][N];  // the elements, then their distance from the mean
+    Two acc[2] = {two(0.f, 0.f), two(0.f, 0.f)};
+    auto take = [&](int k, const uint4& raw) {
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      xr[k] = slot_vector<T>(mine + stage * slot, shift, k * g + t, cols);
-#pragma unroll
-      for (int i = 0; i < VW; ++i) sum += Conv<T>::up(xr[k].v[i]);
-    }
-    const float mean = group_sum(sum, scratch[threadIdx.y], 0) * inv;
-    if (g == 32) __syncwarp();
-    if (t == 0 && row + kRing * step < a.rows) issue(row + kRing * step, stage);  // the group has read the slot
-    float sq = 0.f;
-#pragma unroll
-    for (int k = 0; k < NV; ++k)
-#pragma unroll
-      for (int i = 0; i < VW; ++i) {
-        const float d = Conv<T>::up(xr[k].v[i]) - mean;
-        if ((k * g + t) * VW + i < cols) sq = fmaf(d, d, sq);
+      for (int i = 0; i < N; ++i) {
+        e[k][i] = Pairs<T>::get(raw, i);
+        acc[i & 1] = add2(acc[i & 1], e[k][i]);
       }
-    const float rstd = rsqrtf(group_sum(sq, scratch[threadIdx.y], 1) * inv + a.eps);
+    };
+    if (full) {
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
+      for (int k = 0; k < NV; ++k) take(k, *reinterpret_cast<const uint4*>(from + k * 512));
+    } else {
 #pragma unroll
-      for (int i = 0; i < VW; ++i)
-        xr[k].v[i] = Conv<T>::down(fmaf((Conv<T>::up(xr[k].v[i]) - mean) * rstd, Conv<P>::up(w[k].v[i]), Conv<P>::up(b[k].v[i])));
-    write_row<T, NV>(static_cast<T*>(a.y) + row * a.y_stride, xr, cols, mine + kRing * slot);
+      for (int k = 0; k < NV; ++k)
+        take(k, v0 + k * 32 < vecs ? *reinterpret_cast<const uint4*>(from + k * 512) : make_uint4(0, 0, 0, 0));
+    }
+    float lo, hi;
+    split(add2(acc[0], acc[1]), lo, hi);
+    const float mean = group_sum(lo + hi, scratch[threadIdx.y], 0) * inv;
+    if (g == 32) __syncwarp();
+    if (t == 0 && row + stages * step < a.rows) issue(row + stages * step, stage);  // the group has read the slot
+    const Two minus = two(-mean, -mean);
+    acc[0] = acc[1] = two(0.f, 0.f);
+    auto square = [&](int k) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        e[k][i] = add2(e[k][i], minus);
+        acc[i & 1] = fma2(e[k][i], e[k][i], acc[i & 1]);
+      }
+    };
+    if (full) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) square(k);
+    } else {
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+        if (v0 + k * 32 < vecs) square(k);
+    }
+    split(add2(acc[0], acc[1]), lo, hi);
+    const float rstd = rsqrtf(group_sum(lo + hi, scratch[threadIdx.y], 1) * inv + a.eps);
+    const Two scale = two(rstd, rstd);
+    T* y = static_cast<T*>(a.y) + row * a.y_stride + v0 * VW;
+    auto put = [&](int k) {
+      Two w[N], b[N];
+      uint4 out;
+      if constexpr (KEEP) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) Pairs<T>::set(out, i, fma2(mul2(e[k][i], scale), kept_w[k][i], kept_b[k][i]));
+        *reinterpret_cast<uint4*>(y + k * 32 * VW) = out;
+        return;
+      }
+      param_pairs<P, N>(weight + k * 32 * VW, w);
+      if (bias) param_pairs<P, N>(bias + k * 32 * VW, b);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const Two xh = mul2(e[k][i], scale);
+        Pairs<T>::set(out, i, bias ? fma2(xh, w[i], b[i]) : mul2(xh, w[i]));
+      }
+      *reinterpret_cast<uint4*>(y + k * 32 * VW) = out;
+    };
+    if (full) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) put(k);
+    } else {
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+        if (v0 + k * 32 < vecs) put(k);
+    }
     if (t == 0) {
       if (a.mean) a.mean[row] = mean;
       if (a.rstd) a.rstd[row] = rstd;
     }
-    if (++stage == kRing) stage = 0, parity ^= 1;
+    if (++stage == stages) stage = 0, parity ^= 1;
   }
 }
 
-template <class T, class P, int NV, int MAXT>
-__global__ void __launch_bounds__(MAXT) layer_norm_backward_ring_kernel(const LayerNormBackwardArgs a, int slot) {
-  constexpr int VW = 16 / sizeof(T);
+template <class T, class P, int NV>
+__global__ void __maxnreg__(backward_registers(NV * (16 / sizeof(T))))
+    layer_norm_backward_ring_kernel(const LayerNormBackwardArgs a, int slot, int stages) {
+  constexpr int VW = 16 / sizeof(T), N = Pairs<T>::N;
   extern __shared__ __align__(16) uint8_t rows[];
-  __shared__ float scratch[kGroups][2][2][32];
-  __shared__ __align__(8) uint64_t full[kGroups][kRing];
-  const int cols = (int)a.cols, g = blockDim.x, t = threadIdx.x;
+  __shared__ float2 scratch[kGroups][2][16];
+  __shared__ __align__(8) uint64_t filled[kGroups][kRing];
+  const int cols = (int)a.cols, t = threadIdx.x;
   const int64_t step = (int64_t)gridDim.x * blockDim.y;
   const T* x = static_cast<const T*>(a.x);
   const T* dy = static_cast<const T*>(a.dy);
-  uint8_t* mine = rows + (int64_t)threadIdx.y * (2 * kRing + 1) * slot;
-  uint64_t* bars = full[threadIdx.y];
+  const int vecs = cols / VW, v0 = (t >> 5) * 32 * NV + (t & 31);
+  const bool full = ((t >> 5) + 1) * 32 * NV <= vecs;
+  const P* weight = static_cast<const P*>(a.weight) + v0 * VW;
+  uint8_t* mine = rows + (int64_t)threadIdx.y * 2 * stages * slot;
+  uint64_t* bars = filled[threadIdx.y];
   const float inv = 1.0f / (float)cols;
   auto issue = [&](int64_t row, int stage) {
     const int bytes = cols * (int)sizeof(T);
@@ -480,71 +452,289 @@ __global__ void __launch_bounds__(MAXT) layer_norm_backward_ring_kernel(const La
   open_ring(bars);
   int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   if (t == 0)
-    for (int i = 0; i < kRing && row + i * step < a.rows; ++i) issue(row + i * step, i);
+    for (int i = 0; i < stages && row + i * step < a.rows; ++i) issue(row + i * step, i);
 
-  Pack<P, VW> w[NV];
-  float dw[NV][VW], db[NV][VW];
+  Two dw[NV][N], db[NV][N];
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    w[k] = param_vector<P, VW>(static_cast<const P*>(a.weight), (k * g + t) * VW, cols);
+  for (int k = 0; k < NV; ++k)
 #pragma unroll
-    for (int i = 0; i < VW; ++i) dw[k][i] = db[k][i] = 0.f;
-  }
+    for (int i = 0; i < N; ++i) dw[k][i] = db[k][i] = two(0.f, 0.f);
   float mean = 0.f, rstd = 0.f;
   if (row < a.rows) mean = a.mean[row], rstd = a.rstd[row];
   int stage = 0, parity = 0;
-  for (int64_t n = 0; row < a.rows; row += step, ++n) {
+  for (int turn = 0; row < a.rows; row += step, turn ^= 1) {
     float mean_n = 0.f, rstd_n = 0.f;
     if (row + step < a.rows) mean_n = a.mean[row + step], rstd_n = a.rstd[row + step];
     ring_wait(smem_at(bars + stage), parity);
-    Pack<T, VW> xr[NV], dr[NV];
-    const int sx = (int)((uintptr_t)(x + row * a.x_stride) & 15), sd = (int)((uintptr_t)(dy + row * a.dy_stride) & 15);
-    float s1 = 0.f, s2 = 0.f;
+    const Two minus = two(-mean, -mean), scale = two(rstd, rstd);
+    const uint8_t* from = mine + stage * 2 * slot + v0 * 16;
+    Two xh[NV][N], gw[NV][N];
+    Two s1 = two(0.f, 0.f), s2 = two(0.f, 0.f);
+    auto take = [&](int k) {
+      const uint4 xr = *reinterpret_cast<const uint4*>(from + k * 512);
+      const uint4 dr = *reinterpret_cast<const uint4*>(from + slot + k * 512);
+      Two w[N];
+      param_pairs<P, N>(weight + k * 32 * VW, w);
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      xr[k] = slot_vector<T>(mine + stage * 2 * slot, sx, k * g + t, cols);
-      dr[k] = slot_vector<T>(mine + stage * 2 * slot + slot, sd, k * g + t, cols);
-#pragma unroll
-      for (int i = 0; i < VW; ++i) {
-        const float d = Conv<T>::up(dr[k].v[i]);
-        const float xh = (Conv<T>::up(xr[k].v[i]) - mean) * rstd;
-        const float gw = d * Conv<P>::up(w[k].v[i]);
-        dw[k][i] = fmaf(d, xh, dw[k][i]);
-        db[k][i] += d;
-        s1 += gw;
-        s2 = fmaf(gw, xh, s2);
+      for (int i = 0; i < N; ++i) {
+        const Two d = Pairs<T>::get(dr, i);
+        xh[k][i] = mul2(add2(Pairs<T>::get(xr, i), minus), scale);
+        gw[k][i] = mul2(d, w[i]);
+        dw[k][i] = fma2(d, xh[k][i], dw[k][i]);
+        db[k][i] = add2(db[k][i], d);
+        s1 = add2(s1, gw[k][i]);
+        s2 = fma2(gw[k][i], xh[k][i], s2);
       }
-    }
-    s1 = warp_sum(s1);
-    s2 = warp_sum(s2);
-    if (g > 32) {
-      // one barrier a row: the scratch of the row before last is free by then
-      float (*s)[32] = scratch[threadIdx.y][n & 1];
-      const int wp = t >> 5, lane = t & 31;
-      if (lane == 0) s[0][wp] = s1, s[1][wp] = s2;
-      group_barrier();
-      s1 = warp_sum(lane < (g >> 5) ? s[0][lane] : 0.f);
-      s2 = warp_sum(lane < (g >> 5) ? s[1][lane] : 0.f);
+    };
+    if (full) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) take(k);
     } else {
-      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+        if (v0 + k * 32 < vecs) take(k);
     }
-    if (t == 0 && row + kRing * step < a.rows) issue(row + kRing * step, stage);  // the group has read the slot
-    s1 *= inv;
-    s2 *= inv;
+    float a1, b1, a2, b2;
+    split(s1, a1, b1);
+    split(s2, a2, b2);
+    const float2 s = group_sum2(make_float2(a1 + b1, a2 + b2), scratch[threadIdx.y], turn);
+    if (t == 0 && row + stages * step < a.rows) issue(row + stages * step, stage);  // the group has read the slot
+    // dx = rstd gw - rstd s1 / C - xh rstd s2 / C
+    const float m1 = -rstd * (s.x * inv), m2 = -rstd * (s.y * inv);
+    const Two m1s = two(m1, m1), m2s = two(m2, m2);
+    T* dx = static_cast<T*>(a.dx) + row * a.dx_stride + v0 * VW;
+    auto put = [&](int k) {
+      uint4 out;
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
+      for (int i = 0; i < N; ++i) Pairs<T>::set(out, i, fma2(xh[k][i], m2s, fma2(gw[k][i], scale, m1s)));
+      *reinterpret_cast<uint4*>(dx + k * 32 * VW) = out;
+    };
+    if (full) {
 #pragma unroll
-      for (int i = 0; i < VW; ++i) {
-        const float xh = (Conv<T>::up(xr[k].v[i]) - mean) * rstd;
-        const float gw = Conv<T>::up(dr[k].v[i]) * Conv<P>::up(w[k].v[i]);
-        xr[k].v[i] = Conv<T>::down(rstd * (gw - s1 - xh * s2));
-      }
-    write_row<T, NV>(static_cast<T*>(a.dx) + row * a.dx_stride, xr, cols, mine + 2 * kRing * slot);
+      for (int k = 0; k < NV; ++k) put(k);
+    } else {
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+        if (v0 + k * 32 < vecs) put(k);
+    }
     mean = mean_n;
     rstd = rstd_n;
-    if (++stage == kRing) stage = 0, parity ^= 1;
+    if (++stage == stages) stage = 0, parity ^= 1;
   }
-  join_params<VW, NV>(dw, db, reinterpret_cast<float*>(rows), a.partial, cols);
+  float dw1[NV][VW], db1[NV][VW];
+#pragma unroll
+  for (int k = 0; k < NV; ++k)
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      split(dw[k][i], dw1[k][2 * i], dw1[k][2 * i + 1]);
+      split(db[k][i], db1[k][2 * i], db1[k][2 * i + 1]);
+    }
+  join_params<VW, NV>(dw1, db1, reinterpret_cast<float*>(rows), a.partial, cols,
+                      [&](int k) { return (v0 + k * 32) * VW; });
+}
+
+// Rows that are not whole vectors, or begin anywhere: a warp has 32 NE
+// elements in a row, its lanes every 32nd of them, so its accesses are
+// contiguous whatever the addresses; a thread's parameters stay in its
+// registers.  (Vectors put right by shifts, on their way in and, through
+// shared memory, out again, took 28 instructions an element and 125 us for
+// 16384 x 5121 bf16 forward.)  Elements 2 i and 2 i + 1 of a thread go through
+// the arithmetic as a pair.
+template <class P, int N>
+__device__ __forceinline__ void strided_params(const P* p, int c0, int cols, Two (&out)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int c = c0 + i * 64;
+    out[i] = two(p && c < cols ? Conv<P>::up(p[c]) : 0.f, p && c + 32 < cols ? Conv<P>::up(p[c + 32]) : 0.f);
+  }
+}
+
+// Pair i of the elements from `row` on; left: how many there are (FULL: enough).
+template <bool FULL, class T>
+__device__ __forceinline__ Two strided_pair(const T* row, int i, int left) {
+  if constexpr (FULL) return two(Conv<T>::up(row[i * 64]), Conv<T>::up(row[i * 64 + 32]));
+  else
+    return two(i * 64 < left ? Conv<T>::up(row[i * 64]) : 0.f, i * 64 + 32 < left ? Conv<T>::up(row[i * 64 + 32]) : 0.f);
+}
+template <bool FULL, class T>
+__device__ __forceinline__ void strided_store(T* row, int i, int left, Two v) {
+  float lo, hi;
+  split(v, lo, hi);
+  if constexpr (sizeof(T) == 2) {
+    const uint32_t both = pack2<T>(lo, hi);
+    uint16_t* to = reinterpret_cast<uint16_t*>(row);
+    if (FULL || i * 64 < left) to[i * 64] = (uint16_t)both;
+    if (FULL || i * 64 + 32 < left) to[i * 64 + 32] = (uint16_t)(both >> 16);
+  } else {
+    if (FULL || i * 64 < left) row[i * 64] = lo;
+    if (FULL || i * 64 + 32 < left) row[i * 64 + 32] = hi;
+  }
+}
+
+template <class T, class P, int NE>
+__global__ void __maxnreg__(NE <= 8 ? 56 : 80)
+    layer_norm_strided_kernel(const LayerNormArgs a, int slot, int stages) {
+  constexpr int N = NE / 2;
+  extern __shared__ __align__(16) uint8_t rows[];
+  __shared__ float scratch[kGroups][2][32];
+  __shared__ __align__(8) uint64_t filled[kGroups][kRing];
+  const int cols = (int)a.cols, g = blockDim.x, t = threadIdx.x;
+  const int64_t step = (int64_t)gridDim.x * blockDim.y;
+  const T* x = static_cast<const T*>(a.x);
+  uint8_t* mine = rows + (int64_t)threadIdx.y * stages * slot;
+  uint64_t* bars = filled[threadIdx.y];
+  const float inv = 1.0f / (float)cols;
+  auto issue = [&](int64_t row, int stage) {
+    const T* from = x + row * a.x_stride;
+    const uint32_t bar = smem_at(bars + stage);
+    ring_expect(bar, covering(from, cols * (int)sizeof(T)));
+    ring_copy(smem_at(mine + stage * slot), from, cols * (int)sizeof(T), bar);
+  };
+  open_ring(bars);
+  int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  if (t == 0)
+    for (int i = 0; i < stages && row + i * step < a.rows; ++i) issue(row + i * step, i);
+  const int c0 = (t >> 5) * 32 * NE + (t & 31), left = cols - c0;
+  const bool full = ((t >> 5) + 1) * 32 * NE <= cols;
+  Two w[N], b[N];
+  strided_params<P, N>(static_cast<const P*>(a.weight), c0, cols, w);
+  strided_params<P, N>(static_cast<const P*>(a.bias), c0, cols, b);
+
+  int stage = 0, parity = 0;
+  for (; row < a.rows; row += step) {
+    ring_wait(smem_at(bars + stage), parity);
+    const T* from = reinterpret_cast<const T*>(mine + stage * slot + ((uintptr_t)(x + row * a.x_stride) & 15)) + c0;
+    Two e[N], acc[2] = {two(0.f, 0.f), two(0.f, 0.f)};
+    if (full) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) e[i] = strided_pair<true>(from, i, left);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) e[i] = strided_pair<false>(from, i, left);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[i & 1] = add2(acc[i & 1], e[i]);
+    float lo, hi;
+    split(add2(acc[0], acc[1]), lo, hi);
+    const float mean = group_sum(lo + hi, scratch[threadIdx.y], 0) * inv;
+    if (g == 32) __syncwarp();
+    if (t == 0 && row + stages * step < a.rows) issue(row + stages * step, stage);  // the group has read the slot
+    const Two minus = two(-mean, -mean);
+    acc[0] = acc[1] = two(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      e[i] = add2(e[i], minus);
+      if (!full) {
+        split(e[i], lo, hi);
+        e[i] = two(i * 64 < left ? lo : 0.f, i * 64 + 32 < left ? hi : 0.f);
+      }
+      acc[i & 1] = fma2(e[i], e[i], acc[i & 1]);
+    }
+    split(add2(acc[0], acc[1]), lo, hi);
+    const float rstd = rsqrtf(group_sum(lo + hi, scratch[threadIdx.y], 1) * inv + a.eps);
+    const Two scale = two(rstd, rstd);
+    T* y = static_cast<T*>(a.y) + row * a.y_stride + c0;
+    if (full) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) strided_store<true>(y, i, left, fma2(mul2(e[i], scale), w[i], b[i]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) strided_store<false>(y, i, left, fma2(mul2(e[i], scale), w[i], b[i]));
+    }
+    if (t == 0) {
+      if (a.mean) a.mean[row] = mean;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+    if (++stage == stages) stage = 0, parity ^= 1;
+  }
+}
+
+template <class T, class P, int NE>
+__global__ void __maxnreg__(backward_registers(NE))
+    layer_norm_backward_strided_kernel(const LayerNormBackwardArgs a, int slot, int stages) {
+  constexpr int N = NE / 2;
+  extern __shared__ __align__(16) uint8_t rows[];
+  __shared__ float2 scratch[kGroups][2][16];
+  __shared__ __align__(8) uint64_t filled[kGroups][kRing];
+  const int cols = (int)a.cols, t = threadIdx.x;
+  const int64_t step = (int64_t)gridDim.x * blockDim.y;
+  const T* x = static_cast<const T*>(a.x);
+  const T* dy = static_cast<const T*>(a.dy);
+  uint8_t* mine = rows + (int64_t)threadIdx.y * 2 * stages * slot;
+  uint64_t* bars = filled[threadIdx.y];
+  const float inv = 1.0f / (float)cols;
+  auto issue = [&](int64_t row, int stage) {
+    const int bytes = cols * (int)sizeof(T);
+    const T *fx = x + row * a.x_stride, *fd = dy + row * a.dy_stride;
+    const uint32_t bar = smem_at(bars + stage), to = smem_at(mine + stage * 2 * slot);
+    ring_expect(bar, covering(fx, bytes) + covering(fd, bytes));
+    ring_copy(to, fx, bytes, bar);
+    ring_copy(to + slot, fd, bytes, bar);
+  };
+  open_ring(bars);
+  int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  if (t == 0)
+    for (int i = 0; i < stages && row + i * step < a.rows; ++i) issue(row + i * step, i);
+  const int c0 = (t >> 5) * 32 * NE + (t & 31), left = cols - c0;
+  const bool full = ((t >> 5) + 1) * 32 * NE <= cols;
+  Two w[N], dw[N], db[N];
+  strided_params<P, N>(static_cast<const P*>(a.weight), c0, cols, w);
+#pragma unroll
+  for (int i = 0; i < N; ++i) dw[i] = db[i] = two(0.f, 0.f);
+  float mean = 0.f, rstd = 0.f;
+  if (row < a.rows) mean = a.mean[row], rstd = a.rstd[row];
+  int stage = 0, parity = 0;
+  for (int turn = 0; row < a.rows; row += step, turn ^= 1) {
+    float mean_n = 0.f, rstd_n = 0.f;
+    if (row + step < a.rows) mean_n = a.mean[row + step], rstd_n = a.rstd[row + step];
+    ring_wait(smem_at(bars + stage), parity);
+    const Two minus = two(-mean, -mean), scale = two(rstd, rstd);
+    const uint8_t* from = mine + stage * 2 * slot;
+    const T* xs = reinterpret_cast<const T*>(from + ((uintptr_t)(x + row * a.x_stride) & 15)) + c0;
+    const T* ds = reinterpret_cast<const T*>(from + slot + ((uintptr_t)(dy + row * a.dy_stride) & 15)) + c0;
+    Two xh[N], gw[N], s1 = two(0.f, 0.f), s2 = two(0.f, 0.f);
+    auto take = [&](int i, Two xv, Two d) {
+      // dy is 0 outside the row, so what stands for x there does not count
+      xh[i] = mul2(add2(xv, minus), scale);
+      gw[i] = mul2(d, w[i]);
+      dw[i] = fma2(d, xh[i], dw[i]);
+      db[i] = add2(db[i], d);
+      s1 = add2(s1, gw[i]);
+      s2 = fma2(gw[i], xh[i], s2);
+    };
+    if (full) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) take(i, strided_pair<true>(xs, i, left), strided_pair<true>(ds, i, left));
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) take(i, strided_pair<false>(xs, i, left), strided_pair<false>(ds, i, left));
+    }
+    float a1, b1, a2, b2;
+    split(s1, a1, b1);
+    split(s2, a2, b2);
+    const float2 s = group_sum2(make_float2(a1 + b1, a2 + b2), scratch[threadIdx.y], turn);
+    if (t == 0 && row + stages * step < a.rows) issue(row + stages * step, stage);  // the group has read the slot
+    const float m1 = -rstd * (s.x * inv), m2 = -rstd * (s.y * inv);
+    const Two m1s = two(m1, m1), m2s = two(m2, m2);
+    T* dx = static_cast<T*>(a.dx) + row * a.dx_stride + c0;
+    if (full) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) strided_store<true>(dx, i, left, fma2(xh[i], m2s, fma2(gw[i], scale, m1s)));
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) strided_store<false>(dx, i, left, fma2(xh[i], m2s, fma2(gw[i], scale, m1s)));
+    }
+    mean = mean_n;
+    rstd = rstd_n;
+    if (++stage == stages) stage = 0, parity ^= 1;
+  }
+  float dw1[NE][1], db1[NE][1];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    split(dw[i], dw1[2 * i][0], dw1[2 * i + 1][0]);
+    split(db[i], db1[2 * i][0], db1[2 * i + 1][0]);
+  }
+  join_params<1, NE>(dw1, db1, reinterpret_cast<float*>(rows), a.partial, cols, [&](int k) { return c0 + k * 32; });
 }
 
 // Rows of any width: dx in three passes over a row by one block.
@@ -637,15 +827,6 @@ Deal deal(int64_t vecs, const int (&counts)[N], int max_threads) {
   return best;
 }
 
-template <class T, class P, int VW, int NV, int MAXT>
-cudaError_t run_forward(const LayerNormArgs& a, int threads, cudaStream_t s) {
-  const int groups = std::max(1, std::min(kGroups - 1, 128 / threads));
-  const int64_t blocks = (a.rows + groups - 1) / groups;
-  layer_norm_kernel<T, P, VW, NV, MAXT><<<(unsigned)blocks, dim3(threads, groups), 0, s>>>(a);
-  count_launch();
-  return cudaGetLastError();
-}
-
 // A row's place in a ring: the words it may lie in, and one more that a
 // shifted read may touch.
 template <class T>
@@ -653,7 +834,6 @@ int ring_slot(int64_t cols) {
   return (int)((cols * (int64_t)sizeof(T) + 15 + 15) / 16 * 16) + 16;
 }
 
-constexpr int kRingMinBytes = 1024;       // shorter rows: one warp takes one at a time, without a ring
 constexpr int kRingMaxShared = 200 * 1024;
 
 // How many blocks of a persistent kernel the device holds.
@@ -665,50 +845,103 @@ cudaError_t resident(K* kernel, int threads, int smem, int64_t* blocks) {
   return e;
 }
 
-template <class T, class P, int NV, int MAXT>
-cudaError_t run_ring(const LayerNormArgs& a, int threads, cudaStream_t s) {
-  auto* kernel = layer_norm_ring_kernel<T, P, NV, MAXT>;
-  static std::atomic<unsigned long long> opened[256];
-  const int slot = ring_slot<T>(a.cols), ring = (kRing + 1) * slot;
-  const int groups = std::max(1, std::min({kGroups - 1, 256 / threads, kRingMaxShared / ring}));
+// How deep a group's ring is.  A row is in registers while it is worked on and
+// its place is being filled again, so one place is enough to keep loads on
+// their way; more where the groups that fit a multiprocessor (by registers)
+// have less than 64 KB of places.  Not more than that: what shared memory does
+// not take is the L1 cache that the parameters are read from (16384 x 4096
+// bf16 with f32 parameters, forward, with places for 128 KB: 80 us).
+int ring_stages(int row_bytes, int threads, int registers) {
+  const int groups = std::max(1, 65536 / registers / threads);
+  return std::max(1, std::min(kRing, (64 * 1024 / groups + row_bytes / 2) / row_bytes));
+}
+
+template <class T, class P>
+bool params_aligned(const void* p) {
+  return (uintptr_t)p % (16 / sizeof(T) * sizeof(P)) == 0;
+}
+
+// Groups in a block: enough of them to fill 256 threads, but not so many that
+// few rows leave multiprocessors idle.
+int ring_groups(int threads, int64_t rows) {
+  const int64_t each = rows / sm_count();
+  return (int)std::max<int64_t>(1, std::min<int64_t>({kGroups - 1, 256 / threads, each}));
+}
+
+template <class T>
+cudaError_t start_ring(void (*kernel)(LayerNormArgs, int, int), std::atomic<unsigned long long>* opened, int threads,
+                       int registers, const LayerNormArgs& a, cudaStream_t s) {
+  const int slot = ring_slot<T>(a.cols), stages = ring_stages(slot, threads, registers), groups = threads >= 128 ? 1 : ring_groups(threads, a.rows);
+  const int smem = groups * stages * slot;
   cudaError_t e = open_kernel((const void*)kernel, kRingMaxShared, false, opened);
   if (e != cudaSuccess) return e;
   int64_t blocks = 0;
-  if ((e = resident(kernel, threads * groups, groups * ring, &blocks)) != cudaSuccess) return e;
+  if ((e = resident(kernel, threads * groups, smem, &blocks)) != cudaSuccess) return e;
   blocks = std::min<int64_t>(blocks, (a.rows + groups - 1) / groups);
-  kernel<<<(unsigned)blocks, dim3(threads, groups), groups * ring, s>>>(a, slot);
+  kernel<<<(unsigned)blocks, dim3(threads, groups), smem, s>>>(a, slot, stages);
   count_launch();
   return cudaGetLastError();
+}
+
+template <class T, class P, int NV, bool KEEP = false>
+cudaError_t run_ring(const LayerNormArgs& a, int threads, cudaStream_t s) {
+  static std::atomic<unsigned long long> opened[256];
+  return start_ring<T>(layer_norm_ring_kernel<T, P, NV, KEEP>, opened, threads,
+                       KEEP ? 88 : forward_registers(NV * (16 / (int)sizeof(T))), a, s);
+}
+template <class T, class P, int NE>
+cudaError_t run_strided(const LayerNormArgs& a, int threads, cudaStream_t s) {
+  static std::atomic<unsigned long long> opened[256];
+  return start_ring<T>(layer_norm_strided_kernel<T, P, NE>, opened, threads, NE <= 8 ? 56 : 80, a, s);
 }
 
 template <class T, class P>
 bool forward_ring(const LayerNormArgs& a, cudaStream_t s, cudaError_t* e) {
   constexpr int VW = 16 / sizeof(T), A = VW == 8 ? 1 : 2;
-  if (a.cols * (int64_t)sizeof(T) < kRingMinBytes || (kRing + 1) * (int64_t)ring_slot<T>(a.cols) > kRingMaxShared) return false;
-  static const int counts[2] = {A, 2 * A};
-  const Deal d = deal((a.cols + VW - 1) / VW, counts, 512);
-  if (d.nv == A) *e = run_ring<T, P, A, 512>(a, d.threads, s);
-  else if (d.nv) *e = run_ring<T, P, 2 * A, 512>(a, d.threads, s);
-  else return false;
-  return true;
+  if (a.cols > 32768 || ring_slot<T>(a.cols) > kRingMaxShared) return false;
+  const bool whole = a.cols % VW == 0 && rows_aligned16(a.x, a.x_stride, a.rows, sizeof(T)) &&
+                     rows_aligned16(a.y, a.y_stride, a.rows, sizeof(T)) && params_aligned<T, P>(a.weight) &&
+                     params_aligned<T, P>(a.bias);
+  if (!whole) {
+    static const int counts[2] = {8, 16};
+    const Deal d = deal(a.cols, counts, 512);
+    if (d.nv == 8) *e = run_strided<T, P, 8>(a, d.threads, s);
+    else if (d.nv) *e = run_strided<T, P, 16>(a, d.threads, s);
+    return d.nv != 0;
+  }
+  static const int counts[5] = {1, A, 2 * A, 3 * A, 4 * A};
+  if constexpr (sizeof(P) == 4 && sizeof(T) == 2) {
+    if (a.cols >= 2048) {
+      static const int two[1] = {2 * A};
+      const Deal d = deal(a.cols / VW, two, 512);
+      if (d.nv) {
+        *e = run_ring<T, P, 2 * A, true>(a, d.threads, s);
+        return true;
+      }
+    }
+  }
+  const Deal d = deal(a.cols / VW, counts, 512);
+  if (d.nv == 1) {
+    *e = run_ring<T, P, 1>(a, d.threads, s);
+    return true;
+  }
+  switch (d.nv) {
+    case A: *e = run_ring<T, P, A>(a, d.threads, s); return true;
+    case 2 * A: *e = run_ring<T, P, 2 * A>(a, d.threads, s); return true;
+    case 3 * A: *e = run_ring<T, P, 3 * A>(a, d.threads, s); return true;
+    case 4 * A: *e = run_ring<T, P, 4 * A>(a, d.threads, s); return true;
+  }
+  return false;
 }
 
 template <class T, class P, int VW>
-cudaError_t forward(const LayerNormArgs& a, cudaStream_t s) {
-  const int64_t vecs = (a.cols + VW - 1) / VW;
-  // a row of up to 32 elements a thread stays in registers
-  constexpr int A = VW == 1 ? 4 : VW == 8 ? 1 : 2, B = 2 * A, C = VW == 1 ? 16 : 3 * A, D = VW == 1 ? 32 : 4 * A;
-  static const int counts[4] = {A, B, C, D};
-  const Deal d = deal(vecs, counts, 512);
-  switch (d.nv) {
-    case A: return run_forward<T, P, VW, A, 512>(a, d.threads, s);
-    case B: return run_forward<T, P, VW, B, 512>(a, d.threads, s);
-    case C: return run_forward<T, P, VW, C, 512>(a, d.threads, s);
-    case D: return run_forward<T, P, VW, D, 512>(a, d.threads, s);
-  }
-  static const int most[1] = {D};
-  if (const Deal w = deal(vecs, most, 1024); w.nv) return run_forward<T, P, VW, D, 1024>(a, w.threads, s);
-  layer_norm_wide_kernel<T, P><<<(unsigned)a.rows, 1024, 0, s>>>(a);
+cudaError_t forward_wide(const LayerNormArgs& a, cudaStream_t s) {
+  constexpr int NV = 32 / VW;
+  static const int counts[1] = {NV};
+  if (const Deal d = deal((a.cols + VW - 1) / VW, counts, 1024); d.nv)
+    layer_norm_kernel<T, P, VW, NV><<<(unsigned)a.rows, d.threads, 0, s>>>(a);
+  else
+    layer_norm_wide_kernel<T, P><<<(unsigned)a.rows, 1024, 0, s>>>(a);
   count_launch();
   return cudaGetLastError();
 }
@@ -730,80 +963,73 @@ cudaError_t run_params(const LayerNormBackwardArgs& a, int blocks, cudaStream_t 
   return e;
 }
 
-template <class T, class P, int VW, int NV, int MAXT>
-cudaError_t run_backward(const LayerNormBackwardArgs& a, int threads, cudaStream_t s) {
-  auto* kernel = layer_norm_backward_kernel<T, P, VW, NV, MAXT>;
-  const int groups = std::max(1, std::min(kGroups - 1, std::min(MAXT, 512) / threads));
-  const int smem = groups > 1 ? 2 * threads * NV * VW * (int)sizeof(float) : 0;
-  int per_sm = 0;
-  cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads * groups, smem);
-  if (e != cudaSuccess) return e;
-  const int64_t want = std::min<int64_t>((int64_t)sm_count() * std::max(per_sm, 1), kLayerNormMaxBlocks);
-  const int blocks = (int)std::min<int64_t>(want, (a.rows + groups - 1) / groups);
-  kernel<<<blocks, dim3(threads, groups), smem, s>>>(a);
-  count_launch();
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return run_params<P>(a, blocks, s);
-}
-
-template <class T, class P, int NV, int MAXT>
-cudaError_t run_backward_ring(const LayerNormBackwardArgs& a, int threads, cudaStream_t s) {
-  constexpr int VW = 16 / sizeof(T);
-  auto* kernel = layer_norm_backward_ring_kernel<T, P, NV, MAXT>;
-  static std::atomic<unsigned long long> opened[256];
-  const int slot = ring_slot<T>(a.cols), ring = (2 * kRing + 1) * slot;
-  const int groups = std::max(1, std::min({kGroups - 1, 256 / threads, kRingMaxShared / ring}));
-  const int smem = std::max(groups * ring, groups > 1 ? 2 * threads * NV * VW * (int)sizeof(float) : 0);
+// columns: what one thread sums for
+template <class T, class P>
+cudaError_t start_backward_ring(void (*kernel)(LayerNormBackwardArgs, int, int), std::atomic<unsigned long long>* opened,
+                                int threads, int columns, const LayerNormBackwardArgs& a, cudaStream_t s) {
+  const int slot = ring_slot<T>(a.cols), stages = ring_stages(2 * slot, threads, backward_registers(columns));
+  const int groups = ring_groups(threads, a.rows);
+  const int smem = std::max(groups * 2 * stages * slot, groups > 1 ? 2 * threads * columns * (int)sizeof(float) : 0);
   cudaError_t e = open_kernel((const void*)kernel, kRingMaxShared, false, opened);
   if (e != cudaSuccess) return e;
   int64_t blocks = 0;
   if ((e = resident(kernel, threads * groups, smem, &blocks)) != cudaSuccess) return e;
   blocks = std::min<int64_t>({blocks, kLayerNormMaxBlocks, (a.rows + groups - 1) / groups});
-  kernel<<<(unsigned)blocks, dim3(threads, groups), smem, s>>>(a, slot);
+  kernel<<<(unsigned)blocks, dim3(threads, groups), smem, s>>>(a, slot, stages);
   count_launch();
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return run_params<P>(a, (int)blocks, s);
 }
 
+template <class T, class P, int NV>
+cudaError_t run_backward_ring(const LayerNormBackwardArgs& a, int threads, cudaStream_t s) {
+  static std::atomic<unsigned long long> opened[256];
+  return start_backward_ring<T, P>(layer_norm_backward_ring_kernel<T, P, NV>, opened, threads, NV * (16 / (int)sizeof(T)), a, s);
+}
+template <class T, class P, int NE>
+cudaError_t run_backward_strided(const LayerNormBackwardArgs& a, int threads, cudaStream_t s) {
+  static std::atomic<unsigned long long> opened[256];
+  return start_backward_ring<T, P>(layer_norm_backward_strided_kernel<T, P, NE>, opened, threads, NE, a, s);
+}
+
 template <class T, class P>
 bool backward_ring(const LayerNormBackwardArgs& a, cudaStream_t s, cudaError_t* e) {
   constexpr int VW = 16 / sizeof(T), A = VW == 8 ? 1 : 2;
-  if (a.cols * (int64_t)sizeof(T) < kRingMinBytes || (2 * kRing + 1) * (int64_t)ring_slot<T>(a.cols) > kRingMaxShared) return false;
-  static const int counts[2] = {A, 2 * A};
-  const Deal d = deal((a.cols + VW - 1) / VW, counts, 512);
-  if (d.nv == A) *e = run_backward_ring<T, P, A, 512>(a, d.threads, s);
-  else if (d.nv) *e = run_backward_ring<T, P, 2 * A, 512>(a, d.threads, s);
-  else return false;
-  return true;
+  if (a.cols > 32768 || 2 * ring_slot<T>(a.cols) > kRingMaxShared) return false;
+  const bool whole = a.cols % VW == 0 && rows_aligned16(a.x, a.x_stride, a.rows, sizeof(T)) &&
+                     rows_aligned16(a.dy, a.dy_stride, a.rows, sizeof(T)) &&
+                     rows_aligned16(a.dx, a.dx_stride, a.rows, sizeof(T)) && params_aligned<T, P>(a.weight);
+  if (!whole) {
+    static const int counts[2] = {8, 16};
+    const Deal d = deal(a.cols, counts, 512);
+    if (d.nv == 8) *e = run_backward_strided<T, P, 8>(a, d.threads, s);
+    else if (d.nv) *e = run_backward_strided<T, P, 16>(a, d.threads, s);
+    return d.nv != 0;
+  }
+  static const int counts[3] = {1, A, 2 * A};
+  const Deal d = deal(a.cols / VW, counts, 512);
+  if (d.nv == 1) *e = run_backward_ring<T, P, 1>(a, d.threads, s);
+  else if (d.nv == A) *e = run_backward_ring<T, P, A>(a, d.threads, s);
+  else if (d.nv) *e = run_backward_ring<T, P, 2 * A>(a, d.threads, s);
+  return d.nv != 0;
 }
 
 template <class T, class P, int VW>
-cudaError_t backward(const LayerNormBackwardArgs& a, cudaStream_t s) {
-  const int64_t vecs = (a.cols + VW - 1) / VW;
-  // up to 16 columns a thread: their two sums, weights and rows fit its registers
-  constexpr int A = VW == 8 ? 1 : VW == 4 ? 1 : 4, B = 2 * A, C = 4 * A;
-  Deal d;
-  if constexpr (VW == 8) {
-    static const int counts[2] = {A, B};
-    d = deal(vecs, counts, 512);
-    if (d.nv == A) return run_backward<T, P, VW, A, 512>(a, d.threads, s);
-    if (d.nv == B) return run_backward<T, P, VW, B, 512>(a, d.threads, s);
-    d = deal(vecs, counts, 1024);
-    if (d.nv) return run_backward<T, P, VW, B, 1024>(a, (int)((vecs + 32 * B - 1) / (32 * B) * 32), s);
-  } else {
-    static const int counts[3] = {A, B, C};
-    d = deal(vecs, counts, 512);
-    if (d.nv == A) return run_backward<T, P, VW, A, 512>(a, d.threads, s);
-    if (d.nv == B) return run_backward<T, P, VW, B, 512>(a, d.threads, s);
-    if (d.nv == C) return run_backward<T, P, VW, C, 512>(a, d.threads, s);
-    d = deal(vecs, counts, 1024);
-    if (d.nv) return run_backward<T, P, VW, C, 1024>(a, (int)((vecs + 32 * C - 1) / (32 * C) * 32), s);
+cudaError_t backward_wide(const LayerNormBackwardArgs& a, cudaStream_t s) {
+  constexpr int NV = 16 / VW;
+  static const int counts[1] = {NV};
+  cudaError_t e;
+  if (const Deal d = deal((a.cols + VW - 1) / VW, counts, 1024); d.nv) {
+    const int blocks = (int)std::min<int64_t>(std::min(sm_count(), kLayerNormMaxBlocks), a.rows);
+    layer_norm_backward_kernel<T, P, VW, NV><<<blocks, d.threads, 0, s>>>(a);
+    count_launch();
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    return run_params<P>(a, blocks, s);
   }
   const int slices = (int)std::min<int64_t>(a.rows, 64);
   layer_norm_params_wide_kernel<T><<<dim3((unsigned)((a.cols + 255) / 256), slices), 256, 0, s>>>(a);
   count_launch();
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   layer_norm_backward_wide_kernel<T, P><<<(unsigned)a.rows, 1024, 0, s>>>(a);
   count_launch();
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
@@ -832,7 +1058,7 @@ cudaError_t launch_layer_norm(int dtype, int pdtype, const LayerNormArgs& a, cud
     const bool vec = rows_aligned16(a.x, a.x_stride, a.rows, sizeof(T)) &&
                      rows_aligned16(a.y, a.y_stride, a.rows, sizeof(T)) &&
                      (uintptr_t)a.weight % (VW * sizeof(P)) == 0 && (uintptr_t)a.bias % (VW * sizeof(P)) == 0;
-    return vec ? forward<T, P, VW>(a, s) : forward<T, P, 1>(a, s);
+    return vec ? forward_wide<T, P, VW>(a, s) : forward_wide<T, P, 1>(a, s);
   });
 }
 
@@ -847,7 +1073,7 @@ cudaError_t launch_layer_norm_backward(int dtype, int pdtype, const LayerNormBac
                      rows_aligned16(a.dy, a.dy_stride, a.rows, sizeof(T)) &&
                      rows_aligned16(a.dx, a.dx_stride, a.rows, sizeof(T)) &&
                      (uintptr_t)a.weight % (VW * sizeof(P)) == 0;
-    return vec ? backward<T, P, VW>(a, s) : backward<T, P, 1>(a, s);
+    return vec ? backward_wide<T, P, VW>(a, s) : backward_wide<T, P, 1>(a, s);
   });
 }
 

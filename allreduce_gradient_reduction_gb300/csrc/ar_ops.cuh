@@ -72,8 +72,147 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
+// Two binary32 values in one register pair, and the operations that take pairs.
+struct Two {
+  uint64_t v;
+};
+__device__ __forceinline__ Two two(float lo, float hi) {
+  Two r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void split(Two t, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(t.v));
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+  Two r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ Two add2(Two a, Two b) {
+  Two r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ Two mul2(Two a, Two b) {
+  Two r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// ---- pairs of 16-bit elements in one word ------------------------------------------
+
+template <class T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+  const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+  const __half2 r = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// The two elements of a word, widened.
+template <class T>
+__device__ __forceinline__ Two unpack2(uint32_t w);
+template <>
+__device__ __forceinline__ Two unpack2<__nv_bfloat16>(uint32_t w) {
+  return two(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+template <>
+__device__ __forceinline__ Two unpack2<__half>(uint32_t w) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return two(f.x, f.y);
+}
+// The larger of each pair; a NaN gives way to a number.
+template <class T>
+__device__ __forceinline__ uint32_t max_pairs(uint32_t a, uint32_t b);
+template <>
+__device__ __forceinline__ uint32_t max_pairs<__nv_bfloat16>(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 r = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+template <>
+__device__ __forceinline__ uint32_t max_pairs<__half>(uint32_t a, uint32_t b) {
+  const __half2 r = __hmax2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// 16 bytes of elements as pairs of binary32 values, and back.
+template <class T>
+struct Pairs {
+  static constexpr int N = 4;  // pairs in 16 bytes
+  static __device__ __forceinline__ Two get(const uint4& v, int i) {
+    return unpack2<T>(i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w);
+  }
+  static __device__ __forceinline__ void set(uint4& v, int i, Two t) {
+    float lo, hi;
+    split(t, lo, hi);
+    (i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w) = pack2<T>(lo, hi);
+  }
+};
+template <>
+struct Pairs<float> {
+  static constexpr int N = 2;
+  static __device__ __forceinline__ Two get(const uint4& v, int i) {
+    return i == 0 ? two(__uint_as_float(v.x), __uint_as_float(v.y)) : two(__uint_as_float(v.z), __uint_as_float(v.w));
+  }
+  static __device__ __forceinline__ void set(uint4& v, int i, Two t) {
+    float lo, hi;
+    split(t, lo, hi);
+    (i == 0 ? v.x : v.z) = __float_as_uint(lo);
+    (i == 0 ? v.y : v.w) = __float_as_uint(hi);
+  }
+};
+
 __device__ __forceinline__ void named_barrier(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// ---- bulk copies into shared memory, announced on an mbarrier ---------------------
+
+__device__ __forceinline__ uint32_t smem_at(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+
+__device__ __forceinline__ void ring_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+// The aligned words of `bytes` bytes at `from`.
+__device__ __forceinline__ uint32_t covering(const void* from, int bytes) {
+  return (((uint32_t)(uintptr_t)from & 15) + bytes + 15) & ~15u;
+}
+__device__ __forceinline__ void ring_copy(uint32_t to, const void* from, int bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to),
+               "l"((uintptr_t)from & ~(uintptr_t)15), "r"(covering(from, bytes)), "r"(bar)
+               : "memory");
+}
+
+// A copy ends by itself, so this wait does; the limit (two seconds) is for a
+// launch that has gone wrong, whose results are then wrong too but which ends.
+__device__ __forceinline__ void ring_wait(uint32_t bar, uint32_t parity) {
+  for (int i = 0; i < 200; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\nselp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(10000000)
+        : "memory");
+    if (ok) return;
+  }
 }
 
 // Applies a launch's element type to a function object: fn(T()).
