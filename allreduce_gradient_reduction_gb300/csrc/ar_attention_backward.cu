@@ -33,25 +33,29 @@ constexpr int kThreads = 576;
 constexpr int kIssuer = 16, kLoader = 17;  // warps
 constexpr int kWorkers = 512;              // threads of the others
 
-// delta[head][token] = dout . out: 16 threads to a row, 16 bytes each.
-template <class T>
+// delta[head][token] = dout . out: LANES threads to a row, 16 bytes each.
+template <class T, int LANES>
 __global__ void __launch_bounds__(256) attention_delta_kernel(const AttnArgs a) {
-  const int64_t rows = a.tokens * a.heads;
-  const int64_t r = (int64_t)blockIdx.x * 16 + threadIdx.x / 16;
-  const int c = threadIdx.x % 16 * 8;
+  // the gradients' kernel may be set up meanwhile; it waits for this one's end
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t row = blockIdx.x * (256 / LANES) + threadIdx.x / LANES, token = row / a.heads, head = row % a.heads;
+  const int c = threadIdx.x % LANES * 8;
   float s = 0.f;
-  const int64_t token = r / a.heads, head = r % a.heads;
-  if (r < rows && c < a.dim) {
-    const Pack<T, 8> x = *reinterpret_cast<const Pack<T, 8>*>(static_cast<const T*>(a.out.ptr) + token * a.out.token_stride +
-                                                              head * a.out.head_stride + c);
-    const Pack<T, 8> y = *reinterpret_cast<const Pack<T, 8>*>(static_cast<const T*>(a.dout.ptr) + token * a.dout.token_stride +
-                                                              head * a.dout.head_stride + c);
+  if (token < a.tokens && c < a.dim) {
+    const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.out.ptr) + token * a.out.token_stride +
+                                                    head * a.out.head_stride + c);
+    const uint4 y = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.dout.ptr) + token * a.dout.token_stride +
+                                                    head * a.dout.head_stride + c);
+    Two acc = two(0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s = fmaf(Conv<T>::up(x.v[i]), Conv<T>::up(y.v[i]), s);
+    for (int i = 0; i < 4; ++i) acc = fma2(Pairs<T>::get(x, i), Pairs<T>::get(y, i), acc);
+    float lo, hi;
+    split(acc, lo, hi);
+    s = lo + hi;
   }
 #pragma unroll
-  for (int m = 8; m; m >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, m);
-  if (r < rows && c == 0) a.delta[head * a.tokens + token] = s;
+  for (int m = LANES / 2; m; m >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, m);
+  if (token < a.tokens && c == 0) a.delta[(int64_t)head * a.tokens + token] = s;
 }
 
 // Writes 16 columns of a thread's row of sums, times `scale`, rounded.
@@ -122,6 +126,10 @@ __device__ __forceinline__ void score_gradients(float (&p)[32], float (&d)[32], 
   }
 }
 
+struct Maps {
+  CUtensorMap q, k, v, dout;
+};
+
 // ---- dk and dv ---------------------------------------------------------------------
 
 constexpr int kMostStages = 4;
@@ -139,17 +147,12 @@ struct SharedKV {
 };
 
 template <class T, int PANELS>
-__global__ void __launch_bounds__(kThreads, 1)
-    attention_dkv_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
-                         const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap do_map,
-                         const AttnArgs a) {
+__device__ __forceinline__ void dkv_block(const Maps& maps, const AttnArgs& a, int block, uint8_t* tiles, SharedKV& sh) {
   constexpr int kStages = query_stages(PANELS);
-  extern __shared__ __align__(1024) uint8_t tiles[];
-  __shared__ SharedKV sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int kv_head = blockIdx.x % a.kv_heads;
+  const int kv_head = block % a.kv_heads;
   if (warp == 0) {
-    const SeqUnit u = find_unit(a.cu_seqlens, a.seqs, (int)a.tokens, kTile, blockIdx.x / a.kv_heads);
+    const SeqUnit u = find_unit(a.cu_seqlens, a.seqs, (int)a.tokens, kTile, block / a.kv_heads);
     if (lane == 0) {
       sh.unit = u;
       sh.gave_up = 0;
@@ -199,8 +202,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t bar = smem_addr(&sh.kv_full);
       mbar_expect(bar, 2 * kTileBytes);
       for (int p = 0; p < PANELS; ++p) {
-        tma_load(k_tile + p * kPanelBytes, &k_map, p * 64, kv_head, unit.begin + unit.index * kTile, bar);
-        tma_load(v_tile + p * kPanelBytes, &v_map, p * 64, kv_head, unit.begin + unit.index * kTile, bar);
+        tma_load(k_tile + p * kPanelBytes, &maps.k, p * 64, kv_head, unit.begin + unit.index * kTile, bar);
+        tma_load(v_tile + p * kPanelBytes, &maps.v, p * 64, kv_head, unit.begin + unit.index * kTile, bar);
       }
     }
     uint32_t own_parity = 0;
@@ -208,9 +211,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int stage = n % kStages;
       if (n >= kStages && !mbar_wait(smem_addr(&sh.empty[stage]), (n / kStages - 1) & 1, gave_up)) break;
       const int head = kv_head * group + n / per, query = (unit.index + n % per) * kTile;
-      if (!load_tile(&q_map, q_tile + stage * kTileBytes, PANELS, head, unit.begin + query, unit.length - query,
+      if (!load_tile(&maps.q, q_tile + stage * kTileBytes, PANELS, head, unit.begin + query, unit.length - query,
                      smem_addr(&sh.q_full[stage]), smem_addr(&sh.own), &own_parity, gave_up) ||
-          !load_tile(&do_map, do_tile + stage * kTileBytes, PANELS, head, unit.begin + query, unit.length - query,
+          !load_tile(&maps.dout, do_tile + stage * kTileBytes, PANELS, head, unit.begin + query, unit.length - query,
                      smem_addr(&sh.do_full[stage]), smem_addr(&sh.own), &own_parity, gave_up))
         break;
     }
@@ -350,16 +353,11 @@ struct SharedQ {
 };
 
 template <class T, int PANELS>
-__global__ void __launch_bounds__(kThreads, 1)
-    attention_dq_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
-                        const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap do_map,
-                        const AttnArgs a) {
-  extern __shared__ __align__(1024) uint8_t tiles[];
-  __shared__ SharedQ sh;
+__device__ __forceinline__ void dq_block(const Maps& maps, const AttnArgs& a, int block, uint8_t* tiles, SharedQ& sh) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int head = blockIdx.x % a.heads;
+  const int head = block % a.heads;
   if (warp == 0) {
-    const SeqUnit u = find_unit(a.cu_seqlens, a.seqs, (int)a.tokens, kTile, blockIdx.x / a.heads);
+    const SeqUnit u = find_unit(a.cu_seqlens, a.seqs, (int)a.tokens, kTile, block / a.heads);
     if (lane == 0) {
       sh.unit = u;
       sh.gave_up = 0;
@@ -404,8 +402,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t bar = smem_addr(&sh.q_full);
       mbar_expect(bar, 2 * kTileBytes);
       for (int p = 0; p < PANELS; ++p) {
-        tma_load(q_tile + p * kPanelBytes, &q_map, p * 64, head, unit.begin + query, bar);
-        tma_load(do_tile + p * kPanelBytes, &do_map, p * 64, head, unit.begin + query, bar);
+        tma_load(q_tile + p * kPanelBytes, &maps.q, p * 64, head, unit.begin + query, bar);
+        tma_load(do_tile + p * kPanelBytes, &maps.dout, p * 64, head, unit.begin + query, bar);
       }
     }
     uint32_t own_parity = 0;
@@ -413,11 +411,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int ks = n % kKStages, vs = n % kVStages, key = n * kTile;
       if (n >= kKStages && !mbar_wait(smem_addr(&sh.k_empty[ks]), (n / kKStages - 1) & 1, gave_up)) break;
       // dq sums over the rows of K: those of another sequence are cleared
-      if (!load_tile(&k_map, k_tile + ks * kTileBytes, PANELS, kv_head, unit.begin + key, unit.length - key,
+      if (!load_tile(&maps.k, k_tile + ks * kTileBytes, PANELS, kv_head, unit.begin + key, unit.length - key,
                      smem_addr(&sh.k_full[ks]), smem_addr(&sh.own), &own_parity, gave_up))
         break;
       if (n >= kVStages && !mbar_wait(smem_addr(&sh.v_empty[vs]), (n / kVStages - 1) & 1, gave_up)) break;
-      if (!load_tile(&v_map, v_tile + vs * kTileBytes, PANELS, kv_head, unit.begin + key, kTile,
+      if (!load_tile(&maps.v, v_tile + vs * kTileBytes, PANELS, kv_head, unit.begin + key, kTile,
                      smem_addr(&sh.v_full[vs]), smem_addr(&sh.own), &own_parity, gave_up))
         break;
     }
@@ -496,31 +494,61 @@ __global__ void __launch_bounds__(kThreads, 1)
   leave(&sh.gave_up, warp, tmem);
 }
 
+// ---- both ---------------------------------------------------------------------------
+
+union Shared {
+  SharedKV kv;
+  SharedQ q;
+  __device__ Shared() {}
+};
+
+// One launch, so that the second kind's blocks fill the first's last wave; the
+// first `kv_blocks` blocks make dk and dv.
+template <class T, int PANELS>
+__global__ void __launch_bounds__(kThreads, 1)
+    attention_backward_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a, int kv_blocks) {
+  extern __shared__ __align__(1024) uint8_t tiles[];
+  __shared__ Shared sh;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // for delta
+  const int block = blockIdx.x;
+  if (block < kv_blocks) dkv_block<T, PANELS>(maps, a, block, tiles, sh.kv);
+  else dq_block<T, PANELS>(maps, a, block - kv_blocks, tiles, sh.q);
+}
+
 template <class T, int PANELS>
 cudaError_t run(int dtype, const AttnArgs& a, cudaStream_t s) {
-  static std::atomic<unsigned long long> opened_kv[256], opened_q[256];
-  constexpr int smem_kv = (2 + 2 * query_stages(PANELS)) * PANELS * (int)kPanelBytes;
-  constexpr int smem_q = (2 + kKStages + kVStages) * PANELS * (int)kPanelBytes;
-  cudaError_t e = open_kernel((const void*)attention_dkv_kernel<T, PANELS>, smem_kv, false, opened_kv);
+  static std::atomic<unsigned long long> opened[256];
+  constexpr int tiles = std::max(2 + 2 * query_stages(PANELS), 2 + kKStages + kVStages);
+  constexpr int smem = tiles * PANELS * (int)kPanelBytes;
+  auto* kernel = attention_backward_kernel<T, PANELS>;
+  cudaError_t e = open_kernel((const void*)kernel, smem, false, opened);
   if (e != cudaSuccess) return e;
-  if ((e = open_kernel((const void*)attention_dq_kernel<T, PANELS>, smem_q, false, opened_q)) != cudaSuccess) return e;
-  CUtensorMap q, k, v, d;
-  if (!make_tensor_map(&q, dtype, a.q, a.tokens, a.heads, a.dim) ||
-      !make_tensor_map(&k, dtype, a.k, a.tokens, a.kv_heads, a.dim) ||
-      !make_tensor_map(&v, dtype, a.v, a.tokens, a.kv_heads, a.dim) ||
-      !make_tensor_map(&d, dtype, a.dout, a.tokens, a.heads, a.dim))
+  Maps maps;
+  if (!make_tensor_map(&maps.q, dtype, a.q, a.tokens, a.heads, a.dim) ||
+      !make_tensor_map(&maps.k, dtype, a.k, a.tokens, a.kv_heads, a.dim) ||
+      !make_tensor_map(&maps.v, dtype, a.v, a.tokens, a.kv_heads, a.dim) ||
+      !make_tensor_map(&maps.dout, dtype, a.dout, a.tokens, a.heads, a.dim))
     return cudaErrorInvalidValue;
-  attention_delta_kernel<T><<<(unsigned)((a.tokens * a.heads + 15) / 16), 256, 0, s>>>(a);
+  constexpr int kLanes = PANELS * 8, kRows = 256 / kLanes;
+  attention_delta_kernel<T, kLanes><<<(unsigned)((a.tokens * a.heads + kRows - 1) / kRows), 256, 0, s>>>(a);
   count_launch();
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   // at most this many tiles, however the tokens are split
   const int64_t most = a.tokens / kTile + std::min<int64_t>(a.seqs, a.tokens);
-  attention_dkv_kernel<T, PANELS><<<(unsigned)(most * a.kv_heads), kThreads, smem_kv, s>>>(q, k, v, d, a);
+  const int kv_blocks = (int)(most * a.kv_heads);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(kv_blocks + most * a.heads));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kernel, maps, a, kv_blocks);
   count_launch();
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  attention_dq_kernel<T, PANELS><<<(unsigned)(most * a.heads), kThreads, smem_q, s>>>(q, k, v, d, a);
-  count_launch();
-  return cudaGetLastError();
+  return e;
 }
 
 }  // namespace

@@ -154,7 +154,9 @@ int check_attention(int64_t tokens, int64_t seqs, int64_t heads, int64_t kv_head
   if (tokens < 0 || seqs < 0 || heads < 1 || kv_heads < 1 || dim < 1 || heads % kv_heads) return AR_ERR_INVALID_ARG;
   if (dtype < AR_F32 || dtype > AR_F16 || !(scale > 0.f) || !std::isfinite(scale)) return AR_ERR_INVALID_ARG;
   if ((dtype != AR_BF16 && dtype != AR_F16) || dim % 8 || dim > AR_ATTENTION_MAX_DIM) return AR_ERR_UNSUPPORTED;
-  if (tokens > (1 << 30) || seqs > (1 << 24) || heads > 4096 || (tokens / 128 + seqs) * heads > INT32_MAX) return AR_ERR_TOO_LARGE;
+  if (tokens > (1 << 30) || seqs > (1 << 24) || heads > 4096 || (tokens / 128 + seqs) * (heads + kv_heads) > INT32_MAX ||
+      tokens * heads > INT32_MAX)
+    return AR_ERR_TOO_LARGE;
   return AR_OK;
 }
 
