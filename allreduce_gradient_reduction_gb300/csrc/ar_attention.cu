@@ -119,9 +119,9 @@ __global__ void __launch_bounds__(Form<PANELS>::kThreads, Form<PANELS>::kBlocks)
   uint32_t own_parity = 0;
   auto load = [&](int n) {
     const int stage = n % kStages, key = (n >> 1) * kTile;
-    return load_tile(n & 1 ? &v_map : &k_map, kv_tile + stage * kTileBytes, PANELS, kv_head, unit.begin + key,
-                     n & 1 ? unit.length - key : kTile, smem_addr(&sh.kv_full[stage]), smem_addr(&sh.own), &own_parity,
-                     gave_up);
+    return load_tile<PANELS, kTile>(n & 1 ? &v_map : &k_map, kv_tile + stage * kTileBytes, kv_head, unit.begin + key,
+                                    n & 1 ? unit.length - key : kTile, smem_addr(&sh.kv_full[stage]),
+                                    smem_addr(&sh.own), &own_parity, gave_up);
   };
   if (warp == F::kLoader) {
     if (lane == 0) {
@@ -359,9 +359,9 @@ cudaError_t run(int dtype, const AttnArgs& a, cudaStream_t s) {
   }();
   if (F::kThreads == 384 && registers != kLaunchRegisters) return cudaErrorInvalidConfiguration;
   CUtensorMap q, k, v;
-  if (!make_tensor_map(&q, dtype, a.q, a.tokens, a.heads, a.dim) ||
-      !make_tensor_map(&k, dtype, a.k, a.tokens, a.kv_heads, a.dim) ||
-      !make_tensor_map(&v, dtype, a.v, a.tokens, a.kv_heads, a.dim))
+  if (!make_tensor_map(&q, dtype, a.q, a.tokens, a.heads, a.dim, kTile) ||
+      !make_tensor_map(&k, dtype, a.k, a.tokens, a.kv_heads, a.dim, kTile) ||
+      !make_tensor_map(&v, dtype, a.v, a.tokens, a.kv_heads, a.dim, kTile))
     return cudaErrorInvalidValue;
   // at most this many units, however the tokens are split
   const int64_t units = a.tokens / F::kQueries + std::min<int64_t>(a.seqs, a.tokens);
@@ -372,7 +372,7 @@ cudaError_t run(int dtype, const AttnArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-bool make_tensor_map(CUtensorMap* map, int dtype, const AttnTensor& t, int64_t tokens, int heads, int dim) {
+bool make_tensor_map(CUtensorMap* map, int dtype, const AttnTensor& t, int64_t tokens, int heads, int dim, int rows) {
   typedef CUresult (*Encode)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -387,7 +387,7 @@ bool make_tensor_map(CUtensorMap* map, int dtype, const AttnTensor& t, int64_t t
   if (!encode) return false;
   const cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)tokens};
   const cuuint64_t strides[2] = {(cuuint64_t)t.head_stride * 2, (cuuint64_t)t.token_stride * 2};
-  const cuuint32_t box[3] = {64, 1, kTile}, unit[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {64, 1, (cuuint32_t)rows}, unit[3] = {1, 1, 1};
   return encode(map, dtype == BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
                 const_cast<void*>(t.ptr), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
                 CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

@@ -12,8 +12,7 @@
 // products where five are the least; a single kernel would have to add dq from
 // many blocks to memory, in an order that changes.
 //
-// In both, sixteen warps take the exponentials: four threads share a row of
-// the tile, 32 columns each.  p and ds take the places of the scores and of
+// In both, a thread takes the exponentials of 32 columns of a row.  p and ds take the places of the scores and of
 // dout v^T in tensor memory, as 16-bit pairs, and are the left operands of the
 // sums' products there.  The next tiles' products are issued between the
 // current one's sums, so the tensor cores work while exponentials are taken.
@@ -29,9 +28,24 @@ namespace {
 __device__ int g_status;  // AR_ERR_TIMEOUT once a wait has run out
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kThreads = 576;
-constexpr int kIssuer = 16, kLoader = 17;  // warps
-constexpr int kWorkers = 512;              // threads of the others
+// A block keeps 128 keys (or queries) and walks over tiles of kWalk queries
+// (keys).  Heads of up to 64 elements (one panel) need half of tensor memory
+// with 64 of them, so that two blocks share a multiprocessor and one's
+// exponentials, or its start and end, overlap the other's products
+// (8192 tokens in 13 sequences, 12 heads of 64: 95.7 us with one block and
+// tiles of 128, 71.7 us so; 8192 tokens of one, 32 heads of 64: 967 and 879).  Four threads, or two, have a row's columns.
+template <int PANELS>
+struct Form {
+  static constexpr int kWalk = PANELS == 1 ? 64 : 128;
+  static constexpr int kQuarters = kWalk / 32;
+  static constexpr int kWorkers = kTile * kQuarters;                          // threads
+  static constexpr int kIssuer = kWorkers / 32, kLoader = kWorkers / 32 + 1;  // warps
+  static constexpr int kThreads = kWorkers + 64;
+  static constexpr int kBlocks = PANELS == 1 ? 2 : 1;  // on a multiprocessor
+  static constexpr int kColumns = PANELS == 1 ? 256 : 512;
+  static constexpr uint32_t kKeptBytes = PANELS * kPanelBytes, kWalkBytes = PANELS * kWalk * 128;
+  static constexpr int kStages = PANELS == 1 ? 4 : 2;  // tiles of q and dout in flight
+};
 
 // delta[head][token] = dout . out: LANES threads to a row, 16 bytes each.
 template <class T, int LANES>
@@ -75,6 +89,16 @@ __device__ __forceinline__ void write16(uint32_t from, T* row, int column, int d
   }
 }
 
+// The kept tile, in boxes of kWalk rows.
+template <int PANELS>
+__device__ __forceinline__ void load_kept(const CUtensorMap* map, uint32_t dst, int head, int token, uint32_t bar) {
+  constexpr int kWalk = Form<PANELS>::kWalk;
+  for (int p = 0; p < PANELS; ++p)
+    for (int r = 0; r < kTile; r += kWalk)
+      tma_load(dst + p * kPanelBytes + r * 128, map, p * 64, head, token + r, bar);
+}
+
+template <int PANELS>
 __device__ __forceinline__ void leave(int* gave_up, int warp, uint32_t tmem) {
   tc_fence_before();
   __syncthreads();
@@ -84,7 +108,7 @@ __device__ __forceinline__ void leave(int* gave_up, int warp, uint32_t tmem) {
     if (threadIdx.x == 0) g_status = AR_ERR_TIMEOUT;
     __syncthreads();
   }
-  if (warp == kIssuer) tmem_free(tmem, 512);
+  if (warp == Form<PANELS>::kIssuer) tmem_free(tmem, Form<PANELS>::kColumns);
 }
 
 // 32 scores of a thread become probabilities 2^(c s - lse) in place, and pairs
@@ -134,12 +158,9 @@ struct Maps {
 
 constexpr int kMostStages = 4;
 
-// Tiles of queries (q and dout) in flight: as many as fit beside k and v.
-__host__ __device__ constexpr int query_stages(int panels) { return panels == 1 ? kMostStages : 2; }
-
 struct SharedKV {
-  alignas(8) uint64_t kv_full, q_full[kMostStages], do_full[kMostStages], empty[kMostStages], s_full, s_read, dp_full,
-      dp_read, p_ready, ds_ready, dv_done, dk_done, done, own;
+  alignas(8) uint64_t kv_full, q_full[kMostStages], do_full[kMostStages], empty[kMostStages], s_full, dp_full, p_ready,
+      ds_ready, done, own;
   alignas(16) float lse[2][4][32], delta[2][4][32];  // [turn][quarter]
   uint32_t tmem;
   int gave_up;
@@ -148,7 +169,8 @@ struct SharedKV {
 
 template <class T, int PANELS>
 __device__ __forceinline__ void dkv_block(const Maps& maps, const AttnArgs& a, int block, uint8_t* tiles, SharedKV& sh) {
-  constexpr int kStages = query_stages(PANELS);
+  using F = Form<PANELS>;
+  constexpr int kStages = F::kStages, kWalk = F::kWalk;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int kv_head = block % a.kv_heads;
   if (warp == 0) {
@@ -157,16 +179,16 @@ __device__ __forceinline__ void dkv_block(const Maps& maps, const AttnArgs& a, i
       sh.unit = u;
       sh.gave_up = 0;
     }
-  } else if (warp == kLoader && lane == 0) {
-    uint64_t* const one[] = {&sh.kv_full, &sh.s_full, &sh.dp_full, &sh.dv_done, &sh.dk_done, &sh.done, &sh.own};
+  } else if (warp == F::kLoader && lane == 0) {
+    uint64_t* const one[] = {&sh.kv_full, &sh.s_full, &sh.dp_full, &sh.done, &sh.own};
     for (uint64_t* b : one) mbar_init(smem_addr(b), 1);
     for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_addr(&sh.q_full[i]), 1);
       mbar_init(smem_addr(&sh.do_full[i]), 1);
       mbar_init(smem_addr(&sh.empty[i]), 1);
     }
-    uint64_t* const all[] = {&sh.s_read, &sh.dp_read, &sh.p_ready, &sh.ds_ready};
-    for (uint64_t* b : all) mbar_init(smem_addr(b), kWorkers / 32);
+    mbar_init(smem_addr(&sh.p_ready), F::kWorkers / 32);
+    mbar_init(smem_addr(&sh.ds_ready), F::kWorkers / 32);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncthreads();
@@ -174,53 +196,46 @@ __device__ __forceinline__ void dkv_block(const Maps& maps, const AttnArgs& a, i
   SeqUnit unit = sh.unit;
   unit.index = unit.count - 1 - unit.index;  // the first keys are seen by the most queries
 
-  constexpr uint32_t kTileBytes = PANELS * kPanelBytes;
-  const uint32_t k_tile = smem_addr(tiles), v_tile = k_tile + kTileBytes, q_tile = v_tile + kTileBytes,
-                 do_tile = q_tile + kStages * kTileBytes;
+  const uint32_t k_tile = smem_addr(tiles), v_tile = k_tile + F::kKeptBytes, q_tile = v_tile + F::kKeptBytes,
+                 do_tile = q_tile + kStages * F::kWalkBytes;
   volatile int* gave_up = &sh.gave_up;
-  if (warp == kIssuer) tmem_alloc(smem_addr(&sh.tmem), 512);
+  if (warp == F::kIssuer) tmem_alloc(smem_addr(&sh.tmem), F::kColumns);
+  // step n: head n / per of the group, tile first + n % per of the sequence's queries
+  const int group = a.heads / a.kv_heads, first = unit.index * (kTile / kWalk);
+  const int per = (unit.length + kWalk - 1) / kWalk - first, steps = group * per;
+  const int dim16 = (a.dim + 15) / 16;
+  if (warp == F::kLoader && lane == 0) {
+    const uint32_t bar = smem_addr(&sh.kv_full);
+    mbar_expect(bar, 2 * F::kKeptBytes);
+    load_kept<PANELS>(&maps.k, k_tile, kv_head, unit.begin + unit.index * kTile, bar);
+    load_kept<PANELS>(&maps.v, v_tile, kv_head, unit.begin + unit.index * kTile, bar);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sh.tmem;
-  // Tensor memory: scores 0, dout v^T 128, dv 256.  Heads of up to 64 leave
-  // room for p and ds beside them, so that the next tile's products run as
-  // soon as the current scores and dout v^T have been read; otherwise they
-  // take those places, each quarter's 16 columns of pairs at the front of the
-  // 32 that it read.
-  constexpr bool kApart = PANELS == 1;
-  const uint32_t dv_at = tmem + 256, dk_at = tmem + (kApart ? 320 : 384);
-  auto p_at = [&](int quarter) { return tmem + (kApart ? 384 + quarter * 16 : quarter * 32); };
-  auto ds_at = [&](int quarter) { return tmem + (kApart ? 448 + quarter * 16 : 128 + quarter * 32); };
+  // Tensor memory: scores, dout v^T, dv, dk.  p and ds take the places of the
+  // first two, each quarter's 16 columns of pairs at the front of the 32 that
+  // it read.
+  const uint32_t tmem = sh.tmem, dp_at = tmem + kWalk, dv_at = tmem + 2 * kWalk, dk_at = dv_at + 64 * PANELS;
 
-  // step n: head n / per of the group, tile of queries unit.index + n % per
-  const int group = a.heads / a.kv_heads, per = unit.count - unit.index, steps = group * per;
-  const int dim16 = (a.dim + 15) / 16;
-
-  if (warp == kLoader) {
-    if (lane == 0) {
-      const uint32_t bar = smem_addr(&sh.kv_full);
-      mbar_expect(bar, 2 * kTileBytes);
-      for (int p = 0; p < PANELS; ++p) {
-        tma_load(k_tile + p * kPanelBytes, &maps.k, p * 64, kv_head, unit.begin + unit.index * kTile, bar);
-        tma_load(v_tile + p * kPanelBytes, &maps.v, p * 64, kv_head, unit.begin + unit.index * kTile, bar);
-      }
-    }
+  if (warp == F::kLoader) {
     uint32_t own_parity = 0;
     for (int n = 0; n < steps; ++n) {
       const int stage = n % kStages;
       if (n >= kStages && !mbar_wait(smem_addr(&sh.empty[stage]), (n / kStages - 1) & 1, gave_up)) break;
-      const int head = kv_head * group + n / per, query = (unit.index + n % per) * kTile;
-      if (!load_tile(&maps.q, q_tile + stage * kTileBytes, PANELS, head, unit.begin + query, unit.length - query,
-                     smem_addr(&sh.q_full[stage]), smem_addr(&sh.own), &own_parity, gave_up) ||
-          !load_tile(&maps.dout, do_tile + stage * kTileBytes, PANELS, head, unit.begin + query, unit.length - query,
-                     smem_addr(&sh.do_full[stage]), smem_addr(&sh.own), &own_parity, gave_up))
+      const int head = kv_head * group + n / per, query = (first + n % per) * kWalk;
+      if (!load_tile<PANELS, kWalk>(&maps.q, q_tile + stage * F::kWalkBytes, head, unit.begin + query,
+                                    unit.length - query, smem_addr(&sh.q_full[stage]), smem_addr(&sh.own), &own_parity,
+                                    gave_up) ||
+          !load_tile<PANELS, kWalk>(&maps.dout, do_tile + stage * F::kWalkBytes, head, unit.begin + query,
+                                    unit.length - query, smem_addr(&sh.do_full[stage]), smem_addr(&sh.own), &own_parity,
+                                    gave_up))
         break;
     }
-  } else if (warp == kIssuer) {
+  } else if (warp == F::kIssuer) {
     if (elect_one()) {
-      const uint32_t wide = mma_shape<T>(kTile, false), sums = mma_shape<T>(dim16 * 16, true);
-      auto at = [&](uint32_t tile, int n) { return tile + (n % kStages) * kTileBytes; };
+      const uint32_t wide = mma_shape<T>(kWalk, false), sums = mma_shape<T>(dim16 * 16, true);
+      auto at = [&](uint32_t tile, int n) { return tile + (n % kStages) * F::kWalkBytes; };
       auto scores = [&](int n) {  // K Q^T
         if (!mbar_wait(smem_addr(&sh.q_full[n % kStages]), (n / kStages) & 1, gave_up)) return false;
         product_ss<4 * PANELS>(tmem, k_tile, at(q_tile, n), wide, dim16);
@@ -229,37 +244,23 @@ __device__ __forceinline__ void dkv_block(const Maps& maps, const AttnArgs& a, i
       };
       auto dprob = [&](int n) {  // V dout^T
         if (!mbar_wait(smem_addr(&sh.do_full[n % kStages]), (n / kStages) & 1, gave_up)) return false;
-        product_ss<4 * PANELS>(tmem + 128, v_tile, at(do_tile, n), wide, dim16);
+        product_ss<4 * PANELS>(dp_at, v_tile, at(do_tile, n), wide, dim16);
         mma_commit(smem_addr(&sh.dp_full));
         return true;
       };
-      auto ready = [&](uint64_t& bar, int n) {
-        if (!mbar_wait(smem_addr(&bar), n & 1, gave_up)) return false;
+      auto sum = [&](uint64_t& ready, uint32_t to, uint32_t left, uint32_t right, int n) {
+        if (!mbar_wait(smem_addr(&ready), n & 1, gave_up)) return false;
         tc_fence_after();
-        return true;
-      };
-      auto sum_dv = [&](int n) {
-        if (!ready(sh.p_ready, n)) return false;
-        for (int h = 0; h < 4; ++h) product_ts<2>(dv_at, p_at(h), at(do_tile, n), h, sums, n > 0 || h > 0);
-        if (kApart) mma_commit(smem_addr(&sh.dv_done));
-        return true;
-      };
-      auto sum_dk = [&](int n) {
-        if (!ready(sh.ds_ready, n)) return false;
-        for (int h = 0; h < 4; ++h) product_ts<2>(dk_at, ds_at(h), at(q_tile, n), h, sums, n > 0 || h > 0);
-        if (kApart) mma_commit(smem_addr(&sh.dk_done));
-        mma_commit(smem_addr(&sh.empty[n % kStages]));
+        for (int h = 0; h < F::kQuarters; ++h) product_ts<2>(to, left + h * 32, right, h, sums, n > 0 || h > 0);
         return true;
       };
       bool ok = mbar_wait(smem_addr(&sh.kv_full), 0, gave_up) && scores(0) && dprob(0);
       for (int n = 0; n < steps && ok; ++n) {
         const bool more = n + 1 < steps;
-        if constexpr (kApart) {
-          ok = (!more || (ready(sh.s_read, n) && scores(n + 1))) && sum_dv(n) &&
-               (!more || (ready(sh.dp_read, n) && dprob(n + 1))) && sum_dk(n);
-        } else {
-          ok = sum_dv(n) && (!more || scores(n + 1)) && sum_dk(n) && (!more || dprob(n + 1));
-        }
+        ok = sum(sh.p_ready, dv_at, tmem, at(do_tile, n), n) && (!more || scores(n + 1)) &&
+             sum(sh.ds_ready, dk_at, dp_at, at(q_tile, n), n);
+        if (ok) mma_commit(smem_addr(&sh.empty[n % kStages]));
+        if (ok && more) ok = dprob(n + 1);
       }
       if (ok) mma_commit(smem_addr(&sh.done));
     }
@@ -271,7 +272,7 @@ __device__ __forceinline__ void dkv_block(const Maps& maps, const AttnArgs& a, i
     const float c = a.scale * kLog2e;
     // threads 0..31 of a quarter fetch its queries' -lse in powers of two, the next 32 their -delta
     auto fetch = [&](int n) {
-      const int query = (unit.index + n % per) * kTile + quarter * 32 + (t & 31);
+      const int query = (first + n % per) * kWalk + quarter * 32 + (t & 31);
       if (t >= 64) return 0.f;
       if (query >= unit.length) return t < 32 ? -INFINITY : 0.f;  // p = 0 after the sequence's end
       const int64_t at = (int64_t)(kv_head * group + n / per) * a.tokens + unit.begin + query;
@@ -285,7 +286,8 @@ __device__ __forceinline__ void dkv_block(const Maps& maps, const AttnArgs& a, i
     bool ok = true;
     for (int n = 0; n < steps; ++n) {
       const float next = n + 1 < steps ? fetch(n + 1) : 0.f;
-      const bool diagonal = n % per == 0;
+      const int from = n % per * kWalk;  // the tile's first query, counted from the first key
+      const bool diagonal = from < kTile;
       if (!(ok = mbar_wait(smem_addr(&sh.s_full), n & 1, gave_up))) break;
       tc_fence_after();
       float p[32], d[32];
@@ -293,35 +295,20 @@ __device__ __forceinline__ void dkv_block(const Maps& maps, const AttnArgs& a, i
       tmem_load32(s_at, p);
       tmem_wait_load();
       tmem_loaded(p);
-      if constexpr (kApart) {
-        warp_arrive(smem_addr(&sh.s_read));
-      }
       const float* lse = sh.lse[n & 1][quarter];
       probabilities<T>(p, packed, c, [&](int x) { return Two{*reinterpret_cast<const uint64_t*>(lse + x)}; }, diagonal,
-                       [&](int x) { return quarter * 32 + x >= row; });
-      if (kApart && n > 0) {
-        // the last sums have read what these replace
-        if (!(ok = mbar_wait(smem_addr(&sh.dv_done), (n - 1) & 1, gave_up))) break;
-        tc_fence_after();
-      }
-      tmem_store16(lane0 + p_at(quarter), packed);
+                       [&](int x) { return from + quarter * 32 + x >= row; });
+      tmem_store16(s_at, packed);
       tmem_wait_store();
       warp_arrive(smem_addr(&sh.p_ready));
       if (!(ok = mbar_wait(smem_addr(&sh.dp_full), n & 1, gave_up))) break;
       tc_fence_after();
-      tmem_load32(s_at + 128, d);
+      tmem_load32(s_at + kWalk, d);
       tmem_wait_load();
       tmem_loaded(d);
-      if constexpr (kApart) {
-        warp_arrive(smem_addr(&sh.dp_read));
-      }
       const float* delta = sh.delta[n & 1][quarter];
       score_gradients<T>(p, d, packed, [&](int x) { return Two{*reinterpret_cast<const uint64_t*>(delta + x)}; }, diagonal);
-      if (kApart && n > 0) {
-        if (!(ok = mbar_wait(smem_addr(&sh.dk_done), (n - 1) & 1, gave_up))) break;
-        tc_fence_after();
-      }
-      tmem_store16(lane0 + ds_at(quarter), packed);
+      tmem_store16(s_at + kWalk, packed);
       tmem_wait_store();
       warp_arrive(smem_addr(&sh.ds_ready));
       put(n + 1, next);
@@ -333,11 +320,11 @@ __device__ __forceinline__ void dkv_block(const Maps& maps, const AttnArgs& a, i
       const AttnTensor& to = is_dk ? a.dk : a.dv;
       T* out = static_cast<T*>(const_cast<void*>(to.ptr)) + (int64_t)(unit.begin + key) * to.token_stride +
                kv_head * to.head_stride;
-      for (int x = quarter >> 1; x < dim16; x += 2)
+      for (int x = quarter >> 1; x < dim16; x += F::kQuarters / 2)
         write16<T>(lane0 + (is_dk ? dk_at : dv_at), out, x * 16, a.dim, is_dk ? a.scale : 1.f, key < unit.length);
     }
   }
-  leave(&sh.gave_up, warp, tmem);
+  leave<PANELS>(&sh.gave_up, warp, tmem);
 }
 
 // ---- dq ---------------------------------------------------------------------------
@@ -354,6 +341,8 @@ struct SharedQ {
 
 template <class T, int PANELS>
 __device__ __forceinline__ void dq_block(const Maps& maps, const AttnArgs& a, int block, uint8_t* tiles, SharedQ& sh) {
+  using F = Form<PANELS>;
+  constexpr int kWalk = F::kWalk;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int head = block % a.heads;
   if (warp == 0) {
@@ -362,7 +351,7 @@ __device__ __forceinline__ void dq_block(const Maps& maps, const AttnArgs& a, in
       sh.unit = u;
       sh.gave_up = 0;
     }
-  } else if (warp == kLoader && lane == 0) {
+  } else if (warp == F::kLoader && lane == 0) {
     uint64_t* const one[] = {&sh.q_full, &sh.s_full, &sh.dp_full[0], &sh.dp_full[1], &sh.done, &sh.own};
     for (uint64_t* b : one) mbar_init(smem_addr(b), 1);
     for (int i = 0; i < kKStages; ++i) {
@@ -373,64 +362,62 @@ __device__ __forceinline__ void dq_block(const Maps& maps, const AttnArgs& a, in
       mbar_init(smem_addr(&sh.v_full[i]), 1);
       mbar_init(smem_addr(&sh.v_empty[i]), 1);
     }
-    mbar_init(smem_addr(&sh.s_read), kWorkers / 32);
-    mbar_init(smem_addr(&sh.ds_ready), kWorkers / 32);
+    mbar_init(smem_addr(&sh.s_read), F::kWorkers / 32);
+    mbar_init(smem_addr(&sh.ds_ready), F::kWorkers / 32);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncthreads();
   if (sh.unit.count == 0) return;
   const SeqUnit unit = sh.unit;
 
-  constexpr uint32_t kTileBytes = PANELS * kPanelBytes;
-  const uint32_t q_tile = smem_addr(tiles), do_tile = q_tile + kTileBytes, k_tile = do_tile + kTileBytes,
-                 v_tile = k_tile + kKStages * kTileBytes;
+  const uint32_t q_tile = smem_addr(tiles), do_tile = q_tile + F::kKeptBytes, k_tile = do_tile + F::kKeptBytes,
+                 v_tile = k_tile + kKStages * F::kWalkBytes;
   volatile int* gave_up = &sh.gave_up;
-  if (warp == kIssuer) tmem_alloc(smem_addr(&sh.tmem), 512);
+  if (warp == F::kIssuer) tmem_alloc(smem_addr(&sh.tmem), F::kColumns);
+  const int query = unit.index * kTile;
+  const int steps = min(query + kTile, unit.length + kWalk - 1) / kWalk;  // tiles of keys that the queries see
+  const int dim16 = (a.dim + 15) / 16;
+  if (warp == F::kLoader && lane == 0) {
+    const uint32_t bar = smem_addr(&sh.q_full);
+    mbar_expect(bar, 2 * F::kKeptBytes);
+    load_kept<PANELS>(&maps.q, q_tile, head, unit.begin + query, bar);
+    load_kept<PANELS>(&maps.dout, do_tile, head, unit.begin + query, bar);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  // Tensor memory: scores 0, dout v^T 128 and 256 (by turns), dq 384.  The
-  // next tile's scores and dout v^T are under way while this one's ds is made.
-  const uint32_t tmem = sh.tmem;
+  // Tensor memory: scores, dout v^T (in two places by turns), dq.  The next
+  // tile's scores and dout v^T are under way while this one's ds is made.
+  const uint32_t tmem = sh.tmem, dq_at = tmem + 3 * kWalk;
+  auto dp_at = [&](int n) { return tmem + kWalk * (1 + (n & 1)); };
 
-  const int steps = unit.index + 1, query = unit.index * kTile;
-  const int dim16 = (a.dim + 15) / 16;
-
-  if (warp == kLoader) {
+  if (warp == F::kLoader) {
     const int kv_head = head / (a.heads / a.kv_heads);
-    if (lane == 0) {
-      const uint32_t bar = smem_addr(&sh.q_full);
-      mbar_expect(bar, 2 * kTileBytes);
-      for (int p = 0; p < PANELS; ++p) {
-        tma_load(q_tile + p * kPanelBytes, &maps.q, p * 64, head, unit.begin + query, bar);
-        tma_load(do_tile + p * kPanelBytes, &maps.dout, p * 64, head, unit.begin + query, bar);
-      }
-    }
     uint32_t own_parity = 0;
     for (int n = 0; n < steps; ++n) {
-      const int ks = n % kKStages, vs = n % kVStages, key = n * kTile;
+      const int ks = n % kKStages, vs = n % kVStages, key = n * kWalk;
       if (n >= kKStages && !mbar_wait(smem_addr(&sh.k_empty[ks]), (n / kKStages - 1) & 1, gave_up)) break;
       // dq sums over the rows of K: those of another sequence are cleared
-      if (!load_tile(&maps.k, k_tile + ks * kTileBytes, PANELS, kv_head, unit.begin + key, unit.length - key,
-                     smem_addr(&sh.k_full[ks]), smem_addr(&sh.own), &own_parity, gave_up))
+      if (!load_tile<PANELS, kWalk>(&maps.k, k_tile + ks * F::kWalkBytes, kv_head, unit.begin + key, unit.length - key,
+                                    smem_addr(&sh.k_full[ks]), smem_addr(&sh.own), &own_parity, gave_up))
         break;
       if (n >= kVStages && !mbar_wait(smem_addr(&sh.v_empty[vs]), (n / kVStages - 1) & 1, gave_up)) break;
-      if (!load_tile(&maps.v, v_tile + vs * kTileBytes, PANELS, kv_head, unit.begin + key, kTile,
-                     smem_addr(&sh.v_full[vs]), smem_addr(&sh.own), &own_parity, gave_up))
+      if (!load_tile<PANELS, kWalk>(&maps.v, v_tile + vs * F::kWalkBytes, kv_head, unit.begin + key, kWalk,
+                                    smem_addr(&sh.v_full[vs]), smem_addr(&sh.own), &own_parity, gave_up))
         break;
     }
-  } else if (warp == kIssuer) {
+  } else if (warp == F::kIssuer) {
     if (elect_one()) {
-      const uint32_t wide = mma_shape<T>(kTile, false), sums = mma_shape<T>(dim16 * 16, true);
+      const uint32_t wide = mma_shape<T>(kWalk, false), sums = mma_shape<T>(dim16 * 16, true);
       auto scores = [&](int n) {  // Q K^T
         if (!mbar_wait(smem_addr(&sh.k_full[n % kKStages]), (n / kKStages) & 1, gave_up)) return false;
-        product_ss<4 * PANELS>(tmem, q_tile, k_tile + (n % kKStages) * kTileBytes, wide, dim16);
+        product_ss<4 * PANELS>(tmem, q_tile, k_tile + (n % kKStages) * F::kWalkBytes, wide, dim16);
         mma_commit(smem_addr(&sh.s_full));
         return true;
       };
       auto dprob = [&](int n) {  // dout V^T
         if (!mbar_wait(smem_addr(&sh.v_full[n % kVStages]), (n / kVStages) & 1, gave_up)) return false;
-        product_ss<4 * PANELS>(tmem + 128 + (n & 1) * 128, do_tile, v_tile + (n % kVStages) * kTileBytes, wide, dim16);
+        product_ss<4 * PANELS>(dp_at(n), do_tile, v_tile + (n % kVStages) * F::kWalkBytes, wide, dim16);
         mma_commit(smem_addr(&sh.dp_full[n & 1]));
         mma_commit(smem_addr(&sh.v_empty[n % kVStages]));
         return true;
@@ -444,9 +431,8 @@ __device__ __forceinline__ void dq_block(const Maps& maps, const AttnArgs& a, in
         }
         if (!(ok = mbar_wait(smem_addr(&sh.ds_ready), n & 1, gave_up))) break;
         tc_fence_after();
-        for (int h = 0; h < 4; ++h)
-          product_ts<2>(tmem + 384, tmem + 128 + (n & 1) * 128 + h * 32, k_tile + (n % kKStages) * kTileBytes, h, sums,
-                        n > 0 || h > 0);
+        for (int h = 0; h < F::kQuarters; ++h)
+          product_ts<2>(dq_at, dp_at(n) + h * 32, k_tile + (n % kKStages) * F::kWalkBytes, h, sums, n > 0 || h > 0);
         mma_commit(smem_addr(&sh.k_empty[n % kKStages]));
       }
       if (ok) mma_commit(smem_addr(&sh.done));
@@ -455,7 +441,7 @@ __device__ __forceinline__ void dq_block(const Maps& maps, const AttnArgs& a, in
   } else {
     // thread: query row, keys [32 quarter, 32 quarter + 32) of each tile
     const int quarter = warp >> 2, row = (warp & 3) * 32 + lane;
-    const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
+    const uint32_t lane0 = (uint32_t)(warp & 3) << 21;
     const float c = a.scale * kLog2e;
     const bool valid = query + row < unit.length;
     const int64_t at = (int64_t)head * a.tokens + unit.begin + query + row;
@@ -463,24 +449,24 @@ __device__ __forceinline__ void dq_block(const Maps& maps, const AttnArgs& a, in
     const Two lse = two(l, l), delta = two(dl, dl);
     bool ok = true;
     for (int n = 0; n < steps; ++n) {
-      const bool diagonal = n == steps - 1;
+      const bool diagonal = (n + 1) * kWalk > query;
       if (!(ok = mbar_wait(smem_addr(&sh.s_full), n & 1, gave_up))) break;
       tc_fence_after();
       float p[32], d[32];
       uint32_t packed[16];
-      tmem_load32(lanes + quarter * 32, p);
+      tmem_load32(lane0 + tmem + quarter * 32, p);
       tmem_wait_load();
       tmem_loaded(p);
       warp_arrive(smem_addr(&sh.s_read));
-      probabilities<T>(p, packed, c, [&](int) { return lse; }, diagonal, [&](int x) { return quarter * 32 + x <= row; });
-      const uint32_t dp_at = lanes + 128 + (n & 1) * 128 + quarter * 32;
+      probabilities<T>(p, packed, c, [&](int) { return lse; }, diagonal, [&](int x) { return n * kWalk + quarter * 32 + x <= query + row; });
+      const uint32_t dp = lane0 + dp_at(n) + quarter * 32;
       if (!(ok = mbar_wait(smem_addr(&sh.dp_full[n & 1]), (n >> 1) & 1, gave_up))) break;
       tc_fence_after();
-      tmem_load32(dp_at, d);
+      tmem_load32(dp, d);
       tmem_wait_load();
       tmem_loaded(d);
       score_gradients<T>(p, d, packed, [&](int) { return delta; }, diagonal);
-      tmem_store16(dp_at, packed);
+      tmem_store16(dp, packed);
       tmem_wait_store();
       warp_arrive(smem_addr(&sh.ds_ready));
     }
@@ -488,10 +474,10 @@ __device__ __forceinline__ void dq_block(const Maps& maps, const AttnArgs& a, in
       tc_fence_after();
       T* out = static_cast<T*>(const_cast<void*>(a.dq.ptr)) + (int64_t)(unit.begin + query + row) * a.dq.token_stride +
                head * a.dq.head_stride;
-      for (int x = quarter; x < dim16; x += 4) write16<T>(lanes + 384, out, x * 16, a.dim, a.scale, valid);
+      for (int x = quarter; x < dim16; x += F::kQuarters) write16<T>(lane0 + dq_at, out, x * 16, a.dim, a.scale, valid);
     }
   }
-  leave(&sh.gave_up, warp, tmem);
+  leave<PANELS>(&sh.gave_up, warp, tmem);
 }
 
 // ---- both ---------------------------------------------------------------------------
@@ -505,7 +491,7 @@ union Shared {
 // One launch, so that the second kind's blocks fill the first's last wave; the
 // first `kv_blocks` blocks make dk and dv.
 template <class T, int PANELS>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Form<PANELS>::kThreads, Form<PANELS>::kBlocks)
     attention_backward_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a, int kv_blocks) {
   extern __shared__ __align__(1024) uint8_t tiles[];
   __shared__ Shared sh;
@@ -518,16 +504,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <class T, int PANELS>
 cudaError_t run(int dtype, const AttnArgs& a, cudaStream_t s) {
   static std::atomic<unsigned long long> opened[256];
-  constexpr int tiles = std::max(2 + 2 * query_stages(PANELS), 2 + kKStages + kVStages);
-  constexpr int smem = tiles * PANELS * (int)kPanelBytes;
+  using F = Form<PANELS>;
+  constexpr int smem = 2 * F::kKeptBytes + std::max(2 * F::kStages, kKStages + kVStages) * F::kWalkBytes;
   auto* kernel = attention_backward_kernel<T, PANELS>;
   cudaError_t e = open_kernel((const void*)kernel, smem, false, opened);
   if (e != cudaSuccess) return e;
   Maps maps;
-  if (!make_tensor_map(&maps.q, dtype, a.q, a.tokens, a.heads, a.dim) ||
-      !make_tensor_map(&maps.k, dtype, a.k, a.tokens, a.kv_heads, a.dim) ||
-      !make_tensor_map(&maps.v, dtype, a.v, a.tokens, a.kv_heads, a.dim) ||
-      !make_tensor_map(&maps.dout, dtype, a.dout, a.tokens, a.heads, a.dim))
+  if (!make_tensor_map(&maps.q, dtype, a.q, a.tokens, a.heads, a.dim, F::kWalk) ||
+      !make_tensor_map(&maps.k, dtype, a.k, a.tokens, a.kv_heads, a.dim, F::kWalk) ||
+      !make_tensor_map(&maps.v, dtype, a.v, a.tokens, a.kv_heads, a.dim, F::kWalk) ||
+      !make_tensor_map(&maps.dout, dtype, a.dout, a.tokens, a.heads, a.dim, F::kWalk))
     return cudaErrorInvalidValue;
   constexpr int kLanes = PANELS * 8, kRows = 256 / kLanes;
   attention_delta_kernel<T, kLanes><<<(unsigned)((a.tokens * a.heads + kRows - 1) / kRows), 256, 0, s>>>(a);
@@ -538,7 +524,7 @@ cudaError_t run(int dtype, const AttnArgs& a, cudaStream_t s) {
   const int kv_blocks = (int)(most * a.kv_heads);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(kv_blocks + most * a.heads));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(F::kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute at;

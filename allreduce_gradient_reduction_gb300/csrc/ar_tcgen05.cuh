@@ -93,32 +93,30 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, i
       ::"r"(dst), "l"(map), "r"(column), "r"(head), "r"(token), "r"(bar)
       : "memory");
 }
-__device__ __forceinline__ void tma_prefetch(const CUtensorMap* map) {
-  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
-}
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// One warp loads `panels` panels of a tile whose first `rows` rows belong to
-// the sequence.  The rows after them are another sequence's: they are
-// overwritten with zeros before the tile is announced on `full`, so that what
-// they hold (an infinity, a NaN) cannot reach a sum through a zero weight.
-// `own` is a barrier of this warp's alone for that case.
-__device__ __forceinline__ bool load_tile(const CUtensorMap* map, uint32_t dst, int panels, int head, int token,
-                                          int rows, uint32_t full, uint32_t own, uint32_t* own_parity,
-                                          volatile int* gave_up) {
+// One warp loads the panels of a tile of ROWS rows, of which the first `rows`
+// belong to the sequence.  The rows after them are another sequence's: they
+// are overwritten with zeros before the tile is announced on `full`, so that
+// what they hold (an infinity, a NaN) cannot reach a sum through a zero
+// weight.  `own` is a barrier of this warp's alone for that case.
+template <int PANELS, int ROWS>
+__device__ __forceinline__ bool load_tile(const CUtensorMap* map, uint32_t dst, int head, int token, int rows,
+                                          uint32_t full, uint32_t own, uint32_t* own_parity, volatile int* gave_up) {
+  constexpr uint32_t kBytes = ROWS * 128;
   const int lane = threadIdx.x & 31;
-  const bool cut = rows < kTile;
+  const bool cut = rows < ROWS;
   if (lane == 0) {
     const uint32_t bar = cut ? own : full;
-    mbar_expect(bar, panels * kPanelBytes);
-    for (int p = 0; p < panels; ++p) tma_load(dst + p * kPanelBytes, map, p * 64, head, token, bar);
+    mbar_expect(bar, PANELS * kBytes);
+    for (int p = 0; p < PANELS; ++p) tma_load(dst + p * kBytes, map, p * 64, head, token, bar);
   }
   if (!cut) return true;
   if (!mbar_wait(own, *own_parity, gave_up)) return false;
   *own_parity ^= 1;
-  for (int p = 0; p < panels; ++p)
-    for (uint32_t b = rows * 128 + lane * 16; b < kPanelBytes; b += 512)
-      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + p * kPanelBytes + b), "r"(0) : "memory");
+  for (int p = 0; p < PANELS; ++p)
+    for (uint32_t b = rows * 128 + lane * 16; b < kBytes; b += 512)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + p * kBytes + b), "r"(0) : "memory");
   fence_async_shared();
   __syncwarp();
   if (lane == 0) mbar_arrive(full);
@@ -337,8 +335,8 @@ __device__ __forceinline__ SeqUnit find_unit(const int32_t* cu_seqlens, int seqs
   return SeqUnit{0, 0, 0, 0};
 }
 
-// Host: the tensor map of a [tokens][heads][dim] operand, one panel to a box.
-// False if the driver refuses it.
-bool make_tensor_map(CUtensorMap* map, int dtype, const AttnTensor& t, int64_t tokens, int heads, int dim);
+// Host: the tensor map of a [tokens][heads][dim] operand, `rows` rows of one
+// panel to a box.  False if the driver refuses it.
+bool make_tensor_map(CUtensorMap* map, int dtype, const AttnTensor& t, int64_t tokens, int heads, int dim, int rows);
 
 }  // namespace ar
