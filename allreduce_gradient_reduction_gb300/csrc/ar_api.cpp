@@ -1128,8 +1128,10 @@ int ar_device_status(ar_stream_t stream, int* status) {
     int dev = 0;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return cuda_fail(e);
     *status = AR_OK;
-    // a wait inside an attention kernel that ran out is reported first
-    if ((e = ar::attention_take_status(status)) != cudaSuccess) return cuda_fail(e);
+    // waits inside kernels of one GPU's work that ran out are reported first
+    for (auto take : {ar::layer_norm_take_status, ar::distill_take_status, ar::attention_take_status,
+                      ar::attention_backward_take_status})
+      if ((e = take(status)) != cudaSuccess) return cuda_fail(e);
     if (*status != AR_OK) return AR_OK;
     ar::SyncBlock* sb = nullptr;
     unsigned long long ctx = 0;

@@ -376,6 +376,15 @@ constexpr int kMostPieces = 19;
 constexpr int kStreamPieces = 7;  // places where a row is not kept: 84 KB, two blocks to a multiprocessor
 constexpr int kRingMaxShared = 224 * 1024;
 
+// The loop of a wait that is not over at the first look, out of line (8192 x
+// 30000 f16, forward: 113.6 us with it in line, 108.2 us so).
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* gave_up) {
+  return ring_wait(bar, parity, gave_up);
+}
+__device__ __forceinline__ bool wait(uint64_t* bar, int parity, volatile int* gave_up) {
+  return ring_try(smem_at(bar), parity) || wait_on(smem_at(bar), parity, gave_up);
+}
+
 __device__ __forceinline__ void workers_barrier() { named_barrier(1, kWorkers); }
 __device__ __forceinline__ void arrive_on(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_at(bar)) : "memory");
@@ -398,6 +407,7 @@ __global__ void __launch_bounds__(kRingThreads, 2) distill_ring_kernel(const Dis
   __shared__ Stat scratch[2][32];
   __shared__ Divergence divergence[kListWarps];
   __shared__ __align__(8) uint64_t filled[kMostPieces], empty[kMostPieces], list_made[kListWarps], list_used[kListWarps];
+  __shared__ int gave_up;
 
   const int t = threadIdx.x, lane = t & 31, vocab = (int)a.vocab, top = a.top;
   const float tau = a.temperature, c = kLog2e / tau, inv_tau = 1.f / tau;
@@ -408,6 +418,7 @@ __global__ void __launch_bounds__(kRingThreads, 2) distill_ring_kernel(const Dis
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_at(bar)), "r"(count) : "memory");
   };
   if (t == 0) {
+    gave_up = 0;
     for (int i = 0; i < places; ++i) {
       init(&filled[i], 1);
       init(&empty[i], kWorkers / 32);
@@ -430,7 +441,7 @@ __global__ void __launch_bounds__(kRingThreads, 2) distill_ring_kernel(const Dis
         const int bytes = (int)covering(z, vocab * (int)sizeof(T));
         for (int pass = 0; pass < (twice && !keep ? 2 : 1); ++pass)
           for (int i = 0; i < pieces; ++i, at.next(places)) {
-            if (at.round > 0) ring_wait(smem_at(&empty[at.slot]), (at.round - 1) & 1);
+            if (at.round > 0 && !wait(&empty[at.slot], (at.round - 1) & 1, &gave_up)) return;
             // rows that begin at other places in their first word may have a piece less
             const int n = min(kPieceBytes, bytes - i * kPieceBytes);
             const uint32_t bar = smem_at(&filled[at.slot]);
@@ -446,7 +457,7 @@ __global__ void __launch_bounds__(kRingThreads, 2) distill_ring_kernel(const Dis
     const int i = (t - kWorkers) >> 5;
     int round = 0;
     for (int64_t row = blockIdx.x + (int64_t)i * gridDim.x; row < a.rows; row += (int64_t)kListWarps * gridDim.x, ++round) {
-      if (round > 0) ring_wait(smem_at(&list_used[i]), (round - 1) & 1);
+      if (round > 0) wait(&list_used[i], (round - 1) & 1, &gave_up);
       const Divergence d = make_list<T, V>(a, row, logits + row * a.logits_stride, vocab, inv_tau, a.dlogits != nullptr, list_of(i));
       if (lane == 0) divergence[i] = d;
       __syncwarp();
@@ -485,7 +496,7 @@ __global__ void __launch_bounds__(kRingThreads, 2) distill_ring_kernel(const Dis
       Stat st{-INFINITY, 0.f};
       Place p1 = at;
       for (int i = 0; i < pieces; ++i, p1.next(places)) {
-        ring_wait(smem_at(&filled[p1.slot]), p1.round & 1);
+        wait(&filled[p1.slot], p1.round & 1, &gave_up);
         const uint8_t* piece = buffer + p1.slot * kPieceBytes;
         const int v = i * kPieceVectors + t;
         if (v + kWorkers < vecs) {
@@ -505,7 +516,7 @@ __global__ void __launch_bounds__(kRingThreads, 2) distill_ring_kernel(const Dis
       st = warp_join(st, c);
       lse = st.m / tau + logf(st.s);
     }
-    ring_wait(smem_at(&list_made[list_at.slot]), list_at.round & 1);
+    wait(&list_made[list_at.slot], list_at.round & 1, &gave_up);
     const Divergence d = divergence[list_at.slot];
     if (!BACKWARD && t == 0) {
       a.loss[row] = d.some ? (d.value + lse) * tau * tau : 0.f;
@@ -522,7 +533,7 @@ __global__ void __launch_bounds__(kRingThreads, 2) distill_ring_kernel(const Dis
     T* dz = static_cast<T*>(a.dlogits) + row * a.dlogits_stride;
     const bool same = (((uintptr_t)dz ^ (uintptr_t)z) & 15) == 0;
     for (int i = 0; i < pieces; ++i, at.next(places)) {
-      if (BACKWARD || !keep) ring_wait(smem_at(&filled[at.slot]), at.round & 1);
+      if (BACKWARD || !keep) wait(&filled[at.slot], at.round & 1, &gave_up);
       const uint8_t* piece = buffer + at.slot * kPieceBytes;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
@@ -596,5 +607,7 @@ cudaError_t launch_distill(int dtype, int vdtype, bool backward, const DistillAr
     return backward ? run<T, T, true>(a, s) : run<T, T, false>(a, s);
   });
 }
+
+cudaError_t distill_take_status(int* status) { return take_status(status); }
 
 }  // namespace ar

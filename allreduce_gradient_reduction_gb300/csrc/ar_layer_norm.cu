@@ -265,8 +265,9 @@ __device__ __forceinline__ void param_pairs(const P* p, Two (&out)[N]) {
 
 constexpr int kRing = 4;  // most rows of a group in flight
 
-__device__ __forceinline__ void open_ring(uint64_t* full) {
+__device__ __forceinline__ void open_ring(uint64_t* full, int* gave_up) {
   if (threadIdx.x == 0) {
+    *gave_up = 0;
     for (int i = 0; i < kRing; ++i)
       asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_at(full + i)) : "memory");
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -292,7 +293,6 @@ __device__ __forceinline__ float2 group_sum2(float2 v, float2 (*scratch)[16], in
   return make_float2(warp_sum(v.x), warp_sum(v.y));
 }
 
-
 // Registers of the forward kernel, which holds a thread's columns widened.
 __host__ __device__ constexpr int forward_registers(int columns) { return columns <= 16 ? 64 : columns <= 24 ? 80 : 96; }
 // Registers of the backward kernel: two sums for each of a thread's columns,
@@ -309,6 +309,7 @@ __global__ void __maxnreg__(KEEP ? 88 : forward_registers(NV * (16 / sizeof(T)))
   extern __shared__ __align__(16) uint8_t rows[];
   __shared__ float scratch[kGroups][2][32];
   __shared__ __align__(8) uint64_t filled[kGroups][kRing];
+  __shared__ int gave_up;
   const int cols = (int)a.cols, g = blockDim.x, t = threadIdx.x;
   const int64_t step = (int64_t)gridDim.x * blockDim.y;
   const T* x = static_cast<const T*>(a.x);
@@ -326,7 +327,7 @@ __global__ void __maxnreg__(KEEP ? 88 : forward_registers(NV * (16 / sizeof(T)))
     ring_expect(bar, covering(from, cols * (int)sizeof(T)));
     ring_copy(smem_at(mine + stage * slot), from, cols * (int)sizeof(T), bar);
   };
-  open_ring(bars);
+  open_ring(bars, &gave_up);
   int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   if (t == 0)
     for (int i = 0; i < stages && row + i * step < a.rows; ++i) issue(row + i * step, i);
@@ -345,7 +346,7 @@ __global__ void __maxnreg__(KEEP ? 88 : forward_registers(NV * (16 / sizeof(T)))
   }
   int stage = 0, parity = 0;
   for (; row < a.rows; row += step) {
-    ring_wait(smem_at(bars + stage), parity);
+    const bool came = ring_wait(smem_at(bars + stage), parity, &gave_up);
     const uint8_t* from = mine + stage * slot + v0 * 16;
     Two e[NV][N];  // the elements, then their distance from the mean
     Two acc[2] = {two(0.f, 0.f), two(0.f, 0.f)};
@@ -368,7 +369,7 @@ __global__ void __maxnreg__(KEEP ? 88 : forward_registers(NV * (16 / sizeof(T)))
     split(add2(acc[0], acc[1]), lo, hi);
     const float mean = group_sum(lo + hi, scratch[threadIdx.y], 0) * inv;
     if (g == 32) __syncwarp();
-    if (t == 0 && row + stages * step < a.rows) issue(row + stages * step, stage);  // the group has read the slot
+    if (t == 0 && came && row + stages * step < a.rows) issue(row + stages * step, stage);  // the group has read the slot
     const Two minus = two(-mean, -mean);
     acc[0] = acc[1] = two(0.f, 0.f);
     auto square = [&](int k) {
@@ -431,6 +432,7 @@ __global__ void __maxnreg__(backward_registers(NV * (16 / sizeof(T))))
   extern __shared__ __align__(16) uint8_t rows[];
   __shared__ float2 scratch[kGroups][2][16];
   __shared__ __align__(8) uint64_t filled[kGroups][kRing];
+  __shared__ int gave_up;
   const int cols = (int)a.cols, t = threadIdx.x;
   const int64_t step = (int64_t)gridDim.x * blockDim.y;
   const T* x = static_cast<const T*>(a.x);
@@ -449,7 +451,7 @@ __global__ void __maxnreg__(backward_registers(NV * (16 / sizeof(T))))
     ring_copy(to, fx, bytes, bar);
     ring_copy(to + slot, fd, bytes, bar);
   };
-  open_ring(bars);
+  open_ring(bars, &gave_up);
   int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   if (t == 0)
     for (int i = 0; i < stages && row + i * step < a.rows; ++i) issue(row + i * step, i);
@@ -465,7 +467,7 @@ __global__ void __maxnreg__(backward_registers(NV * (16 / sizeof(T))))
   for (int turn = 0; row < a.rows; row += step, turn ^= 1) {
     float mean_n = 0.f, rstd_n = 0.f;
     if (row + step < a.rows) mean_n = a.mean[row + step], rstd_n = a.rstd[row + step];
-    ring_wait(smem_at(bars + stage), parity);
+    const bool came = ring_wait(smem_at(bars + stage), parity, &gave_up);
     const Two minus = two(-mean, -mean), scale = two(rstd, rstd);
     const uint8_t* from = mine + stage * 2 * slot + v0 * 16;
     Two xh[NV][N], gw[NV][N];
@@ -498,7 +500,7 @@ __global__ void __maxnreg__(backward_registers(NV * (16 / sizeof(T))))
     split(s1, a1, b1);
     split(s2, a2, b2);
     const float2 s = group_sum2(make_float2(a1 + b1, a2 + b2), scratch[threadIdx.y], turn);
-    if (t == 0 && row + stages * step < a.rows) issue(row + stages * step, stage);  // the group has read the slot
+    if (t == 0 && came && row + stages * step < a.rows) issue(row + stages * step, stage);  // the group has read the slot
     // dx = rstd gw - rstd s1 / C - xh rstd s2 / C
     const float m1 = -rstd * (s.x * inv), m2 = -rstd * (s.y * inv);
     const Two m1s = two(m1, m1), m2s = two(m2, m2);
@@ -578,6 +580,7 @@ __global__ void __maxnreg__(NE <= 8 ? 56 : 80)
   extern __shared__ __align__(16) uint8_t rows[];
   __shared__ float scratch[kGroups][2][32];
   __shared__ __align__(8) uint64_t filled[kGroups][kRing];
+  __shared__ int gave_up;
   const int cols = (int)a.cols, g = blockDim.x, t = threadIdx.x;
   const int64_t step = (int64_t)gridDim.x * blockDim.y;
   const T* x = static_cast<const T*>(a.x);
@@ -590,7 +593,7 @@ __global__ void __maxnreg__(NE <= 8 ? 56 : 80)
     ring_expect(bar, covering(from, cols * (int)sizeof(T)));
     ring_copy(smem_at(mine + stage * slot), from, cols * (int)sizeof(T), bar);
   };
-  open_ring(bars);
+  open_ring(bars, &gave_up);
   int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   if (t == 0)
     for (int i = 0; i < stages && row + i * step < a.rows; ++i) issue(row + i * step, i);
@@ -602,7 +605,7 @@ __global__ void __maxnreg__(NE <= 8 ? 56 : 80)
 
   int stage = 0, parity = 0;
   for (; row < a.rows; row += step) {
-    ring_wait(smem_at(bars + stage), parity);
+    const bool came = ring_wait(smem_at(bars + stage), parity, &gave_up);
     const T* from = reinterpret_cast<const T*>(mine + stage * slot + ((uintptr_t)(x + row * a.x_stride) & 15)) + c0;
     Two e[N], acc[2] = {two(0.f, 0.f), two(0.f, 0.f)};
     if (full) {
@@ -618,7 +621,7 @@ __global__ void __maxnreg__(NE <= 8 ? 56 : 80)
     split(add2(acc[0], acc[1]), lo, hi);
     const float mean = group_sum(lo + hi, scratch[threadIdx.y], 0) * inv;
     if (g == 32) __syncwarp();
-    if (t == 0 && row + stages * step < a.rows) issue(row + stages * step, stage);  // the group has read the slot
+    if (t == 0 && came && row + stages * step < a.rows) issue(row + stages * step, stage);  // the group has read the slot
     const Two minus = two(-mean, -mean);
     acc[0] = acc[1] = two(0.f, 0.f);
 #pragma unroll
@@ -656,6 +659,7 @@ __global__ void __maxnreg__(backward_registers(NE))
   extern __shared__ __align__(16) uint8_t rows[];
   __shared__ float2 scratch[kGroups][2][16];
   __shared__ __align__(8) uint64_t filled[kGroups][kRing];
+  __shared__ int gave_up;
   const int cols = (int)a.cols, t = threadIdx.x;
   const int64_t step = (int64_t)gridDim.x * blockDim.y;
   const T* x = static_cast<const T*>(a.x);
@@ -671,7 +675,7 @@ __global__ void __maxnreg__(backward_registers(NE))
     ring_copy(to, fx, bytes, bar);
     ring_copy(to + slot, fd, bytes, bar);
   };
-  open_ring(bars);
+  open_ring(bars, &gave_up);
   int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   if (t == 0)
     for (int i = 0; i < stages && row + i * step < a.rows; ++i) issue(row + i * step, i);
@@ -687,7 +691,7 @@ __global__ void __maxnreg__(backward_registers(NE))
   for (int turn = 0; row < a.rows; row += step, turn ^= 1) {
     float mean_n = 0.f, rstd_n = 0.f;
     if (row + step < a.rows) mean_n = a.mean[row + step], rstd_n = a.rstd[row + step];
-    ring_wait(smem_at(bars + stage), parity);
+    const bool came = ring_wait(smem_at(bars + stage), parity, &gave_up);
     const Two minus = two(-mean, -mean), scale = two(rstd, rstd);
     const uint8_t* from = mine + stage * 2 * slot;
     const T* xs = reinterpret_cast<const T*>(from + ((uintptr_t)(x + row * a.x_stride) & 15)) + c0;
@@ -713,7 +717,7 @@ __global__ void __maxnreg__(backward_registers(NE))
     split(s1, a1, b1);
     split(s2, a2, b2);
     const float2 s = group_sum2(make_float2(a1 + b1, a2 + b2), scratch[threadIdx.y], turn);
-    if (t == 0 && row + stages * step < a.rows) issue(row + stages * step, stage);  // the group has read the slot
+    if (t == 0 && came && row + stages * step < a.rows) issue(row + stages * step, stage);  // the group has read the slot
     const float m1 = -rstd * (s.x * inv), m2 = -rstd * (s.y * inv);
     const Two m1s = two(m1, m1), m2s = two(m2, m2);
     T* dx = static_cast<T*>(a.dx) + row * a.dx_stride + c0;
@@ -912,8 +916,8 @@ bool forward_ring(const LayerNormArgs& a, cudaStream_t s, cudaError_t* e) {
   static const int counts[5] = {1, A, 2 * A, 3 * A, 4 * A};
   if constexpr (sizeof(P) == 4 && sizeof(T) == 2) {
     if (a.cols >= 2048) {
-      static const int two[1] = {2 * A};
-      const Deal d = deal(a.cols / VW, two, 512);
+      static const int kept[1] = {2 * A};
+      const Deal d = deal(a.cols / VW, kept, 512);
       if (d.nv) {
         *e = run_ring<T, P, 2 * A, true>(a, d.threads, s);
         return true;
@@ -1076,5 +1080,7 @@ cudaError_t launch_layer_norm_backward(int dtype, int pdtype, const LayerNormBac
     return vec ? backward_wide<T, P, VW>(a, s) : backward_wide<T, P, 1>(a, s);
   });
 }
+
+cudaError_t layer_norm_take_status(int* status) { return take_status(status); }
 
 }  // namespace ar

@@ -7,9 +7,23 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
+#include "../../include/ar.h"
 #include "ar_ops.h"
 
 namespace ar {
+
+// AR_ERR_TIMEOUT once a wait of one of the including file's kernels has run out.
+static __device__ int g_status;
+
+// Host: reads it into *status if it is set, and clears it.
+static inline cudaError_t take_status(int* status) {
+  int v = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_status, sizeof(int));
+  if (e != cudaSuccess || !v) return e;
+  *status = v;
+  v = 0;
+  return cudaMemcpyToSymbol(g_status, &v, sizeof(int));
+}
 
 template <class T> struct Conv;
 template <> struct Conv<float> {
@@ -201,18 +215,32 @@ __device__ __forceinline__ void ring_copy(uint32_t to, const void* from, int byt
                : "memory");
 }
 
-// A copy ends by itself, so this wait does; the limit (two seconds) is for a
-// launch that has gone wrong, whose results are then wrong too but which ends.
-__device__ __forceinline__ void ring_wait(uint32_t bar, uint32_t parity) {
+// Looks for the end of the phase of the given parity, asleep for up to 10 ms.
+__device__ __forceinline__ bool ring_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\nselp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(10000000)
+      : "memory");
+  return ok != 0;
+}
+
+// Waits for the phase of the given parity to end.  A copy ends by itself, so
+// this does too; the limit (two seconds) is for a launch that has gone wrong.
+// One wait that runs out ends the block's others, through `gave_up`, and is
+// reported in g_status.  The threads go on to the kernel's end all the same,
+// so that none is missing at a barrier, but begin no more copies (the last
+// ones began two seconds before).
+__device__ __forceinline__ bool ring_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
+#pragma unroll 1
   for (int i = 0; i < 200; ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\nselp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(10000000)
-        : "memory");
-    if (ok) return;
+    if (ring_try(bar, parity)) return true;
+    if (*gave_up) return false;
   }
+  *gave_up = 1;
+  g_status = AR_ERR_TIMEOUT;
+  return false;
 }
 
 // Applies a launch's element type to a function object: fn(T()).

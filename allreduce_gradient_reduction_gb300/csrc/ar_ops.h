@@ -86,8 +86,12 @@ struct AttnArgs {
 
 cudaError_t launch_attention(int dtype, const AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_attention_backward(int dtype, const AttnArgs& a, cudaStream_t stream);
-// Reads and clears what a kernel of the current device left when one of its
-// waits ran out: AR_ERR_TIMEOUT, or AR_OK.  The caller has synchronised.
+// What kernels of the current device left when one of their waits ran out:
+// AR_ERR_TIMEOUT is stored in *status, and cleared.  The caller has
+// synchronised.
+cudaError_t layer_norm_take_status(int* status);
+cudaError_t distill_take_status(int* status);
 cudaError_t attention_take_status(int* status);
+cudaError_t attention_backward_take_status(int* status);
 
 }  // namespace ar

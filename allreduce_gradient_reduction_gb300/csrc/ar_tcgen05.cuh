@@ -2,10 +2,10 @@
 // with bounded waits, tiled TMA loads, and the tensor cores' products from
 // shared and tensor memory (tcgen05) with their descriptors.
 //
-// Tiles in shared memory are 128 rows of 64 16-bit elements ("panels" of 16
-// KB), in the 128-byte swizzle: row r is the 128 bytes at r * 128, its 16-byte
-// pieces permuted within the row by r mod 8.  A row-major matrix of 128
-// columns is two panels.  The same panel serves a product in both readings:
+// Tiles in shared memory are 128 (or 64) rows of 64 16-bit elements ("panels"
+// of 16 KB), in the 128-byte swizzle: row r is the 128 bytes at r * 128, its
+// 16-byte pieces permuted within the row by r mod 8.  A row-major matrix of
+// 128 columns is two panels, of 128 rows each.  The same panel serves a product in both readings:
 // rows as the M or N axis and columns as K ("K-major"), or rows as K and
 // columns as the N axis ("MN-major").
 #pragma once
@@ -176,16 +176,6 @@ __device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&r)[16
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(at),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
 __device__ __forceinline__ void tmem_store16(uint32_t at, const float (&r)[16]) {
   uint32_t bits[16];
 #pragma unroll

@@ -288,6 +288,26 @@ def test_later_keys_do_not_matter(ar):
     assert torch.isnan(got[300:]).all()
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("tokens", [100, 300, 449])
+def test_a_key_of_minus_infinity(ar, tokens, dim):
+    """A key whose scores are all -inf has no weight: it and its value get zero
+    gradients, others finite ones, also where the last tile of queries is cut."""
+    q, k, v = make(tokens, 2, 1, dim, "bf16", 40)
+    dout = make(tokens, 2, 1, dim, "bf16", 41)[0]
+    q[:, :, 0] = q[:, :, 0].abs() + 0.5
+    k[5, :, 0] = -float("inf")
+    cu = packed([tokens])
+    out, lse = torch.empty_like(q), torch.empty(2, tokens, device="cuda")
+    dq, dk, dv = (torch.full_like(x, 7.0) for x in (q, k, v))
+    ws = torch.empty(ar.ar_attention_workspace_bytes(tokens, 2, 1, dim), dtype=torch.uint8, device="cuda")
+    ar.check(ar.ar_attention(q, k, v, cu, out, lse), "forward")
+    ar.check(ar.ar_attention_backward(dout, q, k, v, out, lse, cu, dq, dk, dv, ws), "backward")
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    assert (dk[5] == 0).all() and (dv[5] == 0).all()
+    assert torch.isfinite(dk).all() and torch.isfinite(dv).all() and torch.isfinite(dq[:, :, 1:]).all()
+
+
 def test_first_token_sees_itself_alone(ar):
     q, k, v = make(50, 2, 2, 64, "f16", 23)
     cu = packed([1, 30, 19])
