@@ -437,10 +437,12 @@ def _distill_operands(logits, teacher_index, teacher_logits, rows_f32, dlogits):
     """(status, element types of the logits and of the teacher's, row strides of logits and dlogits)."""
     types = _TORCH_DTYPE or _dtypes()
     shape, lists, dtype, vdtype = logits.shape, teacher_index.shape, logits.dtype, teacher_logits.dtype
+    if len(shape) != 2:
+        return AR_ERR_INVALID_ARG, 0, 0, 0, 0
     dt, vt = types.get(dtype), types.get(vdtype)
     if dt is None or vt is None:
         return AR_ERR_UNSUPPORTED, 0, 0, 0, 0
-    zs = _row_stride(logits, shape, dtype) if len(shape) == 2 else None
+    zs = _row_stride(logits, shape, dtype)
     ds = 0 if dlogits is None else _row_stride(dlogits, shape, dtype)
     if (zs is None or ds is None or len(lists) != 2 or lists[0] != shape[0] or teacher_logits.shape != lists
             or types.get(teacher_index.dtype) != 2 or not teacher_index.is_contiguous()
@@ -496,8 +498,10 @@ def _attention_operands(q, k, queries, keys, cu_seqlens, lse):
         return AR_ERR_UNSUPPORTED, 0, None
     flat = []
     for t, shape in ((q, qshape), (k, kshape), *((t, kshape) for t in keys), *((t, qshape) for t in queries)):
+        if t.dtype is not dtype or t.shape != shape:
+            return AR_ERR_INVALID_ARG, 0, None
         token, head, inner = t.stride()
-        if t.dtype is not dtype or t.shape != shape or (inner != 1 and shape[2] > 1):
+        if inner != 1 and shape[2] > 1:
             return AR_ERR_INVALID_ARG, 0, None
         flat += (t.data_ptr(), token, head)
     if (types.get(cu_seqlens.dtype) != 2 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1
