@@ -134,9 +134,9 @@ typedef enum {
   AR_ERR_INVALID_ARG = -1, /* null/duplicate/overlapping/misaligned pointer, bad size or enum */
   AR_ERR_UNSUPPORTED = -2, /* AVG on i32, tree order with N not a power of two, ... */
   AR_ERR_CUDA = -3,        /* a CUDA call failed; ar_last_cuda_error() holds the cause */
-  AR_ERR_TIMEOUT = -4,     /* asynchronous: a step-wise grid barrier gave up (see ar_device_status) */
+  AR_ERR_TIMEOUT = -4,     /* asynchronous: a wait inside a kernel gave up (see ar_device_status) */
   AR_ERR_NO_DEVICE = -5,   /* no usable CUDA device */
-  AR_ERR_TOO_LARGE = -6,   /* the call needs more descriptor space than one launch holds */
+  AR_ERR_TOO_LARGE = -6,   /* more descriptor space than one launch holds, or sizes past a kernel's counters */
   AR_ERR_HOST = -7         /* host-side failure (out of host memory) */
 } ar_status;
 
