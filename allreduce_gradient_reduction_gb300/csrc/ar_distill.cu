@@ -399,9 +399,12 @@ struct Place {
 };
 
 // pieces: to a row; places: of shared memory; keep: a row's pieces stay for a
-// second pass (places == pieces then)
+// second pass (places == pieces then).  The gradient alone is dealt out by
+// 2^`split` parts of a row, as its pieces do not depend on one another (0 in
+// the forward direction).
 template <class T, class V, bool BACKWARD>
-__global__ void __launch_bounds__(kRingThreads, 2) distill_ring_kernel(const DistillArgs a, int pieces, int places, bool keep) {
+__global__ void __launch_bounds__(kRingThreads, 2)
+    distill_ring_kernel(const DistillArgs a, int pieces, int places, bool keep, int split) {
   constexpr int VN = 16 / sizeof(T);
   extern __shared__ __align__(16) uint8_t buffer[];  // the places, then the lists
   __shared__ Stat scratch[2][32];
@@ -413,6 +416,11 @@ __global__ void __launch_bounds__(kRingThreads, 2) distill_ring_kernel(const Dis
   const float tau = a.temperature, c = kLog2e / tau, inv_tau = 1.f / tau;
   const T* logits = static_cast<const T*>(a.logits);
   const bool twice = !BACKWARD && a.dlogits;
+  const int64_t units = BACKWARD ? a.rows << split : a.rows;
+  auto row_of = [&](int64_t unit) { return BACKWARD ? unit >> split : unit; };
+  auto part_of = [&](int64_t unit) { return BACKWARD ? (int)unit & ((1 << split) - 1) : 0; };
+  // the pieces of a part of a row: from edge(part) to edge(part + 1)
+  auto edge = [&](int part) { return BACKWARD ? pieces * part >> split : pieces * part; };
   auto list_of = [&](int i) { return List(buffer + places * kPieceBytes + i * kListBytes * top, top); };
   auto init = [](uint64_t* bar, int count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_at(bar)), "r"(count) : "memory");
@@ -435,12 +443,13 @@ __global__ void __launch_bounds__(kRingThreads, 2) distill_ring_kernel(const Dis
     // ---- loads
     if (lane == 0) {
       Place at;
-      for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-        const T* z = logits + row * a.logits_stride;
+      for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
+        const T* z = logits + row_of(unit) * a.logits_stride;
+        const int begin = edge(part_of(unit)), end = edge(part_of(unit) + 1);
         const uint8_t* from = reinterpret_cast<const uint8_t*>((uintptr_t)z & ~(uintptr_t)15);
         const int bytes = (int)covering(z, vocab * (int)sizeof(T));
         for (int pass = 0; pass < (twice && !keep ? 2 : 1); ++pass)
-          for (int i = 0; i < pieces; ++i, at.next(places)) {
+          for (int i = begin; i < end; ++i, at.next(places)) {
             if (at.round > 0 && !wait(&empty[at.slot], (at.round - 1) & 1, &gave_up)) return;
             // rows that begin at other places in their first word may have a piece less
             const int n = min(kPieceBytes, bytes - i * kPieceBytes);
@@ -453,10 +462,11 @@ __global__ void __launch_bounds__(kRingThreads, 2) distill_ring_kernel(const Dis
     return;
   }
   if (t >= kWorkers) {
-    // ---- lists: warp i makes those of the block's rows i, i + 3, ...
+    // ---- lists: warp i makes those of the block's rows (or parts) i, i + 3, ...
     const int i = (t - kWorkers) >> 5;
     int round = 0;
-    for (int64_t row = blockIdx.x + (int64_t)i * gridDim.x; row < a.rows; row += (int64_t)kListWarps * gridDim.x, ++round) {
+    for (int64_t unit = blockIdx.x + (int64_t)i * gridDim.x; unit < units; unit += (int64_t)kListWarps * gridDim.x, ++round) {
+      const int64_t row = row_of(unit);
       if (round > 0) wait(&list_used[i], (round - 1) & 1, &gave_up);
       const Divergence d = make_list<T, V>(a, row, logits + row * a.logits_stride, vocab, inv_tau, a.dlogits != nullptr, list_of(i));
       if (lane == 0) divergence[i] = d;
@@ -468,7 +478,9 @@ __global__ void __launch_bounds__(kRingThreads, 2) distill_ring_kernel(const Dis
 
   Place at, list_at;
   int turn = 0;
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1, list_at.next(kListWarps)) {
+  for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x, turn ^= 1, list_at.next(kListWarps)) {
+    const int64_t row = row_of(unit);
+    const int begin = edge(part_of(unit)), end = edge(part_of(unit) + 1);
     const T* z = logits + row * a.logits_stride;
     const RowVectors<T> rv(z, vocab);
     const int vecs = rv.count();
@@ -495,7 +507,7 @@ __global__ void __launch_bounds__(kRingThreads, 2) distill_ring_kernel(const Dis
     } else {
       Stat st{-INFINITY, 0.f};
       Place p1 = at;
-      for (int i = 0; i < pieces; ++i, p1.next(places)) {
+      for (int i = begin; i < end; ++i, p1.next(places)) {
         wait(&filled[p1.slot], p1.round & 1, &gave_up);
         const uint8_t* piece = buffer + p1.slot * kPieceBytes;
         const int v = i * kPieceVectors + t;
@@ -532,7 +544,7 @@ __global__ void __launch_bounds__(kRingThreads, 2) distill_ring_kernel(const Dis
     const Gradient<T> gradient(scale * tau, lse, c, inv_tau);
     T* dz = static_cast<T*>(a.dlogits) + row * a.dlogits_stride;
     const bool same = (((uintptr_t)dz ^ (uintptr_t)z) & 15) == 0;
-    for (int i = 0; i < pieces; ++i, at.next(places)) {
+    for (int i = begin; i < end; ++i, at.next(places)) {
       if (BACKWARD || !keep) wait(&filled[at.slot], at.round & 1, &gave_up);
       const uint8_t* piece = buffer + at.slot * kPieceBytes;
 #pragma unroll
@@ -553,7 +565,9 @@ __global__ void __launch_bounds__(kRingThreads, 2) distill_ring_kernel(const Dis
       release(&empty[at.slot]);
     }
     workers_barrier();
-    if (live) correct_listed<T>(list_of(list_at.slot), top, 0, vocab, t, kWorkers, gradient, dz);
+    if (live)
+      correct_listed<T>(list_of(list_at.slot), top, max(rv.first(begin * kPieceVectors), 0),
+                        min(rv.first(end * kPieceVectors), vocab), t, kWorkers, gradient, dz);
     release(&list_used[list_at.slot]);
   }
 }
@@ -573,8 +587,20 @@ cudaError_t run(const DistillArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     int per_sm = 0;
     if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kRingThreads, (size_t)shared)) != cudaSuccess) return e;
-    const int64_t blocks = std::min<int64_t>(a.rows, (int64_t)sm_count() * std::max(per_sm, 1));
-    kernel<<<(unsigned)blocks, kRingThreads, (size_t)shared, s>>>(a, pieces, places, keep);
+    // What the blocks that finish last leave idle: whole rows to a block where
+    // that is under 4%, else halves or quarters with at least four pieces
+    // (1023 x 128003 f16, 3.4 rows to a block: 109.5 us by rows, 105 us by
+    // quarters; each part makes the row's list again).
+    const int64_t most = (int64_t)sm_count() * std::max(per_sm, 1);
+    int split = 0;
+    auto idle = [&] {
+      const int64_t units = a.rows << split, turns = (units + most - 1) / most;
+      return (double)(turns * most - units) / (double)(turns * most);
+    };
+    if (BACKWARD)
+      while (split < 2 && pieces >> split >= 8 && idle() > 0.04) ++split;
+    const int64_t blocks = std::min<int64_t>(a.rows << split, most);
+    kernel<<<(unsigned)blocks, kRingThreads, (size_t)shared, s>>>(a, pieces, places, keep, split);
     count_launch();
     return cudaGetLastError();
   }

@@ -257,3 +257,21 @@ def test_refusals(ar):
     none = torch.empty(0, 100, dtype=torch.bfloat16, device="cuda")
     ar.check(ar.ar_distill_loss(none, index[:0], value[:0], loss[:0], lse[:0]), "no rows")
     assert ar.ar_kernel_launches() == launches
+
+
+@pytest.mark.parametrize("dtype,vocab,pad,offset", [("bf16", 50257, 0, 0), ("f16", 100003, 5, 3), ("f32", 30001, 0, 1)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_gradient_alone_of_many_long_rows(ar, dtype, vocab, pad, offset, in_place):
+    """Rows dealt out in parts: the bits of the call that makes loss and
+    gradient, whose first rows are checked against the formula."""
+    rows, tau = 310, 1.5
+    z, index, value, scale = make(rows, vocab, 20, dtype, 50, pad, offset)
+    loss, lse = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    want = torch.full_like(z, 7.0)
+    ar.check(ar.ar_distill_loss(z, index, value, loss, lse, scale=scale, dlogits=want, temperature=tau), "step")
+    n = 3
+    exact = formula(z[:n], index[:n], value[:n], scale[:n], tau)
+    within(f64(want[:n]), exact[2], U[dtype] * np.abs(exact[2]) + 2.0 ** -16 * exact[4] + TINY[dtype], "dlogits")
+    got = z if in_place else torch.full_like(z, 7.0)
+    ar.check(ar.ar_distill_loss_backward(z, index, value, lse, scale, got, temperature=tau), "backward")
+    assert torch.equal(got, want) and ar.ar_device_status() == (0, 0)
