@@ -42,6 +42,7 @@ __device__ __forceinline__ Stat warp_join(Stat a, float c) {
 #pragma unroll
   for (int i = 16; i; i >>= 1)
     a = join(a, Stat{__shfl_xor_sync(0xFFFFFFFFu, a.m, i), __shfl_xor_sync(0xFFFFFFFFu, a.s, i)}, c);
+  a.s = __shfl_sync(0xFFFFFFFFu, a.s, 0);  // the lanes' sums differ in their last bits
   return a;
 }
 
