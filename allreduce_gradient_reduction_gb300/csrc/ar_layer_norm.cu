@@ -915,13 +915,16 @@ bool forward_ring(const LayerNormArgs& a, cudaStream_t s, cudaError_t* e) {
   }
   static const int counts[5] = {1, A, 2 * A, 3 * A, 4 * A};
   if constexpr (sizeof(P) == 4 && sizeof(T) == 2) {
-    if (a.cols >= 2048) {
-      static const int kept[1] = {2 * A};
-      const Deal d = deal(a.cols / VW, kept, 512);
-      if (d.nv) {
-        *e = run_ring<T, P, 2 * A, true>(a, d.threads, s);
-        return true;
-      }
+    // f32 parameters of 16-bit rows stay in registers, two vectors to a thread,
+    // unless that leaves more than an eighth of a narrow row's threads without
+    // work (16384 rows; parameters kept, and read again for each row: 512
+    // columns 7.8 and 10.1 us, 768 15.9 and 12.7, 1536 22.9 and 25.6, 2048 31.0
+    // and 36.5, 4096 58.1 and 67.2).
+    static const int kept[1] = {2 * A};
+    const Deal d = deal(a.cols / VW, kept, 512);
+    if (d.nv && (a.cols >= 2048 || (int64_t)d.threads * d.nv * VW * 8 <= a.cols * 9)) {
+      *e = run_ring<T, P, 2 * A, true>(a, d.threads, s);
+      return true;
     }
   }
   const Deal d = deal(a.cols / VW, counts, 512);
