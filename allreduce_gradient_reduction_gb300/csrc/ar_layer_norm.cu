@@ -20,6 +20,7 @@
 #include "ar_ops.cuh"
 
 #include <algorithm>
+#include <type_traits>
 
 #include "ar_device.cuh"
 
@@ -159,8 +160,8 @@ __device__ __forceinline__ void join_params(const float (&dw)[NV][VW], const flo
   }
 }
 
-// Rows too wide for a ring: a block walks over the rows with a stride of all
-// blocks, up to 16 columns in each of up to 1024 threads.
+// f32 rows too wide for a ring: a block walks over the rows with a stride of
+// all blocks, up to 16 columns in each of up to 1024 threads.
 template <class T, class P, int VW, int NV>
 __global__ void __launch_bounds__(1024) layer_norm_backward_kernel(const LayerNormBackwardArgs a) {
   __shared__ float scratch[2][2][32];
@@ -277,7 +278,8 @@ __device__ __forceinline__ void open_ring(uint64_t* full, int* gave_up) {
 
 // Sums of two values over the group, through one of two halves of its scratch
 // by turns: one barrier a call.
-__device__ __forceinline__ float2 group_sum2(float2 v, float2 (*scratch)[16], int turn) {
+template <int WARPS>
+__device__ __forceinline__ float2 group_sum2(float2 v, float2 (*scratch)[WARPS], int turn) {
   v.x = warp_sum(v.x);
   v.y = warp_sum(v.y);
   const int warps = blockDim.x >> 5;
@@ -425,12 +427,15 @@ __global__ void __maxnreg__(KEEP ? 88 : forward_registers(NV * (16 / sizeof(T)))
   }
 }
 
-template <class T, class P, int NV>
-__global__ void __maxnreg__(backward_registers(NV * (16 / sizeof(T))))
+// WIDE: a group of more than 512 threads.  They have 64 registers each, so xh
+// and dy w are made again from shared memory after the sums, and a row's place
+// is filled again only after that.
+template <class T, class P, int NV, bool WIDE>
+__global__ void __maxnreg__(WIDE ? 64 : backward_registers(NV * (16 / sizeof(T))))
     layer_norm_backward_ring_kernel(const LayerNormBackwardArgs a, int slot, int stages) {
   constexpr int VW = 16 / sizeof(T), N = Pairs<T>::N;
   extern __shared__ __align__(16) uint8_t rows[];
-  __shared__ float2 scratch[kGroups][2][16];
+  __shared__ float2 scratch[WIDE ? 1 : kGroups][2][WIDE ? 32 : 16];
   __shared__ __align__(8) uint64_t filled[kGroups][kRing];
   __shared__ int gave_up;
   const int cols = (int)a.cols, t = threadIdx.x;
@@ -470,9 +475,10 @@ __global__ void __maxnreg__(backward_registers(NV * (16 / sizeof(T))))
     const bool came = ring_wait(smem_at(bars + stage), parity, &gave_up);
     const Two minus = two(-mean, -mean), scale = two(rstd, rstd);
     const uint8_t* from = mine + stage * 2 * slot + v0 * 16;
-    Two xh[NV][N], gw[NV][N];
+    Two xh[WIDE ? 1 : NV][N], gw[WIDE ? 1 : NV][N];
     Two s1 = two(0.f, 0.f), s2 = two(0.f, 0.f);
-    auto take = [&](int k) {
+    auto take = [&](int k, bool again) {
+      const int at = WIDE ? 0 : k;
       const uint4 xr = *reinterpret_cast<const uint4*>(from + k * 512);
       const uint4 dr = *reinterpret_cast<const uint4*>(from + slot + k * 512);
       Two w[N];
@@ -480,35 +486,38 @@ __global__ void __maxnreg__(backward_registers(NV * (16 / sizeof(T))))
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const Two d = Pairs<T>::get(dr, i);
-        xh[k][i] = mul2(add2(Pairs<T>::get(xr, i), minus), scale);
-        gw[k][i] = mul2(d, w[i]);
-        dw[k][i] = fma2(d, xh[k][i], dw[k][i]);
+        xh[at][i] = mul2(add2(Pairs<T>::get(xr, i), minus), scale);
+        gw[at][i] = mul2(d, w[i]);
+        if (again) continue;
+        dw[k][i] = fma2(d, xh[at][i], dw[k][i]);
         db[k][i] = add2(db[k][i], d);
-        s1 = add2(s1, gw[k][i]);
-        s2 = fma2(gw[k][i], xh[k][i], s2);
+        s1 = add2(s1, gw[at][i]);
+        s2 = fma2(gw[at][i], xh[at][i], s2);
       }
     };
     if (full) {
 #pragma unroll
-      for (int k = 0; k < NV; ++k) take(k);
+      for (int k = 0; k < NV; ++k) take(k, false);
     } else {
 #pragma unroll
       for (int k = 0; k < NV; ++k)
-        if (v0 + k * 32 < vecs) take(k);
+        if (v0 + k * 32 < vecs) take(k, false);
     }
     float a1, b1, a2, b2;
     split(s1, a1, b1);
     split(s2, a2, b2);
     const float2 s = group_sum2(make_float2(a1 + b1, a2 + b2), scratch[threadIdx.y], turn);
-    if (t == 0 && came && row + stages * step < a.rows) issue(row + stages * step, stage);  // the group has read the slot
+    if (!WIDE && t == 0 && came && row + stages * step < a.rows) issue(row + stages * step, stage);  // the group has read the slot
     // dx = rstd gw - rstd s1 / C - xh rstd s2 / C
     const float m1 = -rstd * (s.x * inv), m2 = -rstd * (s.y * inv);
     const Two m1s = two(m1, m1), m2s = two(m2, m2);
     T* dx = static_cast<T*>(a.dx) + row * a.dx_stride + v0 * VW;
     auto put = [&](int k) {
+      const int at = WIDE ? 0 : k;
+      if (WIDE) take(k, true);
       uint4 out;
 #pragma unroll
-      for (int i = 0; i < N; ++i) Pairs<T>::set(out, i, fma2(xh[k][i], m2s, fma2(gw[k][i], scale, m1s)));
+      for (int i = 0; i < N; ++i) Pairs<T>::set(out, i, fma2(xh[at][i], m2s, fma2(gw[at][i], scale, m1s)));
       *reinterpret_cast<uint4*>(dx + k * 32 * VW) = out;
     };
     if (full) {
@@ -518,6 +527,10 @@ __global__ void __maxnreg__(backward_registers(NV * (16 / sizeof(T))))
 #pragma unroll
       for (int k = 0; k < NV; ++k)
         if (v0 + k * 32 < vecs) put(k);
+    }
+    if (WIDE) {
+      group_barrier();
+      if (t == 0 && came && row + stages * step < a.rows) issue(row + stages * step, stage);
     }
     mean = mean_n;
     rstd = rstd_n;
@@ -573,8 +586,10 @@ __device__ __forceinline__ void strided_store(T* row, int i, int left, Two v) {
   }
 }
 
+__host__ __device__ constexpr int strided_registers(int columns) { return columns <= 8 ? 56 : columns <= 16 ? 80 : 128; }
+
 template <class T, class P, int NE>
-__global__ void __maxnreg__(NE <= 8 ? 56 : 80)
+__global__ void __maxnreg__(strided_registers(NE))
     layer_norm_strided_kernel(const LayerNormArgs a, int slot, int stages) {
   constexpr int N = NE / 2;
   extern __shared__ __align__(16) uint8_t rows[];
@@ -652,12 +667,12 @@ __global__ void __maxnreg__(NE <= 8 ? 56 : 80)
   }
 }
 
-template <class T, class P, int NE>
-__global__ void __maxnreg__(backward_registers(NE))
+template <class T, class P, int NE, bool WIDE>
+__global__ void __maxnreg__(WIDE ? 64 : backward_registers(NE))
     layer_norm_backward_strided_kernel(const LayerNormBackwardArgs a, int slot, int stages) {
   constexpr int N = NE / 2;
   extern __shared__ __align__(16) uint8_t rows[];
-  __shared__ float2 scratch[kGroups][2][16];
+  __shared__ float2 scratch[WIDE ? 1 : kGroups][2][WIDE ? 32 : 16];
   __shared__ __align__(8) uint64_t filled[kGroups][kRing];
   __shared__ int gave_up;
   const int cols = (int)a.cols, t = threadIdx.x;
@@ -681,8 +696,9 @@ __global__ void __maxnreg__(backward_registers(NE))
     for (int i = 0; i < stages && row + i * step < a.rows; ++i) issue(row + i * step, i);
   const int c0 = (t >> 5) * 32 * NE + (t & 31), left = cols - c0;
   const bool full = ((t >> 5) + 1) * 32 * NE <= cols;
-  Two w[N], dw[N], db[N];
-  strided_params<P, N>(static_cast<const P*>(a.weight), c0, cols, w);
+  const P* weight = static_cast<const P*>(a.weight);
+  Two w[WIDE ? 1 : N], dw[N], db[N];
+  if constexpr (!WIDE) strided_params<P, N>(weight, c0, cols, w);
 #pragma unroll
   for (int i = 0; i < N; ++i) dw[i] = db[i] = two(0.f, 0.f);
   float mean = 0.f, rstd = 0.f;
@@ -696,37 +712,51 @@ __global__ void __maxnreg__(backward_registers(NE))
     const uint8_t* from = mine + stage * 2 * slot;
     const T* xs = reinterpret_cast<const T*>(from + ((uintptr_t)(x + row * a.x_stride) & 15)) + c0;
     const T* ds = reinterpret_cast<const T*>(from + slot + ((uintptr_t)(dy + row * a.dy_stride) & 15)) + c0;
-    Two xh[N], gw[N], s1 = two(0.f, 0.f), s2 = two(0.f, 0.f);
-    auto take = [&](int i, Two xv, Two d) {
+    Two xh[WIDE ? 1 : N], gw[WIDE ? 1 : N], s1 = two(0.f, 0.f), s2 = two(0.f, 0.f);
+    auto take = [&](auto full_row, int i, bool again) {
+      constexpr bool FULL = decltype(full_row)::value;
+      const int at = WIDE ? 0 : i;
       // dy is 0 outside the row, so what stands for x there does not count
-      xh[i] = mul2(add2(xv, minus), scale);
-      gw[i] = mul2(d, w[i]);
-      dw[i] = fma2(d, xh[i], dw[i]);
+      const Two d = strided_pair<FULL>(ds, i, left);
+      if constexpr (WIDE) w[0] = strided_pair<FULL>(weight + c0, i, left);
+      xh[at] = mul2(add2(strided_pair<FULL>(xs, i, left), minus), scale);
+      gw[at] = mul2(d, w[at]);
+      if (again) return;
+      dw[i] = fma2(d, xh[at], dw[i]);
       db[i] = add2(db[i], d);
-      s1 = add2(s1, gw[i]);
-      s2 = fma2(gw[i], xh[i], s2);
+      s1 = add2(s1, gw[at]);
+      s2 = fma2(gw[at], xh[at], s2);
     };
     if (full) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) take(i, strided_pair<true>(xs, i, left), strided_pair<true>(ds, i, left));
+      for (int i = 0; i < N; ++i) take(std::true_type(), i, false);
     } else {
 #pragma unroll
-      for (int i = 0; i < N; ++i) take(i, strided_pair<false>(xs, i, left), strided_pair<false>(ds, i, left));
+      for (int i = 0; i < N; ++i) take(std::false_type(), i, false);
     }
     float a1, b1, a2, b2;
     split(s1, a1, b1);
     split(s2, a2, b2);
     const float2 s = group_sum2(make_float2(a1 + b1, a2 + b2), scratch[threadIdx.y], turn);
-    if (t == 0 && came && row + stages * step < a.rows) issue(row + stages * step, stage);  // the group has read the slot
+    if (!WIDE && t == 0 && came && row + stages * step < a.rows) issue(row + stages * step, stage);  // the group has read the slot
     const float m1 = -rstd * (s.x * inv), m2 = -rstd * (s.y * inv);
     const Two m1s = two(m1, m1), m2s = two(m2, m2);
     T* dx = static_cast<T*>(a.dx) + row * a.dx_stride + c0;
+    auto put = [&](auto full_row, int i) {
+      const int at = WIDE ? 0 : i;
+      if (WIDE) take(full_row, i, true);
+      strided_store<decltype(full_row)::value>(dx, i, left, fma2(xh[at], m2s, fma2(gw[at], scale, m1s)));
+    };
     if (full) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) strided_store<true>(dx, i, left, fma2(xh[i], m2s, fma2(gw[i], scale, m1s)));
+      for (int i = 0; i < N; ++i) put(std::true_type(), i);
     } else {
 #pragma unroll
-      for (int i = 0; i < N; ++i) strided_store<false>(dx, i, left, fma2(xh[i], m2s, fma2(gw[i], scale, m1s)));
+      for (int i = 0; i < N; ++i) put(std::false_type(), i);
+    }
+    if (WIDE) {
+      group_barrier();
+      if (t == 0 && came && row + stages * step < a.rows) issue(row + stages * step, stage);
     }
     mean = mean_n;
     rstd = rstd_n;
@@ -896,7 +926,7 @@ cudaError_t run_ring(const LayerNormArgs& a, int threads, cudaStream_t s) {
 template <class T, class P, int NE>
 cudaError_t run_strided(const LayerNormArgs& a, int threads, cudaStream_t s) {
   static std::atomic<unsigned long long> opened[256];
-  return start_ring<T>(layer_norm_strided_kernel<T, P, NE>, opened, threads, NE <= 8 ? 56 : 80, a, s);
+  return start_ring<T>(layer_norm_strided_kernel<T, P, NE>, opened, threads, strided_registers(NE), a, s);
 }
 
 template <class T, class P>
@@ -907,10 +937,14 @@ bool forward_ring(const LayerNormArgs& a, cudaStream_t s, cudaError_t* e) {
                      rows_aligned16(a.y, a.y_stride, a.rows, sizeof(T)) && params_aligned<T, P>(a.weight) &&
                      params_aligned<T, P>(a.bias);
   if (!whole) {
-    static const int counts[2] = {8, 16};
-    const Deal d = deal(a.cols, counts, 512);
+    // 32 elements to a thread only where 16 do not reach (8192 x 16383 f16: 128
+    // us, and 397 with rows in 1024 threads' registers, without a ring)
+    static const int counts[2] = {8, 16}, wide[1] = {32};
+    Deal d = deal(a.cols, counts, 512);
+    if (!d.nv) d = deal(a.cols, wide, 512);
     if (d.nv == 8) *e = run_strided<T, P, 8>(a, d.threads, s);
-    else if (d.nv) *e = run_strided<T, P, 16>(a, d.threads, s);
+    else if (d.nv == 16) *e = run_strided<T, P, 16>(a, d.threads, s);
+    else if (d.nv) *e = run_strided<T, P, 32>(a, d.threads, s);
     return d.nv != 0;
   }
   static const int counts[5] = {1, A, 2 * A, 3 * A, 4 * A};
@@ -973,9 +1007,11 @@ cudaError_t run_params(const LayerNormBackwardArgs& a, int blocks, cudaStream_t 
 // columns: what one thread sums for
 template <class T, class P>
 cudaError_t start_backward_ring(void (*kernel)(LayerNormBackwardArgs, int, int), std::atomic<unsigned long long>* opened,
-                                int threads, int columns, const LayerNormBackwardArgs& a, cudaStream_t s) {
-  const int slot = ring_slot<T>(a.cols), stages = ring_stages(2 * slot, threads, backward_registers(columns));
-  const int groups = ring_groups(threads, a.rows);
+                                int threads, int columns, bool wide, const LayerNormBackwardArgs& a, cudaStream_t s) {
+  const int slot = ring_slot<T>(a.cols);
+  const int stages = wide ? std::min(2, kRingMaxShared / (2 * slot))
+                          : ring_stages(2 * slot, threads, backward_registers(columns));
+  const int groups = wide ? 1 : ring_groups(threads, a.rows);
   const int smem = std::max(groups * 2 * stages * slot, groups > 1 ? 2 * threads * columns * (int)sizeof(float) : 0);
   cudaError_t e = open_kernel((const void*)kernel, kRingMaxShared, false, opened);
   if (e != cudaSuccess) return e;
@@ -988,15 +1024,16 @@ cudaError_t start_backward_ring(void (*kernel)(LayerNormBackwardArgs, int, int),
   return run_params<P>(a, (int)blocks, s);
 }
 
-template <class T, class P, int NV>
+template <class T, class P, int NV, bool WIDE = false>
 cudaError_t run_backward_ring(const LayerNormBackwardArgs& a, int threads, cudaStream_t s) {
   static std::atomic<unsigned long long> opened[256];
-  return start_backward_ring<T, P>(layer_norm_backward_ring_kernel<T, P, NV>, opened, threads, NV * (16 / (int)sizeof(T)), a, s);
+  return start_backward_ring<T, P>(layer_norm_backward_ring_kernel<T, P, NV, WIDE>, opened, threads,
+                                   NV * (16 / (int)sizeof(T)), WIDE, a, s);
 }
-template <class T, class P, int NE>
+template <class T, class P, int NE, bool WIDE = false>
 cudaError_t run_backward_strided(const LayerNormBackwardArgs& a, int threads, cudaStream_t s) {
   static std::atomic<unsigned long long> opened[256];
-  return start_backward_ring<T, P>(layer_norm_backward_strided_kernel<T, P, NE>, opened, threads, NE, a, s);
+  return start_backward_ring<T, P>(layer_norm_backward_strided_kernel<T, P, NE, WIDE>, opened, threads, NE, WIDE, a, s);
 }
 
 template <class T, class P>
@@ -1007,31 +1044,45 @@ bool backward_ring(const LayerNormBackwardArgs& a, cudaStream_t s, cudaError_t* 
                      rows_aligned16(a.dy, a.dy_stride, a.rows, sizeof(T)) &&
                      rows_aligned16(a.dx, a.dx_stride, a.rows, sizeof(T)) && params_aligned<T, P>(a.weight);
   if (!whole) {
-    static const int counts[2] = {8, 16};
-    const Deal d = deal(a.cols, counts, 512);
+    static const int counts[2] = {8, 16}, wide[1] = {16};
+    Deal d = deal(a.cols, counts, 512);
     if (d.nv == 8) *e = run_backward_strided<T, P, 8>(a, d.threads, s);
     else if (d.nv) *e = run_backward_strided<T, P, 16>(a, d.threads, s);
+    else if ((d = deal(a.cols, wide, 1024)).nv) *e = run_backward_strided<T, P, 16, true>(a, d.threads, s);
     return d.nv != 0;
   }
-  static const int counts[3] = {1, A, 2 * A};
-  const Deal d = deal(a.cols / VW, counts, 512);
+  static const int counts[3] = {1, A, 2 * A}, wide[1] = {2 * A};
+  Deal d = deal(a.cols / VW, counts, 512);
+  if (!d.nv) {
+    // More than 8192 columns.  16-bit rows: 8192 x 16384 bf16 278 us, and 353
+    // with rows in 1024 threads' registers, without a ring.  An f32 row leaves
+    // no room for a second one in shared memory (4096 x 16384: 220 us, and 173
+    // without a ring) unless it is read element by element anyway (4096 x
+    // 16381: 260 and 293).
+    if constexpr (sizeof(T) == 4) return false;
+    else if ((d = deal(a.cols / VW, wide, 1024)).nv) *e = run_backward_ring<T, P, 2 * A, true>(a, d.threads, s);
+    return d.nv != 0;
+  }
   if (d.nv == 1) *e = run_backward_ring<T, P, 1>(a, d.threads, s);
   else if (d.nv == A) *e = run_backward_ring<T, P, A>(a, d.threads, s);
   else if (d.nv) *e = run_backward_ring<T, P, 2 * A>(a, d.threads, s);
   return d.nv != 0;
 }
 
-template <class T, class P, int VW>
+template <class T, class P>
 cudaError_t backward_wide(const LayerNormBackwardArgs& a, cudaStream_t s) {
-  constexpr int NV = 16 / VW;
-  static const int counts[1] = {NV};
   cudaError_t e;
-  if (const Deal d = deal((a.cols + VW - 1) / VW, counts, 1024); d.nv) {
-    const int blocks = (int)std::min<int64_t>(std::min(sm_count(), kLayerNormMaxBlocks), a.rows);
-    layer_norm_backward_kernel<T, P, VW, NV><<<blocks, d.threads, 0, s>>>(a);
-    count_launch();
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    return run_params<P>(a, blocks, s);
+  if constexpr (sizeof(T) == 4) {
+    static const int counts[1] = {4};
+    const Deal d = deal((a.cols + 3) / 4, counts, 1024);
+    if (d.nv && rows_aligned16(a.x, a.x_stride, a.rows, 4) && rows_aligned16(a.dy, a.dy_stride, a.rows, 4) &&
+        rows_aligned16(a.dx, a.dx_stride, a.rows, 4) && params_aligned<T, P>(a.weight)) {
+      const int blocks = (int)std::min<int64_t>(std::min(sm_count(), kLayerNormMaxBlocks), a.rows);
+      layer_norm_backward_kernel<T, P, 4, 4><<<blocks, d.threads, 0, s>>>(a);
+      count_launch();
+      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+      return run_params<P>(a, blocks, s);
+    }
   }
   const int slices = (int)std::min<int64_t>(a.rows, 64);
   layer_norm_params_wide_kernel<T><<<dim3((unsigned)((a.cols + 255) / 256), slices), 256, 0, s>>>(a);
@@ -1073,14 +1124,8 @@ cudaError_t launch_layer_norm_backward(int dtype, int pdtype, const LayerNormBac
   return with_types(dtype, pdtype, [&](auto t, auto p) {
     using T = decltype(t);
     using P = decltype(p);
-    constexpr int VW = 16 / sizeof(T);
     cudaError_t e;
-    if (backward_ring<T, P>(a, s, &e)) return e;
-    const bool vec = rows_aligned16(a.x, a.x_stride, a.rows, sizeof(T)) &&
-                     rows_aligned16(a.dy, a.dy_stride, a.rows, sizeof(T)) &&
-                     rows_aligned16(a.dx, a.dx_stride, a.rows, sizeof(T)) &&
-                     (uintptr_t)a.weight % (VW * sizeof(P)) == 0;
-    return vec ? backward_wide<T, P, VW>(a, s) : backward_wide<T, P, 1>(a, s);
+    return backward_ring<T, P>(a, s, &e) ? e : backward_wide<T, P>(a, s);
   });
 }
 

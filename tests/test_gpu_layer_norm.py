@@ -285,3 +285,22 @@ def test_captured_into_a_graph(ar):
     ar.check(ar.ar_layer_norm(x, w, b, y, m, r), "forward")
     ar.check(ar.ar_layer_norm_backward(dy, x, w, m, r, dx, dw, db, ws), "backward")
     assert all(torch.equal(a, c) for a, c in itertools.zip_longest(got, (y, dx, dw, db)))
+
+
+@pytest.mark.parametrize("dtype,params", [("f32", "f32"), ("bf16", "f32"), ("f16", "f16")])
+@pytest.mark.parametrize("rows,cols,pad", [(470, 9001, 0), (500, 12008, 0), (330, 16383, 5), (330, 16384, 0)])
+def test_wide_rows_in_place(ar, rows, cols, pad, dtype, params):
+    """Several rows to a block, so that places in shared memory are filled again."""
+    x, dy, w, b = make(rows, cols, dtype, params, 60, pad)
+    y = torch.empty_like(x)
+    mean, rstd = check_forward(ar, x, w, b, dtype, y)
+    own = rows_of(f64(x), dtype, pad)
+    ar.check(ar.ar_layer_norm(own, w, b, own), "in place")
+    assert torch.equal(own, y)
+    want = torch.empty_like(x)
+    grads = check_backward(ar, dy, x, w, mean, rstd, want, dtype, params)
+    ws = torch.empty(ar.ar_layer_norm_workspace_bytes(rows, cols), dtype=torch.uint8, device="cuda")
+    dw, db = torch.empty_like(w), torch.empty_like(w)
+    ar.check(ar.ar_layer_norm_backward(dy, x, w, mean, rstd, dy, dw, db, ws), "in place")
+    assert torch.equal(dy, want) and torch.equal(dw, grads[0]) and torch.equal(db, grads[1])
+    assert ar.ar_device_status() == (0, 0)
