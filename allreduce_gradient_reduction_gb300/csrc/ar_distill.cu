@@ -9,10 +9,16 @@
 // each of its elements needs one exponential a pass.  One block (or, with few
 // rows, several) streams a row once with a running maximum and sum; when the
 // gradient is wanted too, it goes over the row a second time while the row is
-// still in L2 (at four blocks of 512 threads on each of 152 multiprocessors
-// 61 MB of rows are in flight, under half of L2), so HBM sees one read and one
-// write.  The few listed words are corrected afterwards, each computed once in
-// binary32 and rounded once.
+// in shared memory or still in L2 (four blocks on each of 152 multiprocessors
+// have 61 MB of such rows in flight, under half of L2), so HBM sees one read
+// and one write.  The few listed words are corrected afterwards, each computed
+// once in binary32 and rounded once.
+//
+// Measured (device time, share of the measured copy bandwidth): loss of 2048 x
+// 50257 f32 64 us, 97%; loss and gradient of 8192 x 50257 bf16 341 us, 73%
+// (two exponentials, a maximum and three conversions an element: the pipe that
+// has the last two is 44% busy, the multiprocessor waits for itself more than
+// for memory); gradient alone of 1023 x 128003 f16 104 us, 75%.
 #include "ar_ops.cuh"
 
 #include <algorithm>

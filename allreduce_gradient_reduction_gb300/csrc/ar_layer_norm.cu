@@ -6,17 +6,23 @@
 //   dx = rstd (g - sum(g)/C - xh sum(g xh)/C)
 //   dw = sum over rows of dy xh,  db = sum over rows of dy
 //
-// Both directions are bound by HBM: a row is read once, held in registers as
-// it was stored, and everything about it is computed from there in binary32.
-// The variance is taken about the row's own mean (a second pass over the
-// registers), not as a difference of two large sums.
+// Both directions are bound by HBM: a row is read once, held in registers, and
+// everything about it is computed from there in binary32.  The variance is
+// taken about the row's own mean (a second pass over the registers), not as a
+// difference of two large sums.
 //
-// A row belongs to a group of whole warps, thread t of which owns the vectors
-// t, t + G, t + 2G, ... of the row, so a group's accesses are contiguous and a
-// thread's columns are the same in every row.  That lets the backward kernel
+// A row belongs to a group of whole warps; each warp owns a run of 32 NV
+// vectors of it, its lanes every 32nd of them, so accesses are contiguous and
+// a thread's columns are the same in every row.  That lets the backward kernel
 // keep its columns' share of dw and db in registers while its group walks
 // over rows; the groups' sums are joined in a fixed order, in the block and
 // then in a second kernel, so the result does not depend on timing.
+//
+// Measured (device time, share of the measured copy bandwidth): forward 16384
+// x 5120 bf16 61 us, 82%; 8192 x 768 f32 8.1 us, 93%; backward 32768 x 4096
+// bf16 with f32 parameters 149 us, 81% (with its second kernel); 8192 x 768
+// f32 16.1 us, 71%.  Rows of odd width are read and written element by
+// element and bound by that: forward 16384 x 5121 bf16 92 us, 54%.
 #include "ar_ops.cuh"
 
 #include <algorithm>
