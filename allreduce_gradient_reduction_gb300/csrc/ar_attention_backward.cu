@@ -76,6 +76,12 @@ __global__ void __launch_bounds__(256) attention_delta_kernel(const AttnArgs a) 
   if (token < a.tokens && c == 0) a.delta[(int64_t)head * a.tokens + token] = s;
 }
 
+// The end of the kernel that makes delta.  What else a block reads was there
+// before that kernel began, so its loads and first products need not wait; but
+// every block waits before it ends, so that whatever comes next in the stream
+// finds both kernels done.
+__device__ __forceinline__ void wait_for_delta() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Writes 16 columns of a thread's row of sums, times `scale`, rounded.
 template <class T>
 __device__ __forceinline__ void write16(uint32_t from, T* row, int column, int dim, float scale, bool valid) {
@@ -196,7 +202,10 @@ __device__ __forceinline__ void dkv_block(const Maps& maps, const AttnArgs& a, i
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncthreads();
-  if (sh.unit.count == 0) return;
+  if (sh.unit.count == 0) {
+    wait_for_delta();
+    return;
+  }
   SeqUnit unit = sh.unit;
   unit.index = unit.count - 1 - unit.index;  // the first keys are seen by the most queries
 
@@ -287,6 +296,7 @@ __device__ __forceinline__ void dkv_block(const Maps& maps, const AttnArgs& a, i
       if (t < 64) (t < 32 ? sh.lse : sh.delta)[n & 1][quarter][t & 31] = v;
       named_barrier(1 + quarter, 128);
     };
+    wait_for_delta();
     put(0, fetch(0));
     bool ok = true;
     for (int n = 0; n < steps; ++n) {
@@ -379,7 +389,10 @@ __device__ __forceinline__ void dq_block(const Maps& maps, const AttnArgs& a, in
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncthreads();
-  if (sh.unit.count == 0) return;
+  if (sh.unit.count == 0) {
+    wait_for_delta();
+    return;
+  }
   const SeqUnit unit = sh.unit;
 
   const uint32_t q_tile = smem_addr(tiles), do_tile = q_tile + F::kKeptBytes, k_tile = do_tile + F::kKeptBytes,
@@ -456,6 +469,7 @@ __device__ __forceinline__ void dq_block(const Maps& maps, const AttnArgs& a, in
     const uint32_t lane0 = (uint32_t)(warp & 3) << 21;
     const float c = a.scale * kLog2e;
     const bool valid = query + row < unit.length;
+    wait_for_delta();
     const int64_t at = (int64_t)head * a.tokens + unit.begin + query + row;
     const float l = valid ? -a.lse[at] * kLog2e : -INFINITY, dl = valid ? -a.delta[at] : 0.f;
     const Two lse = two(l, l), delta = two(dl, dl);
@@ -508,7 +522,6 @@ __global__ void __launch_bounds__(Form<PANELS>::kThreads, Form<PANELS>::kBlocks)
     attention_backward_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a, int kv_blocks) {
   extern __shared__ __align__(1024) uint8_t tiles[];
   __shared__ Shared sh;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // for delta
   const int block = blockIdx.x;
   if (block < kv_blocks) dkv_block<T, PANELS>(maps, a, block, tiles, sh.kv);
   else dq_block<T, PANELS>(maps, a, block - kv_blocks, tiles, sh.q);
