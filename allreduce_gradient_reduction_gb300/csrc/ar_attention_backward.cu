@@ -31,6 +31,8 @@ namespace ar {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kKStages = 3, kVStages = 2;  // tiles of k and v in flight, for dq
+
 // A block keeps 128 keys (or queries) and walks over tiles of kWalk queries
 // (keys).  Heads of up to 64 elements (one panel) need half of tensor memory
 // with 64 of them, so that two blocks share a multiprocessor and one's
@@ -49,6 +51,9 @@ struct Form {
   static constexpr int kColumns = PANELS == 1 ? 256 : 512;
   static constexpr uint32_t kKeptBytes = PANELS * kPanelBytes, kWalkBytes = PANELS * kWalk * 128;
   static constexpr int kStages = PANELS == 1 ? 4 : 2;  // tiles of q and dout in flight
+  // shared memory of the two kinds of block; the first has 128 floats for each worker warp after its tiles
+  static constexpr uint32_t kTilesKV = 2 * kKeptBytes + 2 * kStages * kWalkBytes;
+  static constexpr uint32_t kTilesQ = 2 * kKeptBytes + (kKStages + kVStages) * kWalkBytes;
 };
 
 // delta[head][token] = dout . out: LANES threads to a row, 16 bytes each.
@@ -81,23 +86,6 @@ __global__ void __launch_bounds__(256) attention_delta_kernel(const AttnArgs a) 
 // every block waits before it ends, so that whatever comes next in the stream
 // finds both kernels done.
 __device__ __forceinline__ void wait_for_delta() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
-// Writes 16 columns of a thread's row of sums, times `scale`, rounded.
-template <class T>
-__device__ __forceinline__ void write16(uint32_t from, T* row, int column, int dim, float scale, bool valid) {
-  float o[16];
-  tmem_load16(from + column, o);
-  tmem_wait_load();
-  tmem_loaded(o);
-  if (!valid) return;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    if (column + h * 8 >= dim) break;
-    *reinterpret_cast<uint4*>(row + column + h * 8) =
-        make_uint4(pack2<T>(o[h * 8] * scale, o[h * 8 + 1] * scale), pack2<T>(o[h * 8 + 2] * scale, o[h * 8 + 3] * scale),
-                   pack2<T>(o[h * 8 + 4] * scale, o[h * 8 + 5] * scale), pack2<T>(o[h * 8 + 6] * scale, o[h * 8 + 7] * scale));
-  }
-}
 
 // The kept tile, in boxes of kWalk rows.
 template <int PANELS>
@@ -171,7 +159,6 @@ constexpr int kMostStages = 4;
 struct SharedKV {
   alignas(8) uint64_t kv_full, q_full[kMostStages], do_full[kMostStages], empty[kMostStages], s_full, dp_full, p_ready,
       ds_ready, done, own;
-  alignas(16) float lse[2][4][32], delta[2][4][32];  // [turn][quarter]
   uint32_t tmem;
   int gave_up;
   SeqUnit unit;
@@ -280,54 +267,50 @@ __device__ __forceinline__ void dkv_block(const Maps& maps, const AttnArgs& a, i
     __syncwarp();
   } else {
     // thread: key row, queries [32 quarter, 32 quarter + 32) of each tile
-    const int quarter = warp >> 2, row = (warp & 3) * 32 + lane, t = threadIdx.x & 127;
+    const int quarter = warp >> 2, row = (warp & 3) * 32 + lane;
     const int left = unit.length - unit.index * kTile;  // queries from the first key to the sequence's end
     const uint32_t lane0 = (uint32_t)(warp & 3) << 21, s_at = tmem + lane0 + quarter * 32;
     const float c = a.scale * kLog2e;
-    // threads 0..31 of a quarter fetch its queries' -lse in powers of two, the next 32 their -delta
+    float* stats = reinterpret_cast<float*>(tiles + F::kTilesKV) + warp * 128;  // [turn][lse, delta][32]
+    // Each warp fetches its 32 queries' -lse in powers of two and -delta for
+    // itself: four warps that shared them would meet at every step.
     auto fetch = [&](int n) {
-      const int query = (first + n % per) * kWalk + quarter * 32 + (t & 31);
-      if (t >= 64) return 0.f;
-      if (query >= unit.length) return 0.f;  // masked
+      const int query = (first + n % per) * kWalk + quarter * 32 + lane;
+      if (query >= unit.length) return make_float2(0.f, 0.f);  // masked
       const int64_t at = (int64_t)(kv_head * group + n / per) * a.tokens + unit.begin + query;
-      return t < 32 ? -a.lse[at] * kLog2e : -a.delta[at];
+      return make_float2(-a.lse[at] * kLog2e, -a.delta[at]);
     };
-    auto put = [&](int n, float v) {
-      if (t < 64) (t < 32 ? sh.lse : sh.delta)[n & 1][quarter][t & 31] = v;
-      named_barrier(1 + quarter, 128);
+    auto put = [&](int n, float2 v) {
+      stats[(n & 1) * 64 + lane] = v.x;
+      stats[(n & 1) * 64 + 32 + lane] = v.y;
+      __syncwarp();
     };
     wait_for_delta();
     put(0, fetch(0));
     bool ok = true;
     for (int n = 0; n < steps; ++n) {
-      const float next = n + 1 < steps ? fetch(n + 1) : 0.f;
+      const float2 next = n + 1 < steps ? fetch(n + 1) : make_float2(0.f, 0.f);
       const int from = n % per * kWalk;  // the tile's first query, counted from the first key
       const bool masked = from < kTile || from + kWalk > left;
-      if (!(ok = ok && mbar_wait(smem_addr(&sh.s_full), n & 1, gave_up))) {
-        put(n + 1, next);  // no warp is missing at the quarter's barrier
-        continue;
-      }
+      if (!(ok = mbar_wait(smem_addr(&sh.s_full), n & 1, gave_up))) break;
       tc_fence_after();
       float p[32], d[32];
       uint32_t packed[16];
       tmem_load32(s_at, p);
       tmem_wait_load();
       tmem_loaded(p);
-      const float* lse = sh.lse[n & 1][quarter];
+      const float* lse = stats + (n & 1) * 64;
       probabilities<T>(p, packed, c, [&](int x) { return Two{*reinterpret_cast<const uint64_t*>(lse + x)}; }, masked,
                        [&](int x) { return from + quarter * 32 + x >= row && from + quarter * 32 + x < left; });
       tmem_store16(s_at, packed);
       tmem_wait_store();
       warp_arrive(smem_addr(&sh.p_ready));
-      if (!(ok = mbar_wait(smem_addr(&sh.dp_full), n & 1, gave_up))) {
-        put(n + 1, next);
-        continue;
-      }
+      if (!(ok = mbar_wait(smem_addr(&sh.dp_full), n & 1, gave_up))) break;
       tc_fence_after();
       tmem_load32(s_at + kWalk, d);
       tmem_wait_load();
       tmem_loaded(d);
-      const float* delta = sh.delta[n & 1][quarter];
+      const float* delta = stats + (n & 1) * 64 + 32;
       score_gradients<T>(p, d, packed, [&](int x) { return Two{*reinterpret_cast<const uint64_t*>(delta + x)}; },
                          masked);
       tmem_store16(s_at + kWalk, packed);
@@ -337,21 +320,20 @@ __device__ __forceinline__ void dkv_block(const Maps& maps, const AttnArgs& a, i
     }
     if (ok && mbar_wait(smem_addr(&sh.done), 0, gave_up)) {
       tc_fence_after();
-      const int key = unit.index * kTile + row;
+      // quarter: dv or dk, and which 64 of its columns
       const bool is_dk = quarter & 1;
       const AttnTensor& to = is_dk ? a.dk : a.dv;
+      const int key = unit.index * kTile + (warp & 3) * 32;
       T* out = static_cast<T*>(const_cast<void*>(to.ptr)) + (int64_t)(unit.begin + key) * to.token_stride +
                kv_head * to.head_stride;
-      for (int x = quarter >> 1; x < dim16; x += F::kQuarters / 2)
-        write16<T>(lane0 + (is_dk ? dk_at : dv_at), out, x * 16, a.dim, is_dk ? a.scale : 1.f, key < unit.length);
+      write_rows<T, 64>(lane0 + (is_dk ? dk_at : dv_at), q_tile + warp * 4096, out, to.token_stride, unit.length - key,
+                        (quarter >> 1) * 64, a.dim, is_dk ? a.scale : 1.f);
     }
   }
   leave<PANELS>(&sh.gave_up, warp, tmem);
 }
 
 // ---- dq ---------------------------------------------------------------------------
-
-constexpr int kKStages = 3, kVStages = 2;
 
 struct SharedQ {
   alignas(8) uint64_t q_full, k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages], s_full, s_read,
@@ -499,9 +481,11 @@ __device__ __forceinline__ void dq_block(const Maps& maps, const AttnArgs& a, in
     }
     if (ok && mbar_wait(smem_addr(&sh.done), 0, gave_up)) {
       tc_fence_after();
-      T* out = static_cast<T*>(const_cast<void*>(a.dq.ptr)) + (int64_t)(unit.begin + query + row) * a.dq.token_stride +
+      const int from = query + (warp & 3) * 32;
+      T* out = static_cast<T*>(const_cast<void*>(a.dq.ptr)) + (int64_t)(unit.begin + from) * a.dq.token_stride +
                head * a.dq.head_stride;
-      for (int x = quarter; x < dim16; x += F::kQuarters) write16<T>(lane0 + dq_at, out, x * 16, a.dim, a.scale, valid);
+      write_rows<T, 32>(lane0 + dq_at, k_tile + warp * 2048, out, a.dq.token_stride, unit.length - from, quarter * 32,
+                        a.dim, a.scale);
     }
   }
   leave<PANELS>(&sh.gave_up, warp, tmem);
@@ -531,7 +515,7 @@ template <class T, int PANELS>
 cudaError_t run(int dtype, const AttnArgs& a, cudaStream_t s) {
   static std::atomic<unsigned long long> opened[256];
   using F = Form<PANELS>;
-  constexpr int smem = 2 * F::kKeptBytes + std::max(2 * F::kStages, kKStages + kVStages) * F::kWalkBytes;
+  constexpr int smem = (int)std::max(F::kTilesKV + F::kWorkers / 32 * 512, F::kTilesQ);
   auto* kernel = attention_backward_kernel<T, PANELS>;
   cudaError_t e = open_kernel((const void*)kernel, smem, false, opened);
   if (e != cudaSuccess) return e;

@@ -183,6 +183,46 @@ __device__ __forceinline__ void tmem_store16(uint32_t at, const float (&r)[16]) 
   tmem_store16(at, bits);
 }
 
+// A warp writes COLS columns of its 32 rows of sums from tensor memory, times
+// `scale`, rounded: `rows` of them, `dim` columns in all, from `column` on.
+// The rows go through 64 COLS bytes of shared memory at `stage`, so that the
+// lanes write runs of 2 COLS bytes and not 32 rows at a time.
+template <class T, int COLS>
+__device__ __forceinline__ void write_rows(uint32_t sums, uint32_t stage, T* out, int64_t stride, int rows, int column,
+                                           int dim, float scale) {
+  constexpr int kPieces = COLS / 8;  // 16-byte pieces of a row
+  const int lane = threadIdx.x & 31;
+  auto place = [&](int row, int piece) {  // pieces of a row change places, so that eight lanes reach all banks
+    return stage + row * (COLS * 2) + ((piece ^ (row / (8 / kPieces) & (kPieces - 1))) << 4);
+  };
+#pragma unroll
+  for (int c = 0; c < COLS; c += 16) {
+    if (column + c >= dim) break;
+    float o[16];
+    tmem_load16(sums + column + c, o);
+    tmem_wait_load();
+    tmem_loaded(o);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(place(lane, c / 8 + h)),
+                   "r"(pack2<T>(o[h * 8] * scale, o[h * 8 + 1] * scale)),
+                   "r"(pack2<T>(o[h * 8 + 2] * scale, o[h * 8 + 3] * scale)),
+                   "r"(pack2<T>(o[h * 8 + 4] * scale, o[h * 8 + 5] * scale)),
+                   "r"(pack2<T>(o[h * 8 + 6] * scale, o[h * 8 + 7] * scale))
+                   : "memory");
+  }
+  __syncwarp();
+  const int piece = lane % kPieces, at = column + piece * 8;
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    const int row = lane / kPieces + i * (32 / kPieces);
+    if (row >= rows || at >= dim) continue;
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(place(row, piece)) : "memory");
+    *reinterpret_cast<uint4*>(out + row * stride + at) = v;
+  }
+}
+
 // ---- products -------------------------------------------------------------------------
 
 // Instruction descriptor: f32 sums, A and B of the same 16-bit type, M = 128.
@@ -298,7 +338,9 @@ __device__ __forceinline__ SeqUnit find_unit(const int32_t* cu_seqlens, int seqs
     int above = 0;
     for (int s0 = 0; s0 < seqs; s0 += 32) {
       const int n = look(s0), here = min(32, seqs - s0);
-      for (int k = 0; k < here; ++k) above += max(__shfl_sync(kAll, n, k) - mine, 0);
+      for (int k = 0; k < here; k += 8)  // lanes without a sequence have no units
+#pragma unroll
+        for (int i = 0; i < 8; ++i) above += max(__shfl_sync(kAll, n, k + i) - mine, 0);
     }
     const uint32_t more = __ballot_sync(kAll, above > unit);
     if (!more) return SeqUnit{0, 0, 0, 0};
