@@ -291,25 +291,14 @@ __global__ void __launch_bounds__(Form<PANELS>::kThreads, Form<PANELS>::kBlocks)
     }
     if (n && ok && mbar_wait(smem_addr(&sh.o_done[i]), (n - 1) & 1, gave_up)) {
       tc_fence_after();
-      const int at = first + i * kTile + row;  // within the sequence
+      const int from = first + i * kTile + (warp & 3) * 32, at = from + lane;  // within the sequence
       const int64_t token = unit.begin + at;
-      const float inv = 1.f / sum;
-      T* out = static_cast<T*>(const_cast<void*>(a.out.ptr)) + token * a.out.token_stride + head * a.out.head_stride;
-      for (int d = 0; d < dim16; ++d) {
-        float o[16];
-        tmem_load16(o_at + d * 16, o);
-        tmem_wait_load();
-        tmem_loaded(o);
-        if (at < unit.length) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (d * 16 + h * 8 >= a.dim) break;
-            *reinterpret_cast<uint4*>(out + d * 16 + h * 8) =
-                make_uint4(pack2<T>(o[h * 8] * inv, o[h * 8 + 1] * inv), pack2<T>(o[h * 8 + 2] * inv, o[h * 8 + 3] * inv),
-                           pack2<T>(o[h * 8 + 4] * inv, o[h * 8 + 5] * inv), pack2<T>(o[h * 8 + 6] * inv, o[h * 8 + 7] * inv));
-          }
-        }
-      }
+      T* out = static_cast<T*>(const_cast<void*>(a.out.ptr)) + (int64_t)(unit.begin + from) * a.out.token_stride +
+               head * a.out.head_stride;
+      // through the tile's queries, which nothing reads any more
+      for (int p = 0; p < PANELS; ++p)
+        write_rows<T, 64>(o_at, q_tile + i * kTileBytes + (warp & 3) * 4096, out, a.out.token_stride,
+                          unit.length - from, p * 64, a.dim, 1.f / sum);
       if (a.lse && at < unit.length) a.lse[(int64_t)head * a.tokens + token] = (m * c + log2f(sum)) * kLn2;
     }
   }

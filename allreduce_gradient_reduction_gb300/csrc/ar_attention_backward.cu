@@ -19,10 +19,10 @@
 // each term).  The next tiles' products are issued between the current one's
 // sums, so the tensor cores work while exponentials are taken.
 //
-// Measured: 8192 tokens, 32 heads of 128 over 8 K/V heads, 1.12 ms as one
-// sequence (1.23 PFLOP/s counting five products, 1.72 with the two that are
-// made twice: 90% of the rate of a plain matrix product on the same device),
-// 520 us as three.
+// Measured: 8192 tokens, 32 heads of 128 over 8 K/V heads, 1.10 ms as one
+// sequence (1.26 PFLOP/s counting five products, 1.76 with the two that are
+// made twice: 92% of the rate of a plain matrix product on the same device),
+// 497 us as three; 12 heads of 64, as 13 sequences, 65 us.
 #include "ar_tcgen05.cuh"
 
 #include <algorithm>

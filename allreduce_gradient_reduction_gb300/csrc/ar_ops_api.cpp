@@ -77,7 +77,11 @@ struct Operands {
   }
 };
 
-int status_of(cudaError_t e) { return e == cudaSuccess ? AR_OK : ar::note_cuda_failure(e); }
+int status_of(cudaError_t e) {
+  if (e == cudaSuccess) return AR_OK;
+  (void)cudaGetLastError();  // the next call's launch must not find this one's failure
+  return ar::note_cuda_failure(e);
+}
 
 // Nothing may unwind through the C ABI.
 template <class F>

@@ -192,6 +192,7 @@ __device__ __forceinline__ void write_rows(uint32_t sums, uint32_t stage, T* out
                                            int dim, float scale) {
   constexpr int kPieces = COLS / 8;  // 16-byte pieces of a row
   const int lane = threadIdx.x & 31;
+  __syncwarp();
   auto place = [&](int row, int piece) {  // pieces of a row change places, so that eight lanes reach all banks
     return stage + row * (COLS * 2) + ((piece ^ (row / (8 / kPieces) & (kPieces - 1))) << 4);
   };
