@@ -148,6 +148,12 @@ __device__ __forceinline__ void score_gradients(float (&p)[32], float (&d)[32], 
   }
 }
 
+// Elements x and x + 1 of a vector in shared memory, x even, read four at a time.
+__device__ __forceinline__ Two two_of(const float* v, int x) {
+  const ulonglong2 four = *reinterpret_cast<const ulonglong2*>(v + (x & ~3));
+  return Two{x & 2 ? four.y : four.x};
+}
+
 struct Maps {
   CUtensorMap q, k, v, dout;
 };
@@ -176,6 +182,8 @@ __device__ __forceinline__ void dkv_block(const Maps& maps, const AttnArgs& a, i
       sh.unit = u;
       sh.gave_up = 0;
     }
+  } else if (warp == F::kIssuer) {
+    tmem_alloc(smem_addr(&sh.tmem), F::kColumns);
   } else if (warp == F::kLoader && lane == 0) {
     uint64_t* const one[] = {&sh.kv_full, &sh.s_full, &sh.dp_full, &sh.done, &sh.own};
     for (uint64_t* b : one) mbar_init(smem_addr(b), 1);
@@ -188,8 +196,11 @@ __device__ __forceinline__ void dkv_block(const Maps& maps, const AttnArgs& a, i
     mbar_init(smem_addr(&sh.ds_ready), F::kWorkers / 32);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
   if (sh.unit.count == 0) {
+    if (warp == F::kIssuer) tmem_free(sh.tmem, F::kColumns);
     wait_for_delta();
     return;
   }
@@ -199,8 +210,8 @@ __device__ __forceinline__ void dkv_block(const Maps& maps, const AttnArgs& a, i
   const uint32_t k_tile = smem_addr(tiles), v_tile = k_tile + F::kKeptBytes, q_tile = v_tile + F::kKeptBytes,
                  do_tile = q_tile + kStages * F::kWalkBytes;
   volatile int* gave_up = &sh.gave_up;
-  if (warp == F::kIssuer) tmem_alloc(smem_addr(&sh.tmem), F::kColumns);
-  // step n: head n / per of the group, tile first + n % per of the sequence's queries
+  // each step takes a tile of the sequence's queries from the first that sees
+  // the keys, head after head of the group
   const int group = a.heads / a.kv_heads, first = unit.index * (kTile / kWalk);
   const int per = (unit.length + kWalk - 1) / kWalk - first, steps = group * per;
   const int dim16 = (a.dim + 15) / 16;
@@ -210,9 +221,6 @@ __device__ __forceinline__ void dkv_block(const Maps& maps, const AttnArgs& a, i
     load_kept<PANELS>(&maps.k, k_tile, kv_head, unit.begin + unit.index * kTile, bar);
     load_kept<PANELS>(&maps.v, v_tile, kv_head, unit.begin + unit.index * kTile, bar);
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
   // Tensor memory: scores, dout v^T, dv, dk.  p and ds take the places of the
   // first two, each quarter's 16 columns of pairs at the front of the 32 that
   // it read.
@@ -220,10 +228,11 @@ __device__ __forceinline__ void dkv_block(const Maps& maps, const AttnArgs& a, i
 
   if (warp == F::kLoader) {
     uint32_t own_parity = 0;
+    int head = kv_head * group, tile = 0;
     for (int n = 0; n < steps; ++n) {
       const int stage = n % kStages;
       if (n >= kStages && !mbar_wait(smem_addr(&sh.empty[stage]), (n / kStages - 1) & 1, gave_up)) break;
-      const int head = kv_head * group + n / per, query = (first + n % per) * kWalk;
+      const int query = (first + tile) * kWalk;
       if (!load_tile<PANELS, kWalk>(&maps.q, q_tile + stage * F::kWalkBytes, head, unit.begin + query,
                                     unit.length - query, smem_addr(&sh.q_full[stage]), smem_addr(&sh.own), &own_parity,
                                     gave_up) ||
@@ -231,6 +240,7 @@ __device__ __forceinline__ void dkv_block(const Maps& maps, const AttnArgs& a, i
                                     unit.length - query, smem_addr(&sh.do_full[stage]), smem_addr(&sh.own), &own_parity,
                                     gave_up))
         break;
+      if (++tile == per) tile = 0, ++head;
     }
   } else if (warp == F::kIssuer) {
     if (elect_one()) {
@@ -274,10 +284,13 @@ __device__ __forceinline__ void dkv_block(const Maps& maps, const AttnArgs& a, i
     float* stats = reinterpret_cast<float*>(tiles + F::kTilesKV) + warp * 128;  // [turn][lse, delta][32]
     // Each warp fetches its 32 queries' -lse in powers of two and -delta for
     // itself: four warps that shared them would meet at every step.
-    auto fetch = [&](int n) {
-      const int query = (first + n % per) * kWalk + quarter * 32 + lane;
+    int next_tile = 0;
+    int64_t next_head = (int64_t)kv_head * group * a.tokens + unit.begin;
+    auto fetch = [&]() {  // of the next step, and on
+      const int query = (first + next_tile) * kWalk + quarter * 32 + lane;
+      const int64_t at = next_head + query;
+      if (++next_tile == per) next_tile = 0, next_head += a.tokens;
       if (query >= unit.length) return make_float2(0.f, 0.f);  // masked
-      const int64_t at = (int64_t)(kv_head * group + n / per) * a.tokens + unit.begin + query;
       return make_float2(-a.lse[at] * kLog2e, -a.delta[at]);
     };
     auto put = [&](int n, float2 v) {
@@ -286,11 +299,12 @@ __device__ __forceinline__ void dkv_block(const Maps& maps, const AttnArgs& a, i
       __syncwarp();
     };
     wait_for_delta();
-    put(0, fetch(0));
+    put(0, fetch());
+    int tile = 0;
     bool ok = true;
     for (int n = 0; n < steps; ++n) {
-      const float2 next = n + 1 < steps ? fetch(n + 1) : make_float2(0.f, 0.f);
-      const int from = n % per * kWalk;  // the tile's first query, counted from the first key
+      const float2 next = n + 1 < steps ? fetch() : make_float2(0.f, 0.f);
+      const int from = tile * kWalk;  // the tile's first query, counted from the first key
       const bool masked = from < kTile || from + kWalk > left;
       if (!(ok = mbar_wait(smem_addr(&sh.s_full), n & 1, gave_up))) break;
       tc_fence_after();
@@ -300,7 +314,7 @@ __device__ __forceinline__ void dkv_block(const Maps& maps, const AttnArgs& a, i
       tmem_wait_load();
       tmem_loaded(p);
       const float* lse = stats + (n & 1) * 64;
-      probabilities<T>(p, packed, c, [&](int x) { return Two{*reinterpret_cast<const uint64_t*>(lse + x)}; }, masked,
+      probabilities<T>(p, packed, c, [&](int x) { return two_of(lse, x); }, masked,
                        [&](int x) { return from + quarter * 32 + x >= row && from + quarter * 32 + x < left; });
       tmem_store16(s_at, packed);
       tmem_wait_store();
@@ -311,12 +325,13 @@ __device__ __forceinline__ void dkv_block(const Maps& maps, const AttnArgs& a, i
       tmem_wait_load();
       tmem_loaded(d);
       const float* delta = stats + (n & 1) * 64 + 32;
-      score_gradients<T>(p, d, packed, [&](int x) { return Two{*reinterpret_cast<const uint64_t*>(delta + x)}; },
+      score_gradients<T>(p, d, packed, [&](int x) { return two_of(delta, x); },
                          masked);
       tmem_store16(s_at + kWalk, packed);
       tmem_wait_store();
       warp_arrive(smem_addr(&sh.ds_ready));
       put(n + 1, next);
+      if (++tile == per) tile = 0;
     }
     if (ok && mbar_wait(smem_addr(&sh.done), 0, gave_up)) {
       tc_fence_after();
@@ -355,6 +370,8 @@ __device__ __forceinline__ void dq_block(const Maps& maps, const AttnArgs& a, in
       sh.unit = u;
       sh.gave_up = 0;
     }
+  } else if (warp == F::kIssuer) {
+    tmem_alloc(smem_addr(&sh.tmem), F::kColumns);
   } else if (warp == F::kLoader && lane == 0) {
     uint64_t* const one[] = {&sh.q_full, &sh.s_full, &sh.dp_full[0], &sh.dp_full[1], &sh.done, &sh.own};
     for (uint64_t* b : one) mbar_init(smem_addr(b), 1);
@@ -370,8 +387,11 @@ __device__ __forceinline__ void dq_block(const Maps& maps, const AttnArgs& a, in
     mbar_init(smem_addr(&sh.ds_ready), F::kWorkers / 32);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
   if (sh.unit.count == 0) {
+    if (warp == F::kIssuer) tmem_free(sh.tmem, F::kColumns);
     wait_for_delta();
     return;
   }
@@ -380,7 +400,6 @@ __device__ __forceinline__ void dq_block(const Maps& maps, const AttnArgs& a, in
   const uint32_t q_tile = smem_addr(tiles), do_tile = q_tile + F::kKeptBytes, k_tile = do_tile + F::kKeptBytes,
                  v_tile = k_tile + kKStages * F::kWalkBytes;
   volatile int* gave_up = &sh.gave_up;
-  if (warp == F::kIssuer) tmem_alloc(smem_addr(&sh.tmem), F::kColumns);
   const int query = unit.index * kTile;
   const int steps = min(query + kTile, unit.length + kWalk - 1) / kWalk;  // tiles of keys that the queries see
   const int dim16 = (a.dim + 15) / 16;
@@ -390,9 +409,6 @@ __device__ __forceinline__ void dq_block(const Maps& maps, const AttnArgs& a, in
     load_kept<PANELS>(&maps.q, q_tile, head, unit.begin + query, bar);
     load_kept<PANELS>(&maps.dout, do_tile, head, unit.begin + query, bar);
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
   // Tensor memory: scores, dout v^T (in two places by turns), dq.  The next
   // tile's scores and dout v^T are under way while this one's ds is made.
   const uint32_t tmem = sh.tmem, dq_at = tmem + 3 * kWalk;
