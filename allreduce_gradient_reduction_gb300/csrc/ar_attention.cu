@@ -86,6 +86,8 @@ __global__ void __launch_bounds__(Form<PANELS>::kThreads, Form<PANELS>::kBlocks)
       sh.unit = u;
       sh.gave_up = 0;
     }
+  } else if (warp == F::kIssuer) {
+    tmem_alloc(smem_addr(&sh.tmem), F::kColumns);
   } else if (warp == F::kLoader && lane == 0) {
     for (int i = 0; i < kTiles; ++i) {
       mbar_init(smem_addr(&sh.q_full[i]), 1);
@@ -102,10 +104,14 @@ __global__ void __launch_bounds__(Form<PANELS>::kThreads, Form<PANELS>::kBlocks)
     mbar_init(smem_addr(&sh.own), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  tc_fence_before();
   __syncthreads();
-  if (sh.unit.count == 0) return;
+  tc_fence_after();
+  if (sh.unit.count == 0) {
+    if (warp == F::kIssuer) tmem_free(sh.tmem, F::kColumns);
+    return;
+  }
   const SeqUnit unit = sh.unit;
-  if (warp == F::kIssuer) tmem_alloc(smem_addr(&sh.tmem), F::kColumns);
 
   constexpr uint32_t kTileBytes = PANELS * kPanelBytes;
   const uint32_t q_tile = smem_addr(tiles), kv_tile = q_tile + kTiles * kTileBytes;
@@ -117,8 +123,7 @@ __global__ void __launch_bounds__(Form<PANELS>::kThreads, Form<PANELS>::kBlocks)
   const int most = max(blocks[0], blocks[kTiles - 1]);
   const int dim16 = (a.dim + 15) / 16;
 
-  // The loads need no tensor memory: they begin before it has been given.
-  // Q tiles first, then K 0, V 0, K 1, V 1, ...
+  // loads: Q tiles first, then K 0, V 0, K 1, V 1, ...
   const int kv_head = head / (a.heads / a.kv_heads);
   uint32_t own_parity = 0;
   auto load = [&](int n) {
@@ -127,21 +132,6 @@ __global__ void __launch_bounds__(Form<PANELS>::kThreads, Form<PANELS>::kBlocks)
                                     n & 1 ? unit.length - key : kTile, smem_addr(&sh.kv_full[stage]),
                                     smem_addr(&sh.own), &own_parity, gave_up);
   };
-  if (warp == F::kLoader) {
-    if (lane == 0) {
-      for (int i = 0; i < kTiles; ++i) {
-        if (!blocks[i]) continue;
-        const uint32_t bar = smem_addr(&sh.q_full[i]);
-        mbar_expect(bar, kTileBytes);
-        for (int p = 0; p < PANELS; ++p)
-          tma_load(q_tile + i * kTileBytes + p * kPanelBytes, &q_map, p * 64, head, unit.begin + first + i * kTile, bar);
-      }
-    }
-    load(0);
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
   // tensor memory: each tile's scores, then probabilities where they are apart, then outputs
   const uint32_t tmem = sh.tmem;
   auto p_at = [&](int i, int half) { return tmem + (F::kApart ? 128 + half * 32 : i * 128 + half * 32); };
@@ -150,7 +140,16 @@ __global__ void __launch_bounds__(Form<PANELS>::kThreads, Form<PANELS>::kBlocks)
   if (warp >= F::kIssuer) {
     if constexpr (F::kThreads == 384) give_registers();
     if (warp == F::kLoader) {
-      for (int n = 1; n < 2 * most; ++n) {
+      if (lane == 0) {
+        for (int i = 0; i < kTiles; ++i) {
+          if (!blocks[i]) continue;
+          const uint32_t bar = smem_addr(&sh.q_full[i]);
+          mbar_expect(bar, kTileBytes);
+          for (int p = 0; p < PANELS; ++p)
+            tma_load(q_tile + i * kTileBytes + p * kPanelBytes, &q_map, p * 64, head, unit.begin + first + i * kTile, bar);
+        }
+      }
+      for (int n = 0; n < 2 * most; ++n) {
         if (n >= kStages && !mbar_wait(smem_addr(&sh.kv_empty[n % kStages]), (n / kStages - 1) & 1, gave_up)) break;
         if (!load(n)) break;
       }
