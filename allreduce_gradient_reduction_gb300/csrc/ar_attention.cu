@@ -14,7 +14,7 @@
 //
 // Measured: 8192 tokens of one sequence, 32 heads of 128 over 8 K/V heads, 351
 // us (1.57 PFLOP/s, 82% of the rate of a plain matrix product on the same
-// device); 32 heads of 64, 289 us (the products alone are half of it: 128 x 128
+// device); 32 heads of 64, 283 us (the products alone are half of it: 128 x 128
 // exponentials at one every eight cycles a lane take as long as 64 elements'
 // products).
 //

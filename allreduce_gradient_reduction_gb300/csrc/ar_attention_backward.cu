@@ -19,10 +19,12 @@
 // each term).  The next tiles' products are issued between the current one's
 // sums, so the tensor cores work while exponentials are taken.
 //
-// Measured: 8192 tokens, 32 heads of 128 over 8 K/V heads, 1.10 ms as one
-// sequence (1.26 PFLOP/s counting five products, 1.76 with the two that are
-// made twice: 92% of the rate of a plain matrix product on the same device),
-// 497 us as three; 12 heads of 64, as 13 sequences, 65 us.
+// Measured: 8192 tokens, 32 heads of 128 over 8 K/V heads, 1.07 ms as one
+// sequence (1.29 PFLOP/s counting five products, 1.80 with the two that are
+// made twice: 95% of the rate of a plain matrix product on the same device),
+// 484 us as three; 12 heads of 64, as 13 sequences, 62 us.  The blocks of dq
+// spend 93% of a step in products, those of dk and dv 77%: there a step's
+// exponentials come between two products that need them.
 #include "ar_tcgen05.cuh"
 
 #include <algorithm>
@@ -38,7 +40,8 @@ constexpr int kKStages = 3, kVStages = 2;  // tiles of k and v in flight, for dq
 // with 64 of them, so that two blocks share a multiprocessor and one's
 // exponentials, or its start and end, overlap the other's products
 // (8192 tokens in 13 sequences, 12 heads of 64: 95.7 us with one block and
-// tiles of 128, 71.7 us so; 8192 tokens of one, 32 heads of 64: 967 and 879).
+// tiles of 128, 71.7 us so, with nothing else changed; 8192 tokens of one, 32
+// heads of 64: 967 and 879).
 // Four threads, or two, have a row's columns.
 template <int PANELS>
 struct Form {
