@@ -20,8 +20,8 @@
 //
 // Measured (device time, share of the measured copy bandwidth): forward 16384
 // x 5120 bf16 61 us, 82%; 8192 x 768 f32 8.1 us, 93%; backward 32768 x 4096
-// bf16 with f32 parameters 149 us, 81% (with its second kernel); 8192 x 768
-// f32 16.1 us, 71%.  Rows of odd width are read and written element by
+// bf16 with f32 parameters 143 us, 84% (with its second kernel); 8192 x 768
+// f32 15.4 us, 74%.  Rows of odd width are read and written element by
 // element and bound by that: forward 16384 x 5121 bf16 92 us, 54%.
 #include "ar_ops.cuh"
 
@@ -888,12 +888,15 @@ cudaError_t resident(K* kernel, int threads, int smem, int64_t* blocks) {
 // How deep a group's ring is.  A row is in registers while it is worked on and
 // its place is being filled again, so one place is enough to keep loads on
 // their way; more where the groups that fit a multiprocessor (by registers)
-// have less than 64 KB of places.  Not more than that: what shared memory does
-// not take is the L1 cache that the parameters are read from (16384 x 4096
-// bf16 with f32 parameters, forward, with places for 128 KB: 80 us).
-int ring_stages(int row_bytes, int threads, int registers) {
+// have less than `bytes` of places.  Not more than that: what shared memory
+// does not take is the L1 cache that the parameters are read from (16384 x
+// 4096 bf16 with f32 parameters read again for each row, forward: 64 KB 65 us,
+// 128 KB 80 us; backward, from HBM, 8192 x 768 f32 and 32768 x 4096 bf16: 64 KB
+// 23.7 and 152 us, 96 KB 21.8 and 147, 128 KB 21.9 and 149).
+constexpr int kForwardRing = 64 * 1024, kBackwardRing = 96 * 1024;
+int ring_stages(int bytes, int row_bytes, int threads, int registers) {
   const int groups = std::max(1, 65536 / registers / threads);
-  return std::max(1, std::min(kRing, (64 * 1024 / groups + row_bytes / 2) / row_bytes));
+  return std::max(1, std::min(kRing, (bytes / groups + row_bytes / 2) / row_bytes));
 }
 
 template <class T, class P>
@@ -911,7 +914,8 @@ int ring_groups(int threads, int64_t rows) {
 template <class T>
 cudaError_t start_ring(void (*kernel)(LayerNormArgs, int, int), std::atomic<unsigned long long>* opened, int threads,
                        int registers, const LayerNormArgs& a, cudaStream_t s) {
-  const int slot = ring_slot<T>(a.cols), stages = ring_stages(slot, threads, registers), groups = threads >= 128 ? 1 : ring_groups(threads, a.rows);
+  const int slot = ring_slot<T>(a.cols), stages = ring_stages(kForwardRing, slot, threads, registers);
+  const int groups = threads >= 128 ? 1 : ring_groups(threads, a.rows);
   const int smem = groups * stages * slot;
   cudaError_t e = open_kernel((const void*)kernel, kRingMaxShared, false, opened);
   if (e != cudaSuccess) return e;
@@ -1016,7 +1020,7 @@ cudaError_t start_backward_ring(void (*kernel)(LayerNormBackwardArgs, int, int),
                                 int threads, int columns, bool wide, const LayerNormBackwardArgs& a, cudaStream_t s) {
   const int slot = ring_slot<T>(a.cols);
   const int stages = wide ? std::min(2, kRingMaxShared / (2 * slot))
-                          : ring_stages(2 * slot, threads, backward_registers(columns));
+                          : ring_stages(kBackwardRing, 2 * slot, threads, backward_registers(columns));
   const int groups = wide ? 1 : ring_groups(threads, a.rows);
   const int smem = std::max(groups * 2 * stages * slot, groups > 1 ? 2 * threads * columns * (int)sizeof(float) : 0);
   cudaError_t e = open_kernel((const void*)kernel, kRingMaxShared, false, opened);
