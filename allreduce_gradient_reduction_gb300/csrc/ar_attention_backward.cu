@@ -33,6 +33,17 @@ namespace ar {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
+
+// Probabilities are at most one.  f16, whose smallest number is 2^-24 and
+// largest 2^16, holds them times 2^15 in the product for dv, so that one of
+// 2^-40 is not lost yet (thousands of them may add up to a normal number); the
+// power is part of the exponential's argument and is taken out of the sums.
+// bf16 has the range of binary32.
+template <class T>
+constexpr float kShift = __is_same(T, __half) ? 15.f : 0.f;
+template <class T>
+constexpr float kUnshift = __is_same(T, __half) ? 1.f / 32768.f : 1.f;
+
 constexpr int kKStages = 3, kVStages = 2;  // tiles of k and v in flight, for dq
 
 // A block keeps 128 keys (or queries) and walks over tiles of kWalk queries
@@ -133,11 +144,12 @@ __device__ __forceinline__ void probabilities(float (&p)[32], uint32_t (&packed)
   for (int x = 0; x < 32; x += 2) packed[x / 2] = pack2<T>(p[x], p[x + 1]);
 }
 
-// Pairs of ds = p (d - delta).  What is not seen has p = 0 and no ds, whatever
-// d holds there (tokens of another sequence, zeros times an infinity).
+// Pairs of ds = p (by d - by delta).  What is not seen has p = 0 and no ds,
+// whatever d holds there (tokens of another sequence, zeros times an infinity).
 template <class T, class L>
-__device__ __forceinline__ void score_gradients(float (&p)[32], float (&d)[32], uint32_t (&packed)[16], L minus_delta,
-                                                bool masked) {
+__device__ __forceinline__ void score_gradients(float (&p)[32], float (&d)[32], uint32_t (&packed)[16], float by,
+                                                L minus_delta, bool masked) {
+  const Two by2 = two(by, by);
   if (masked) {
 #pragma unroll
     for (int x = 0; x < 32; ++x)
@@ -146,7 +158,7 @@ __device__ __forceinline__ void score_gradients(float (&p)[32], float (&d)[32], 
 #pragma unroll
   for (int x = 0; x < 32; x += 2) {
     float lo, hi;
-    split(mul2(two(p[x], p[x + 1]), add2(two(d[x], d[x + 1]), minus_delta(x))), lo, hi);
+    split(mul2(two(p[x], p[x + 1]), fma2(two(d[x], d[x + 1]), by2, minus_delta(x))), lo, hi);
     packed[x / 2] = pack2<T>(lo, hi);
   }
 }
@@ -286,7 +298,8 @@ __device__ __forceinline__ void dkv_block(const Maps& maps, const AttnArgs& a, i
     const float c = a.scale * kLog2e;
     float* stats = reinterpret_cast<float*>(tiles + F::kTilesKV) + warp * 128;  // [turn][lse, delta][32]
     // Each warp fetches its 32 queries' -lse in powers of two and -delta for
-    // itself: four warps that shared them would meet at every step.
+    // itself: four warps that shared them would meet at every step.  What the
+    // probabilities are held times is in the first and out of the second.
     int next_tile = 0;
     int64_t next_head = (int64_t)kv_head * group * a.tokens + unit.begin;
     auto fetch = [&]() {  // of the next step, and on
@@ -294,7 +307,7 @@ __device__ __forceinline__ void dkv_block(const Maps& maps, const AttnArgs& a, i
       const int64_t at = next_head + query;
       if (++next_tile == per) next_tile = 0, next_head += a.tokens;
       if (query >= unit.length) return make_float2(0.f, 0.f);  // masked
-      return make_float2(-a.lse[at] * kLog2e, -a.delta[at]);
+      return make_float2(fmaf(-a.lse[at], kLog2e, kShift<T>), -a.delta[at] * kUnshift<T>);
     };
     auto put = [&](int n, float2 v) {
       stats[(n & 1) * 64 + lane] = v.x;
@@ -328,8 +341,7 @@ __device__ __forceinline__ void dkv_block(const Maps& maps, const AttnArgs& a, i
       tmem_wait_load();
       tmem_loaded(d);
       const float* delta = stats + (n & 1) * 64 + 32;
-      score_gradients<T>(p, d, packed, [&](int x) { return two_of(delta, x); },
-                         masked);
+      score_gradients<T>(p, d, packed, kUnshift<T>, [&](int x) { return two_of(delta, x); }, masked);
       tmem_store16(s_at + kWalk, packed);
       tmem_wait_store();
       warp_arrive(smem_addr(&sh.ds_ready));
@@ -345,7 +357,7 @@ __device__ __forceinline__ void dkv_block(const Maps& maps, const AttnArgs& a, i
       T* out = static_cast<T*>(const_cast<void*>(to.ptr)) + (int64_t)(unit.begin + key) * to.token_stride +
                kv_head * to.head_stride;
       write_rows<T, 64>(lane0 + (is_dk ? dk_at : dv_at), q_tile + warp * 4096, out, to.token_stride, unit.length - key,
-                        (quarter >> 1) * 64, a.dim, is_dk ? a.scale : 1.f);
+                        (quarter >> 1) * 64, a.dim, is_dk ? a.scale : kUnshift<T>);
     }
   }
   leave<PANELS>(&sh.gave_up, warp, tmem);
@@ -493,7 +505,7 @@ __device__ __forceinline__ void dq_block(const Maps& maps, const AttnArgs& a, in
       tmem_load32(dp, d);
       tmem_wait_load();
       tmem_loaded(d);
-      score_gradients<T>(p, d, packed, [&](int) { return delta; }, masked);
+      score_gradients<T>(p, d, packed, 1.f, [&](int) { return delta; }, masked);
       tmem_store16(dp, packed);
       tmem_wait_store();
       warp_arrive(smem_addr(&sh.ds_ready));

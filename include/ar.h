@@ -559,7 +559,8 @@ int ar_attention(const ar_attention_tensor* q, const ar_attention_tensor* k, con
  *   out, lse    of the forward call on the same q, k, v and cu_seqlens
  *   workspace   16-byte aligned device memory of at least
  *               ar_attention_workspace_bytes bytes
- * p and da are rounded to dtype for their products.
+ * p and da are rounded to dtype for their products; f16 holds p times 2^15
+ * meanwhile, so that it counts down to 2^-40.
  */
 int ar_attention_backward(const ar_attention_tensor* dout, const ar_attention_tensor* q, const ar_attention_tensor* k,
                           const ar_attention_tensor* v, const ar_attention_tensor* out, const float* lse,
