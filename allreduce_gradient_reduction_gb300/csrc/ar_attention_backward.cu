@@ -367,7 +367,7 @@ __device__ __forceinline__ void dkv_block(const Maps& maps, const AttnArgs& a, i
 
 struct SharedQ {
   alignas(8) uint64_t q_full, k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages], s_full, s_read,
-      dp_full[2], ds_ready, done, own;
+      dp_full[2], ds_ready[2], done, own;
   uint32_t tmem;
   int gave_up;
   SeqUnit unit;
@@ -399,7 +399,7 @@ __device__ __forceinline__ void dq_block(const Maps& maps, const AttnArgs& a, in
       mbar_init(smem_addr(&sh.v_empty[i]), 1);
     }
     mbar_init(smem_addr(&sh.s_read), F::kWorkers / 32);
-    mbar_init(smem_addr(&sh.ds_ready), F::kWorkers / 32);
+    for (int i = 0; i < 2; ++i) mbar_init(smem_addr(&sh.ds_ready[i]), F::kWorkers / 32);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   tc_fence_before();
@@ -425,7 +425,10 @@ __device__ __forceinline__ void dq_block(const Maps& maps, const AttnArgs& a, in
     load_kept<PANELS>(&maps.dout, do_tile, head, unit.begin + query, bar);
   }
   // Tensor memory: scores, dout v^T (in two places by turns), dq.  The next
-  // tile's scores and dout v^T are under way while this one's ds is made.
+  // tile's scores and dout v^T are under way while this one's ds is made.  So a
+  // warp may have finished the next step before another has this one, though
+  // not one more (the scores after it wait for every warp's s_read): ds_ready is
+  // two barriers by turns, as one would count the first warp in both places.
   const uint32_t tmem = sh.tmem, dq_at = tmem + 3 * kWalk;
   auto dp_at = [&](int n) { return tmem + kWalk * (1 + (n & 1)); };
 
@@ -467,7 +470,7 @@ __device__ __forceinline__ void dq_block(const Maps& maps, const AttnArgs& a, in
           tc_fence_after();
           if (!(ok = scores(n + 1) && dprob(n + 1))) break;
         }
-        if (!(ok = mbar_wait(smem_addr(&sh.ds_ready), n & 1, gave_up))) break;
+        if (!(ok = mbar_wait(smem_addr(&sh.ds_ready[n & 1]), (n >> 1) & 1, gave_up))) break;
         tc_fence_after();
         for (int h = 0; h < F::kQuarters; ++h)
           product_ts<2>(dq_at, dp_at(n) + h * 32, k_tile + (n % kKStages) * F::kWalkBytes, h, sums, n > 0 || h > 0);
@@ -508,7 +511,7 @@ __device__ __forceinline__ void dq_block(const Maps& maps, const AttnArgs& a, in
       score_gradients<T>(p, d, packed, 1.f, [&](int) { return delta; }, masked);
       tmem_store16(dp, packed);
       tmem_wait_store();
-      warp_arrive(smem_addr(&sh.ds_ready));
+      warp_arrive(smem_addr(&sh.ds_ready[n & 1]));
     }
     if (ok && mbar_wait(smem_addr(&sh.done), 0, gave_up)) {
       tc_fence_after();
