@@ -44,6 +44,29 @@ constexpr float kShift = __is_same(T, __half) ? 15.f : 0.f;
 template <class T>
 constexpr float kUnshift = __is_same(T, __half) ? 1.f / 32768.f : 1.f;
 
+// Score gradients are as large as dout, whose size is the user's (a loss may be
+// scaled by any power of two), times a probability.  f16 holds them as they are
+// where the block's largest lies in [2^-12, 65504], so that what is too small
+// to count is below 2^-13 of it.  Otherwise the block walks again, with them
+// times another power of two:
+//   - One past 65504 is an infinity in f16 and leaves none of its row's sums
+//     finite, which is seen when they are written: 2^-13 and, if need be, 2^-26,
+//     which no product of f16 operands outgrows.  What is lost is below 2^-28
+//     of the largest.
+//   - A thread looks at one of its 32 in each step.  If none of the block's is
+//     2^-12, 2^26; should larger ones overflow then, 2^13 and 1.
+// Device time of 8191 tokens in 13 sequences, 12 heads of 64: 79.1 us, and 76.8
+// without any of this; 82.2 with a look at all 32 for the exact power, 81.3 with
+// all walks in one loop (the first is compiled apart, its power a constant).
+// Walks that follow cost as much each: 3000 tokens, 12 heads of 64, 67 us with
+// one walk, 124 with two.  (A power that is known beforehand would have to bound
+// v and dout over a whole sequence, a pass of its own over both; a fixed one
+// loses either kind.)
+template <class T>
+constexpr bool kScaled = __is_same(T, __half);
+constexpr float kTooSmall = 0x1p-12f, kUnknown = 0x1p-100f;
+constexpr float kRaised = 0x1p26f, kLowered = 0x1p-13f, kLeast = 0x1p-26f;
+
 constexpr int kKStages = 3, kVStages = 2;  // tiles of k and v in flight, for dq
 
 // A block keeps 128 keys (or queries) and walks over tiles of kWalk queries
@@ -110,8 +133,40 @@ __device__ __forceinline__ void load_kept(const CUtensorMap* map, uint32_t dst, 
       tma_load(dst + p * kPanelBytes + r * 128, map, p * 64, head, token + r, bar);
 }
 
-template <int PANELS>
-__device__ __forceinline__ void leave(int* gave_up, int warp, uint32_t tmem) {
+// Where a first walk has met nothing but zeros: whether a worker's part of its
+// row of dout (64 of the tile's bytes) holds anything else.
+__device__ __forceinline__ bool any_element(uint32_t at) {
+  uint32_t any = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at + i * 16) : "memory");
+    any |= v.x | v.y | v.z | v.w;
+  }
+  return (any & 0x7FFF7FFFu) != 0;
+}
+
+// What a worker has seen, for leave(): infinity where sums are not finite, zero
+// if there is nothing but zeros.
+template <class T>
+__device__ __forceinline__ void put_most(float most, bool finite, float* each) {
+  if constexpr (!kScaled<T>) return;
+  __syncwarp();
+  most = warp_max(finite ? most : INFINITY);
+  if ((threadIdx.x & 31) == 0) each[threadIdx.x >> 5] = most;
+}
+
+// What a block keeps from one walk to the next.
+struct State {
+  float by = 1.f;           // what the score gradients are held times
+  int walks = 0;            // made
+  uint32_t own_parity = 0;  // the loader's
+};
+
+// The end of a walk: true, with another power, if the block has to walk again.
+template <class T, int PANELS>
+__device__ __forceinline__ bool leave(int* gave_up, int warp, uint32_t tmem, const float* each, State& state) {
+  using F = Form<PANELS>;
   tc_fence_before();
   __syncthreads();
   if (*(volatile int*)gave_up) {
@@ -119,8 +174,23 @@ __device__ __forceinline__ void leave(int* gave_up, int warp, uint32_t tmem) {
     for (int i = 0; i < 100; ++i) __nanosleep(100000);
     if (threadIdx.x == 0) g_status = AR_ERR_TIMEOUT;
     __syncthreads();
+  } else if (kScaled<T>) {
+    float most = 0.f;
+#pragma unroll
+    for (int i = 0; i < F::kWorkers / 32; ++i) most = fmaxf(most, each[i]);
+    const bool lower = most == INFINITY && state.by > kLeast;
+    const bool raise = state.walks == 0 && most > 0.f && most < kTooSmall;
+    if (lower || raise) {
+      state.by = lower ? state.by * kLowered : kRaised;
+      ++state.walks;
+      fence_async_shared();  // tiles are copied to where results have been
+      __syncthreads();
+      tc_fence_after();
+      return true;
+    }
   }
-  if (warp == Form<PANELS>::kIssuer) tmem_free(tmem, Form<PANELS>::kColumns);
+  if (warp == F::kIssuer) tmem_free(tmem, F::kColumns);
+  return false;
 }
 
 // 32 scores of a thread become probabilities 2^(c s - lse) in place, and pairs
@@ -146,6 +216,7 @@ __device__ __forceinline__ void probabilities(float (&p)[32], uint32_t (&packed)
 
 // Pairs of ds = p (by d - by delta).  What is not seen has p = 0 and no ds,
 // whatever d holds there (tokens of another sequence, zeros times an infinity).
+// The first of them is left in d, where f16 looks at it.
 template <class T, class L>
 __device__ __forceinline__ void score_gradients(float (&p)[32], float (&d)[32], uint32_t (&packed)[16], float by,
                                                 L minus_delta, bool masked) {
@@ -157,9 +228,8 @@ __device__ __forceinline__ void score_gradients(float (&p)[32], float (&d)[32], 
   }
 #pragma unroll
   for (int x = 0; x < 32; x += 2) {
-    float lo, hi;
-    split(mul2(two(p[x], p[x + 1]), fma2(two(d[x], d[x + 1]), by2, minus_delta(x))), lo, hi);
-    packed[x / 2] = pack2<T>(lo, hi);
+    split(mul2(two(p[x], p[x + 1]), fma2(two(d[x], d[x + 1]), by2, minus_delta(x))), d[x], d[x + 1]);
+    packed[x / 2] = pack2<T>(d[x], d[x + 1]);
   }
 }
 
@@ -183,42 +253,32 @@ struct SharedKV {
   uint32_t tmem;
   int gave_up;
   SeqUnit unit;
+  float most[16];  // what each worker warp has seen of the score gradients
 };
 
-template <class T, int PANELS>
-__device__ __forceinline__ void dkv_block(const Maps& maps, const AttnArgs& a, int block, uint8_t* tiles, SharedKV& sh) {
+template <int PANELS>
+__device__ __forceinline__ void init_barriers(SharedKV& sh) {
+  using F = Form<PANELS>;
+  uint64_t* const one[] = {&sh.kv_full, &sh.s_full, &sh.dp_full, &sh.done, &sh.own};
+  for (uint64_t* b : one) mbar_init(smem_addr(b), 1);
+  for (int i = 0; i < F::kStages; ++i) {
+    mbar_init(smem_addr(&sh.q_full[i]), 1);
+    mbar_init(smem_addr(&sh.do_full[i]), 1);
+    mbar_init(smem_addr(&sh.empty[i]), 1);
+  }
+  mbar_init(smem_addr(&sh.p_ready), F::kWorkers / 32);
+  mbar_init(smem_addr(&sh.ds_ready), F::kWorkers / 32);
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+}
+
+// A walk over the queries.  True if the block has to make another one; the
+// barriers' phases go on counting.
+template <class T, int PANELS, bool FIRST>
+__device__ __forceinline__ bool dkv_walk(const Maps& maps, const AttnArgs& a, int kv_head, uint8_t* tiles, SharedKV& sh,
+                                         State& state) {
   using F = Form<PANELS>;
   constexpr int kStages = F::kStages, kWalk = F::kWalk;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int kv_head = block % a.kv_heads;
-  if (warp == 0) {
-    const SeqUnit u = find_unit(a.cu_seqlens, a.seqs, (int)a.tokens, kTile, block / a.kv_heads);
-    if (lane == 0) {
-      sh.unit = u;
-      sh.gave_up = 0;
-    }
-  } else if (warp == F::kIssuer) {
-    tmem_alloc(smem_addr(&sh.tmem), F::kColumns);
-  } else if (warp == F::kLoader && lane == 0) {
-    uint64_t* const one[] = {&sh.kv_full, &sh.s_full, &sh.dp_full, &sh.done, &sh.own};
-    for (uint64_t* b : one) mbar_init(smem_addr(b), 1);
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(smem_addr(&sh.q_full[i]), 1);
-      mbar_init(smem_addr(&sh.do_full[i]), 1);
-      mbar_init(smem_addr(&sh.empty[i]), 1);
-    }
-    mbar_init(smem_addr(&sh.p_ready), F::kWorkers / 32);
-    mbar_init(smem_addr(&sh.ds_ready), F::kWorkers / 32);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  if (sh.unit.count == 0) {
-    if (warp == F::kIssuer) tmem_free(sh.tmem, F::kColumns);
-    wait_for_delta();
-    return;
-  }
   SeqUnit unit = sh.unit;
   unit.index = unit.count - 1 - unit.index;  // the first keys are seen by the most queries
 
@@ -230,7 +290,9 @@ __device__ __forceinline__ void dkv_block(const Maps& maps, const AttnArgs& a, i
   const int group = a.heads / a.kv_heads, first = unit.index * (kTile / kWalk);
   const int per = (unit.length + kWalk - 1) / kWalk - first, steps = group * per;
   const int dim16 = (a.dim + 15) / 16;
-  if (warp == F::kLoader && lane == 0) {
+  const int base = FIRST ? 0 : state.walks * steps, end = base + steps;  // steps made before, and after
+  const float by = FIRST ? 1.f : state.by;
+  if (FIRST && warp == F::kLoader && lane == 0) {
     const uint32_t bar = smem_addr(&sh.kv_full);
     mbar_expect(bar, 2 * F::kKeptBytes);
     load_kept<PANELS>(&maps.k, k_tile, kv_head, unit.begin + unit.index * kTile, bar);
@@ -242,18 +304,17 @@ __device__ __forceinline__ void dkv_block(const Maps& maps, const AttnArgs& a, i
   const uint32_t tmem = sh.tmem, dp_at = tmem + kWalk, dv_at = tmem + 2 * kWalk, dk_at = dv_at + 64 * PANELS;
 
   if (warp == F::kLoader) {
-    uint32_t own_parity = 0;
     int head = kv_head * group, tile = 0;
-    for (int n = 0; n < steps; ++n) {
+    for (int n = base; n < end; ++n) {
       const int stage = n % kStages;
       if (n >= kStages && !mbar_wait(smem_addr(&sh.empty[stage]), (n / kStages - 1) & 1, gave_up)) break;
       const int query = (first + tile) * kWalk;
       if (!load_tile<PANELS, kWalk>(&maps.q, q_tile + stage * F::kWalkBytes, head, unit.begin + query,
-                                    unit.length - query, smem_addr(&sh.q_full[stage]), smem_addr(&sh.own), &own_parity,
-                                    gave_up) ||
+                                    unit.length - query, smem_addr(&sh.q_full[stage]), smem_addr(&sh.own),
+                                    &state.own_parity, gave_up) ||
           !load_tile<PANELS, kWalk>(&maps.dout, do_tile + stage * F::kWalkBytes, head, unit.begin + query,
-                                    unit.length - query, smem_addr(&sh.do_full[stage]), smem_addr(&sh.own), &own_parity,
-                                    gave_up))
+                                    unit.length - query, smem_addr(&sh.do_full[stage]), smem_addr(&sh.own),
+                                    &state.own_parity, gave_up))
         break;
       if (++tile == per) tile = 0, ++head;
     }
@@ -276,12 +337,12 @@ __device__ __forceinline__ void dkv_block(const Maps& maps, const AttnArgs& a, i
       auto sum = [&](uint64_t& ready, uint32_t to, uint32_t left, uint32_t right, int n) {
         if (!mbar_wait(smem_addr(&ready), n & 1, gave_up)) return false;
         tc_fence_after();
-        for (int h = 0; h < F::kQuarters; ++h) product_ts<2>(to, left + h * 32, right, h, sums, n > 0 || h > 0);
+        for (int h = 0; h < F::kQuarters; ++h) product_ts<2>(to, left + h * 32, right, h, sums, n > base || h > 0);
         return true;
       };
-      bool ok = mbar_wait(smem_addr(&sh.kv_full), 0, gave_up) && scores(0) && dprob(0);
-      for (int n = 0; n < steps && ok; ++n) {
-        const bool more = n + 1 < steps;
+      bool ok = mbar_wait(smem_addr(&sh.kv_full), 0, gave_up) && scores(base) && dprob(base);
+      for (int n = base; n < end && ok; ++n) {
+        const bool more = n + 1 < end;
         ok = sum(sh.p_ready, dv_at, tmem, at(do_tile, n), n) && (!more || scores(n + 1)) &&
              sum(sh.ds_ready, dk_at, dp_at, at(q_tile, n), n);
         if (ok) mma_commit(smem_addr(&sh.empty[n % kStages]));
@@ -302,12 +363,13 @@ __device__ __forceinline__ void dkv_block(const Maps& maps, const AttnArgs& a, i
     // probabilities are held times is in the first and out of the second.
     int next_tile = 0;
     int64_t next_head = (int64_t)kv_head * group * a.tokens + unit.begin;
+    const float by_unshift = by * kUnshift<T>, unscale = 1.f / by;
     auto fetch = [&]() {  // of the next step, and on
       const int query = (first + next_tile) * kWalk + quarter * 32 + lane;
       const int64_t at = next_head + query;
       if (++next_tile == per) next_tile = 0, next_head += a.tokens;
       if (query >= unit.length) return make_float2(0.f, 0.f);  // masked
-      return make_float2(fmaf(-a.lse[at], kLog2e, kShift<T>), -a.delta[at] * kUnshift<T>);
+      return make_float2(fmaf(-a.lse[at], kLog2e, kShift<T>), -a.delta[at] * by_unshift);
     };
     auto put = [&](int n, float2 v) {
       stats[(n & 1) * 64 + lane] = v.x;
@@ -315,11 +377,12 @@ __device__ __forceinline__ void dkv_block(const Maps& maps, const AttnArgs& a, i
       __syncwarp();
     };
     wait_for_delta();
-    put(0, fetch());
+    put(base, fetch());
     int tile = 0;
-    bool ok = true;
-    for (int n = 0; n < steps; ++n) {
-      const float2 next = n + 1 < steps ? fetch() : make_float2(0.f, 0.f);
+    bool ok = true, finite = true;
+    float most = kUnknown;
+    for (int n = base; n < end; ++n) {
+      const float2 next = n + 1 < end ? fetch() : make_float2(0.f, 0.f);
       const int from = tile * kWalk;  // the tile's first query, counted from the first key
       const bool masked = from < kTile || from + kWalk > left;
       if (!(ok = mbar_wait(smem_addr(&sh.s_full), n & 1, gave_up))) break;
@@ -341,14 +404,15 @@ __device__ __forceinline__ void dkv_block(const Maps& maps, const AttnArgs& a, i
       tmem_wait_load();
       tmem_loaded(d);
       const float* delta = stats + (n & 1) * 64 + 32;
-      score_gradients<T>(p, d, packed, kUnshift<T>, [&](int x) { return two_of(delta, x); }, masked);
+      score_gradients<T>(p, d, packed, by_unshift, [&](int x) { return two_of(delta, x); }, masked);
       tmem_store16(s_at + kWalk, packed);
       tmem_wait_store();
       warp_arrive(smem_addr(&sh.ds_ready));
+      if (kScaled<T>) most = fmaxf(most, fabsf(d[0]));
       put(n + 1, next);
       if (++tile == per) tile = 0;
     }
-    if (ok && mbar_wait(smem_addr(&sh.done), 0, gave_up)) {
+    if (ok && mbar_wait(smem_addr(&sh.done), FIRST ? 0 : state.walks & 1, gave_up)) {
       tc_fence_after();
       // quarter: dv or dk, and which 64 of its columns
       const bool is_dk = quarter & 1;
@@ -356,11 +420,44 @@ __device__ __forceinline__ void dkv_block(const Maps& maps, const AttnArgs& a, i
       const int key = unit.index * kTile + (warp & 3) * 32;
       T* out = static_cast<T*>(const_cast<void*>(to.ptr)) + (int64_t)(unit.begin + key) * to.token_stride +
                kv_head * to.head_stride;
-      write_rows<T, 64>(lane0 + (is_dk ? dk_at : dv_at), q_tile + warp * 4096, out, to.token_stride, unit.length - key,
-                        (quarter >> 1) * 64, a.dim, is_dk ? a.scale : kUnshift<T>);
+      finite = write_rows<T, 64>(lane0 + (is_dk ? dk_at : dv_at), q_tile + warp * 4096, out, to.token_stride,
+                                 unit.length - key, (quarter >> 1) * 64, a.dim, is_dk ? a.scale * unscale : kUnshift<T>) ||
+               !is_dk;
     }
+    put_most<T>(most, finite, sh.most);
   }
-  leave<PANELS>(&sh.gave_up, warp, tmem);
+  return leave<T, PANELS>(&sh.gave_up, warp, tmem, sh.most, state);
+}
+
+template <class T, int PANELS>
+__device__ __forceinline__ void dkv_block(const Maps& maps, const AttnArgs& a, int block, uint8_t* tiles, SharedKV& sh) {
+  using F = Form<PANELS>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int kv_head = block % a.kv_heads;
+  if (warp == 0) {
+    const SeqUnit u = find_unit(a.cu_seqlens, a.seqs, (int)a.tokens, kTile, block / a.kv_heads);
+    if (lane == 0) {
+      sh.unit = u;
+      sh.gave_up = 0;
+    }
+  } else if (warp == F::kIssuer) {
+    tmem_alloc(smem_addr(&sh.tmem), F::kColumns);
+  } else if (warp == F::kLoader && lane == 0) {
+    init_barriers<PANELS>(sh);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (sh.unit.count == 0) {
+    if (warp == F::kIssuer) tmem_free(sh.tmem, F::kColumns);
+    wait_for_delta();
+    return;
+  }
+  State state;
+  if (dkv_walk<T, PANELS, true>(maps, a, kv_head, tiles, sh, state)) {
+    if constexpr (kScaled<T>)
+      while (dkv_walk<T, PANELS, false>(maps, a, kv_head, tiles, sh, state)) {}
+  }
 }
 
 // ---- dq ---------------------------------------------------------------------------
@@ -371,45 +468,34 @@ struct SharedQ {
   uint32_t tmem;
   int gave_up;
   SeqUnit unit;
+  float most[16];
 };
 
-template <class T, int PANELS>
-__device__ __forceinline__ void dq_block(const Maps& maps, const AttnArgs& a, int block, uint8_t* tiles, SharedQ& sh) {
+template <int PANELS>
+__device__ __forceinline__ void init_barriers(SharedQ& sh) {
+  using F = Form<PANELS>;
+  uint64_t* const one[] = {&sh.q_full, &sh.s_full, &sh.dp_full[0], &sh.dp_full[1], &sh.done, &sh.own};
+  for (uint64_t* b : one) mbar_init(smem_addr(b), 1);
+  for (int i = 0; i < kKStages; ++i) {
+    mbar_init(smem_addr(&sh.k_full[i]), 1);
+    mbar_init(smem_addr(&sh.k_empty[i]), 1);
+  }
+  for (int i = 0; i < kVStages; ++i) {
+    mbar_init(smem_addr(&sh.v_full[i]), 1);
+    mbar_init(smem_addr(&sh.v_empty[i]), 1);
+  }
+  mbar_init(smem_addr(&sh.s_read), F::kWorkers / 32);
+  for (int i = 0; i < 2; ++i) mbar_init(smem_addr(&sh.ds_ready[i]), F::kWorkers / 32);
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+}
+
+// A walk over the keys, as dkv_walk.
+template <class T, int PANELS, bool FIRST>
+__device__ __forceinline__ bool dq_walk(const Maps& maps, const AttnArgs& a, int head, uint8_t* tiles, SharedQ& sh,
+                                        State& state) {
   using F = Form<PANELS>;
   constexpr int kWalk = F::kWalk;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int head = block % a.heads;
-  if (warp == 0) {
-    const SeqUnit u = find_unit(a.cu_seqlens, a.seqs, (int)a.tokens, kTile, block / a.heads);
-    if (lane == 0) {
-      sh.unit = u;
-      sh.gave_up = 0;
-    }
-  } else if (warp == F::kIssuer) {
-    tmem_alloc(smem_addr(&sh.tmem), F::kColumns);
-  } else if (warp == F::kLoader && lane == 0) {
-    uint64_t* const one[] = {&sh.q_full, &sh.s_full, &sh.dp_full[0], &sh.dp_full[1], &sh.done, &sh.own};
-    for (uint64_t* b : one) mbar_init(smem_addr(b), 1);
-    for (int i = 0; i < kKStages; ++i) {
-      mbar_init(smem_addr(&sh.k_full[i]), 1);
-      mbar_init(smem_addr(&sh.k_empty[i]), 1);
-    }
-    for (int i = 0; i < kVStages; ++i) {
-      mbar_init(smem_addr(&sh.v_full[i]), 1);
-      mbar_init(smem_addr(&sh.v_empty[i]), 1);
-    }
-    mbar_init(smem_addr(&sh.s_read), F::kWorkers / 32);
-    for (int i = 0; i < 2; ++i) mbar_init(smem_addr(&sh.ds_ready[i]), F::kWorkers / 32);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  if (sh.unit.count == 0) {
-    if (warp == F::kIssuer) tmem_free(sh.tmem, F::kColumns);
-    wait_for_delta();
-    return;
-  }
   const SeqUnit unit = sh.unit;
 
   const uint32_t q_tile = smem_addr(tiles), do_tile = q_tile + F::kKeptBytes, k_tile = do_tile + F::kKeptBytes,
@@ -418,7 +504,9 @@ __device__ __forceinline__ void dq_block(const Maps& maps, const AttnArgs& a, in
   const int query = unit.index * kTile;
   const int steps = min(query + kTile, unit.length + kWalk - 1) / kWalk;  // tiles of keys that the queries see
   const int dim16 = (a.dim + 15) / 16;
-  if (warp == F::kLoader && lane == 0) {
+  const int base = FIRST ? 0 : state.walks * steps, end = base + steps;  // steps made before, and after
+  const float by = FIRST ? 1.f : state.by;
+  if (FIRST && warp == F::kLoader && lane == 0) {
     const uint32_t bar = smem_addr(&sh.q_full);
     mbar_expect(bar, 2 * F::kKeptBytes);
     load_kept<PANELS>(&maps.q, q_tile, head, unit.begin + query, bar);
@@ -434,17 +522,16 @@ __device__ __forceinline__ void dq_block(const Maps& maps, const AttnArgs& a, in
 
   if (warp == F::kLoader) {
     const int kv_head = head / (a.heads / a.kv_heads);
-    uint32_t own_parity = 0;
-    for (int n = 0; n < steps; ++n) {
-      const int ks = n % kKStages, vs = n % kVStages, key = n * kWalk;
+    for (int n = base; n < end; ++n) {
+      const int ks = n % kKStages, vs = n % kVStages, key = (n - base) * kWalk;
       if (n >= kKStages && !mbar_wait(smem_addr(&sh.k_empty[ks]), (n / kKStages - 1) & 1, gave_up)) break;
       // dq sums over the rows of K: those of another sequence are cleared
       if (!load_tile<PANELS, kWalk>(&maps.k, k_tile + ks * F::kWalkBytes, kv_head, unit.begin + key, unit.length - key,
-                                    smem_addr(&sh.k_full[ks]), smem_addr(&sh.own), &own_parity, gave_up))
+                                    smem_addr(&sh.k_full[ks]), smem_addr(&sh.own), &state.own_parity, gave_up))
         break;
       if (n >= kVStages && !mbar_wait(smem_addr(&sh.v_empty[vs]), (n / kVStages - 1) & 1, gave_up)) break;
       if (!load_tile<PANELS, kWalk>(&maps.v, v_tile + vs * F::kWalkBytes, kv_head, unit.begin + key, kWalk,
-                                    smem_addr(&sh.v_full[vs]), smem_addr(&sh.own), &own_parity, gave_up))
+                                    smem_addr(&sh.v_full[vs]), smem_addr(&sh.own), &state.own_parity, gave_up))
         break;
     }
   } else if (warp == F::kIssuer) {
@@ -463,9 +550,9 @@ __device__ __forceinline__ void dq_block(const Maps& maps, const AttnArgs& a, in
         mma_commit(smem_addr(&sh.v_empty[n % kVStages]));
         return true;
       };
-      bool ok = mbar_wait(smem_addr(&sh.q_full), 0, gave_up) && scores(0) && dprob(0);
-      for (int n = 0; n < steps && ok; ++n) {
-        if (n + 1 < steps) {
+      bool ok = mbar_wait(smem_addr(&sh.q_full), 0, gave_up) && scores(base) && dprob(base);
+      for (int n = base; n < end && ok; ++n) {
+        if (n + 1 < end) {
           if (!(ok = mbar_wait(smem_addr(&sh.s_read), n & 1, gave_up))) break;
           tc_fence_after();
           if (!(ok = scores(n + 1) && dprob(n + 1))) break;
@@ -473,7 +560,7 @@ __device__ __forceinline__ void dq_block(const Maps& maps, const AttnArgs& a, in
         if (!(ok = mbar_wait(smem_addr(&sh.ds_ready[n & 1]), (n >> 1) & 1, gave_up))) break;
         tc_fence_after();
         for (int h = 0; h < F::kQuarters; ++h)
-          product_ts<2>(dq_at, dp_at(n) + h * 32, k_tile + (n % kKStages) * F::kWalkBytes, h, sums, n > 0 || h > 0);
+          product_ts<2>(dq_at, dp_at(n) + h * 32, k_tile + (n % kKStages) * F::kWalkBytes, h, sums, n > base || h > 0);
         mma_commit(smem_addr(&sh.k_empty[n % kKStages]));
       }
       if (ok) mma_commit(smem_addr(&sh.done));
@@ -488,10 +575,12 @@ __device__ __forceinline__ void dq_block(const Maps& maps, const AttnArgs& a, in
     wait_for_delta();
     const int64_t at = (int64_t)head * a.tokens + unit.begin + query + row;
     const float l = valid ? -a.lse[at] * kLog2e : -INFINITY, dl = valid ? -a.delta[at] : 0.f;
-    const Two lse = two(l, l), delta = two(dl, dl);
-    bool ok = true;
-    for (int n = 0; n < steps; ++n) {
-      const bool masked = (n + 1) * kWalk > query;
+    const Two lse = two(l, l), delta = two(dl * by, dl * by);
+    bool ok = true, finite = true;
+    float most = 0.f;
+    for (int n = base; n < end; ++n) {
+      const int key = (n - base) * kWalk;  // the tile's first
+      const bool masked = key + kWalk > query;
       if (!(ok = mbar_wait(smem_addr(&sh.s_full), n & 1, gave_up))) break;
       tc_fence_after();
       float p[32], d[32];
@@ -501,28 +590,66 @@ __device__ __forceinline__ void dq_block(const Maps& maps, const AttnArgs& a, in
       tmem_loaded(p);
       warp_arrive(smem_addr(&sh.s_read));
       probabilities<T>(p, packed, c, [&](int) { return lse; }, masked,
-                       [&](int x) { return n * kWalk + quarter * 32 + x <= query + row; });
+                       [&](int x) { return key + quarter * 32 + x <= query + row; });
       const uint32_t dp = lane0 + dp_at(n) + quarter * 32;
       if (!(ok = mbar_wait(smem_addr(&sh.dp_full[n & 1]), (n >> 1) & 1, gave_up))) break;
       tc_fence_after();
       tmem_load32(dp, d);
       tmem_wait_load();
       tmem_loaded(d);
-      score_gradients<T>(p, d, packed, 1.f, [&](int) { return delta; }, masked);
+      score_gradients<T>(p, d, packed, by, [&](int) { return delta; }, masked);
       tmem_store16(dp, packed);
       tmem_wait_store();
       warp_arrive(smem_addr(&sh.ds_ready[n & 1]));
+      if (kScaled<T>) most = fmaxf(most, fabsf(d[0]));
     }
-    if (ok && mbar_wait(smem_addr(&sh.done), 0, gave_up)) {
+    if (ok && mbar_wait(smem_addr(&sh.done), FIRST ? 0 : state.walks & 1, gave_up)) {
       tc_fence_after();
       const int from = query + (warp & 3) * 32;
       T* out = static_cast<T*>(const_cast<void*>(a.dq.ptr)) + (int64_t)(unit.begin + from) * a.dq.token_stride +
                head * a.dq.head_stride;
-      write_rows<T, 32>(lane0 + dq_at, k_tile + warp * 2048, out, a.dq.token_stride, unit.length - from, quarter * 32,
-                        a.dim, a.scale);
+      finite = write_rows<T, 32>(lane0 + dq_at, k_tile + warp * 2048, out, a.dq.token_stride, unit.length - from,
+                                 quarter * 32, a.dim, a.scale * (1.f / by));
     }
+    if (kScaled<T> && FIRST && ok && !__any_sync(0xFFFFFFFFu, most > 0.f)) {
+      // a prompt's queries often have no gradient at all, and need no other power
+      ok = mbar_wait(smem_addr(&sh.q_full), 0, gave_up);
+      if (valid && any_element(do_tile + (quarter >> 1) * kPanelBytes + row * 128 + (quarter & 1) * 64)) most = kUnknown;
+    }
+    put_most<T>(most, finite, sh.most);
   }
-  leave<PANELS>(&sh.gave_up, warp, tmem);
+  return leave<T, PANELS>(&sh.gave_up, warp, tmem, sh.most, state);
+}
+
+template <class T, int PANELS>
+__device__ __forceinline__ void dq_block(const Maps& maps, const AttnArgs& a, int block, uint8_t* tiles, SharedQ& sh) {
+  using F = Form<PANELS>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int head = block % a.heads;
+  if (warp == 0) {
+    const SeqUnit u = find_unit(a.cu_seqlens, a.seqs, (int)a.tokens, kTile, block / a.heads);
+    if (lane == 0) {
+      sh.unit = u;
+      sh.gave_up = 0;
+    }
+  } else if (warp == F::kIssuer) {
+    tmem_alloc(smem_addr(&sh.tmem), F::kColumns);
+  } else if (warp == F::kLoader && lane == 0) {
+    init_barriers<PANELS>(sh);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (sh.unit.count == 0) {
+    if (warp == F::kIssuer) tmem_free(sh.tmem, F::kColumns);
+    wait_for_delta();
+    return;
+  }
+  State state;
+  if (dq_walk<T, PANELS, true>(maps, a, head, tiles, sh, state)) {
+    if constexpr (kScaled<T>)
+      while (dq_walk<T, PANELS, false>(maps, a, head, tiles, sh, state)) {}
+  }
 }
 
 // ---- both ---------------------------------------------------------------------------

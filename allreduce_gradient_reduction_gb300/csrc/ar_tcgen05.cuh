@@ -186,12 +186,14 @@ __device__ __forceinline__ void tmem_store16(uint32_t at, const float (&r)[16]) 
 // A warp writes COLS columns of its 32 rows of sums from tensor memory, times
 // `scale`, rounded: `rows` of them, `dim` columns in all, from `column` on.
 // The rows go through 64 COLS bytes of shared memory at `stage`, so that the
-// lanes write runs of 2 COLS bytes and not 32 rows at a time.
+// lanes write runs of 2 COLS bytes and not 32 rows at a time.  Whether all sums
+// of the lane's row, if it is one of the `rows`, are finite.
 template <class T, int COLS>
-__device__ __forceinline__ void write_rows(uint32_t sums, uint32_t stage, T* out, int64_t stride, int rows, int column,
+__device__ __forceinline__ bool write_rows(uint32_t sums, uint32_t stage, T* out, int64_t stride, int rows, int column,
                                            int dim, float scale) {
   constexpr int kPieces = COLS / 8;  // 16-byte pieces of a row
   const int lane = threadIdx.x & 31;
+  Two nothing = two(0.f, 0.f);  // NaN once a sum is not finite
   __syncwarp();
   auto place = [&](int row, int piece) {  // pieces of a row change places, so that eight lanes reach all banks
     return stage + row * (COLS * 2) + ((piece ^ (row / (8 / kPieces) & (kPieces - 1))) << 4);
@@ -203,6 +205,8 @@ __device__ __forceinline__ void write_rows(uint32_t sums, uint32_t stage, T* out
     tmem_load16(sums + column + c, o);
     tmem_wait_load();
     tmem_loaded(o);
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) nothing = fma2(two(o[i], o[i + 1]), two(0.f, 0.f), nothing);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
       asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(place(lane, c / 8 + h)),
@@ -222,6 +226,9 @@ __device__ __forceinline__ void write_rows(uint32_t sums, uint32_t stage, T* out
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(place(row, piece)) : "memory");
     *reinterpret_cast<uint4*>(out + row * stride + at) = v;
   }
+  float lo, hi;
+  split(nothing, lo, hi);
+  return lane >= rows || lo + hi == 0.f;
 }
 
 // ---- products -------------------------------------------------------------------------

@@ -559,8 +559,12 @@ int ar_attention(const ar_attention_tensor* q, const ar_attention_tensor* k, con
  *   out, lse    of the forward call on the same q, k, v and cu_seqlens
  *   workspace   16-byte aligned device memory of at least
  *               ar_attention_workspace_bytes bytes
- * p and da are rounded to dtype for their products; f16 holds p times 2^15
- * meanwhile, so that it counts down to 2^-40.
+ * p and da are rounded to dtype for their products.  f16 holds p times 2^15
+ * meanwhile, so that it counts down to 2^-40, and da times powers of two that
+ * follow its size, so that dq and dk are finite wherever they themselves are
+ * numbers of f16 and lose nothing above 2^-13 of the largest da of 128 keys'
+ * or queries' (2^-51 where all of them are small); where the power has to be
+ * changed the call takes up to two or three times as long.
  */
 int ar_attention_backward(const ar_attention_tensor* dout, const ar_attention_tensor* q, const ar_attention_tensor* k,
                           const ar_attention_tensor* v, const ar_attention_tensor* out, const float* lse,
