@@ -21,7 +21,10 @@
 // The running maximum that scales the output is moved only when a row's true
 // maximum has grown by more than 8 in the exponent of two: until then the
 // probabilities stay below 2^8, exact enough in either 16-bit type, and the
-// output need not be touched.
+// output need not be touched.  f16 holds them times 2^7, below 2^15 then, so that
+// one of 2^-32 of the row's largest is not lost yet: thousands of keys may have
+// no more each and a value that counts.  The power is part of the exponential's
+// argument and of the sum that divides.
 #include "ar_tcgen05.cuh"
 
 #include <algorithm>
@@ -33,6 +36,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.f;  // powers of two that a row's maximum may grow by before the output is rescaled
 constexpr int kStages = 4;     // tiles of K or V in flight
+template <class T>
+constexpr float kShift = __is_same(T, __half) ? 7.f : 0.f;  // powers of two that probabilities are held times
 
 // What differs with the head size.  A tensor core product of 128 x 128 scores
 // takes 4 cycles for each element of the head, the exponentials of a tile at
@@ -257,7 +262,7 @@ __global__ void __launch_bounds__(Form<PANELS>::kThreads, Form<PANELS>::kBlocks)
         }
       }
       const float base = m == -INFINITY ? 0.f : m * c;
-      const Two base2 = two(-base, -base);
+      const Two base2 = two(kShift<T> - base, kShift<T> - base);
       if (F::kApart && j > 0) {
         // the last product has read the probabilities that these replace
         if (!(ok = mbar_wait(smem_addr(&sh.o_done[i]), (j - 1) & 1, gave_up))) break;
@@ -298,7 +303,7 @@ __global__ void __launch_bounds__(Form<PANELS>::kThreads, Form<PANELS>::kBlocks)
       for (int p = 0; p < PANELS; ++p)
         write_rows<T, 64>(o_at, q_tile + i * kTileBytes + (warp & 3) * 4096, out, a.out.token_stride,
                           unit.length - from, p * 64, a.dim, 1.f / sum);
-      if (a.lse && at < unit.length) a.lse[(int64_t)head * a.tokens + token] = (m * c + log2f(sum)) * kLn2;
+      if (a.lse && at < unit.length) a.lse[(int64_t)head * a.tokens + token] = (m * c + (log2f(sum) - kShift<T>)) * kLn2;
     }
   }
 

@@ -544,7 +544,8 @@ typedef struct {
  * do not reach a sequence's results.  Within a sequence a value of v that is
  * not finite reaches its own token's result and later ones, and may reach
  * those of up to 127 earlier tokens.
- * The unnormalised probabilities are rounded to dtype for their product with v.
+ * The unnormalised probabilities are rounded to dtype for their product with v
+ * (f16 counts those of 2^-32 of a row's largest and more).
  */
 int ar_attention(const ar_attention_tensor* q, const ar_attention_tensor* k, const ar_attention_tensor* v,
                  const int32_t* cu_seqlens, const ar_attention_tensor* out, float* lse, int64_t tokens, int64_t seqs,
