@@ -157,7 +157,7 @@ struct RowVectors {
 //   logit  the student's logit of the word
 //   prob   the teacher's probability
 //   sum    the word's probability with all of its entries, for the first of
-//          them; -1 for the others
+//          them; -1 for the others (NaN is one that counts)
 struct List {
   int* word;
   float *logit, *prob, *sum;
@@ -198,10 +198,10 @@ __device__ __forceinline__ Divergence make_list(const DistillArgs& a, int64_t ro
   total = warp_sum(total);
   const float log_total = logf(total);
   float value_sum = 0.f;
-  const bool some = total > 0.f;
+  const bool some = total != 0.f;  // NaN (of a teacher's NaN or +inf) is some, and goes on to the results
   for (int k = lane; k < top; k += 32) {
     const float p = list.prob[k] / total;
-    if (some && p > 0.f) value_sum += p * ((list.sum[k] - tmax - log_total) - list.logit[k] * inv_tau);
+    if (some && p != 0.f && list.word[k] >= 0) value_sum += p * ((list.sum[k] - tmax - log_total) - list.logit[k] * inv_tau);
     list.prob[k] = p;
   }
   value_sum = warp_sum(value_sum);
@@ -261,7 +261,7 @@ __device__ __forceinline__ void correct_listed(const List& list, int top, int lo
                                                const Gradient<T>& gradient, T* dz) {
   for (int k = t; k < top; k += threads) {
     const int w = list.word[k];
-    if (w >= lo && w < hi && list.sum[k] >= 0.f)
+    if (w >= lo && w < hi && !(list.sum[k] < 0.f))
       dz[w] = Conv<T>::down(gradient.one(list.logit[k]) - gradient.coef * list.sum[k]);
   }
 }

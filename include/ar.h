@@ -492,7 +492,9 @@ int64_t ar_layer_norm_workspace_bytes(int64_t rows, int64_t cols);
  *   temperature finite, > 0
  * A row without entries (or with teacher logits of -inf alone) has loss 0
  * and a zero gradient; so has a row with scale 0 a zero gradient, whatever
- * its logits hold.  Student logits of -inf have q = 0.
+ * its logits hold.  NaN or +inf among a row's teacher logits makes its p NaN,
+ * and so its loss and its listed words' gradients; at an entry that is no word
+ * they do not matter.  Student logits of -inf have q = 0.
  * top may be 0 and is at most 1024 (AR_ERR_TOO_LARGE beyond).
  */
 int ar_distill_loss(const void* logits, int64_t logits_stride, const int32_t* teacher_index,
