@@ -10,14 +10,48 @@ PyTorch's), ar_bucketed_allreduce of all ranks' gradients, and the same plain
 update on every rank; the copies stay equal bit for bit.
 
 layer_norm, packed_attention and distill_loss are the operators as PyTorch
-functions with gradients, for use in other models as well.
+functions with gradients, for use in other models as well.  The gradients have
+none of their own: asking for second derivatives raises.
 """
 import argparse
+import functools
 
 import torch
 import torch.nn.functional as F
 
 from . import binding as ar
+
+
+class _NoSecondDerivative(torch.autograd.Function):
+    """Its first `count` tensors, which depend on all of them in a way that is
+    not differentiable."""
+    @staticmethod
+    def forward(ctx, count, *tensors):
+        return tuple(t.view_as(t) for t in tensors[:count])
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("the gradients of layer_norm, packed_attention and distill_loss have no derivative: "
+                           "second derivatives through them are not available")
+
+
+def _once(backward):
+    """For a Function's backward that is made of calls autograd does not see.
+    Where a graph of the gradients is asked for, they are tied to what they
+    depend on, so that differentiating them again raises.  (torch's own
+    once_differentiable ties them to nothing: autograd.grad with respect to
+    the inputs then takes them for constants.)"""
+    @functools.wraps(backward)
+    def wrapped(ctx, *grads):
+        with torch.no_grad():
+            out = backward(ctx, *grads)
+        if not torch.is_grad_enabled():
+            return out
+        out = out if isinstance(out, tuple) else (out,)
+        made = [t for t in out if t is not None]
+        tied = iter(_NoSecondDerivative.apply(len(made), *made, *grads, *ctx.saved_tensors))
+        return tuple(None if t is None else next(tied) for t in out)
+    return wrapped
 
 
 class _LayerNorm(torch.autograd.Function):
@@ -30,6 +64,7 @@ class _LayerNorm(torch.autograd.Function):
         return y
 
     @staticmethod
+    @_once
     def backward(ctx, dy):
         x, weight, mean, rstd = ctx.saved_tensors
         dx, dweight, dbias = torch.empty_like(x), torch.empty_like(weight), torch.empty_like(weight)
@@ -54,6 +89,7 @@ class _PackedAttention(torch.autograd.Function):
         return out
 
     @staticmethod
+    @_once
     def backward(ctx, dout):
         q, k, v, cu_seqlens, out, lse = ctx.saved_tensors
         dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))
@@ -81,6 +117,7 @@ class _DistillLoss(torch.autograd.Function):
         return loss
 
     @staticmethod
+    @_once
     def backward(ctx, dloss):
         logits, teacher_index, teacher_logits, lse = ctx.saved_tensors
         dlogits = torch.empty_like(logits)
