@@ -61,13 +61,15 @@ class _LayerNorm(torch.autograd.Function):
         mean, rstd = torch.empty((2, x.shape[0]), dtype=torch.float32, device=x.device)
         ar.check(ar.ar_layer_norm(x, weight, bias, y, mean, rstd, eps), "ar_layer_norm")
         ctx.save_for_backward(x, weight, mean, rstd)
+        ctx.has_bias = bias is not None
         return y
 
     @staticmethod
     @_once
     def backward(ctx, dy):
         x, weight, mean, rstd = ctx.saved_tensors
-        dx, dweight, dbias = torch.empty_like(x), torch.empty_like(weight), torch.empty_like(weight)
+        dx, dweight = torch.empty_like(x), torch.empty_like(weight)
+        dbias = torch.empty_like(weight) if ctx.has_bias else None
         workspace = torch.empty(ar.ar_layer_norm_workspace_bytes(*x.shape), dtype=torch.uint8, device=x.device)
         ar.check(ar.ar_layer_norm_backward(dy.contiguous(), x, weight, mean, rstd, dx, dweight, dbias, workspace),
                  "ar_layer_norm_backward")
@@ -75,7 +77,7 @@ class _LayerNorm(torch.autograd.Function):
 
 
 def layer_norm(x, weight, bias, eps=1e-5):
-    """x [rows, cols]; weight and bias of x's type or f32."""
+    """x [rows, cols]; weight and bias of x's type or f32, bias may be None."""
     return _LayerNorm.apply(x, weight, bias, eps)
 
 

@@ -69,6 +69,7 @@ def cases(ex):
     index = torch.randint(9, (5, 3), generator=g, dtype=torch.int32)
     cu = torch.tensor([0, 6], dtype=torch.int32)
     return {"layer_norm": (ex.layer_norm, (normal(5, 8), normal(8), normal(8))),
+            "layer_norm without bias": (lambda x, w: ex.layer_norm(x, w, None), (normal(5, 8), normal(8))),
             "packed_attention": (lambda q, k, v: ex.packed_attention(q, k, v, cu), tuple(normal(6, 2, 8) for _ in range(3))),
             "distill_loss": (lambda z: ex.distill_loss(z, index, torch.zeros(5, 3), 2.0), (normal(5, 9),))}
 
@@ -76,7 +77,7 @@ def cases(ex):
 NAMES = ["layer_norm", "packed_attention", "distill_loss"]
 
 
-@pytest.mark.parametrize("name", NAMES)
+@pytest.mark.parametrize("name", NAMES + ["layer_norm without bias"])
 def test_first_derivatives(ex, name):
     """Against differences of the replaced calls in 32 bits: off by 1e-3 of the
     magnitudes at a step of 1e-2 (its cube's third and binary32's rounding)."""
