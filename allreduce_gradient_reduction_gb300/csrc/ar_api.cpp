@@ -587,6 +587,16 @@ cudaError_t open_kernel(const void* kernel, int smem_bytes, bool big_clusters,
 
 std::atomic<int64_t> g_launches{0};
 void count_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
+
+cudaError_t take_word(void* at, int* value, cudaStream_t stream) {
+  int v = 0;
+  cudaError_t e = cudaMemcpyAsync(&v, at, sizeof(int), cudaMemcpyDeviceToHost, stream);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+  if (e != cudaSuccess || !v) return e;
+  *value = v;
+  if ((e = cudaMemsetAsync(at, 0, sizeof(int), stream)) != cudaSuccess) return e;
+  return cudaStreamSynchronize(stream);
+}
 }  // namespace ar
 
 // ---- overlapped bucket reduction (DDP's reducer) --------------------------------
@@ -1120,9 +1130,29 @@ int ar_plan_destroy(ar_plan* plan) {
   });
 }
 
+}  // extern "C"
+
+namespace {
+
+// While it lives, this thread may copy and synchronise in a stream of its own
+// although another stream is being captured.
+class RelaxedCapture {
+ public:
+  RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode_); }
+  ~RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode_); }
+
+ private:
+  cudaStreamCaptureMode mode_ = cudaStreamCaptureModeRelaxed;
+};
+
+}  // namespace
+
+extern "C" {
+
 int ar_device_status(ar_stream_t stream, int* status) {
   return guarded([&]() -> int {
     if (!status) return AR_ERR_INVALID_ARG;
+    RelaxedCapture relaxed;
     cudaError_t e = cudaStreamSynchronize((cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e);
     int dev = 0;
@@ -1131,7 +1161,7 @@ int ar_device_status(ar_stream_t stream, int* status) {
     // waits inside kernels of one GPU's work that ran out are reported first
     for (auto take : {ar::layer_norm_take_status, ar::distill_take_status, ar::attention_take_status,
                       ar::attention_backward_take_status})
-      if ((e = take(status)) != cudaSuccess) return cuda_fail(e);
+      if ((e = take(status, (cudaStream_t)stream)) != cudaSuccess) return cuda_fail(e);
     if (*status != AR_OK) return AR_OK;
     ar::SyncBlock* sb = nullptr;
     unsigned long long ctx = 0;
@@ -1143,10 +1173,7 @@ int ar_device_status(ar_stream_t stream, int* status) {
       if (dev >= 0 && dev < 256 && g_sync_ctx[dev] == ctx) sb = g_sync[dev];
     }
     if (!sb) return AR_OK;
-    int v = 0;
-    if ((e = cudaMemcpy(&v, &sb->status, sizeof(int), cudaMemcpyDeviceToHost)) != cudaSuccess) return cuda_fail(e);
-    if ((e = cudaMemset(&sb->status, 0, sizeof(int))) != cudaSuccess) return cuda_fail(e);
-    *status = v;
+    if ((e = ar::take_word(&sb->status, status, (cudaStream_t)stream)) != cudaSuccess) return cuda_fail(e);
     return AR_OK;
   });
 }

@@ -339,7 +339,7 @@ cudaError_t run(int dtype, const AttnArgs& a, cudaStream_t s) {
   // at most this many units, however the tokens are split
   const int64_t units = a.tokens / F::kQueries + std::min<int64_t>(a.seqs, a.tokens);
   attention_kernel<T, PANELS><<<(unsigned)(units * a.heads), F::kThreads, smem, s>>>(q, k, v, a);
-  count_launch();
+  note_launch();
   return cudaGetLastError();
 }
 
@@ -372,6 +372,6 @@ cudaError_t launch_attention(int dtype, const AttnArgs& a, cudaStream_t s) {
   return a.dim <= 64 ? run<__half, 1>(dtype, a, s) : run<__half, 2>(dtype, a, s);
 }
 
-cudaError_t attention_take_status(int* status) { return take_status(status); }
+cudaError_t attention_take_status(int* status, cudaStream_t s) { return take_status(status, s); }
 
 }  // namespace ar

@@ -688,7 +688,7 @@ cudaError_t run(int dtype, const AttnArgs& a, cudaStream_t s) {
     return cudaErrorInvalidValue;
   constexpr int kLanes = PANELS * 8, kRows = 256 / kLanes;
   attention_delta_kernel<T, kLanes><<<(unsigned)((a.tokens * a.heads + kRows - 1) / kRows), 256, 0, s>>>(a);
-  count_launch();
+  note_launch();
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   // at most this many tiles, however the tokens are split
   const int64_t most = a.tokens / kTile + std::min<int64_t>(a.seqs, a.tokens);
@@ -704,7 +704,7 @@ cudaError_t run(int dtype, const AttnArgs& a, cudaStream_t s) {
   cfg.attrs = &at;
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kernel, maps, a, kv_blocks);
-  count_launch();
+  note_launch();
   return e;
 }
 
@@ -715,6 +715,6 @@ cudaError_t launch_attention_backward(int dtype, const AttnArgs& a, cudaStream_t
   return a.dim <= 64 ? run<__half, 1>(dtype, a, s) : run<__half, 2>(dtype, a, s);
 }
 
-cudaError_t attention_backward_take_status(int* status) { return take_status(status); }
+cudaError_t attention_backward_take_status(int* status, cudaStream_t s) { return take_status(status, s); }
 
 }  // namespace ar

@@ -612,7 +612,7 @@ cudaError_t run(const DistillArgs& a, cudaStream_t s) {
       while (split < 2 && pieces >> split >= 8 && idle() > 0.04) ++split;
     const int64_t blocks = std::min<int64_t>(a.rows << split, most);
     kernel<<<(unsigned)blocks, kRingThreads, (size_t)shared, s>>>(a, pieces, places, keep, split);
-    count_launch();
+    note_launch();
     return cudaGetLastError();
   }
   // Few rows: several blocks to a row, until there are about two for each
@@ -633,7 +633,7 @@ cudaError_t run(const DistillArgs& a, cudaStream_t s) {
   cfg.attrs = &at;
   cfg.numAttrs = !BACKWARD && parts > 1 ? 1 : 0;
   cudaError_t e = cudaLaunchKernelEx(&cfg, distill_kernel<T, V, BACKWARD>, a, parts);
-  count_launch();
+  note_launch();
   return e;
 }
 
@@ -647,6 +647,6 @@ cudaError_t launch_distill(int dtype, int vdtype, bool backward, const DistillAr
   });
 }
 
-cudaError_t distill_take_status(int* status) { return take_status(status); }
+cudaError_t distill_take_status(int* status, cudaStream_t s) { return take_status(status, s); }
 
 }  // namespace ar

@@ -205,5 +205,8 @@ cudaError_t open_kernel(const void* kernel, int smem_bytes, bool big_clusters,
 
 // Counts every kernel launch the library enqueues (ar_kernel_launches).
 void count_launch();
+// Reads a 32-bit word of device memory into *value if it is not zero, and
+// clears it, in `stream` alone; returns when that is done.
+cudaError_t take_word(void* at, int* value, cudaStream_t stream);
 
 }  // namespace ar

@@ -923,7 +923,7 @@ cudaError_t start_ring(void (*kernel)(LayerNormArgs, int, int), std::atomic<unsi
   if ((e = resident(kernel, threads * groups, smem, &blocks)) != cudaSuccess) return e;
   blocks = std::min<int64_t>(blocks, (a.rows + groups - 1) / groups);
   kernel<<<(unsigned)blocks, dim3(threads, groups), smem, s>>>(a, slot, stages);
-  count_launch();
+  note_launch();
   return cudaGetLastError();
 }
 
@@ -993,7 +993,7 @@ cudaError_t forward_wide(const LayerNormArgs& a, cudaStream_t s) {
     layer_norm_kernel<T, P, VW, NV><<<(unsigned)a.rows, d.threads, 0, s>>>(a);
   else
     layer_norm_wide_kernel<T, P><<<(unsigned)a.rows, 1024, 0, s>>>(a);
-  count_launch();
+  note_launch();
   return cudaGetLastError();
 }
 
@@ -1010,7 +1010,7 @@ cudaError_t run_params(const LayerNormBackwardArgs& a, int blocks, cudaStream_t 
   cfg.numAttrs = 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, layer_norm_params_kernel<P>, (const float*)a.partial, blocks, a.cols,
                                      static_cast<P*>(a.dweight), static_cast<P*>(a.dbias));
-  count_launch();
+  note_launch();
   return e;
 }
 
@@ -1029,7 +1029,7 @@ cudaError_t start_backward_ring(void (*kernel)(LayerNormBackwardArgs, int, int),
   if ((e = resident(kernel, threads * groups, smem, &blocks)) != cudaSuccess) return e;
   blocks = std::min<int64_t>({blocks, kLayerNormMaxBlocks, (a.rows + groups - 1) / groups});
   kernel<<<(unsigned)blocks, dim3(threads, groups), smem, s>>>(a, slot, stages);
-  count_launch();
+  note_launch();
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return run_params<P>(a, (int)blocks, s);
 }
@@ -1089,17 +1089,17 @@ cudaError_t backward_wide(const LayerNormBackwardArgs& a, cudaStream_t s) {
         rows_aligned16(a.dx, a.dx_stride, a.rows, 4) && params_aligned<T, P>(a.weight)) {
       const int blocks = (int)std::min<int64_t>(std::min(sm_count(), kLayerNormMaxBlocks), a.rows);
       layer_norm_backward_kernel<T, P, 4, 4><<<blocks, d.threads, 0, s>>>(a);
-      count_launch();
+      note_launch();
       if ((e = cudaGetLastError()) != cudaSuccess) return e;
       return run_params<P>(a, blocks, s);
     }
   }
   const int slices = (int)std::min<int64_t>(a.rows, 64);
   layer_norm_params_wide_kernel<T><<<dim3((unsigned)((a.cols + 255) / 256), slices), 256, 0, s>>>(a);
-  count_launch();
+  note_launch();
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   layer_norm_backward_wide_kernel<T, P><<<(unsigned)a.rows, 1024, 0, s>>>(a);
-  count_launch();
+  note_launch();
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return run_params<P>(a, slices, s);
 }
@@ -1139,6 +1139,6 @@ cudaError_t launch_layer_norm_backward(int dtype, int pdtype, const LayerNormBac
   });
 }
 
-cudaError_t layer_norm_take_status(int* status) { return take_status(status); }
+cudaError_t layer_norm_take_status(int* status, cudaStream_t s) { return take_status(status, s); }
 
 }  // namespace ar

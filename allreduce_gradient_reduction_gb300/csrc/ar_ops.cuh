@@ -7,6 +7,8 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/ar.h"
 #include "ar_ops.h"
 
@@ -15,14 +17,20 @@ namespace ar {
 // AR_ERR_TIMEOUT once a wait of one of the including file's kernels has run out.
 static __device__ int g_status;
 
-// Host: reads it into *status if it is set, and clears it.
-static inline cudaError_t take_status(int* status) {
-  int v = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(&v, g_status, sizeof(int));
-  if (e != cudaSuccess || !v) return e;
-  *status = v;
-  v = 0;
-  return cudaMemcpyToSymbol(g_status, &v, sizeof(int));
+// Host: a kernel of the including file has been launched (or captured).
+static std::atomic<bool> g_launched{false};
+static inline void note_launch() {
+  g_launched.store(true, std::memory_order_relaxed);
+  count_launch();
+}
+
+// Host: reads it into *status if it is set, and clears it, in `stream` alone.
+// Nothing is asked of the device before a first launch.
+static inline cudaError_t take_status(int* status, cudaStream_t stream) {
+  if (!g_launched.load(std::memory_order_relaxed)) return cudaSuccess;
+  void* at = nullptr;
+  cudaError_t e = cudaGetSymbolAddress(&at, g_status);
+  return e == cudaSuccess ? take_word(at, status, stream) : e;
 }
 
 template <class T> struct Conv;

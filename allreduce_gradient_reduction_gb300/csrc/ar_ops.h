@@ -87,11 +87,11 @@ struct AttnArgs {
 cudaError_t launch_attention(int dtype, const AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_attention_backward(int dtype, const AttnArgs& a, cudaStream_t stream);
 // What kernels of the current device left when one of their waits ran out:
-// AR_ERR_TIMEOUT is stored in *status, and cleared.  The caller has
-// synchronised.
-cudaError_t layer_norm_take_status(int* status);
-cudaError_t distill_take_status(int* status);
-cudaError_t attention_take_status(int* status);
-cudaError_t attention_backward_take_status(int* status);
+// AR_ERR_TIMEOUT is stored in *status, and cleared.  Every operation is in
+// `stream`, which the caller has synchronised.
+cudaError_t layer_norm_take_status(int* status, cudaStream_t stream);
+cudaError_t distill_take_status(int* status, cudaStream_t stream);
+cudaError_t attention_take_status(int* status, cudaStream_t stream);
+cudaError_t attention_backward_take_status(int* status, cudaStream_t stream);
 
 }  // namespace ar

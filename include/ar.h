@@ -587,7 +587,8 @@ int ar_chunk_range(int64_t count, int nranks, int c, int64_t* lo, int64_t* hi);
  * asynchronous status word: *status = AR_OK, or AR_ERR_TIMEOUT when a
  * step-wise barrier, or a wait inside a kernel of the training-step operators,
  * gave up waiting since the last read (the kernel then stopped early and its
- * buffers hold partial results).
+ * buffers hold partial results).  Works in `stream` alone, so other streams run
+ * on, and may be captured meanwhile.
  * Errors: AR_ERR_INVALID_ARG (status NULL), AR_ERR_CUDA.
  */
 int ar_device_status(ar_stream_t stream, int* status);
