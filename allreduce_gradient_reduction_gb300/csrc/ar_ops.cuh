@@ -223,7 +223,9 @@ __device__ __forceinline__ void ring_copy(uint32_t to, const void* from, int byt
                : "memory");
 }
 
-// Looks for the end of the phase of the given parity, asleep for up to 10 ms.
+// Looks for the end of the phase of the given parity, asleep for a while: the
+// instruction comes back by itself after 3.8 us, however long a time it is
+// given, so a limit has to be counted on the clock and not in looks.
 __device__ __forceinline__ bool ring_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -234,6 +236,13 @@ __device__ __forceinline__ bool ring_try(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
+__device__ __forceinline__ uint64_t global_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+  return t;
+}
+constexpr uint64_t kWaitLimitNs = 2000000000ull;  // one wait
+
 // Waits for the phase of the given parity to end.  A copy ends by itself, so
 // this does too; the limit (two seconds) is for a launch that has gone wrong.
 // One wait that runs out ends the block's others, through `gave_up`, and is
@@ -241,11 +250,13 @@ __device__ __forceinline__ bool ring_try(uint32_t bar, uint32_t parity) {
 // so that none is missing at a barrier, but begin no more copies (the last
 // ones began two seconds before).
 __device__ __forceinline__ bool ring_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
+  if (ring_try(bar, parity)) return true;
+  const uint64_t until = global_ns() + kWaitLimitNs;
 #pragma unroll 1
-  for (int i = 0; i < 200; ++i) {
+  do {
     if (ring_try(bar, parity)) return true;
     if (*gave_up) return false;
-  }
+  } while (global_ns() < until);
   *gave_up = 1;
   g_status = AR_ERR_TIMEOUT;
   return false;

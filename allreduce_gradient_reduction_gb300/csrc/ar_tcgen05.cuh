@@ -57,14 +57,7 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity, uint32_t
       : "memory");
   return ok != 0;
 }
-__device__ __forceinline__ uint64_t global_ns() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-  return t;
-}
-
-constexpr uint32_t kSleepNs = 10000000;           // one look
-constexpr uint64_t kWaitLimitNs = 2000000000ull;  // one wait
+constexpr uint32_t kSleepNs = 10000000;  // one look: as long as the instruction sleeps at most (3.8 us)
 
 // Waits for the phase of the given parity to end.  Every wait is bounded: one
 // that runs out (no correct launch does) sets the block's `gave_up`, which
