@@ -336,8 +336,7 @@ cudaError_t run(int dtype, const AttnArgs& a, cudaStream_t s) {
       !make_tensor_map(&k, dtype, a.k, a.tokens, a.kv_heads, a.dim, kTile) ||
       !make_tensor_map(&v, dtype, a.v, a.tokens, a.kv_heads, a.dim, kTile))
     return cudaErrorInvalidValue;
-  // at most this many units, however the tokens are split
-  const int64_t units = a.tokens / F::kQueries + std::min<int64_t>(a.seqs, a.tokens);
+  const int64_t units = most_units(a.tokens, a.seqs, F::kQueries);
   attention_kernel<T, PANELS><<<(unsigned)(units * a.heads), F::kThreads, smem, s>>>(q, k, v, a);
   note_launch();
   return cudaGetLastError();

@@ -690,8 +690,7 @@ cudaError_t run(int dtype, const AttnArgs& a, cudaStream_t s) {
   attention_delta_kernel<T, kLanes><<<(unsigned)((a.tokens * a.heads + kRows - 1) / kRows), 256, 0, s>>>(a);
   note_launch();
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  // at most this many tiles, however the tokens are split
-  const int64_t most = a.tokens / kTile + std::min<int64_t>(a.seqs, a.tokens);
+  const int64_t most = most_units(a.tokens, a.seqs, kTile);
   const int kv_blocks = (int)(most * a.kv_heads);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(kv_blocks + most * a.heads));
