@@ -16,10 +16,13 @@ namespace {
 int esize_of(int dtype) { return dtype == AR_BF16 || dtype == AR_F16 ? 2 : 4; }
 bool is_float(int dtype) { return dtype == AR_F32 || dtype == AR_BF16 || dtype == AR_F16; }
 
-// Rows of `width` bytes, `stride` bytes apart.
+// Rows of `width` bytes, `stride` bytes apart; with `pitch`, each of them is
+// pieces of `piece` bytes, `pitch` bytes apart, and what lies between those is
+// not the operand's.
 struct Rows {
   uintptr_t lo;
   uint64_t width, stride, n;
+  uint64_t piece = 0, pitch = 0;
   uintptr_t hi() const { return lo + (n - 1) * stride + width; }
 };
 
@@ -30,18 +33,28 @@ bool make_rows(const void* p, int64_t rows, int64_t width, int64_t stride, int e
   if (rows == 1) stride = width;
   const __int128 bytes = ((__int128)(rows - 1) * stride + width) * esize;
   if (bytes >= ((__int128)1 << 62) || lo > UINTPTR_MAX - (uintptr_t)bytes) return false;
-  *out = Rows{lo, (uint64_t)width * esize, (uint64_t)stride * esize, (uint64_t)rows};
+  *out = Rows{lo, (uint64_t)width * esize, (uint64_t)stride * esize, (uint64_t)rows, 0, 0};
   return true;
 }
 
-// Whether two sets of rows share a byte.  Column ranges of the same wide
-// buffer lie between each other's rows and do not.
+// Whether b, of `b_width` bytes in each period, comes to lie on a's.
+bool meet(uintptr_t a, uint64_t a_width, uintptr_t b, uint64_t b_width, uint64_t period) {
+  const uint64_t d = a <= b ? (b - a) % period : period - (a - b) % period;
+  const uint64_t at = d % period;  // where b begins within a's period
+  return !(at >= a_width && at + b_width <= period);
+}
+
+// Whether two sets of rows share a byte (or may: not every arrangement is told
+// apart).  Column ranges of the same wide buffer lie between each other's rows
+// and do not; nor do parts that alternate piece by piece, where every piece of
+// both begins a whole number of pitches from its operand's first.
 bool overlap(const Rows& a, const Rows& b) {
   if (a.hi() <= b.lo || b.hi() <= a.lo) return false;
+  auto on_pitch = [](const Rows& r) { return r.n == 1 || r.stride % r.pitch == 0; };
+  if (a.pitch && a.pitch == b.pitch && on_pitch(a) && on_pitch(b) && !meet(a.lo, a.piece, b.lo, b.piece, a.pitch))
+    return false;
   if (a.n == 1 || b.n == 1 || a.stride != b.stride) return true;
-  const uint64_t d = a.lo <= b.lo ? (b.lo - a.lo) % a.stride : a.stride - (a.lo - b.lo) % a.stride;
-  const uint64_t at = d % a.stride;  // where b's rows begin within a's period
-  return !(at >= a.width && at + b.width <= a.stride);
+  return meet(a.lo, a.width, b.lo, b.width, a.stride);
 }
 
 bool same(const Rows& a, const Rows& b) {
@@ -180,6 +193,10 @@ bool add_tensor(Operands& o, ar::AttnTensor& t, const ar_attention_tensor& p, in
   std::vector<Rows>* to = written ? &o.out : &o.in;
   if (token_major) o.add(p.data, tokens, (heads - 1) * hs + dim, ts, 2, to);
   else o.add(p.data, heads, (tokens - 1) * ts + dim, hs, 2, to);
+  if (!o.bad && (token_major ? heads : tokens) > 1) {
+    to->back().piece = (uint64_t)dim * 2;
+    to->back().pitch = (uint64_t)(token_major ? hs : ts) * 2;
+  }
   t = ar::AttnTensor{p.data, ts, hs};
   return true;
 }

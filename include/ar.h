@@ -518,8 +518,9 @@ int ar_distill_loss_backward(const void* logits, int64_t logits_stride, const in
  * data + token * token_stride + head * head_stride + i (strides in elements).
  * data is 16-byte aligned, the strides are multiples of 8 (a stride along an
  * axis of length one is not looked at), and either tokens or heads are the
- * outer axis.  The three parts of one projection's output fit, and so do
- * [heads][tokens][dim] buffers. */
+ * outer axis.  The three parts of one projection's output fit, one after
+ * another in each token or head by head, and so do [heads][tokens][dim]
+ * buffers. */
 typedef struct {
   void* data;
   int64_t token_stride, head_stride;
