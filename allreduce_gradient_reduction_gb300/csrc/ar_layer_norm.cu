@@ -1027,7 +1027,7 @@ cudaError_t start_backward_ring(void (*kernel)(LayerNormBackwardArgs, int, int),
   if (e != cudaSuccess) return e;
   int64_t blocks = 0;
   if ((e = resident(kernel, threads * groups, smem, &blocks)) != cudaSuccess) return e;
-  blocks = std::min<int64_t>({blocks, kLayerNormMaxBlocks, (a.rows + groups - 1) / groups});
+  blocks = std::min<int64_t>({blocks, layer_norm_partial_rows(a.rows, a.cols), (a.rows + groups - 1) / groups});
   kernel<<<(unsigned)blocks, dim3(threads, groups), smem, s>>>(a, slot, stages);
   note_launch();
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
@@ -1049,7 +1049,7 @@ cudaError_t run_backward_strided(const LayerNormBackwardArgs& a, int threads, cu
 template <class T, class P>
 bool backward_ring(const LayerNormBackwardArgs& a, cudaStream_t s, cudaError_t* e) {
   constexpr int VW = 16 / sizeof(T), A = VW == 8 ? 1 : 2;
-  if (a.cols > 32768 || 2 * ring_slot<T>(a.cols) > kRingMaxShared) return false;
+  if (a.cols > kLayerNormKeptCols || 2 * ring_slot<T>(a.cols) > kRingMaxShared) return false;
   const bool whole = a.cols % VW == 0 && rows_aligned16(a.x, a.x_stride, a.rows, sizeof(T)) &&
                      rows_aligned16(a.dy, a.dy_stride, a.rows, sizeof(T)) &&
                      rows_aligned16(a.dx, a.dx_stride, a.rows, sizeof(T)) && params_aligned<T, P>(a.weight);
@@ -1087,14 +1087,14 @@ cudaError_t backward_wide(const LayerNormBackwardArgs& a, cudaStream_t s) {
     const Deal d = deal((a.cols + 3) / 4, counts, 1024);
     if (d.nv && rows_aligned16(a.x, a.x_stride, a.rows, 4) && rows_aligned16(a.dy, a.dy_stride, a.rows, 4) &&
         rows_aligned16(a.dx, a.dx_stride, a.rows, 4) && params_aligned<T, P>(a.weight)) {
-      const int blocks = (int)std::min<int64_t>(std::min(sm_count(), kLayerNormMaxBlocks), a.rows);
+      const int blocks = (int)std::min<int64_t>(sm_count(), layer_norm_partial_rows(a.rows, a.cols));
       layer_norm_backward_kernel<T, P, 4, 4><<<blocks, d.threads, 0, s>>>(a);
       note_launch();
       if ((e = cudaGetLastError()) != cudaSuccess) return e;
       return run_params<P>(a, blocks, s);
     }
   }
-  const int slices = (int)std::min<int64_t>(a.rows, 64);
+  const int slices = (int)std::min<int64_t>(kLayerNormMaxSlices, layer_norm_partial_rows(a.rows, a.cols));
   layer_norm_params_wide_kernel<T><<<dim3((unsigned)((a.cols + 255) / 256), slices), 256, 0, s>>>(a);
   note_launch();
   if ((e = cudaGetLastError()) != cudaSuccess) return e;

@@ -37,9 +37,15 @@ struct LayerNormBackwardArgs {
   int64_t rows, cols;
 };
 
-// Most blocks whose partial sums of the parameters' gradients are kept: eight
-// on each of the 152 multiprocessors.
-constexpr int kLayerNormMaxBlocks = 1216;
+// Most blocks whose partial sums of the parameters' gradients are kept, one row
+// of them each: eight on each of the 152 multiprocessors; 64 beyond the widest
+// rows that a block keeps.
+constexpr int kLayerNormMaxBlocks = 1216, kLayerNormMaxSlices = 64;
+constexpr int64_t kLayerNormKeptCols = 16384;
+inline int64_t layer_norm_partial_rows(int64_t rows, int64_t cols) {
+  const int64_t most = cols > kLayerNormKeptCols ? kLayerNormMaxSlices : kLayerNormMaxBlocks;
+  return rows < most ? rows : most;
+}
 
 // pdtype: the parameters' type, `dtype` itself or F32
 cudaError_t launch_layer_norm(int dtype, int pdtype, const LayerNormArgs& a, cudaStream_t stream);

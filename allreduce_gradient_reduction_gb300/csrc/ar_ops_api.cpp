@@ -232,8 +232,7 @@ int ar_layer_norm(const void* x, int64_t x_stride, const void* weight, const voi
 
 int64_t ar_layer_norm_workspace_bytes(int64_t rows, int64_t cols) {
   if (rows < 0 || cols < 1 || rows > kMaxRows || cols > kMaxWidth) return AR_ERR_INVALID_ARG;
-  const int64_t blocks = rows < ar::kLayerNormMaxBlocks ? rows : ar::kLayerNormMaxBlocks;
-  return blocks * 2 * cols * (int64_t)sizeof(float);
+  return ar::layer_norm_partial_rows(rows, cols) * 2 * cols * (int64_t)sizeof(float);
 }
 
 int ar_layer_norm_backward(const void* dy, int64_t dy_stride, const void* x, int64_t x_stride, const void* weight,
