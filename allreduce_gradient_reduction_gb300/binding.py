@@ -491,7 +491,7 @@ def _attention_operands(q, k, queries, keys, cu_seqlens, lse):
     dim], all of one type."""
     types = _TORCH_DTYPE or _dtypes()
     qshape, kshape, dtype = q.shape, k.shape, q.dtype
-    if len(qshape) != 3 or len(kshape) != 3 or qshape[0] != kshape[0] or qshape[2] != kshape[2]:
+    if len(qshape) != 3 or len(kshape) != 3 or qshape[0] != kshape[0] or qshape[2] != kshape[2] or qshape[2] < 1:
         return AR_ERR_INVALID_ARG, 0, None
     dt = types.get(dtype)
     if dt is None:
