@@ -12,11 +12,11 @@
 // rounded to the type of v, as the tensor cores need, an error of half a unit
 // in the last place of each; the sum that divides them is of the unrounded.
 //
-// Measured: 8192 tokens of one sequence, 32 heads of 128 over 8 K/V heads, 351
+// Measured: 8192 tokens of one sequence, 32 heads of 128 over 8 K/V heads, 350
 // us (1.57 PFLOP/s, 82% of the rate of a plain matrix product on the same
-// device); 32 heads of 64, 283 us (the products alone are half of it: 128 x 128
-// exponentials at one every eight cycles a lane take as long as 64 elements'
-// products).
+// device); 32 heads of 64, 284 us, of which the products alone are half (the
+// exponentials of a tile take as long as its products, and one block's do not
+// cover the other's products whole).
 //
 // The running maximum that scales the output is moved only when a row's true
 // maximum has grown by more than 8 in the exponent of two: until then the

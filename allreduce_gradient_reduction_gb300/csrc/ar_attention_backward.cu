@@ -19,12 +19,13 @@
 // each term).  The next tiles' products are issued between the current one's
 // sums, so the tensor cores work while exponentials are taken.
 //
-// Measured: 8192 tokens, 32 heads of 128 over 8 K/V heads, 1.07 ms as one
-// sequence (1.29 PFLOP/s counting five products, 1.80 with the two that are
-// made twice: 95% of the rate of a plain matrix product on the same device),
-// 484 us as three; 12 heads of 64, as 13 sequences, 62 us.  The blocks of dq
-// spend 93% of a step in products, those of dk and dv 77%: there a step's
-// exponentials come between two products that need them.
+// Measured (device time, bf16): 8192 tokens, 32 heads of 128 over 8 K/V heads,
+// 1.07 ms as one sequence (1.28 PFLOP/s counting five products, 1.80 with the two
+// that are made twice: 94% of the rate of a plain matrix product on the same
+// device), 489 us as three of equal length, 611 as three of 1215, 1830 and 5147;
+// 12 heads of 64, 65 us as 13 sequences of equal length, 77 as 13 of up to 1757
+// tokens.  The blocks of dq spend 93% of a step in products, those of dk and dv
+// 77%: there a step's exponentials come between two products that need them.
 #include "ar_tcgen05.cuh"
 
 #include <algorithm>

@@ -15,10 +15,13 @@
 // once in binary32 and rounded once.
 //
 // Measured (device time, share of the measured copy bandwidth): loss of 2048 x
-// 50257 f32 64 us, 97%; loss and gradient of 8192 x 50257 bf16 341 us, 73%
-// (two exponentials, a maximum and three conversions an element: the pipe that
-// has the last two is 44% busy, the multiprocessor waits for itself more than
-// for memory); gradient alone of 1023 x 128003 f16 104 us, 75%.
+// 50257 f32 66 us, 94%, of 8192 x 30000 f16 109 us, 68%; loss and gradient of
+// 8192 x 50257 bf16 343 us, 72% (two exponentials, a maximum and three
+// conversions an element: the pipe that has the last two is 44% busy, the
+// multiprocessor waits for itself more than for memory), of 4096 x 50257 f32 333
+// us, 74%; gradient alone of 1023 x 128003 f16 108 us, 73%, f32 196 us, 80%.
+// Lists beyond 88 entries leave room for one block a multiprocessor where rows
+// are kept: 8192 x 50257 bf16 with 128 entries 519 us.
 #include "ar_ops.cuh"
 
 #include <algorithm>

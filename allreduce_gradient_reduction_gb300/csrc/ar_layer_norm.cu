@@ -18,11 +18,17 @@
 // over rows; the groups' sums are joined in a fixed order, in the block and
 // then in a second kernel, so the result does not depend on timing.
 //
-// Measured (device time, share of the measured copy bandwidth): forward 16384
-// x 5120 bf16 61 us, 82%; 8192 x 768 f32 8.1 us, 93%; backward 32768 x 4096
-// bf16 with f32 parameters 143 us, 84% (with its second kernel); 8192 x 768
-// f32 15.4 us, 74%.  Rows of odd width are read and written element by
-// element and bound by that: forward 16384 x 5121 bf16 92 us, 54%.
+// Measured (device time from HBM, share of the measured copy bandwidth): forward
+// 16384 rows of bf16 with f32 parameters, 512 columns 10.4 us, 48%; 768 16.1 us,
+// 47%; 1024 19.2 us, 53%; 2048 29.7 us, 68%; 4096 55.6 us, 72%; 5120 60.0 us,
+// 84% (narrower rows wait for their two reductions, two or three rows to a
+// multiprocessor at a time); 8192 x 768 f32 12.8 us, 59% (8.1 where the rows are
+// in L2).  Backward 32768 x 4096 bf16 with f32 parameters 142 us, 85% (with its
+// second kernel); 8192 x 768 f32 20.0 us, 57% (15.4 from L2); 8192 x 16384 bf16
+// 285 us, 42% (64 registers a thread, which spill).  Rows of odd width are read
+// and written element by element: forward 16384 x 5121 bf16 91 us, 56%, no unit
+// above 39%: few warps, each between two barriers; backward 8192 x 16383 f16 329
+// us, 37%.
 #include "ar_ops.cuh"
 
 #include <algorithm>
@@ -961,9 +967,10 @@ bool forward_ring(const LayerNormArgs& a, cudaStream_t s, cudaError_t* e) {
   if constexpr (sizeof(P) == 4 && sizeof(T) == 2) {
     // f32 parameters of 16-bit rows stay in registers, two vectors to a thread,
     // unless that leaves more than an eighth of a narrow row's threads without
-    // work (16384 rows; parameters kept, and read again for each row: 512
-    // columns 7.8 and 10.1 us, 768 15.9 and 12.7, 1536 22.9 and 25.6, 2048 31.0
-    // and 36.5, 4096 58.1 and 67.2).
+    // work (16384 rows, the same ones again and again, narrow ones in L2;
+    // parameters kept, and read again for each row: 512 columns 7.8 and 10.1 us,
+    // 768 15.9 and 12.7, 1536 22.9 and 25.6, 2048 31.0 and 36.5, 4096 58.1 and
+    // 67.2).
     static const int kept[1] = {2 * A};
     const Deal d = deal(a.cols / VW, kept, 512);
     if (d.nv && (a.cols >= 2048 || (int64_t)d.threads * d.nv * VW * 8 <= a.cols * 9)) {
