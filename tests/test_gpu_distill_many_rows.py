@@ -96,7 +96,7 @@ def check(ar, z, index, value, scale, tau, dtype, into=None):
 # second pass, and of more (copied in twice); the gradient alone by whole rows,
 # halves (8 pieces of 12288 bytes) and quarters (16 of them).
 @pytest.mark.parametrize("dtype,vdtype,vocab,top", [
-    ("bf16", "f32", 1, 1), ("f16", "f16", 5, 3), ("bf16", "bf16", 1003, 40), ("f32", "f32", 3072, 7),
+    ("bf16", "f32", 1, 1), ("f16", "f16", 5, 3), ("bf16", "bf16", 1003, 40), ("f32", "f32", 6144, 7),
     ("bf16", "f32", 6144, 1), ("f16", "f32", 6145, 33), ("f32", "f32", 20011, 64), ("bf16", "f32", 50257, 64),
     ("bf16", "f32", 50257, 128), ("f16", "f16", 100003, 20), ("bf16", "bf16", 120001, 16), ("f32", "f32", 43501, 1024),
     ("f32", "f32", 60013, 100), ("f16", "f32", 2048, 1024)])
