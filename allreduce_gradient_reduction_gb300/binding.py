@@ -39,11 +39,14 @@ EXPORTS = ("ar_allreduce", "ar_reduce_scatter", "ar_all_gather", "ar_reduce", "a
            "ar_reducer_mark_ready", "ar_reducer_finish", "ar_reducer_destroy", "ar_reducer_buckets",
            "ar_reducer_set_max_blocks", "ar_plan_create", "ar_plan_run", "ar_plan_destroy",
            "ar_layer_norm", "ar_layer_norm_backward", "ar_layer_norm_workspace_bytes", "ar_distill_loss",
-           "ar_distill_loss_backward", "ar_attention", "ar_attention_backward", "ar_attention_workspace_bytes")
+           "ar_distill_loss_backward", "ar_attention", "ar_attention_backward", "ar_attention_workspace_bytes",
+           "ar_qk_norm_rope", "ar_qk_norm_rope_backward", "ar_qk_norm_rope_workspace_bytes", "ar_diff_attention",
+           "ar_diff_attention_backward", "ar_diff_attention_workspace_bytes", "ar_activation8",
+           "ar_activation8_backward")
 
 
 class AttentionTensor(ctypes.Structure):
-    """ar_attention_tensor: an operand of the attention calls."""
+    """ar_attention_tensor: an operand of the attention calls and of the norm and rotation."""
     _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
@@ -102,10 +105,22 @@ def _load():
     L.ar_attention_backward.argtypes = [at, at, at, at, at, vp, vp, at, at, at, i64, i64, i64, i64, i64, flt, cint, vp,
                                         i64, vp]
     L.ar_attention_workspace_bytes.argtypes = [i64, i64, i64, i64]
+    dbl = ctypes.c_double
+    how = [i64, i64, i64, i64, i64, dbl, vp, cint, flt, cint, cint]
+    L.ar_qk_norm_rope.argtypes = [at, at, vp, vp, vp, at, at, *how, vp]
+    L.ar_qk_norm_rope_backward.argtypes = [at, at, at, at, vp, vp, vp, at, at, vp, vp, *how, vp, i64, vp]
+    L.ar_qk_norm_rope_workspace_bytes.argtypes = [i64, i64, i64, i64]
+    sizes = [i64, i64, i64, i64, i64, i64, flt, cint]
+    L.ar_diff_attention.argtypes = [at, at, at, vp, vp, at, at, vp, *sizes, vp]
+    L.ar_diff_attention_backward.argtypes = [at, at, at, at, vp, at, at, vp, vp, at, at, at, vp, *sizes, vp, i64, vp]
+    L.ar_diff_attention_workspace_bytes.argtypes = [i64, i64, i64, i64, i64]
+    L.ar_activation8.argtypes = [vp, i64, vp, i64, vp, vp, i64, i64, cint, cint, vp]
+    L.ar_activation8_backward.argtypes = [vp, vp, vp, i64, vp, i64, vp, i64, i64, i64, cint, cint, vp]
     for name in EXPORTS:
         if name != "ar_strerror":
             getattr(L, name).restype = cint
-    for name in ("ar_kernel_launches", "ar_layer_norm_workspace_bytes", "ar_attention_workspace_bytes"):
+    for name in ("ar_kernel_launches", "ar_layer_norm_workspace_bytes", "ar_attention_workspace_bytes",
+                 "ar_qk_norm_rope_workspace_bytes", "ar_diff_attention_workspace_bytes"):
         getattr(L, name).restype = i64
     return L
 
@@ -547,6 +562,235 @@ def ar_attention_backward(dout, q, k, v, out, lse, cu_seqlens, dq, dk, dv, works
                                      cu_seqlens.numel() - 1, heads, k.shape[1], dim,
                                      dim ** -0.5 if scale is None else scale, dt, workspace.data_ptr(),
                                      workspace.nbytes, _stream_of(stream, q))
+
+
+def _heads_of(dtype, dim, tensors):
+    """The operands as an array of ar_attention_tensor; None unless each is
+    [tokens, heads, dim] of this type with the head's elements side by side."""
+    flat = []
+    for t, shape in tensors:
+        if t.dtype is not dtype or t.shape != shape:
+            return None
+        token, head, inner = t.stride()
+        if inner != 1 and dim > 1:
+            return None
+        flat += (t.data_ptr(), token, head)
+    return array.array("q", flat)
+
+
+def _qk(q, k, q_weight, k_weight, positions, queries, keys, weights, rotary_dim, frequencies):
+    """(status, the operands as an array of ar_attention_tensor: q and
+    `queries`, then k and `keys`; the number of key heads, element types, the
+    rotated size, host frequencies)."""
+    types = _TORCH_DTYPE or _dtypes()
+    bad = AR_ERR_INVALID_ARG, None, 0, 0, 0, 0, None
+    shape, dtype = q.shape, q.dtype
+    if len(shape) != 3 or (k is None) != all(t is None for t in keys):
+        return bad
+    wdtype = q_weight.dtype if q_weight is not None else k_weight.dtype if k_weight is not None else dtype
+    dt, wt = types.get(dtype), types.get(wdtype)
+    if dt is None or wt is None:
+        return AR_ERR_UNSUPPORTED, None, 0, 0, 0, 0, None
+    tokens, heads, dim = shape
+    tensors = [(q, shape), *((t, shape) for t in queries)]
+    kv_heads = 0
+    if k is not None:
+        kshape = k.shape
+        if len(kshape) != 3 or kshape[0] != tokens or kshape[2] != dim or any(t is None for t in keys):
+            return bad
+        kv_heads = kshape[1]
+        tensors += [(k, kshape), *((t, kshape) for t in keys)]
+    operands = _heads_of(dtype, dim, tensors)
+    if operands is None or types.get(positions.dtype) != 2 or not _vector(positions, tokens, positions.dtype):
+        return bad
+    for w in (q_weight, k_weight, *weights):
+        if w is not None and not _vector(w, dim, wdtype):
+            return bad
+    rotary = dim if rotary_dim is None else rotary_dim
+    if frequencies is not None:
+        frequencies = array.array("d", frequencies)
+        if 2 * len(frequencies) != rotary:
+            return bad
+    return AR_OK, operands, kv_heads, dt, wt, rotary, frequencies
+
+
+def ar_qk_norm_rope(q, k, q_weight, k_weight, positions, q_out, k_out, rotary_dim=None, base=10000.0,
+                    frequencies=None, interleaved=False, eps=1e-6, stream=None) -> int:
+    """q_out and k_out: the heads of q [tokens, heads, dim] and k [tokens,
+    kv_heads, dim], each normalised, weighted and turned by its token's
+    position.  q_out may be q, k_out k; k, k_weight and k_out may be None, as may
+    either weight.  rotary_dim None: dim.  frequencies: a sequence of rotary_dim / 2
+    numbers, in the place of base."""
+    rc, operands, kv_heads, dt, wt, rotary, freq = _qk(q, k, q_weight, k_weight, positions, (q_out,), (k_out,), (),
+                                                       rotary_dim, frequencies)
+    if rc:
+        return rc
+    tokens, heads, dim = q.shape
+    at, n = operands.buffer_info()[0], _TENSOR_BYTES
+    some = kv_heads > 0
+    return lib.ar_qk_norm_rope(at, at + 2 * n if some else None, None if q_weight is None else q_weight.data_ptr(),
+                               None if k_weight is None else k_weight.data_ptr(), positions.data_ptr(), at + n,
+                               at + 3 * n if some else None, tokens, heads, kv_heads, dim, rotary, base,
+                               None if freq is None else freq.buffer_info()[0], int(interleaved), eps, dt, wt,
+                               _stream_of(stream, q))
+
+
+def ar_qk_norm_rope_workspace_bytes(tokens, heads, kv_heads, dim) -> int:
+    return lib.ar_qk_norm_rope_workspace_bytes(int(tokens), int(heads), int(kv_heads), int(dim))
+
+
+def ar_qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, positions, dq, dk, dq_weight, dk_weight,
+                             workspace=None, rotary_dim=None, base=10000.0, frequencies=None, interleaved=False,
+                             eps=1e-6, stream=None) -> int:
+    """dq (may be dq_out or q), dk, dq_weight and dk_weight (either may be
+    None) for upstream dq_out and dk_out.  workspace: a tensor of at least
+    ar_qk_norm_rope_workspace_bytes(tokens, heads, kv_heads, dim) bytes; None if
+    no weight's gradient is wanted."""
+    rc, operands, kv_heads, dt, wt, rotary, freq = _qk(q, k, q_weight, k_weight, positions, (dq_out, dq),
+                                                       (dk_out, dk), (dq_weight, dk_weight), rotary_dim, frequencies)
+    if rc:
+        return rc
+    if workspace is not None and not workspace.is_contiguous():
+        return AR_ERR_INVALID_ARG
+    tokens, heads, dim = q.shape
+    at, n = operands.buffer_info()[0], _TENSOR_BYTES  # q, dq_out, dq, k, dk_out, dk
+    some = kv_heads > 0
+    return lib.ar_qk_norm_rope_backward(
+        at + n, at + 4 * n if some else None, at, at + 3 * n if some else None,
+        None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(),
+        positions.data_ptr(), at + 2 * n, at + 5 * n if some else None,
+        None if dq_weight is None else dq_weight.data_ptr(), None if dk_weight is None else dk_weight.data_ptr(),
+        tokens, heads, kv_heads, dim, rotary, base, None if freq is None else freq.buffer_info()[0], int(interleaved),
+        eps, dt, wt, None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.nbytes,
+        _stream_of(stream, q))
+
+
+def _diff_operands(q, k, v, lam, cu_seqlens, lse, queries, keys, values, outs):
+    """(status, element type, heads, the operands as an array of
+    ar_attention_tensor: q, k, v, then `queries`, `keys`, `values` and `outs`,
+    which have the shapes of q, k, v and the result)."""
+    types = _TORCH_DTYPE or _dtypes()
+    bad = AR_ERR_INVALID_ARG, 0, 0, None
+    qshape, kshape, vshape, dtype = q.shape, k.shape, v.shape, q.dtype
+    if len(qshape) != 3 or len(kshape) != 3 or len(vshape) != 3 or lam.dim() != 1:
+        return bad
+    heads, tokens = lam.numel(), qshape[0]
+    if (qshape[1] != 2 * heads or kshape[1] != 2 * vshape[1] or kshape[0] != tokens or vshape[0] != tokens
+            or kshape[2] != qshape[2] or qshape[2] < 1 or not _vector(lam, heads, _F32[0])):
+        return bad
+    dt = types.get(dtype)
+    if dt is None:
+        return AR_ERR_UNSUPPORTED, 0, 0, None
+    oshape = (tokens, heads, vshape[2])
+    operands = _heads_of(dtype, 2, ((q, qshape), (k, kshape), (v, vshape), *((t, qshape) for t in queries),
+                                    *((t, kshape) for t in keys), *((t, vshape) for t in values),
+                                    *((t, oshape) for t in outs)))
+    if operands is None:
+        return bad
+    if (types.get(cu_seqlens.dtype) != 2 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1
+            or not cu_seqlens.is_contiguous()):
+        return bad
+    if lse is not None and (lse.dtype is not _F32[0] or lse.shape != (2 * heads, tokens) or not lse.is_contiguous()):
+        return bad
+    return AR_OK, dt, heads, operands
+
+
+def ar_diff_attention(q, k, v, lam, cu_seqlens, out, second=None, lse=None, scale=None, stream=None) -> int:
+    """Differential causal attention of q [tokens, 2 heads, dim] over k
+    [tokens, 2 kv_heads, dim] and v [tokens, kv_heads, value_dim], tokens packed
+    by cu_seqlens [seqs + 1] (i32, on the device), with lam [heads] (f32, the
+    second map's weight).  scale None: dim ** -0.5.  second (as out) and lse
+    [2 heads, tokens] are what the backward call needs."""
+    rc, dt, heads, operands = _diff_operands(q, k, v, lam, cu_seqlens, lse, (), (), (),
+                                             (out,) if second is None else (out, second))
+    if rc:
+        return rc
+    tokens, _, dim = q.shape
+    at, n = operands.buffer_info()[0], _TENSOR_BYTES
+    return lib.ar_diff_attention(at, at + n, at + 2 * n, lam.data_ptr(), cu_seqlens.data_ptr(), at + 3 * n,
+                                 None if second is None else at + 4 * n, None if lse is None else lse.data_ptr(),
+                                 tokens, cu_seqlens.numel() - 1, heads, v.shape[1], dim, v.shape[2],
+                                 dim ** -0.5 if scale is None else scale, dt, _stream_of(stream, q))
+
+
+def ar_diff_attention_workspace_bytes(tokens, heads, kv_heads, dim, value_dim) -> int:
+    return lib.ar_diff_attention_workspace_bytes(int(tokens), int(heads), int(kv_heads), int(dim), int(value_dim))
+
+
+def ar_diff_attention_backward(dout, q, k, v, lam, out, second, lse, cu_seqlens, dq, dk, dv, dlam, workspace,
+                               scale=None, stream=None) -> int:
+    """dq, dk, dv and dlam (which may be None) for an upstream dout, from the
+    forward call's out, second and lse.  workspace: a tensor of at least
+    ar_diff_attention_workspace_bytes(tokens, heads, kv_heads, dim, value_dim)
+    bytes."""
+    rc, dt, heads, operands = _diff_operands(q, k, v, lam, cu_seqlens, lse, (dq,), (dk,), (dv,), (out, second, dout))
+    if rc:
+        return rc
+    if lse is None or not workspace.is_contiguous() or (dlam is not None and not _vector(dlam, heads, _F32[0])):
+        return AR_ERR_INVALID_ARG
+    tokens, _, dim = q.shape
+    at, n = operands.buffer_info()[0], _TENSOR_BYTES  # q, k, v, dq, dk, dv, out, second, dout
+    return lib.ar_diff_attention_backward(at + 8 * n, at, at + n, at + 2 * n, lam.data_ptr(), at + 6 * n, at + 7 * n,
+                                          lse.data_ptr(), cu_seqlens.data_ptr(), at + 3 * n, at + 4 * n, at + 5 * n,
+                                          None if dlam is None else dlam.data_ptr(), tokens, cu_seqlens.numel() - 1,
+                                          heads, v.shape[1], dim, v.shape[2], dim ** -0.5 if scale is None else scale,
+                                          dt, workspace.data_ptr(), workspace.nbytes, _stream_of(stream, q))
+
+
+ACTIVATION = {"identity": 0, "gelu_tanh": 1, "gelu": 2}
+ACTIVATION8_BLOCK = 128
+_I8 = []  # torch.int8
+
+
+def _activation8_operands(rows, cols, codes, scales, dtype, tensors):
+    """(status, element type, row strides of the tensors, 0 for None)."""
+    dt = (_TORCH_DTYPE or _dtypes()).get(dtype)
+    if dt is None:
+        return AR_ERR_UNSUPPORTED, 0, ()
+    if not _I8:
+        import torch
+        _I8.append(torch.int8)
+    blocks, strides = -(-cols // ACTIVATION8_BLOCK), []
+    if (codes.dtype is not _I8[0] or codes.shape != (rows, blocks * ACTIVATION8_BLOCK) or not codes.is_contiguous()
+            or scales.dtype is not _F32[0] or scales.shape != (rows, blocks) or not scales.is_contiguous()):
+        return AR_ERR_INVALID_ARG, 0, ()
+    for t in tensors:
+        stride = 0 if t is None else _row_stride(t, (rows, cols), dtype)
+        if stride is None:
+            return AR_ERR_INVALID_ARG, 0, ()
+        strides.append(stride)
+    return AR_OK, dt, strides
+
+
+def ar_activation8(x, y, codes, scales, kind="gelu_tanh", stream=None) -> int:
+    """y (may be x, or None) = the activation of the matrix x [rows, cols], and x
+    in 8 bits: codes [rows, 128 ceil(cols / 128)] i8 and scales [rows,
+    ceil(cols / 128)] f32."""
+    if x.dim() != 2:
+        return AR_ERR_INVALID_ARG
+    rows, cols = x.shape
+    rc, dt, strides = _activation8_operands(rows, cols, codes, scales, x.dtype, (x, y))
+    if rc:
+        return rc
+    return lib.ar_activation8(x.data_ptr(), strides[0], None if y is None else y.data_ptr(), strides[1],
+                              codes.data_ptr(), scales.data_ptr(), rows, cols, _enum(ACTIVATION, kind), dt,
+                              _stream_of(stream, x))
+
+
+def ar_activation8_backward(codes, scales, dy, dx, y, kind="gelu_tanh", stream=None) -> int:
+    """From what ar_activation8 kept: dx (may be dy) for an upstream dy, and y,
+    the activation again.  dy and dx may be None together, or y."""
+    of = y if y is not None else dx
+    if of is None or of.dim() != 2 or (dx is None) != (dy is None):
+        return AR_ERR_INVALID_ARG
+    rows, cols = of.shape
+    rc, dt, strides = _activation8_operands(rows, cols, codes, scales, of.dtype, (dy, dx, y))
+    if rc:
+        return rc
+    return lib.ar_activation8_backward(codes.data_ptr(), scales.data_ptr(), None if dy is None else dy.data_ptr(),
+                                       strides[0], None if dx is None else dx.data_ptr(), strides[1],
+                                       None if y is None else y.data_ptr(), strides[2], rows, cols,
+                                       _enum(ACTIVATION, kind), dt, _stream_of(stream, of))
 
 
 def ar_chunk_range(count, nranks, c):

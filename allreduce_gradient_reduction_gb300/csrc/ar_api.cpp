@@ -1160,7 +1160,8 @@ int ar_device_status(ar_stream_t stream, int* status) {
     *status = AR_OK;
     // waits inside kernels of one GPU's work that ran out are reported first
     for (auto take : {ar::layer_norm_take_status, ar::distill_take_status, ar::attention_take_status,
-                      ar::attention_backward_take_status})
+                      ar::attention_backward_take_status, ar::diff_attention_take_status,
+                      ar::diff_attention_backward_take_status})
       if ((e = take(status, (cudaStream_t)stream)) != cudaSuccess) return cuda_fail(e);
     if (*status != AR_OK) return AR_OK;
     ar::SyncBlock* sb = nullptr;

@@ -92,6 +92,75 @@ struct AttnArgs {
 
 cudaError_t launch_attention(int dtype, const AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_attention_backward(int dtype, const AttnArgs& a, cudaStream_t stream);
+
+// ---- differential attention ---------------------------------------------------------------
+
+struct DiffArgs {
+  AttnTensor q, k, v, out, second;  // q [tokens][2 heads][dim], k [tokens][2 kv_heads][dim]; second.ptr may be NULL
+  AttnTensor dout, dq, dk, dv;      // backward
+  const float* lambda;              // [heads]
+  float* dlambda;                   // backward: [heads], or NULL
+  float* lse;                       // [2 heads][tokens]
+  float* delta;                     // backward: [2 heads][tokens], workspace
+  const int32_t* cu_seqlens;        // [seqs + 1]
+  int64_t tokens;
+  int32_t seqs, heads, kv_heads, dim, value_dim;
+  float scale;
+};
+
+cudaError_t launch_diff_attention(int dtype, const DiffArgs& a, cudaStream_t stream);
+cudaError_t launch_diff_attention_backward(int dtype, const DiffArgs& a, cudaStream_t stream);
+
+// ---- norm and rotation of queries and keys ---------------------------------------------
+
+constexpr int kQkMaxDim = 256;
+
+struct QkTensor {
+  const void* ptr;
+  int64_t token_stride, head_stride;  // elements
+};
+
+// [0]: queries, [1]: keys, of which there may be none
+struct QkArgs {
+  QkTensor x[2], dy[2];   // dy: backward
+  QkTensor y[2];          // the results; backward: the gradients
+  const void* weight[2];  // NULL: ones
+  void* dweight[2];       // backward; NULL: not wanted
+  const int32_t* positions;
+  float* partial;         // backward: [blocks][2][dim]
+  int64_t tokens;
+  int32_t heads[2];
+  int32_t dim, rotary;
+  float eps;
+  uint64_t turn[kQkMaxDim / 2];  // turns per position of each pair, times 2^64
+};
+
+// Blocks whose partial sums of the weights' gradients are kept, one row each.
+constexpr int kQkMaxBlocks = 608;
+
+cudaError_t launch_qk_norm_rope(int dtype, int wdtype, bool backward, bool interleaved, const QkArgs& a, cudaStream_t stream);
+
+// ---- activation kept in 8 bits ------------------------------------------------------------
+
+constexpr int kActivation8Block = 128;  // elements of a row that share a scale
+
+struct Activation8Args {
+  const void* x;  // backward: dy, or NULL
+  void* y;        // may be NULL
+  void* dx;       // backward; NULL: not wanted
+  const int8_t* codes;
+  int8_t* codes_out;
+  const float* scales;
+  float* scales_out;
+  int64_t x_stride, y_stride, dx_stride;
+  uint32_t total;         // blocks of the matrix, below 2^31
+  int32_t blocks, cols;   // blocks of a row
+  uint32_t magic, shift;  // division by `blocks`
+};
+
+cudaError_t launch_activation8(int dtype, int kind, int64_t rows, const Activation8Args& a, cudaStream_t stream);
+cudaError_t launch_activation8_backward(int dtype, int kind, int64_t rows, const Activation8Args& a, cudaStream_t stream);
+
 // What kernels of the current device left when one of their waits ran out:
 // AR_ERR_TIMEOUT is stored in *status, and cleared.  Every operation is in
 // `stream`, which the caller has synchronised.
@@ -99,5 +168,7 @@ cudaError_t layer_norm_take_status(int* status, cudaStream_t stream);
 cudaError_t distill_take_status(int* status, cudaStream_t stream);
 cudaError_t attention_take_status(int* status, cudaStream_t stream);
 cudaError_t attention_backward_take_status(int* status, cudaStream_t stream);
+cudaError_t diff_attention_take_status(int* status, cudaStream_t stream);
+cudaError_t diff_attention_backward_take_status(int* status, cudaStream_t stream);
 
 }  // namespace ar

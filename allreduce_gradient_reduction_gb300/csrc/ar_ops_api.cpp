@@ -4,8 +4,10 @@
 
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <utility>
 #include <vector>
 
 #include "ar_internal.h"
@@ -58,13 +60,15 @@ bool overlap(const Rows& a, const Rows& b) {
 }
 
 bool same(const Rows& a, const Rows& b) {
-  return a.lo == b.lo && a.width == b.width && a.n == b.n && (a.n == 1 || a.stride == b.stride);
+  return a.lo == b.lo && a.width == b.width && a.n == b.n && (a.n == 1 || a.stride == b.stride) && a.piece == b.piece &&
+         a.pitch == b.pitch;
 }
 
 // The operands of a call: what it writes overlaps nothing else, except where
 // a result may stand in the place of one input.
 struct Operands {
   std::vector<Rows> in, out;
+  std::vector<std::pair<size_t, size_t>> shared;  // an output that may be exactly this input
   bool bad = false;
   Rows add(const void* p, int64_t rows, int64_t width, int64_t stride, int esize, std::vector<Rows>* to) {
     Rows r{};
@@ -74,14 +78,18 @@ struct Operands {
   }
   void read(const void* p, int64_t rows, int64_t width, int64_t stride, int esize) { add(p, rows, width, stride, esize, &in); }
   void write(const void* p, int64_t rows, int64_t width, int64_t stride, int esize) { add(p, rows, width, stride, esize, &out); }
-  // in_place: an output may be exactly one of the first `in_place` inputs
+  bool may_share(size_t i, size_t j, int in_place) const {
+    if (i == 0 && (int)j < in_place) return true;
+    return std::find(shared.begin(), shared.end(), std::make_pair(i, j)) != shared.end();
+  }
+  // in_place: the first output may be exactly one of the first `in_place` inputs
   int check(int in_place) const {
     if (bad) return AR_ERR_INVALID_ARG;
     for (size_t i = 0; i < out.size(); ++i) {
       for (size_t j = 0; j < i; ++j)
         if (overlap(out[i], out[j])) return AR_ERR_INVALID_ARG;
       for (size_t j = 0; j < in.size(); ++j)
-        if (overlap(out[i], in[j]) && !(i == 0 && (int)j < in_place && same(out[i], in[j]))) return AR_ERR_INVALID_ARG;
+        if (overlap(out[i], in[j]) && !(may_share(i, j, in_place) && same(out[i], in[j]))) return AR_ERR_INVALID_ARG;
     }
     std::vector<ar::AddressRange> rs;
     for (const Rows& r : in) rs.push_back({r.lo, r.hi()});
@@ -202,6 +210,176 @@ bool add_tensor(Operands& o, ar::AttnTensor& t, const ar_attention_tensor& p, in
 }
 
 int64_t attention_workspace(int64_t tokens, int64_t heads) { return (tokens * heads * 4 + 15) / 16 * 16; }
+
+int check_diff_attention(int64_t tokens, int64_t seqs, int64_t heads, int64_t kv_heads, int64_t dim, int64_t value_dim,
+                         float scale, int dtype) {
+  const int rc = check_attention(tokens, seqs, heads, kv_heads, dim, scale, dtype);
+  if (value_dim < 1) return AR_ERR_INVALID_ARG;
+  if (rc) return rc;
+  if (dim > AR_DIFF_ATTENTION_MAX_DIM || value_dim % 8 || value_dim > AR_ATTENTION_MAX_DIM) return AR_ERR_UNSUPPORTED;
+  // every head twice, and blocks of their own for the gradient of lambda
+  if (heads > 2048 || (tokens / 128 + seqs) * (heads + kv_heads) > INT32_MAX - heads || 2 * tokens * heads > INT32_MAX)
+    return AR_ERR_TOO_LARGE;
+  return AR_OK;
+}
+
+// ---- norm and rotation of queries and keys
+
+int check_qk(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t dim) {
+  if (tokens < 0 || heads < 1 || kv_heads < 0 || dim < 1) return AR_ERR_INVALID_ARG;
+  if (dim % 2 || dim > AR_QK_MAX_DIM) return AR_ERR_UNSUPPORTED;
+  if (tokens > kMaxRows || heads > (1 << 20) || kv_heads > (1 << 20)) return AR_ERR_TOO_LARGE;
+  return AR_OK;
+}
+
+// A [tokens][heads][dim] operand of any strides with tokens or heads as the
+// outer axis.
+bool add_heads(Operands& o, ar::QkTensor& t, const ar_attention_tensor* p, int64_t tokens, int64_t heads, int64_t dim,
+               int esize, bool written) {
+  if (!p) return false;
+  int64_t ts = p->token_stride, hs = p->head_stride;
+  if (heads == 1) hs = dim;
+  if (tokens == 1) ts = heads * (hs > dim ? hs : dim);
+  if (ts < dim || hs < dim || ts > AR_MAX_COUNT || hs > AR_MAX_COUNT) return false;
+  const bool token_major = ts >= (__int128)(heads - 1) * hs + dim;
+  const bool head_major = hs >= (__int128)(tokens - 1) * ts + dim;
+  if (!token_major && !head_major) return false;
+  std::vector<Rows>* to = written ? &o.out : &o.in;
+  if (token_major) o.add(p->data, tokens, (heads - 1) * hs + dim, ts, esize, to);
+  else o.add(p->data, heads, (tokens - 1) * ts + dim, hs, esize, to);
+  if (!o.bad && (token_major ? heads : tokens) > 1) {
+    to->back().piece = (uint64_t)dim * esize;
+    to->back().pitch = (uint64_t)(token_major ? hs : ts) * esize;
+  }
+  t = ar::QkTensor{p->data, ts, hs};
+  return true;
+}
+
+// Turns per position of each pair, times 2^64.  A training loop asks for the
+// same ones in every call, and powers take longer than the rest of it, so a
+// thread has those of its last base at hand.
+bool fill_turns(uint64_t* turn, int64_t rotary, double base, const double* frequencies) {
+  constexpr double kTurn = 6.283185307179586476925;
+  auto fraction = [](double frequency) {
+    const double turns = frequency / kTurn, part = turns - std::floor(turns);
+    return part < 1.0 ? (uint64_t)std::ldexp(part, 64) : 0;  // a small negative one may round to a whole turn
+  };
+  if (frequencies) {
+    for (int64_t i = 0; i < rotary / 2; ++i) {
+      if (!std::isfinite(frequencies[i])) return false;
+      turn[i] = fraction(frequencies[i]);
+    }
+    return true;
+  }
+  struct Last {
+    double base = 0;
+    int64_t rotary = 0;
+    uint64_t turn[ar::kQkMaxDim / 2];
+  };
+  static thread_local Last last;
+  if (last.base != base || last.rotary != rotary) {
+    last.rotary = -1;
+    for (int64_t i = 0; i < rotary / 2; ++i) {
+      const double f = std::pow(base, -2.0 * (double)i / (double)rotary);
+      if (!std::isfinite(f)) return false;
+      last.turn[i] = fraction(f);
+    }
+    last.base = base;
+    last.rotary = rotary;
+  }
+  std::memcpy(turn, last.turn, (size_t)(rotary / 2) * sizeof(uint64_t));
+  return true;
+}
+
+int64_t qk_workspace(int64_t dim) { return (int64_t)ar::kQkMaxBlocks * 2 * dim * (int64_t)sizeof(float); }
+
+int qk_norm_rope(bool backward, const ar_attention_tensor* q_up, const ar_attention_tensor* k_up,
+                 const ar_attention_tensor* q, const ar_attention_tensor* k, const void* q_weight, const void* k_weight,
+                 const int32_t* positions, const ar_attention_tensor* q_out, const ar_attention_tensor* k_out,
+                 void* dq_weight, void* dk_weight, int64_t tokens, int64_t heads, int64_t kv_heads, int64_t dim,
+                 int64_t rotary, double base, const double* frequencies, bool interleaved, float eps, int dtype,
+                 int wdtype, void* workspace, int64_t workspace_bytes, cudaStream_t s) {
+  int rc = check_qk(tokens, heads, kv_heads, dim);
+  if (rc == AR_ERR_INVALID_ARG) return rc;
+  if (rotary < 0 || rotary > dim || rotary % 2 || !(eps >= 0.f) || !std::isfinite(eps)) return AR_ERR_INVALID_ARG;
+  if (!frequencies && (!(base > 0.0) || !std::isfinite(base))) return AR_ERR_INVALID_ARG;
+  if (dtype < AR_F32 || dtype > AR_F16 || wdtype < AR_F32 || wdtype > AR_F16) return AR_ERR_INVALID_ARG;
+  if (!is_float(dtype) || (wdtype != AR_F32 && wdtype != dtype)) return AR_ERR_UNSUPPORTED;
+  if (rc) return rc;
+  const int es = esize_of(dtype), ws = esize_of(wdtype);
+  ar::QkArgs a{};
+  if (!fill_turns(a.turn, rotary, base, frequencies)) return AR_ERR_INVALID_ARG;
+  if (kv_heads == 0) k_weight = nullptr;
+  Operands o;
+  void* const dweight[2] = {dq_weight, dk_weight};
+  if (tokens == 0) {
+    // empty sums
+    for (void* w : dweight)
+      if (w) o.write(w, 1, dim, 0, ws);
+    if (o.out.empty() && !o.bad) return AR_OK;
+    if ((rc = o.check(0))) return rc;
+    for (void* w : dweight)
+      if (w && (rc = status_of(cudaMemsetAsync(w, 0, (size_t)dim * ws, s)))) return rc;
+    return AR_OK;
+  }
+  const ar_attention_tensor* const x[2] = {q, k};
+  const ar_attention_tensor* const up[2] = {q_up, k_up};
+  const ar_attention_tensor* const y[2] = {q_out, k_out};
+  const int64_t n[2] = {heads, kv_heads};
+  for (int t = 0; t < 2; ++t) {
+    if (!n[t]) continue;
+    if (!add_heads(o, a.x[t], x[t], tokens, n[t], dim, es, false)) return AR_ERR_INVALID_ARG;
+    o.shared.push_back({(size_t)t, o.in.size() - 1});
+    if (backward) {
+      if (!add_heads(o, a.dy[t], up[t], tokens, n[t], dim, es, false)) return AR_ERR_INVALID_ARG;
+      o.shared.push_back({(size_t)t, o.in.size() - 1});
+    }
+    if (!add_heads(o, a.y[t], y[t], tokens, n[t], dim, es, true)) return AR_ERR_INVALID_ARG;
+  }
+  if (q_weight) o.read(q_weight, 1, dim, 0, ws);
+  if (k_weight) o.read(k_weight, 1, dim, 0, ws);
+  o.read(positions, 1, tokens, 0, 4);
+  if (dq_weight || dk_weight) {
+    if (workspace_bytes < qk_workspace(dim)) return AR_ERR_INVALID_ARG;
+    for (void* w : dweight)
+      if (w) o.write(w, 1, dim, 0, ws);
+    o.write(workspace, 1, qk_workspace(dim) / 4, 0, 4);
+    a.partial = static_cast<float*>(workspace);
+  }
+  if ((rc = o.check(0))) return rc;
+  a.weight[0] = q_weight;
+  a.weight[1] = k_weight;
+  a.dweight[0] = dq_weight;
+  a.dweight[1] = dk_weight;
+  a.positions = positions;
+  a.tokens = tokens;
+  a.heads[0] = (int32_t)heads;
+  a.heads[1] = (int32_t)kv_heads;
+  a.dim = (int32_t)dim;
+  a.rotary = (int32_t)rotary;
+  a.eps = eps;
+  return status_of(ar::launch_qk_norm_rope(dtype, wdtype, backward, interleaved, a, s));
+}
+
+// ---- activation kept in 8 bits
+
+int check_activation8(int64_t rows, int64_t cols, int kind, int dtype) {
+  if (rows < 0 || cols < 1 || rows > AR_MAX_COUNT || cols > AR_MAX_COUNT) return AR_ERR_INVALID_ARG;
+  if (dtype < AR_F32 || dtype > AR_F16 || kind < AR_ACT_IDENTITY || kind > AR_ACT_GELU) return AR_ERR_INVALID_ARG;
+  if (!is_float(dtype)) return AR_ERR_UNSUPPORTED;
+  // blocks are counted in 31 bits, past the last by as many as a launch's last threads go
+  const int64_t blocks = (cols + AR_ACTIVATION8_BLOCK - 1) / AR_ACTIVATION8_BLOCK;
+  if (rows > kMaxRows || cols > kMaxWidth || rows * blocks > INT32_MAX - 4096) return AR_ERR_TOO_LARGE;
+  return AR_OK;
+}
+
+ar::Activation8Args activation8_args(int64_t rows, int64_t cols) {
+  ar::Activation8Args a{};
+  a.cols = (int32_t)cols;
+  a.blocks = (int32_t)((cols + AR_ACTIVATION8_BLOCK - 1) / AR_ACTIVATION8_BLOCK);
+  a.total = (uint32_t)(rows * a.blocks);
+  return a;
+}
 
 }  // namespace
 
@@ -359,6 +537,189 @@ int ar_attention_backward(const ar_attention_tensor* dout, const ar_attention_te
     a.dim = (int32_t)dim;
     a.scale = scale;
     return status_of(ar::launch_attention_backward(dtype, a, (cudaStream_t)stream));
+  });
+}
+
+int ar_qk_norm_rope(const ar_attention_tensor* q, const ar_attention_tensor* k, const void* q_weight,
+                    const void* k_weight, const int32_t* positions, const ar_attention_tensor* q_out,
+                    const ar_attention_tensor* k_out, int64_t tokens, int64_t heads, int64_t kv_heads, int64_t dim,
+                    int64_t rotary_dim, double base, const double* frequencies, int interleaved, float eps,
+                    ar_dtype dtype, ar_dtype weight_dtype, ar_stream_t stream) {
+  return guarded([&]() -> int {
+    return qk_norm_rope(false, nullptr, nullptr, q, k, q_weight, k_weight, positions, q_out, k_out, nullptr, nullptr,
+                        tokens, heads, kv_heads, dim, rotary_dim, base, frequencies, interleaved != 0, eps, dtype,
+                        weight_dtype, nullptr, 0, (cudaStream_t)stream);
+  });
+}
+
+int64_t ar_qk_norm_rope_workspace_bytes(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t dim) {
+  const int rc = check_qk(tokens, heads, kv_heads, dim);
+  return rc ? rc : qk_workspace(dim);
+}
+
+int ar_qk_norm_rope_backward(const ar_attention_tensor* dq_out, const ar_attention_tensor* dk_out,
+                             const ar_attention_tensor* q, const ar_attention_tensor* k, const void* q_weight,
+                             const void* k_weight, const int32_t* positions, const ar_attention_tensor* dq,
+                             const ar_attention_tensor* dk, void* dq_weight, void* dk_weight, int64_t tokens,
+                             int64_t heads, int64_t kv_heads, int64_t dim, int64_t rotary_dim, double base,
+                             const double* frequencies, int interleaved, float eps, ar_dtype dtype,
+                             ar_dtype weight_dtype, void* workspace, int64_t workspace_bytes, ar_stream_t stream) {
+  return guarded([&]() -> int {
+    return qk_norm_rope(true, dq_out, dk_out, q, k, q_weight, k_weight, positions, dq, dk, dq_weight, dk_weight, tokens,
+                        heads, kv_heads, dim, rotary_dim, base, frequencies, interleaved != 0, eps, dtype, weight_dtype,
+                        workspace, workspace_bytes, (cudaStream_t)stream);
+  });
+}
+
+int ar_diff_attention(const ar_attention_tensor* q, const ar_attention_tensor* k, const ar_attention_tensor* v,
+                      const float* lambda, const int32_t* cu_seqlens, const ar_attention_tensor* out,
+                      const ar_attention_tensor* second, float* lse, int64_t tokens, int64_t seqs, int64_t heads,
+                      int64_t kv_heads, int64_t dim, int64_t value_dim, float scale, ar_dtype dtype,
+                      ar_stream_t stream) {
+  return guarded([&]() -> int {
+    int rc = check_diff_attention(tokens, seqs, heads, kv_heads, dim, value_dim, scale, dtype);
+    if (rc) return rc;
+    if (!q || !k || !v || !out) return AR_ERR_INVALID_ARG;
+    if (tokens == 0 || seqs == 0) return AR_OK;
+    ar::DiffArgs a{};
+    Operands o;
+    if (!add_tensor(o, a.q, *q, tokens, 2 * heads, dim, false) || !add_tensor(o, a.k, *k, tokens, 2 * kv_heads, dim, false) ||
+        !add_tensor(o, a.v, *v, tokens, kv_heads, value_dim, false) ||
+        !add_tensor(o, a.out, *out, tokens, heads, value_dim, true) ||
+        (second && !add_tensor(o, a.second, *second, tokens, heads, value_dim, true)))
+      return AR_ERR_INVALID_ARG;
+    o.read(lambda, 1, heads, 0, 4);
+    o.read(cu_seqlens, 1, seqs + 1, 0, 4);
+    if (lse) o.write(lse, 1, 2 * tokens * heads, 0, 4);
+    if ((rc = o.check(0))) return rc;
+    a.lambda = lambda;
+    a.lse = lse;
+    a.cu_seqlens = cu_seqlens;
+    a.tokens = tokens;
+    a.seqs = (int32_t)seqs;
+    a.heads = (int32_t)heads;
+    a.kv_heads = (int32_t)kv_heads;
+    a.dim = (int32_t)dim;
+    a.value_dim = (int32_t)value_dim;
+    a.scale = scale;
+    return status_of(ar::launch_diff_attention(dtype, a, (cudaStream_t)stream));
+  });
+}
+
+int64_t ar_diff_attention_workspace_bytes(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t dim,
+                                          int64_t value_dim) {
+  const int rc = check_diff_attention(tokens, 1, heads, kv_heads, dim, value_dim, 1.f, AR_BF16);
+  return rc ? rc : attention_workspace(tokens, 2 * heads);
+}
+
+int ar_diff_attention_backward(const ar_attention_tensor* dout, const ar_attention_tensor* q,
+                               const ar_attention_tensor* k, const ar_attention_tensor* v, const float* lambda,
+                               const ar_attention_tensor* out, const ar_attention_tensor* second, const float* lse,
+                               const int32_t* cu_seqlens, const ar_attention_tensor* dq, const ar_attention_tensor* dk,
+                               const ar_attention_tensor* dv, float* dlambda, int64_t tokens, int64_t seqs,
+                               int64_t heads, int64_t kv_heads, int64_t dim, int64_t value_dim, float scale,
+                               ar_dtype dtype, void* workspace, int64_t workspace_bytes, ar_stream_t stream) {
+  return guarded([&]() -> int {
+    int rc = check_diff_attention(tokens, seqs, heads, kv_heads, dim, value_dim, scale, dtype);
+    if (rc) return rc;
+    if (!dout || !q || !k || !v || !out || !second || !dq || !dk || !dv) return AR_ERR_INVALID_ARG;
+    Operands o;
+    if (tokens == 0 || seqs == 0) {
+      // no tokens: lambda's gradients are empty sums
+      if (!dlambda) return AR_OK;
+      o.write(dlambda, 1, heads, 0, 4);
+      if ((rc = o.check(0))) return rc;
+      return status_of(cudaMemsetAsync(dlambda, 0, (size_t)heads * 4, (cudaStream_t)stream));
+    }
+    const int64_t need = attention_workspace(tokens, 2 * heads);
+    if (workspace_bytes < need || (uintptr_t)workspace % 16) return AR_ERR_INVALID_ARG;
+    ar::DiffArgs a{};
+    if (!add_tensor(o, a.q, *q, tokens, 2 * heads, dim, false) || !add_tensor(o, a.k, *k, tokens, 2 * kv_heads, dim, false) ||
+        !add_tensor(o, a.v, *v, tokens, kv_heads, value_dim, false) ||
+        !add_tensor(o, a.out, *out, tokens, heads, value_dim, false) ||
+        !add_tensor(o, a.second, *second, tokens, heads, value_dim, false) ||
+        !add_tensor(o, a.dout, *dout, tokens, heads, value_dim, false) ||
+        !add_tensor(o, a.dq, *dq, tokens, 2 * heads, dim, true) || !add_tensor(o, a.dk, *dk, tokens, 2 * kv_heads, dim, true) ||
+        !add_tensor(o, a.dv, *dv, tokens, kv_heads, value_dim, true))
+      return AR_ERR_INVALID_ARG;
+    o.read(lambda, 1, heads, 0, 4);
+    o.read(cu_seqlens, 1, seqs + 1, 0, 4);
+    o.read(lse, 1, 2 * tokens * heads, 0, 4);
+    if (dlambda) o.write(dlambda, 1, heads, 0, 4);
+    o.write(workspace, 1, need / 4, 0, 4);
+    if ((rc = o.check(0))) return rc;
+    a.lambda = lambda;
+    a.dlambda = dlambda;
+    a.lse = const_cast<float*>(lse);
+    a.delta = static_cast<float*>(workspace);
+    a.cu_seqlens = cu_seqlens;
+    a.tokens = tokens;
+    a.seqs = (int32_t)seqs;
+    a.heads = (int32_t)heads;
+    a.kv_heads = (int32_t)kv_heads;
+    a.dim = (int32_t)dim;
+    a.value_dim = (int32_t)value_dim;
+    a.scale = scale;
+    return status_of(ar::launch_diff_attention_backward(dtype, a, (cudaStream_t)stream));
+  });
+}
+
+int ar_activation8(const void* x, int64_t x_stride, void* y, int64_t y_stride, int8_t* codes, float* scales,
+                   int64_t rows, int64_t cols, ar_activation kind, ar_dtype dtype, ar_stream_t stream) {
+  return guarded([&]() -> int {
+    int rc = check_activation8(rows, cols, kind, dtype);
+    if (rc) return rc;
+    if (rows > 1 && (x_stride < cols || (y && y_stride < cols))) return AR_ERR_INVALID_ARG;
+    if (rows == 0) return AR_OK;
+    if ((uintptr_t)codes % 16) return AR_ERR_INVALID_ARG;
+    const int es = esize_of(dtype);
+    ar::Activation8Args a = activation8_args(rows, cols);
+    Operands o;
+    o.read(x, rows, cols, x_stride, es);
+    if (y) o.write(y, rows, cols, y_stride, es);
+    o.write(codes, 1, (int64_t)a.total * AR_ACTIVATION8_BLOCK, 0, 1);
+    o.write(scales, 1, a.total, 0, 4);
+    if ((rc = o.check(y ? 1 : 0))) return rc;
+    a.x = x;
+    a.y = y;
+    a.codes_out = codes;
+    a.scales_out = scales;
+    a.x_stride = x_stride;
+    a.y_stride = y_stride;
+    return status_of(ar::launch_activation8(dtype, kind, rows, a, (cudaStream_t)stream));
+  });
+}
+
+int ar_activation8_backward(const int8_t* codes, const float* scales, const void* dy, int64_t dy_stride, void* dx,
+                            int64_t dx_stride, void* y, int64_t y_stride, int64_t rows, int64_t cols,
+                            ar_activation kind, ar_dtype dtype, ar_stream_t stream) {
+  return guarded([&]() -> int {
+    int rc = check_activation8(rows, cols, kind, dtype);
+    if (rc) return rc;
+    if (rows == 0) return AR_OK;
+    if (!dx != !dy || (!dx && !y)) return AR_ERR_INVALID_ARG;
+    if (rows > 1 && ((dx && (dy_stride < cols || dx_stride < cols)) || (y && y_stride < cols))) return AR_ERR_INVALID_ARG;
+    if ((uintptr_t)codes % 16) return AR_ERR_INVALID_ARG;
+    const int es = esize_of(dtype);
+    ar::Activation8Args a = activation8_args(rows, cols);
+    Operands o;
+    if (dx) {
+      o.read(dy, rows, cols, dy_stride, es);
+      o.write(dx, rows, cols, dx_stride, es);
+    }
+    o.read(codes, 1, (int64_t)a.total * AR_ACTIVATION8_BLOCK, 0, 1);
+    o.read(scales, 1, a.total, 0, 4);
+    if (y) o.write(y, rows, cols, y_stride, es);
+    if ((rc = o.check(dx ? 1 : 0))) return rc;
+    a.x = dy;
+    a.y = y;
+    a.dx = dx;
+    a.codes = codes;
+    a.scales = scales;
+    a.x_stride = dy_stride;
+    a.y_stride = y_stride;
+    a.dx_stride = dx_stride;
+    return status_of(ar::launch_activation8_backward(dtype, kind, rows, a, (cudaStream_t)stream));
   });
 }
 

@@ -579,6 +579,158 @@ int ar_attention_backward(const ar_attention_tensor* dout, const ar_attention_te
 /* Host-only; a negative ar_status for sizes the calls would refuse. */
 int64_t ar_attention_workspace_bytes(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t dim);
 
+/*
+ * Norm of each head of the queries and keys, and the rotation by the token's
+ * position, in one pass.  For each token and head of q (and of k, with
+ * k_weight):
+ *   n = x (sum(x^2) / dim + eps)^-1/2 q_weight,
+ *   y_a = n_a cos t - n_b sin t, y_b = n_b cos t + n_a sin t,
+ * where (a, b) is a pair of the first rotary_dim elements and t = position
+ * times the pair's frequency; the other elements are n.
+ *   q, q_out    [tokens][heads][dim], k, k_out [tokens][kv_heads][dim] of
+ *               dtype (f32, bf16 or f16).  Unlike the attention calls' operands
+ *               they need no more than the element's alignment, and any strides
+ *               with tokens or heads as the outer axis; on 16-byte boundaries
+ *               they move in 16-byte vectors.  q_out may be q, and k_out k.
+ *               kv_heads may be 0, and k, k_weight and k_out NULL then.
+ *   q_weight, k_weight  [dim] of weight_dtype (dtype or f32); NULL: ones
+ *   positions   [tokens] i32, any values
+ *   dim         even, up to AR_QK_MAX_DIM
+ *   rotary_dim  even, 0 to dim
+ *   frequencies  host array of rotary_dim / 2, in radians per position, finite;
+ *               NULL: pair i has base^(-2 i / rotary_dim).  Read before the
+ *               call returns.
+ *   base        finite, > 0; not looked at with frequencies
+ *   interleaved  0: pair i is elements i and i + rotary_dim / 2; else 2 i and
+ *               2 i + 1
+ *   eps         finite, >= 0
+ * The angle is exact modulo one turn for the frequency in binary64, so far
+ * positions are as exact as near ones.
+ */
+#define AR_QK_MAX_DIM 256
+int ar_qk_norm_rope(const ar_attention_tensor* q, const ar_attention_tensor* k, const void* q_weight,
+                    const void* k_weight, const int32_t* positions, const ar_attention_tensor* q_out,
+                    const ar_attention_tensor* k_out, int64_t tokens, int64_t heads, int64_t kv_heads, int64_t dim,
+                    int64_t rotary_dim, double base, const double* frequencies, int interleaved, float eps,
+                    ar_dtype dtype, ar_dtype weight_dtype, ar_stream_t stream);
+
+/*
+ * Its gradient: with g the upstream gradient turned back by the same angles
+ * and r = (sum(x^2) / dim + eps)^-1/2,
+ *   dq = r (g q_weight - q r^2 sum(g q_weight q) / dim),
+ *   dq_weight = sum over tokens and heads of g q r, and the same for k.
+ *   dq          may be dq_out or q in place, dk likewise
+ *   dq_weight, dk_weight  [dim] of weight_dtype, overwritten (zeros if there
+ *               are no tokens); either may be NULL
+ *   workspace   device memory of at least ar_qk_norm_rope_workspace_bytes
+ *               bytes, 4-byte aligned; not looked at if both are NULL
+ */
+int ar_qk_norm_rope_backward(const ar_attention_tensor* dq_out, const ar_attention_tensor* dk_out,
+                             const ar_attention_tensor* q, const ar_attention_tensor* k, const void* q_weight,
+                             const void* k_weight, const int32_t* positions, const ar_attention_tensor* dq,
+                             const ar_attention_tensor* dk, void* dq_weight, void* dk_weight, int64_t tokens,
+                             int64_t heads, int64_t kv_heads, int64_t dim, int64_t rotary_dim, double base,
+                             const double* frequencies, int interleaved, float eps, ar_dtype dtype,
+                             ar_dtype weight_dtype, void* workspace, int64_t workspace_bytes, ar_stream_t stream);
+/* Host-only; a negative ar_status for sizes the calls would refuse. */
+int64_t ar_qk_norm_rope_workspace_bytes(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t dim);
+
+#define AR_DIFF_ATTENTION_MAX_DIM 64
+
+/*
+ * Differential attention: the difference of two softmax maps with a learned
+ * weight, causal, over packed sequences, with grouped heads.  Head h has the
+ * query heads 2h and 2h + 1, and of its group g = h / (heads / kv_heads) the key
+ * heads 2g and 2g + 1 and the value head g.  For token i, over the tokens j <= i
+ * of the same sequence, m = 0, 1:
+ *   a_mj = scale q[i,2h+m] . k[j,2g+m], p_m = softmax(a_m),
+ *   out[i,h] = sum_j (p_0j - lambda[h] p_1j) v[j,g],
+ *   second[i,h] = sum_j p_1j v[j,g], lse[2h+m][i] = log sum_j exp(a_mj).
+ *   q           [tokens][2 heads][dim], k [tokens][2 kv_heads][dim] of dtype:
+ *               bf16 or f16; dim a multiple of 8 up to
+ *               AR_DIFF_ATTENTION_MAX_DIM
+ *   v           [tokens][kv_heads][value_dim], out and second
+ *               [tokens][heads][value_dim] of dtype; value_dim a multiple of 8
+ *               up to AR_ATTENTION_MAX_DIM
+ *   lambda      [heads] f32 on the device
+ *   second, lse  what the backward call needs; either may be NULL
+ *   lse         [2 heads][tokens] f32
+ *   cu_seqlens, scale, and what infinities and NaN reach: as in ar_attention
+ */
+int ar_diff_attention(const ar_attention_tensor* q, const ar_attention_tensor* k, const ar_attention_tensor* v,
+                      const float* lambda, const int32_t* cu_seqlens, const ar_attention_tensor* out,
+                      const ar_attention_tensor* second, float* lse, int64_t tokens, int64_t seqs, int64_t heads,
+                      int64_t kv_heads, int64_t dim, int64_t value_dim, float scale, ar_dtype dtype,
+                      ar_stream_t stream);
+
+/*
+ * Its gradient for an upstream dout: with p_m = exp(a_m - lse),
+ *   delta_1 = dout[i,h] . second[i,h], delta_0 = dout[i,h] . out[i,h] + lambda[h] delta_1,
+ *   da_0ij = p_0ij (dout[i,h] . v[j] - delta_0), da_1ij = -lambda[h] p_1ij (dout[i,h] . v[j] - delta_1),
+ *   dq[i,2h+m] = scale sum_j da_mij k[j,2g+m], dk[j,2g+m] = scale sum_i da_mij q[i,2h+m],
+ *   dv[j,g] = sum_i (p_0ij - lambda[h] p_1ij) dout[i,h], dlambda[h] = -sum_i delta_1,
+ * dk and dv summed over the heads of a group, dlambda over the tokens of all
+ * sequences.
+ *   out, second, lse  of the forward call on the same operands
+ *   dlambda     [heads] f32, overwritten (zeros if there are no tokens or no
+ *               sequences); NULL: not wanted
+ *   workspace   16-byte aligned device memory of at least
+ *               ar_diff_attention_workspace_bytes bytes
+ * p_0 - lambda p_1 and da are rounded to dtype for their products, f16 within
+ * the same bounds as in ar_attention_backward.
+ */
+int ar_diff_attention_backward(const ar_attention_tensor* dout, const ar_attention_tensor* q,
+                               const ar_attention_tensor* k, const ar_attention_tensor* v, const float* lambda,
+                               const ar_attention_tensor* out, const ar_attention_tensor* second, const float* lse,
+                               const int32_t* cu_seqlens, const ar_attention_tensor* dq, const ar_attention_tensor* dk,
+                               const ar_attention_tensor* dv, float* dlambda, int64_t tokens, int64_t seqs,
+                               int64_t heads, int64_t kv_heads, int64_t dim, int64_t value_dim, float scale,
+                               ar_dtype dtype, void* workspace, int64_t workspace_bytes, ar_stream_t stream);
+/* Host-only; a negative ar_status for sizes the calls would refuse. */
+int64_t ar_diff_attention_workspace_bytes(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t dim,
+                                          int64_t value_dim);
+
+/* Activations of the calls below. */
+typedef enum {
+  AR_ACT_IDENTITY = 0,
+  AR_ACT_GELU_TANH = 1, /* x (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))) / 2 */
+  AR_ACT_GELU = 2       /* x times the normal distribution's integral at x */
+} ar_activation;
+
+#define AR_ACTIVATION8_BLOCK 128
+
+/*
+ * An activation whose input is kept in 8 bits for the backward pass, in the
+ * place of the input and the output.  The elements of a row are taken in blocks
+ * of AR_ACTIVATION8_BLOCK (the last may be shorter); with m the largest of a
+ * block in size,
+ *   codes = the nearest whole number (ties to even) to x * (127 / m),
+ *   scales = m / 127, y = activation(x),
+ * the quotients and the product each rounded to binary32.  A block with m below
+ * 2^-120 is kept as zeros.  One with a NaN or an infinity has a NaN for its
+ * scale and zeros for codes, so that its gradient is NaN.
+ *   x, y        [rows][cols] of dtype (f32, bf16 or f16); y may be x in place,
+ *               or NULL: the codes alone
+ *   codes       [rows][128 ceil(cols / 128)] i8, 16-byte aligned; zeros past
+ *               a row's end
+ *   scales      [rows][ceil(cols / 128)] f32
+ * With AR_ACT_IDENTITY and y NULL this packs any tensor, and the call below
+ * unpacks it.
+ */
+int ar_activation8(const void* x, int64_t x_stride, void* y, int64_t y_stride, int8_t* codes, float* scales,
+                   int64_t rows, int64_t cols, ar_activation kind, ar_dtype dtype, ar_stream_t stream);
+
+/*
+ * From codes and scales, with xk = codes * scales:
+ *   dx = dy activation'(xk), y = activation(xk): what the next layer's weight
+ * gradient needs, made again and not kept.
+ *   dy, dx      [rows][cols] of dtype; dx may be dy in place; both NULL: y alone
+ *   y           [rows][cols] of dtype; NULL: dx alone
+ */
+int ar_activation8_backward(const int8_t* codes, const float* scales, const void* dy, int64_t dy_stride, void* dx,
+                            int64_t dx_stride, void* y, int64_t y_stride, int64_t rows, int64_t cols,
+                            ar_activation kind, ar_dtype dtype, ar_stream_t stream);
+
 /* Chunk c of a rank buffer of `count` elements split N ways: [*lo, *hi).
  * Host-only; errors: AR_ERR_INVALID_ARG. */
 int ar_chunk_range(int64_t count, int nranks, int c, int64_t* lo, int64_t* hi);
