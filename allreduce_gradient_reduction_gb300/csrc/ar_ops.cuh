@@ -121,6 +121,7 @@ __device__ __forceinline__ Two mul2(Two a, Two b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
   return r;
 }
+__device__ __forceinline__ Two neg2(Two a) { return Two{a.v ^ 0x8000000080000000ull}; }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));

@@ -127,7 +127,7 @@ struct QkArgs {
   const void* weight[2];  // NULL: ones
   void* dweight[2];       // backward; NULL: not wanted
   const int32_t* positions;
-  float* partial;         // backward: [blocks][2][dim]
+  float* partial;         // backward: [blocks][dim]
   int64_t tokens;
   int32_t heads[2];
   int32_t dim, rotary;
@@ -136,7 +136,7 @@ struct QkArgs {
 };
 
 // Blocks whose partial sums of the weights' gradients are kept, one row each.
-constexpr int kQkMaxBlocks = 608;
+constexpr int kQkMaxBlocks = 456;
 
 cudaError_t launch_qk_norm_rope(int dtype, int wdtype, bool backward, bool interleaved, const QkArgs& a, cudaStream_t stream);
 

@@ -291,7 +291,7 @@ bool fill_turns(uint64_t* turn, int64_t rotary, double base, const double* frequ
   return true;
 }
 
-int64_t qk_workspace(int64_t dim) { return (int64_t)ar::kQkMaxBlocks * 2 * dim * (int64_t)sizeof(float); }
+int64_t qk_workspace(int64_t dim) { return (int64_t)ar::kQkMaxBlocks * dim * (int64_t)sizeof(float); }
 
 int qk_norm_rope(bool backward, const ar_attention_tensor* q_up, const ar_attention_tensor* k_up,
                  const ar_attention_tensor* q, const ar_attention_tensor* k, const void* q_weight, const void* k_weight,
