@@ -24,12 +24,34 @@ namespace {
 
 constexpr int kBlock = kActivation8Block;
 constexpr int kThreads = 256;
-constexpr uint32_t kLeastBits = 0x03800000u;  // 2^-120: blocks below it are zeros
-constexpr uint32_t kInfinityBits = 0x7F800000u;
+constexpr float kLeast = 0x1p-120f;  // blocks below it are zeros
 
 __device__ __forceinline__ float reciprocal(float x) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ Two reciprocal(Two t) {
+  float lo, hi;
+  split(t, lo, hi);
+  return two(reciprocal(lo), reciprocal(hi));
+}
+__device__ __forceinline__ Two exp2_approx(Two t) {
+  float lo, hi;
+  split(t, lo, hi);
+  return two(ar::exp2_approx(lo), ar::exp2_approx(hi));
+}
+__device__ __forceinline__ Two both(float v) { return two(v, v); }
+// The largest in size; NaN if there is one.
+__device__ __forceinline__ float most_of(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)), "f"(fabsf(c)));
+  return r;
+}
+__device__ __forceinline__ float most_of(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
   return r;
 }
 
@@ -40,105 +62,207 @@ constexpr float kU1 = 1.5957691216057308f, kU3 = kU1 * 0.044715f, kLog2e = 1.442
 // The normal distribution's integral at -|x|, and e^(-x^2 / 2).  erfc(y)
 // e^(y^2) = t Q(t) with t = 1 / (1 + y / 2); Q of degree 8 was fitted by
 // weighted least squares for the least relative error, 4.4e-8, over y <= 14.7.
-__device__ __forceinline__ float normal_tail(float x, float& bell) {
-  const float t = reciprocal(fmaf(fabsf(x), 0.35355339059327379f, 1.f));
-  bell = exp2_approx(x * x * -0.72134752044448169f);
-  float q = -0.0593869729f;
-  q = fmaf(q, t, 0.286126333f);
-  q = fmaf(q, t, -0.490410976f);
-  q = fmaf(q, t, 0.28173817f);
-  q = fmaf(q, t, -0.0291516083f);
-  q = fmaf(q, t, 0.203753693f);
-  q = fmaf(q, t, 0.242834857f);
-  q = fmaf(q, t, 0.282412128f);
-  q = fmaf(q, t, 0.28208433f);
-  return 0.5f * bell * t * q;
+__device__ __forceinline__ Two normal_tail(Two x, Two& bell) {
+  const Two size = Two{x.v & 0x7FFFFFFF7FFFFFFFull};
+  const Two t = reciprocal(fma2(size, both(0.35355339059327379f), both(1.f)));
+  bell = exp2_approx(mul2(mul2(x, x), both(-0.72134752044448169f)));
+  Two q = fma2(both(-0.0593869729f), t, both(0.286126333f));
+  q = fma2(q, t, both(-0.490410976f));
+  q = fma2(q, t, both(0.28173817f));
+  q = fma2(q, t, both(-0.0291516083f));
+  q = fma2(q, t, both(0.203753693f));
+  q = fma2(q, t, both(0.242834857f));
+  q = fma2(q, t, both(0.282412128f));
+  q = fma2(q, t, both(0.28208433f));
+  return mul2(mul2(bell, both(0.5f)), mul2(t, q));
+}
+// From the integral at -|x| that at x.
+__device__ __forceinline__ Two normal_at(Two x, Two tail) {
+  float x0, x1, t0, t1, u0, u1;
+  split(x, x0, x1);
+  split(tail, t0, t1);
+  split(fma2(tail, both(-1.f), both(1.f)), u0, u1);
+  return two(x0 < 0.f ? t0 : u0, x1 < 0.f ? t1 : u1);
 }
 
+// Two elements at a time.
 template <int KIND>
-__device__ __forceinline__ float activation(float x) {
+__device__ __forceinline__ Two activation(Two x) {
   if constexpr (KIND == AR_ACT_GELU_TANH) {
-    const float u = x * fmaf(kU3 * kLog2e, x * x, kU1 * kLog2e);
-    return x * reciprocal(1.f + exp2_approx(-u));
+    const Two u = mul2(x, fma2(both(-kU3 * kLog2e), mul2(x, x), both(-kU1 * kLog2e)));
+    return mul2(x, reciprocal(add2(both(1.f), exp2_approx(u))));
   } else if constexpr (KIND == AR_ACT_GELU) {
-    float bell;
-    const float tail = normal_tail(x, bell);
-    return x * (x < 0.f ? tail : 1.f - tail);
+    Two bell;
+    const Two tail = normal_tail(x, bell);
+    return mul2(x, normal_at(x, tail));
   } else {
     return x;
   }
 }
 
-// The activation and its slope.  Beyond 10 the slope is that at 10, within
-// 2^-120 of 0 or 1, and so is the activation below -10: what follows would
-// multiply an infinity by zero.
+// The activation and its slope.  `one` is one, or a NaN for a block of those.
+// Beyond 10 (the exact gelu: 18) the slope is that at 10, within 2^-120 of 0 or
+// 1, and so is the activation's factor: what follows would multiply an infinity
+// by zero.
 template <int KIND>
-__device__ __forceinline__ void activation_and_slope(float x, float& y, float& slope) {
+__device__ __forceinline__ void activation_and_slope(Two x, float one, Two& y, Two& slope) {
+  if constexpr (KIND == AR_ACT_IDENTITY) {
+    y = mul2(x, both(one));
+    slope = both(one);
+    return;
+  }
+  constexpr float kFar = KIND == AR_ACT_GELU ? 18.f : 10.f;
+  float x0, x1;
+  split(x, x0, x1);
+  x0 = fmaxf(x0, -kFar);
+  x1 = fmaxf(x1, -kFar);
+  const Two low = two(x0, x1), c = two(fminf(x0, kFar), fminf(x1, kFar));
   if constexpr (KIND == AR_ACT_GELU_TANH) {
-    const float c = fabsf(x) > 10.f ? copysignf(10.f, x) : x;
-    const float sq = c * c;
-    const float e = exp2_approx(-c * fmaf(kU3 * kLog2e, sq, kU1 * kLog2e));
-    const float s = reciprocal(1.f + e);
-    y = (x < 0.f ? c : x) * s;
-    slope = fmaf(c * s * (e * s), fmaf(3.f * kU3, sq, kU1), s);
-  } else if constexpr (KIND == AR_ACT_GELU) {
-    const float c = fabsf(x) > 18.f ? copysignf(18.f, x) : x;  // e^-162 = 0
-    float bell;
-    const float tail = normal_tail(c, bell), all = c < 0.f ? tail : 1.f - tail;
-    y = x * all;
-    slope = fmaf(c * 0.3989422804014327f, bell, all);
+    const Two sq = mul2(c, c);
+    const Two e = exp2_approx(mul2(c, fma2(both(-kU3 * kLog2e), sq, both(-kU1 * kLog2e))));
+    const Two s = reciprocal(add2(both(one), e));
+    y = mul2(low, s);
+    slope = fma2(mul2(mul2(c, s), mul2(e, s)), fma2(both(3.f * kU3), sq, both(kU1)), s);
   } else {
-    y = x;
-    slope = 1.f;
+    Two bell;
+    const Two tail = normal_tail(c, bell);
+    const Two all = mul2(normal_at(c, tail), both(one));
+    y = mul2(low, all);
+    slope = fma2(mul2(c, both(0.3989422804014327f)), bell, all);
   }
 }
 
-// Which elements of a block a lane has.  Side by side: 16 lanes to a block,
-// eight elements each.  Apart: a warp to a block, every 32nd element.
-template <bool SIDE_BY_SIDE>
+// Which elements of a block a lane has, as they are read and written.  Side by
+// side: 16 lanes to a block, eight elements each.  Apart: a warp to a block,
+// every 32nd element.  `left` of the block's elements are in the row; the
+// others are zeros.
+template <class T, bool SIDE_BY_SIDE>
 struct Places {
-  static constexpr int kLanes = SIDE_BY_SIDE ? 16 : 32;
-  static constexpr int kEach = kBlock / kLanes;
+  static constexpr int kLanes = 16, kEach = 8, kTwos = 4;
   static constexpr int kGroups = kThreads / kLanes;  // blocks at a time
-  static __device__ __forceinline__ int at(int lane, int i) { return SIDE_BY_SIDE ? lane * kEach + i : lane + 32 * i; }
+  static constexpr int kPer = 16 / (int)sizeof(T);   // elements of a vector
+  struct Raw {
+    uint4 v[kEach / kPer];
+  };
+  using Codes = uint2;
+  // Vectors of neighbouring lanes lie side by side (f32: two of them in each half
+  // of the block).
+  static __device__ __forceinline__ int vector(int lane, int h) { return h * kLanes * kPer + lane * kPer; }
+  static __device__ __forceinline__ Raw load(const T* from, int left, int lane) {
+    Raw r;
+#pragma unroll
+    for (int h = 0; h < kEach / kPer; ++h) {
+      if (left >= kBlock) {
+        r.v[h] = *reinterpret_cast<const uint4*>(from + vector(lane, h));
+      } else {
+        const Pack<T, kPer> p = load_pack<T, kPer>(from, vector(lane, h), left);
+        r.v[h] = *reinterpret_cast<const uint4*>(&p);
+      }
+    }
+    return r;
+  }
+  static __device__ __forceinline__ Two get(const Raw& r, int i) { return Pairs<T>::get(r.v[i / (kPer / 2)], i % (kPer / 2)); }
+  static __device__ __forceinline__ void store(T* to, int left, int lane, const Two (&f)[kTwos]) {
+#pragma unroll
+    for (int h = 0; h < kEach / kPer; ++h) {
+      uint4 v;
+#pragma unroll
+      for (int i = 0; i < kPer / 2; ++i) Pairs<T>::set(v, i, f[h * (kPer / 2) + i]);
+      if (left >= kBlock) *reinterpret_cast<uint4*>(to + vector(lane, h)) = v;
+      else store_pack<T, kPer>(to, vector(lane, h), left, *reinterpret_cast<const Pack<T, kPer>*>(&v));
+    }
+  }
+  static __device__ __forceinline__ Codes load_codes(const int8_t* from, int lane) {
+    if constexpr (kPer == kEach) return *reinterpret_cast<const uint2*>(from + vector(lane, 0));
+    else return make_uint2(*reinterpret_cast<const uint32_t*>(from + vector(lane, 0)),
+                           *reinterpret_cast<const uint32_t*>(from + vector(lane, 1)));
+  }
+  // 2^23 + 128 + code
+  static __device__ __forceinline__ Two lifted(const Codes& c, int i) {
+    const uint32_t w = (i < 2 ? c.x : c.y) ^ 0x80808080u, at = 2 * (i & 1);
+    return two(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440 | at)),
+               __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440 | (at + 1))));
+  }
+  // from whole numbers that 1.5 * 2^23 was added to
+  static __device__ __forceinline__ void store_codes(int8_t* to, int lane, const Two (&c)[kTwos]) {
+    auto four = [&](int i) {
+      float a0, a1, a2, a3;
+      split(c[i], a0, a1);
+      split(c[i + 1], a2, a3);
+      return __byte_perm(__byte_perm(__float_as_uint(a0), __float_as_uint(a1), 0x0040),
+                         __byte_perm(__float_as_uint(a2), __float_as_uint(a3), 0x0040), 0x5410);
+    };
+    if constexpr (kPer == kEach) {
+      *reinterpret_cast<uint2*>(to + vector(lane, 0)) = make_uint2(four(0), four(2));
+    } else {
+      *reinterpret_cast<uint32_t*>(to + vector(lane, 0)) = four(0);
+      *reinterpret_cast<uint32_t*>(to + vector(lane, 1)) = four(2);
+    }
+  }
 };
-
-// A lane's elements of the block that begins at `row`[c0], `left` of whose
-// elements there are; zeros past them.
-template <class T, bool SIDE_BY_SIDE>
-__device__ __forceinline__ void load_elements(const T* from, int left, int lane, float (&f)[Places<SIDE_BY_SIDE>::kEach]) {
-  using P = Places<SIDE_BY_SIDE>;
-  if constexpr (SIDE_BY_SIDE) {
-    constexpr int kPer = 16 / (int)sizeof(T);
+template <class T>
+struct Places<T, false> {
+  static constexpr int kLanes = 32, kEach = 4, kTwos = 2;
+  static constexpr int kGroups = kThreads / kLanes;
+  struct Raw {
+    T v[kEach];
+  };
+  struct Codes {
+    uint8_t v[kEach];
+  };
+  static __device__ __forceinline__ Raw load(const T* from, int left, int lane) {
+    Raw r;
+    from += lane;
+    if (left >= kBlock) {
 #pragma unroll
-    for (int h = 0; h < P::kEach; h += kPer) {
-      const Pack<T, kPer> p = load_pack<T, kPer>(from, P::at(lane, h), left);
+      for (int i = 0; i < kEach; ++i) r.v[i] = from[32 * i];
+    } else {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) f[h + i] = Conv<T>::up(p.v[i]);
+      for (int i = 0; i < kEach; ++i) r.v[i] = lane + 32 * i < left ? from[32 * i] : Conv<T>::down(0.f);
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < P::kEach; ++i) f[i] = P::at(lane, i) < left ? Conv<T>::up(from[P::at(lane, i)]) : 0.f;
+    return r;
   }
-}
-template <class T, bool SIDE_BY_SIDE>
-__device__ __forceinline__ void store_elements(T* to, int left, int lane, const float (&f)[Places<SIDE_BY_SIDE>::kEach]) {
-  using P = Places<SIDE_BY_SIDE>;
-  if constexpr (SIDE_BY_SIDE) {
-    constexpr int kPer = 16 / (int)sizeof(T);
+  static __device__ __forceinline__ Two get(const Raw& r, int i) {
+    return two(Conv<T>::up(r.v[2 * i]), Conv<T>::up(r.v[2 * i + 1]));
+  }
+  static __device__ __forceinline__ void store(T* to, int left, int lane, const Two (&f)[kTwos]) {
+    to += lane;
+    T v[kEach];
 #pragma unroll
-    for (int h = 0; h < P::kEach; h += kPer) {
-      Pack<T, kPer> p;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) p.v[i] = Conv<T>::down(f[h + i]);
-      store_pack<T, kPer>(to, P::at(lane, h), left, p);
+    for (int i = 0; i < kTwos; ++i) {
+      float lo, hi;
+      split(f[i], lo, hi);
+      v[2 * i] = Conv<T>::down(lo);
+      v[2 * i + 1] = Conv<T>::down(hi);
     }
-  } else {
+    if (left >= kBlock) {
 #pragma unroll
-    for (int i = 0; i < P::kEach; ++i)
-      if (P::at(lane, i) < left) to[P::at(lane, i)] = Conv<T>::down(f[i]);
+      for (int i = 0; i < kEach; ++i) to[32 * i] = v[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < kEach; ++i)
+        if (lane + 32 * i < left) to[32 * i] = v[i];
+    }
   }
-}
+  static __device__ __forceinline__ Codes load_codes(const int8_t* from, int lane) {
+    Codes c;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) c.v[i] = (uint8_t)from[lane + 32 * i];
+    return c;
+  }
+  static __device__ __forceinline__ Two lifted(const Codes& c, int i) {
+    return two(__uint_as_float((c.v[2 * i] ^ 0x80u) | 0x4B000000u), __uint_as_float((c.v[2 * i + 1] ^ 0x80u) | 0x4B000000u));
+  }
+  static __device__ __forceinline__ void store_codes(int8_t* to, int lane, const Two (&c)[kTwos]) {
+#pragma unroll
+    for (int i = 0; i < kTwos; ++i) {
+      float lo, hi;
+      split(c[i], lo, hi);
+      to[lane + 64 * i] = (int8_t)__float_as_uint(lo);
+      to[lane + 64 * i + 32] = (int8_t)__float_as_uint(hi);
+    }
+  }
+};
 
 // Where block n of the matrix lies.
 struct Place {
@@ -152,104 +276,104 @@ __device__ __forceinline__ Place place_of(const Activation8Args& a, uint32_t n) 
 
 template <class T, int KIND, bool SIDE_BY_SIDE, int EACH>
 __global__ void __launch_bounds__(kThreads) activation8_kernel(const __grid_constant__ Activation8Args a) {
-  using P = Places<SIDE_BY_SIDE>;
+  using P = Places<T, SIDE_BY_SIDE>;
   const int lane = threadIdx.x % P::kLanes, group = threadIdx.x / P::kLanes;
   const uint32_t first = (blockIdx.x * EACH) * P::kGroups + group;
-  const T* x = static_cast<const T*>(a.x);
-  float f[EACH][P::kEach];
+  typename P::Raw raw[EACH];
   Place at[EACH];
 #pragma unroll
   for (int u = 0; u < EACH; ++u) {
     const uint32_t n = first + u * P::kGroups;
     at[u] = place_of(a, n);
     // no block n: nothing of the row is left
-    load_elements<T, SIDE_BY_SIDE>(x + (int64_t)at[u].row * a.x_stride + at[u].col, n < a.total ? a.cols - at[u].col : 0,
-                                   lane, f[u]);
+    raw[u] = P::load(static_cast<const T*>(a.x) + (int64_t)at[u].row * a.x_stride + at[u].col,
+                     n < a.total ? a.cols - at[u].col : 0, lane);
   }
+  // Every block's largest, then 127 / m and m / 127 of block u by the group's
+  // lane u: a quotient rounded right takes as many instructions as five elements.
+  float mine = 0.f;
+#pragma unroll
+  for (int u = 0; u < EACH; ++u) {
+    float most = 0.f;
+#pragma unroll
+    for (int i = 0; i < P::kTwos; ++i) {
+      float lo, hi;
+      split(P::get(raw[u], i), lo, hi);
+      most = most_of(lo, hi, most);
+    }
+#pragma unroll
+    for (int m = P::kLanes / 2; m; m >>= 1) most = most_of(most, __shfl_xor_sync(0xFFFFFFFFu, most, m));
+    if (lane == u) mine = most;
+  }
+  const bool some = mine >= kLeast && mine < INFINITY;
+  const float my_by = some ? __fdiv_rn(127.f, mine) : 0.f;
+  if (lane < EACH && first + lane * P::kGroups < a.total)
+    a.scales_out[first + lane * P::kGroups] = some ? __fdiv_rn(mine, 127.f) : mine < kLeast ? 0.f : __uint_as_float(0x7FC00000u);
 #pragma unroll
   for (int u = 0; u < EACH; ++u) {
     const uint32_t n = first + u * P::kGroups;
-    // sizes are compared as bits: a NaN is above all
-    uint32_t most = 0;
-#pragma unroll
-    for (int i = 0; i < P::kEach; ++i) most = max(most, __float_as_uint(f[u][i]) & 0x7FFFFFFFu);
-#pragma unroll
-    for (int m = P::kLanes / 2; m; m >>= 1) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, m));
+    const float by = __shfl_sync(0xFFFFFFFFu, my_by, u, P::kLanes);
     if (n >= a.total) continue;
-    const bool some = most >= kLeastBits && most < kInfinityBits;
-    const float m = __uint_as_float(most);
-    const float by = some ? __fdiv_rn(127.f, m) : 0.f;
-    if (lane == 0) a.scales_out[n] = some ? __fdiv_rn(m, 127.f) : most >= kInfinityBits ? __uint_as_float(0x7FC00000u) : 0.f;
-    // adding 1.5 * 2^23 leaves the nearest whole number in the low bits
-    uint32_t code[P::kEach];
+    Two f[P::kTwos];
 #pragma unroll
-    for (int i = 0; i < P::kEach; ++i)
-      code[i] = some ? __float_as_uint(__fadd_rn(__fmul_rn(f[u][i], by), 12582912.f)) : 0;
-    int8_t* to = a.codes_out + (int64_t)n * kBlock;
-    if constexpr (SIDE_BY_SIDE) {
-      auto four = [&](int i) {
-        return __byte_perm(__byte_perm(code[i], code[i + 1], 0x0040), __byte_perm(code[i + 2], code[i + 3], 0x0040), 0x5410);
-      };
-      *reinterpret_cast<uint2*>(to + lane * 8) = make_uint2(four(0), four(4));
-    } else {
+    for (int i = 0; i < P::kTwos; ++i) f[i] = P::get(raw[u], i);
+    // adding 1.5 * 2^23 leaves the nearest whole number in the low bits (one value
+    // at a time: of a pair's product and sum the compiler makes one rounding)
+    Two code[P::kTwos];
 #pragma unroll
-      for (int i = 0; i < P::kEach; ++i) to[P::at(lane, i)] = (int8_t)code[i];
+    for (int i = 0; i < P::kTwos; ++i) {
+      float lo, hi;
+      split(f[i], lo, hi);
+      lo = __fadd_rn(__fmul_rn(lo, by), 12582912.f);
+      hi = __fadd_rn(__fmul_rn(hi, by), 12582912.f);
+      code[i] = by > 0.f ? two(lo, hi) : both(12582912.f);
     }
+    P::store_codes(a.codes_out + (int64_t)n * kBlock, lane, code);
     if (a.y) {
 #pragma unroll
-      for (int i = 0; i < P::kEach; ++i) f[u][i] = activation<KIND>(f[u][i]);
-      store_elements<T, SIDE_BY_SIDE>(static_cast<T*>(a.y) + (int64_t)at[u].row * a.y_stride + at[u].col,
-                                      a.cols - at[u].col, lane, f[u]);
+      for (int i = 0; i < P::kTwos; ++i) f[i] = activation<KIND>(f[i]);
+      P::store(static_cast<T*>(a.y) + (int64_t)at[u].row * a.y_stride + at[u].col, a.cols - at[u].col, lane, f);
     }
   }
 }
 
 template <class T, int KIND, bool SIDE_BY_SIDE, int EACH>
 __global__ void __launch_bounds__(kThreads) activation8_backward_kernel(const __grid_constant__ Activation8Args a) {
-  using P = Places<SIDE_BY_SIDE>;
+  using P = Places<T, SIDE_BY_SIDE>;
   const int lane = threadIdx.x % P::kLanes, group = threadIdx.x / P::kLanes;
   const uint32_t first = (blockIdx.x * EACH) * P::kGroups + group;
-  const T* dy = static_cast<const T*>(a.x);
-  float d[EACH][P::kEach], scale[EACH];
-  uint32_t codes[EACH][SIDE_BY_SIDE ? 2 : P::kEach];
+  typename P::Raw raw[EACH];
+  typename P::Codes codes[EACH];
+  float scale[EACH];
   Place at[EACH];
 #pragma unroll
   for (int u = 0; u < EACH; ++u) {
     const uint32_t n = first + u * P::kGroups;
     if (n >= a.total) break;
     at[u] = place_of(a, n);
-    const int8_t* from = a.codes + (int64_t)n * kBlock;
-    if constexpr (SIDE_BY_SIDE) {
-      const uint2 c = *reinterpret_cast<const uint2*>(from + lane * 8);
-      codes[u][0] = c.x;
-      codes[u][1] = c.y;
-    } else {
-#pragma unroll
-      for (int i = 0; i < P::kEach; ++i) codes[u][i] = (uint32_t)(int32_t)from[P::at(lane, i)];
-    }
+    codes[u] = P::load_codes(a.codes + (int64_t)n * kBlock, lane);
     scale[u] = a.scales[n];
-    if (a.dx)
-      load_elements<T, SIDE_BY_SIDE>(dy + (int64_t)at[u].row * a.x_stride + at[u].col, a.cols - at[u].col, lane, d[u]);
+    if (a.dx) raw[u] = P::load(static_cast<const T*>(a.x) + (int64_t)at[u].row * a.x_stride + at[u].col, a.cols - at[u].col, lane);
   }
 #pragma unroll
   for (int u = 0; u < EACH; ++u) {
-    const uint32_t n = first + u * P::kGroups;
-    if (n >= a.total) break;
-    float y[P::kEach];
+    if (first + u * P::kGroups >= a.total) break;
+    const float one = scale[u] == scale[u] ? 1.f : scale[u];
+    Two y[P::kTwos], d[P::kTwos];
 #pragma unroll
-    for (int i = 0; i < P::kEach; ++i) {
-      int code;
-      if constexpr (SIDE_BY_SIDE) code = (int)(codes[u][i / 4] << (24 - 8 * (i % 4))) >> 24;
-      else code = (int)codes[u][i];
-      float slope;
-      activation_and_slope<KIND>(scale[u] * (float)code, y[i], slope);
-      d[u][i] *= slope;
+    for (int i = 0; i < P::kTwos; ++i) {
+      const Two x = mul2(add2(P::lifted(codes[u], i), both(-8388736.f)), both(scale[u]));
+      Two slope;
+      activation_and_slope<KIND>(x, one, y[i], slope);
+      d[i] = slope;
     }
     const int left = a.cols - at[u].col;
-    if (a.dx)
-      store_elements<T, SIDE_BY_SIDE>(static_cast<T*>(a.dx) + (int64_t)at[u].row * a.dx_stride + at[u].col, left, lane, d[u]);
-    if (a.y)
-      store_elements<T, SIDE_BY_SIDE>(static_cast<T*>(a.y) + (int64_t)at[u].row * a.y_stride + at[u].col, left, lane, y);
+    if (a.dx) {
+#pragma unroll
+      for (int i = 0; i < P::kTwos; ++i) d[i] = mul2(d[i], P::get(raw[u], i));
+      P::store(static_cast<T*>(a.dx) + (int64_t)at[u].row * a.dx_stride + at[u].col, left, lane, d);
+    }
+    if (a.y) P::store(static_cast<T*>(a.y) + (int64_t)at[u].row * a.y_stride + at[u].col, left, lane, y);
   }
 }
 
@@ -266,7 +390,7 @@ cudaError_t run(const Activation8Args& a, int64_t rows, cudaStream_t s) {
   auto go = [&](auto each, auto side_by_side) {
     constexpr int kEach = decltype(each)::value;
     constexpr bool kSide = decltype(side_by_side)::value;
-    constexpr uint32_t kPer = Places<kSide>::kGroups * kEach;
+    constexpr uint32_t kPer = Places<T, kSide>::kGroups * kEach;
     const unsigned grid = (unsigned)((a.total + kPer - 1) / kPer);
     if constexpr (BACKWARD) activation8_backward_kernel<T, KIND, kSide, kEach><<<grid, kThreads, 0, s>>>(a);
     else activation8_kernel<T, KIND, kSide, kEach><<<grid, kThreads, 0, s>>>(a);
