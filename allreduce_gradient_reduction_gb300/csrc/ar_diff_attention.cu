@@ -22,6 +22,8 @@
 // holds probabilities times 2^7.
 #include "ar_tcgen05.cuh"
 
+#include <type_traits>
+
 namespace ar {
 namespace {
 
@@ -169,8 +171,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Two c2 = two(c, c);
     float m = -INFINITY, sum = 0.f;
     bool ok = true;
-    for (int j = 0; j < n; ++j) {
-      if (!(ok = mbar_wait(smem_addr(&sh.s_full[i]), j & 1, gave_up))) break;
+    auto step = [&](int j, auto last) {
+      if (!mbar_wait(smem_addr(&sh.s_full[i]), j & 1, gave_up)) return false;
       tc_fence_after();
       float s[4][32], top[4];
       tmem_load32(s_at, s[0]);
@@ -179,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait_load();
         tmem_loaded(s[b]);
         if (b < 3) tmem_load32(s_at + (b + 1) * 32, s[b + 1]);  // on its way while these are looked at
-        if (j == n - 1) {
+        if constexpr (decltype(last)::value) {
 #pragma unroll
           for (int x = 0; x < 32; ++x)
             if (b * 32 + x > row) s[b][x] = -INFINITY;
@@ -201,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         m = moved;
         sum *= by;
         // (these scores are later products than that output's, so its phase is the current one or just over)
-        if (!(ok = mbar_wait(smem_addr(&sh.o_done[i]), (j - 1) & 1, gave_up))) break;
+        if (!mbar_wait(smem_addr(&sh.o_done[i]), (j - 1) & 1, gave_up)) return false;
         tc_fence_after();
         for (int d = 0; d < value16; ++d) {
           float o[16];
@@ -239,7 +241,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       float sum_lo, sum_hi;
       split(add2(part[0], part[1]), sum_lo, sum_hi);
       sum += sum_lo + sum_hi;
-    }
+      return true;
+    };
+    // the tile on the diagonal is compiled apart: the others compare nothing
+    for (int j = 0; j + 1 < n && ok; ++j) ok = step(j, std::false_type());
+    ok = ok && step(n - 1, std::true_type());
     const float by = 1.f / sum;
     if (i) sh.by[row] = by * a.lambda[head];
     named_barrier(1, 256);

@@ -13,10 +13,18 @@
 // both dq (scores and dp are made by both kinds).  The last blocks of the launch
 // sum lambda's gradients.
 //
-// Tiles of 64 are walked, so that both maps' scores, dp and all sums fit tensor
-// memory: two threads have a row's 64 columns.  The difference of probabilities
-// has a place of its own (two by turns), so the next scores are computed as soon
-// as the current ones have been read; both ds take dp's place, as 16-bit pairs.
+// Tiles of 64 are walked, so that both maps' scores, dp in two places by turns
+// and all sums fit tensor memory.  Four threads have a row's 64 columns (two left
+// the issue slots empty more than half of the time, with two warps on each quarter
+// of the multiprocessor).  The
+// difference of probabilities takes the second map's scores' place and both ds
+// take dp's, as 16-bit pairs.  So the products of the next step are under way in
+// every phase of a worker's: the first map's scores are made while the second's
+// exponentials are taken, the second's while ds is made, dp a step ahead.
+//
+// What a product of 128 x 64 reads from shared memory takes half as long again as
+// the product; dq's blocks have their kept tiles, the left operands of scores and
+// dp, in tensor memory instead.
 //
 // lambda may differ from one by any factor, and f16 would lose what it makes
 // small: ds_1 is held without it in dq's blocks and relative to the group's
@@ -24,6 +32,7 @@
 #include "ar_attention_backward.cuh"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace ar {
 namespace {
@@ -35,18 +44,19 @@ constexpr uint32_t kPart = kWalk * 128;       // bytes of a panel of a walked ti
 constexpr uint32_t kStageBytes = 2 * kPart;   // of a walked tile
 constexpr int kStages = 4;                    // tiles of q and of dout in flight, for dk and dv
 constexpr int kKStages = 4, kVStages = 4;     // of k and v, for dq
-constexpr int kStats = 8 * 32;                // floats of a worker warp: [turn][lse 0, lse 1, delta 0, delta 1][32]
+constexpr int kCols = 16;                     // of a walked tile's columns that a worker has
+constexpr int kStats = 4 * kWalk + 16;        // floats of a tile of queries: [lse 0, lse 1, delta 0, delta 1][query], lambda
 
 struct Form {
-  static constexpr int kWorkers = 256;  // threads: 128 rows, two halves of the columns
-  static constexpr int kIssuer = 8, kLoader = 9;
-  static constexpr int kThreads = 320;
+  static constexpr int kWorkers = 512;  // threads: 128 rows, four quarters of the columns
+  static constexpr int kIssuer = 16, kLoader = 17, kFetcher = 18;  // warps
+  static constexpr int kThreads = 608;
   static constexpr int kColumns = 512;
 };
 // shared memory of both kinds of block
 constexpr uint32_t kTilesKV = 4 * kPanelBytes + 2 * kStages * kStageBytes;
 constexpr uint32_t kTilesQ = 4 * kPanelBytes + (kKStages + kVStages) * kStageBytes;
-constexpr uint32_t kSmem = kTilesKV + Form::kWorkers / 32 * kStats * 4;
+constexpr uint32_t kSmem = kTilesKV + kStages * kStats * 4;
 static_assert(kTilesQ <= kSmem, "both kinds of block share a launch");
 
 struct Maps {
@@ -150,37 +160,66 @@ __device__ __forceinline__ uint32_t panels_at(uint32_t tiles, int stage) {
   return tiles + (stage >> 1) * 2 * kStageBytes + (stage & 1) * kPart;
 }
 
+// Half a row of a panel in shared memory becomes 16 columns of pairs in the
+// thread's lane of tensor memory, the form of a left operand there.
+__device__ __forceinline__ void keep_half(uint32_t panel, int row, int half, uint32_t to) {
+  uint32_t r[16];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[4 * i]), "=r"(r[4 * i + 1]), "=r"(r[4 * i + 2]), "=r"(r[4 * i + 3])
+                 : "r"(panel + row * 128 + (((4 * half + i) ^ (row & 7)) << 4))
+                 : "memory");
+  tmem_store16(to, r);
+}
+// D = A B^T over `steps` times 16 columns: A's pairs in tensor memory, B K-major.
+template <int MAX>
+__device__ __forceinline__ void product_tk(uint32_t d, uint32_t a, uint32_t b_tile, uint32_t shape, int steps) {
+  const uint64_t b = panel_desc(b_tile, false);
+#pragma unroll
+  for (int k = 0; k < MAX; ++k)
+    if (k < steps) mma_ts(d, a + k * 8, b + k_major_step(k), shape, k > 0);
+}
+
 // ---- a worker's arithmetic ----------------------------------------------------------
 
-// 32 scores become probabilities 2^(c s - lse) in place.
-template <class L, class S>
-__device__ __forceinline__ void probabilities(float (&p)[32], float c, L lse, bool masked, S seen) {
+// A worker's scores become probabilities 2^(c s - lse) in place.  `seen` is asked in
+// masked tiles alone, whose steps are compiled apart (as one, every step took the
+// comparisons).
+template <bool MASKED, class L, class S>
+__device__ __forceinline__ void probabilities(float (&p)[kCols], float c, L lse, S seen) {
   const Two c2 = two(c, c);
 #pragma unroll
-  for (int x = 0; x < 32; x += 2) {
+  for (int x = 0; x < kCols; x += 2) {
     split(fma2(two(p[x], p[x + 1]), c2, lse(x)), p[x], p[x + 1]);
     p[x] = exp2_approx(p[x]);
     p[x + 1] = exp2_approx(p[x + 1]);
   }
-  if (masked) {
+  if constexpr (MASKED) {
 #pragma unroll
-    for (int x = 0; x < 32; ++x)
+    for (int x = 0; x < kCols; ++x)
       if (!seen(x)) p[x] = 0.f;
   }
 }
 
+__device__ __forceinline__ void tmem_store8(uint32_t at, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(at), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
 // Pairs of ds = p (by d + minus_delta).  What is not seen has p = 0 and no ds,
 // whatever d holds there.  The first is returned, where f16 looks at it.
-template <class T, class L>
-__device__ __forceinline__ float score_gradients(const float (&p)[32], const float (&d)[32], uint32_t (&packed)[16],
-                                                 float by, L minus_delta, bool masked) {
+template <class T, bool MASKED, class L>
+__device__ __forceinline__ float score_gradients(const float (&p)[kCols], const float (&d)[kCols], uint32_t (&packed)[kCols / 2],
+                                                 float by, L minus_delta) {
   const Two by2 = two(by, by);
   float first = 0.f;
 #pragma unroll
-  for (int x = 0; x < 32; x += 2) {
+  for (int x = 0; x < kCols; x += 2) {
     float lo, hi;
     split(mul2(two(p[x], p[x + 1]), fma2(two(d[x], d[x + 1]), by2, minus_delta(x))), lo, hi);
-    if (masked) {
+    if constexpr (MASKED) {
       if (p[x] == 0.f) lo = 0.f;
       if (p[x + 1] == 0.f) hi = 0.f;
     }
@@ -193,8 +232,8 @@ __device__ __forceinline__ float score_gradients(const float (&p)[32], const flo
 // ---- dk and dv ---------------------------------------------------------------------
 
 struct SharedKV {
-  alignas(8) uint64_t kv_full, q_full[kStages], do_full[kStages], empty[kStages], s_full, s_read, dp_full, p_ready[2],
-      ds_ready[2], done, own;
+  alignas(8) uint64_t kv_full, q_full[kStages], do_full[kStages], stats_full[kStages], empty[kStages], s_full[2], s_read,
+      dp_full[2], p_ready, ds_ready[2], done, own;
   uint32_t tmem;
   int gave_up;
   SeqUnit unit;
@@ -202,14 +241,15 @@ struct SharedKV {
 };
 
 __device__ __forceinline__ void init_barriers(SharedKV& sh) {
-  uint64_t* const one[] = {&sh.kv_full, &sh.s_full, &sh.dp_full, &sh.done, &sh.own};
+  uint64_t* const one[] = {&sh.kv_full, &sh.s_full[0], &sh.s_full[1], &sh.dp_full[0], &sh.dp_full[1], &sh.done, &sh.own};
   for (uint64_t* b : one) mbar_init(smem_addr(b), 1);
   for (int i = 0; i < kStages; ++i) {
     mbar_init(smem_addr(&sh.q_full[i]), 1);
     mbar_init(smem_addr(&sh.do_full[i]), 1);
+    mbar_init(smem_addr(&sh.stats_full[i]), 1);
     mbar_init(smem_addr(&sh.empty[i]), 1);
   }
-  uint64_t* const warps[] = {&sh.s_read, &sh.p_ready[0], &sh.p_ready[1], &sh.ds_ready[0], &sh.ds_ready[1]};
+  uint64_t* const warps[] = {&sh.s_read, &sh.p_ready, &sh.ds_ready[0], &sh.ds_ready[1]};
   for (uint64_t* b : warps) mbar_init(smem_addr(b), Form::kWorkers / 32);
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 }
@@ -239,13 +279,58 @@ __device__ __forceinline__ bool dkv_walk(const Maps& maps, const DiffArgs& a, in
     load_kept<2, true>(&maps.k, k_tile, kv_head, unit.begin + unit.index * kTile, bar);
     load_kept<VPANELS, false>(&maps.v, v_tile, kv_head, unit.begin + unit.index * kTile, bar);
   }
-  // Tensor memory: both maps' scores, their difference (two places by turns),
-  // dout v^T, dv, both dk.  Both ds take dout v^T's place, of each half's 32
-  // columns 16 each.
-  const uint32_t tmem = sh.tmem, dp_at = tmem + 192, dv_at = tmem + 256, dk_at = tmem + 384;
-  auto diff_at = [&](int n) { return tmem + 128 + (n & 1) * 32; };
+  // Tensor memory: both maps' scores, dout v^T (in two places by turns), dv, both
+  // dk.  The difference of probabilities takes the second scores' place and both
+  // ds take dout v^T's, eight or twice eight of each quarter's 16 columns.  A
+  // warp may have made its ds of the next step before another has this one's,
+  // though not one more (the scores after it wait for every warp's difference):
+  // ds_ready is two barriers by turns.
+  const uint32_t tmem = sh.tmem, diff_at = tmem + 64, dv_at = tmem + 256, dk_at = tmem + 384;
+  auto dp_at = [&](int n) { return tmem + 128 + 64 * (n & 1); };
 
-  if (warp == Form::kLoader) {
+  // The group's largest lambda; f16 holds probabilities times a power of two
+  // that leaves their difference, at most 1 + |lambda| in size, below 2^15.
+  float largest = 0.f, shift = 0.f;
+  for (int h = 0; h < group; ++h) largest = fmaxf(largest, fabsf(a.lambda[kv_head * group + h]));
+  if (kScaled<T>) shift = 14.f - (float)max(0, min(100, (__float_as_int(0.5f * (1.f + largest)) >> 23) - 126));
+  const float unshift = exp2f(-shift), by_unshift = by * unshift, unscale = 1.f / by;
+  const float per_largest = largest > 0.f ? -1.f / largest : 0.f;
+  float* const stats = reinterpret_cast<float*>(tiles + kTilesKV);
+
+  if (warp == Form::kFetcher) {
+    // The queries' numbers, as the workers take them: a warp of its own has the
+    // time to wait for them.
+    int tile = 0, head = kv_head * group;
+    wait_for_delta();
+    for (int n = base; n < end; ++n) {
+      const int stage = n % kStages;
+      if (n >= kStages && !mbar_wait(smem_addr(&sh.empty[stage]), (n / kStages - 1) & 1, gave_up)) break;
+      float* const to = stats + stage * kStats;
+      const float lambda = a.lambda[head];
+      float v[2][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        // (past the sequence's end, where all is masked: its last query's)
+        const int query = min((first + tile) * kWalk + i * 32 + lane, unit.length - 1);
+        const int64_t at = (int64_t)2 * head * a.tokens + unit.begin + query;
+        v[i][0] = a.lse[at];
+        v[i][1] = a.lse[at + a.tokens];
+        v[i][2] = a.delta[at];
+        v[i][3] = a.delta[at + a.tokens];
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        to[i * 32 + lane] = fmaf(-v[i][0], kLog2e, shift);
+        to[kWalk + i * 32 + lane] = fmaf(-v[i][1], kLog2e, shift);
+        to[2 * kWalk + i * 32 + lane] = -v[i][2] * by_unshift;
+        to[3 * kWalk + i * 32 + lane] = -v[i][3] * by_unshift * (lambda * per_largest);
+      }
+      if (lane == 0) to[4 * kWalk] = lambda;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&sh.stats_full[stage]));
+      if (++tile == per) tile = 0, ++head;
+    }
+  } else if (warp == Form::kLoader) {
     int head = kv_head * group, tile = 0;
     for (int n = base; n < end; ++n) {
       const int stage = n % kStages;
@@ -263,146 +348,121 @@ __device__ __forceinline__ bool dkv_walk(const Maps& maps, const DiffArgs& a, in
     if (elect_one()) {
       const uint32_t wide = mma_shape<T>(kWalk, false), keys = mma_shape<T>(dim16 * 16, true),
                      values = mma_shape<T>(value16 * 16, true);
-      auto scores = [&](int n) {  // K_m Q_m^T
+      auto scores = [&](int m, int n) {  // K_m Q_m^T
         if (!mbar_wait(smem_addr(&sh.q_full[n % kStages]), (n / kStages) & 1, gave_up)) return false;
-        for (int m = 0; m < 2; ++m)
-          product_ss<4>(tmem + m * 64, k_tile + m * kPanelBytes, maps_at(q_tile, n % kStages) + m * kPart, wide, dim16);
-        mma_commit(smem_addr(&sh.s_full));
+        product_ss<4>(tmem + m * 64, k_tile + m * kPanelBytes, maps_at(q_tile, n % kStages) + m * kPart, wide, dim16);
+        mma_commit(smem_addr(&sh.s_full[m]));
         return true;
       };
       auto dprob = [&](int n) {  // V dout^T
         if (!mbar_wait(smem_addr(&sh.do_full[n % kStages]), (n / kStages) & 1, gave_up)) return false;
-        product_ss<4 * VPANELS>(dp_at, v_tile, panels_at(do_tile, n % kStages), wide, value16);
-        mma_commit(smem_addr(&sh.dp_full));
+        product_ss<4 * VPANELS>(dp_at(n), v_tile, panels_at(do_tile, n % kStages), wide, value16);
+        mma_commit(smem_addr(&sh.dp_full[n & 1]));
         return true;
       };
-      bool ok = mbar_wait(smem_addr(&sh.kv_full), 0, gave_up) && scores(base) && dprob(base);
+      bool ok = mbar_wait(smem_addr(&sh.kv_full), 0, gave_up) && scores(0, base) && scores(1, base) && dprob(base) &&
+                (base + 1 == end || dprob(base + 1));
       for (int n = base; n < end && ok; ++n) {
         const bool more = n + 1 < end;
         // every warp's look at the scores is waited for in the last step too, so that phases keep in step
         if (!(ok = mbar_wait(smem_addr(&sh.s_read), n & 1, gave_up))) break;
         tc_fence_after();
-        if (more && !(ok = scores(n + 1))) break;
-        if (!(ok = mbar_wait(smem_addr(&sh.p_ready[n & 1]), (n >> 1) & 1, gave_up))) break;
+        if (more && !(ok = scores(0, n + 1))) break;
+        if (!(ok = mbar_wait(smem_addr(&sh.p_ready), n & 1, gave_up))) break;
         tc_fence_after();
-        product_ts<4>(dv_at, diff_at(n), panels_at(do_tile, n % kStages), 0, values, n > base);
+        for (int h = 0; h < 4; ++h)
+          product_ts<1>(dv_at, diff_at + h * kCols, panels_at(do_tile, n % kStages), h, values, n > base || h > 0);
+        if (more && !(ok = scores(1, n + 1))) break;
         if (!(ok = mbar_wait(smem_addr(&sh.ds_ready[n & 1]), (n >> 1) & 1, gave_up))) break;
         tc_fence_after();
         for (int m = 0; m < 2; ++m)
-          for (int h = 0; h < 2; ++h)
-            product_ts<2>(dk_at + m * 64, dp_at + h * 32 + m * 16, maps_at(q_tile, n % kStages) + m * kPart, h, keys,
+          for (int h = 0; h < 4; ++h)
+            product_ts<1>(dk_at + m * 64, dp_at(n) + h * kCols + m * 8, maps_at(q_tile, n % kStages) + m * kPart, h, keys,
                           n > base || h > 0);
         mma_commit(smem_addr(&sh.empty[n % kStages]));
-        if (more) ok = dprob(n + 1);
+        if (n + 2 < end) ok = dprob(n + 2);
       }
       if (ok) mma_commit(smem_addr(&sh.done));
     }
     __syncwarp();
   } else {
-    // thread: key row, queries [32 half, 32 half + 32) of each tile
-    const int half = warp >> 2, row = (warp & 3) * 32 + lane;
+    // thread: key row, queries [16 quarter, 16 quarter + 16) of each tile
+    const int quarter = warp >> 2, row = (warp & 3) * 32 + lane;
     const int left = unit.length - unit.index * kTile;  // queries from the first key to the sequence's end
-    const uint32_t lane0 = (uint32_t)(warp & 3) << 21, s_at = tmem + lane0 + half * 32;
+    const uint32_t lane0 = (uint32_t)(warp & 3) << 21, s_at = tmem + lane0 + quarter * kCols;
     const float c = a.scale * kLog2e;
-    float* stats = reinterpret_cast<float*>(tiles + kTilesKV) + warp * kStats;
-    // The group's largest lambda; f16 holds probabilities times a power of two
-    // that leaves their difference, at most 1 + |lambda| in size, below 2^15.
-    float largest = 0.f;
-    for (int h = 0; h < group; ++h) largest = fmaxf(largest, fabsf(a.lambda[kv_head * group + h]));
-    float shift = 0.f;
-    if (kScaled<T>) shift = 14.f - (float)max(0, min(100, (__float_as_int(0.5f * (1.f + largest)) >> 23) - 126));
-    const float unshift = exp2f(-shift), by_unshift = by * unshift, unscale = 1.f / by;
-    // Each warp fetches its 32 queries' numbers for itself: four warps that
-    // shared them would meet at every step.
-    int next_tile = 0, next_head = kv_head * group;
-    float next_lambda = 0.f;
-    auto fetch = [&]() {  // of the next step, and on
-      const int query = (first + next_tile) * kWalk + half * 32 + lane;
-      const int64_t at = (int64_t)2 * next_head * a.tokens + unit.begin + query;
-      const float l = a.lambda[next_head], relative = largest > 0.f ? -l / largest : 0.f;
-      next_lambda = l;
-      if (++next_tile == per) next_tile = 0, ++next_head;
-      if (query >= unit.length) return make_float4(0.f, 0.f, 0.f, 0.f);  // masked
-      return make_float4(fmaf(-a.lse[at], kLog2e, shift), fmaf(-a.lse[at + a.tokens], kLog2e, shift),
-                         -a.delta[at] * by_unshift, -a.delta[at + a.tokens] * by_unshift * relative);
-    };
-    auto put = [&](int n, float4 v) {
-      float* to = stats + (n & 1) * 128 + lane;
-      to[0] = v.x;
-      to[32] = v.y;
-      to[64] = v.z;
-      to[96] = v.w;
-      __syncwarp();
-    };
-    wait_for_delta();
-    put(base, fetch());
-    float lambda = next_lambda;
     int tile = 0;
     bool ok = true, finite = true;
     float most = kUnknown;
     for (int n = base; n < end; ++n) {
-      const float4 next = n + 1 < end ? fetch() : make_float4(0.f, 0.f, 0.f, 0.f);
       const int from = tile * kWalk;  // the tile's first query, counted from the first key
       const bool masked = from < kTile || from + kWalk > left;
-      auto seen = [&](int x) { return from + half * 32 + x >= row && from + half * 32 + x < left; };
-      const float* at = stats + (n & 1) * 128;
-      if (!(ok = mbar_wait(smem_addr(&sh.s_full), n & 1, gave_up))) break;
-      tc_fence_after();
-      float p0[32], p1[32], d[32];
-      uint32_t packed[16];
-      tmem_load32(s_at, p0);
-      tmem_load32(s_at + 64, p1);
-      tmem_wait_load();
-      tmem_loaded(p0);
-      tmem_loaded(p1);
-      warp_arrive(smem_addr(&sh.s_read));
-      probabilities(p0, c, [&](int x) { return two_of(at, x); }, masked, seen);
-      probabilities(p1, c, [&](int x) { return two_of(at + 32, x); }, masked, seen);
-      const Two less = two(-lambda, -lambda);
+      auto step = [&](auto mask) {
+        constexpr bool kMasked = decltype(mask)::value;
+        auto seen = [&](int x) { return from + quarter * kCols + x >= row && from + quarter * kCols + x < left; };
+        const float* at = stats + n % kStages * kStats + quarter * kCols;
+        float p0[kCols], p1[kCols], d[kCols];
+        uint32_t packed[kCols / 2];
+        if (!mbar_wait(smem_addr(&sh.stats_full[n % kStages]), (n / kStages) & 1, gave_up)) return false;
+        const float lambda = stats[n % kStages * kStats + 4 * kWalk];
+        if (!mbar_wait(smem_addr(&sh.s_full[0]), n & 1, gave_up)) return false;
+        tc_fence_after();
+        tmem_load16(s_at, p0);
+        tmem_wait_load();
+        tmem_loaded(p0);
+        warp_arrive(smem_addr(&sh.s_read));
+        probabilities<kMasked>(p0, c, [&](int x) { return two_of(at, x); }, seen);
+        if (!mbar_wait(smem_addr(&sh.s_full[1]), n & 1, gave_up)) return false;
+        tc_fence_after();
+        tmem_load16(s_at + 64, p1);
+        tmem_wait_load();
+        tmem_loaded(p1);
+        probabilities<kMasked>(p1, c, [&](int x) { return two_of(at + kWalk, x); }, seen);
+        const Two less = two(-lambda, -lambda);
 #pragma unroll
-      for (int x = 0; x < 32; x += 2) {
-        float lo, hi;
-        split(fma2(two(p1[x], p1[x + 1]), less, two(p0[x], p0[x + 1])), lo, hi);
-        packed[x / 2] = pack2<T>(lo, hi);
-      }
-      // (dv's product of the step before last, which read this place, came before these scores)
-      tmem_store16(lane0 + diff_at(n) + half * 16, packed);
-      tmem_wait_store();
-      warp_arrive(smem_addr(&sh.p_ready[n & 1]));
-      if (!(ok = mbar_wait(smem_addr(&sh.dp_full), n & 1, gave_up))) break;
-      tc_fence_after();
-      tmem_load32(lane0 + dp_at + half * 32, d);
-      tmem_wait_load();
-      tmem_loaded(d);
-      const float e0 = score_gradients<T>(p0, d, packed, by_unshift, [&](int x) { return two_of(at + 64, x); }, masked);
-      tmem_store16(lane0 + dp_at + half * 32, packed);
-      const float e1 = score_gradients<T>(p1, d, packed, largest > 0.f ? by_unshift * (-lambda / largest) : 0.f,
-                                          [&](int x) { return two_of(at + 96, x); }, masked);
-      tmem_store16(lane0 + dp_at + half * 32 + 16, packed);
-      tmem_wait_store();
-      warp_arrive(smem_addr(&sh.ds_ready[n & 1]));
-      if (kScaled<T>) most = fmaxf(most, fmaxf(fabsf(e0), fabsf(e1)));
-      put(n + 1, next);
-      lambda = next_lambda;
+        for (int x = 0; x < kCols; x += 2) {
+          float lo, hi;
+          split(fma2(two(p1[x], p1[x + 1]), less, two(p0[x], p0[x + 1])), lo, hi);
+          packed[x / 2] = pack2<T>(lo, hi);
+        }
+        tmem_store8(s_at + 64, packed);
+        tmem_wait_store();
+        warp_arrive(smem_addr(&sh.p_ready));
+        const uint32_t dp = lane0 + dp_at(n) + quarter * kCols;
+        if (!mbar_wait(smem_addr(&sh.dp_full[n & 1]), (n >> 1) & 1, gave_up)) return false;
+        tc_fence_after();
+        tmem_load16(dp, d);
+        tmem_wait_load();
+        tmem_loaded(d);
+        const float e0 = score_gradients<T, kMasked>(p0, d, packed, by_unshift, [&](int x) { return two_of(at + 2 * kWalk, x); });
+        tmem_store8(dp, packed);
+        const float e1 = score_gradients<T, kMasked>(p1, d, packed, by_unshift * (lambda * per_largest),
+                                                     [&](int x) { return two_of(at + 3 * kWalk, x); });
+        tmem_store8(dp + 8, packed);
+        tmem_wait_store();
+        warp_arrive(smem_addr(&sh.ds_ready[n & 1]));
+        if (kScaled<T>) most = fmaxf(most, fmaxf(fabsf(e0), fabsf(e1)));
+        return true;
+      };
+      if (!(ok = masked ? step(std::true_type()) : step(std::false_type()))) break;
       if (++tile == per) tile = 0;
     }
     if (ok && mbar_wait(smem_addr(&sh.done), FIRST ? 0 : state.walks & 1, gave_up)) {
       tc_fence_after();
-      // half: dv, or both dk
+      // quarter: 64 columns of dv, or one of the dk
       const int key = unit.index * kTile + (warp & 3) * 32;
       const uint32_t stage = q_tile + warp * 4096;
       auto place = [&](const AttnTensor& to, int head) {
         return static_cast<T*>(const_cast<void*>(to.ptr)) + (int64_t)(unit.begin + key) * to.token_stride +
                head * to.head_stride;
       };
-      if (half == 0) {
-        for (int p = 0; p < VPANELS; ++p)
-          write_rows<T, 64>(lane0 + dv_at, stage, place(a.dv, kv_head), a.dv.token_stride, unit.length - key, p * 64,
-                            a.value_dim, unshift);
-      } else {
-        for (int m = 0; m < 2; ++m)
-          finite &= write_rows<T, 64>(lane0 + dk_at + m * 64, stage, place(a.dk, 2 * kv_head + m), a.dk.token_stride,
-                                      unit.length - key, 0, a.dim, a.scale * unscale * (m ? largest : 1.f));
+      if (quarter < VPANELS) {
+        write_rows<T, 64>(lane0 + dv_at, stage, place(a.dv, kv_head), a.dv.token_stride, unit.length - key, quarter * 64,
+                          a.value_dim, unshift);
+      } else if (quarter >= 2) {
+        const int m = quarter - 2;
+        finite = write_rows<T, 64>(lane0 + dk_at + m * 64, stage, place(a.dk, 2 * kv_head + m), a.dk.token_stride,
+                                   unit.length - key, 0, a.dim, a.scale * unscale * (m ? largest : 1.f));
       }
     }
     put_most<T>(most, finite, sh.most);
@@ -443,8 +503,8 @@ __device__ __forceinline__ void dkv_block(const Maps& maps, const DiffArgs& a, i
 // ---- dq ---------------------------------------------------------------------------
 
 struct SharedQ {
-  alignas(8) uint64_t q_full, k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages], s_full, s_read,
-      dp_full[2], ds_ready[2], done, own;
+  alignas(8) uint64_t q_full, kept, k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages], s_full,
+      s_read, dp_full[2], ds_ready[2], done, own;
   uint32_t tmem;
   int gave_up;
   SeqUnit unit;
@@ -462,6 +522,7 @@ __device__ __forceinline__ void init_barriers(SharedQ& sh) {
     mbar_init(smem_addr(&sh.v_full[i]), 1);
     mbar_init(smem_addr(&sh.v_empty[i]), 1);
   }
+  mbar_init(smem_addr(&sh.kept), Form::kWorkers / 32);
   mbar_init(smem_addr(&sh.s_read), Form::kWorkers / 32);
   for (int i = 0; i < 2; ++i) mbar_init(smem_addr(&sh.ds_ready[i]), Form::kWorkers / 32);
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -489,10 +550,10 @@ __device__ __forceinline__ bool dq_walk(const Maps& maps, const DiffArgs& a, int
     load_kept<VPANELS, false>(&maps.dout, do_tile, head, unit.begin + query, bar);
   }
   // Tensor memory: both maps' scores, dout v^T (in two places by turns), both
-  // dq.  The next tile's scores and dout v^T are under way while this one's ds
+  // dq, then the kept tiles q_0, q_1 and dout as pairs.  The next tile's scores and dout v^T are under way while this one's ds
   // are made.  So a warp may have finished the next step before another has this
   // one, though not one more: ds_ready is two barriers by turns.
-  const uint32_t tmem = sh.tmem, dq_at = tmem + 256;
+  const uint32_t tmem = sh.tmem, dq_at = tmem + 256, q_at = tmem + 384, do_at = tmem + 448;
   auto dp_at = [&](int n) { return tmem + 128 + 64 * (n & 1); };
 
   if (warp == Form::kLoader) {
@@ -515,18 +576,20 @@ __device__ __forceinline__ bool dq_walk(const Maps& maps, const DiffArgs& a, int
       auto scores = [&](int n) {  // Q_m K_m^T
         if (!mbar_wait(smem_addr(&sh.k_full[n % kKStages]), (n / kKStages) & 1, gave_up)) return false;
         for (int m = 0; m < 2; ++m)
-          product_ss<4>(tmem + m * 64, q_tile + m * kPanelBytes, maps_at(k_tile, n % kKStages) + m * kPart, wide, dim16);
+          product_tk<4>(tmem + m * 64, q_at + m * 32, maps_at(k_tile, n % kKStages) + m * kPart, wide, dim16);
         mma_commit(smem_addr(&sh.s_full));
         return true;
       };
       auto dprob = [&](int n) {  // dout V^T
         if (!mbar_wait(smem_addr(&sh.v_full[n % kVStages]), (n / kVStages) & 1, gave_up)) return false;
-        product_ss<4 * VPANELS>(dp_at(n), do_tile, panels_at(v_tile, n % kVStages), wide, value16);
+        product_tk<4 * VPANELS>(dp_at(n), do_at, panels_at(v_tile, n % kVStages), wide, value16);
         mma_commit(smem_addr(&sh.dp_full[n & 1]));
         mma_commit(smem_addr(&sh.v_empty[n % kVStages]));
         return true;
       };
-      bool ok = mbar_wait(smem_addr(&sh.q_full), 0, gave_up) && scores(base) && dprob(base);
+      bool ok = mbar_wait(smem_addr(&sh.kept), 0, gave_up);
+      tc_fence_after();
+      ok = ok && scores(base) && dprob(base);
       for (int n = base; n < end && ok; ++n) {
         if (!(ok = mbar_wait(smem_addr(&sh.s_read), n & 1, gave_up))) break;
         tc_fence_after();
@@ -534,20 +597,29 @@ __device__ __forceinline__ bool dq_walk(const Maps& maps, const DiffArgs& a, int
         if (!(ok = mbar_wait(smem_addr(&sh.ds_ready[n & 1]), (n >> 1) & 1, gave_up))) break;
         tc_fence_after();
         for (int m = 0; m < 2; ++m)
-          for (int h = 0; h < 2; ++h)
-            product_ts<2>(dq_at + m * 64, dp_at(n) + h * 32 + m * 16, maps_at(k_tile, n % kKStages) + m * kPart, h, sums,
+          for (int h = 0; h < 4; ++h)
+            product_ts<1>(dq_at + m * 64, dp_at(n) + h * kCols + m * 8, maps_at(k_tile, n % kKStages) + m * kPart, h, sums,
                           n > base || h > 0);
         mma_commit(smem_addr(&sh.k_empty[n % kKStages]));
       }
       if (ok) mma_commit(smem_addr(&sh.done));
     }
     __syncwarp();
-  } else {
-    // thread: query row, keys [32 half, 32 half + 32) of each tile
-    const int half = warp >> 2, row = (warp & 3) * 32 + lane;
+  } else if (warp < Form::kIssuer) {
+    // thread: query row, keys [16 quarter, 16 quarter + 16) of each tile
+    const int quarter = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lane0 = (uint32_t)(warp & 3) << 21;
     const float c = a.scale * kLog2e;
     const bool valid = query + row < unit.length;
+    bool ok = true;
+    if (FIRST && (ok = mbar_wait(smem_addr(&sh.q_full), 0, gave_up))) {
+      // each quarter half a panel of both
+      const int panel = quarter >> 1;
+      keep_half(q_tile + panel * kPanelBytes, row, quarter & 1, lane0 + q_at + quarter * 16);
+      if (panel < VPANELS) keep_half(do_tile + panel * kPanelBytes, row, quarter & 1, lane0 + do_at + quarter * 16);
+      tmem_wait_store();
+      warp_arrive(smem_addr(&sh.kept));
+    }
     wait_for_delta();
     const int64_t at = (int64_t)2 * head * a.tokens + unit.begin + query + row;
     Two lse[2], delta[2];
@@ -557,53 +629,58 @@ __device__ __forceinline__ bool dq_walk(const Maps& maps, const DiffArgs& a, int
       lse[m] = two(l, l);
       delta[m] = two(dl, dl);
     }
-    bool ok = true, finite = true;
+    bool finite = true;
     float most = 0.f;
-    for (int n = base; n < end; ++n) {
+    for (int n = base; n < end && ok; ++n) {
       const int key = (n - base) * kWalk;  // the tile's first
       const bool masked = key + kWalk > query;
-      auto seen = [&](int x) { return key + half * 32 + x <= query + row; };
-      if (!(ok = mbar_wait(smem_addr(&sh.s_full), n & 1, gave_up))) break;
-      tc_fence_after();
-      float p0[32], p1[32], d[32];
-      uint32_t packed[16];
-      tmem_load32(lane0 + tmem + half * 32, p0);
-      tmem_load32(lane0 + tmem + 64 + half * 32, p1);
-      tmem_wait_load();
-      tmem_loaded(p0);
-      tmem_loaded(p1);
-      warp_arrive(smem_addr(&sh.s_read));
-      probabilities(p0, c, [&](int) { return lse[0]; }, masked, seen);
-      probabilities(p1, c, [&](int) { return lse[1]; }, masked, seen);
-      const uint32_t dp = lane0 + dp_at(n) + half * 32;
-      if (!(ok = mbar_wait(smem_addr(&sh.dp_full[n & 1]), (n >> 1) & 1, gave_up))) break;
-      tc_fence_after();
-      tmem_load32(dp, d);
-      tmem_wait_load();
-      tmem_loaded(d);
-      const float e0 = score_gradients<T>(p0, d, packed, by, [&](int) { return delta[0]; }, masked);
-      tmem_store16(dp, packed);
-      const float e1 = score_gradients<T>(p1, d, packed, by, [&](int) { return delta[1]; }, masked);
-      tmem_store16(dp + 16, packed);
-      tmem_wait_store();
-      warp_arrive(smem_addr(&sh.ds_ready[n & 1]));
-      if (kScaled<T>) most = fmaxf(most, fmaxf(fabsf(e0), fabsf(e1)));
+      auto step = [&](auto mask) {
+        constexpr bool kMasked = decltype(mask)::value;
+        auto seen = [&](int x) { return key + quarter * kCols + x <= query + row; };
+        if (!mbar_wait(smem_addr(&sh.s_full), n & 1, gave_up)) return false;
+        tc_fence_after();
+        float p0[kCols], p1[kCols], d[kCols];
+        uint32_t packed[kCols / 2];
+        tmem_load16(lane0 + tmem + quarter * kCols, p0);
+        tmem_load16(lane0 + tmem + 64 + quarter * kCols, p1);
+        tmem_wait_load();
+        tmem_loaded(p0);
+        tmem_loaded(p1);
+        warp_arrive(smem_addr(&sh.s_read));
+        probabilities<kMasked>(p0, c, [&](int) { return lse[0]; }, seen);
+        probabilities<kMasked>(p1, c, [&](int) { return lse[1]; }, seen);
+        const uint32_t dp = lane0 + dp_at(n) + quarter * kCols;
+        if (!mbar_wait(smem_addr(&sh.dp_full[n & 1]), (n >> 1) & 1, gave_up)) return false;
+        tc_fence_after();
+        tmem_load16(dp, d);
+        tmem_wait_load();
+        tmem_loaded(d);
+        const float e0 = score_gradients<T, kMasked>(p0, d, packed, by, [&](int) { return delta[0]; });
+        tmem_store8(dp, packed);
+        const float e1 = score_gradients<T, kMasked>(p1, d, packed, by, [&](int) { return delta[1]; });
+        tmem_store8(dp + 8, packed);
+        tmem_wait_store();
+        warp_arrive(smem_addr(&sh.ds_ready[n & 1]));
+        if (kScaled<T>) most = fmaxf(most, fmaxf(fabsf(e0), fabsf(e1)));
+        return true;
+      };
+      if (!(ok = masked ? step(std::true_type()) : step(std::false_type()))) break;
     }
     if (ok && mbar_wait(smem_addr(&sh.done), FIRST ? 0 : state.walks & 1, gave_up)) {
       tc_fence_after();
-      // half: which map
-      const int from = query + (warp & 3) * 32;
+      // quarter: 32 columns of one map's
+      const int from = query + (warp & 3) * 32, m = quarter >> 1;
       T* out = static_cast<T*>(const_cast<void*>(a.dq.ptr)) + (int64_t)(unit.begin + from) * a.dq.token_stride +
-               (2 * head + half) * a.dq.head_stride;
-      finite = write_rows<T, 64>(lane0 + dq_at + half * 64, k_tile + warp * 4096, out, a.dq.token_stride,
-                                 unit.length - from, 0, a.dim, a.scale * (1.f / by) * (half ? -a.lambda[head] : 1.f));
+               (2 * head + m) * a.dq.head_stride;
+      finite = write_rows<T, 32>(lane0 + dq_at + m * 64, k_tile + warp * 2048, out, a.dq.token_stride, unit.length - from,
+                                 (quarter & 1) * 32, a.dim, a.scale * (1.f / by) * (m ? -a.lambda[head] : 1.f));
     }
     if (kScaled<T> && FIRST && ok && !__any_sync(0xFFFFFFFFu, most > 0.f)) {
       // a prompt's queries often have no gradient at all, and need no other power
       ok = mbar_wait(smem_addr(&sh.q_full), 0, gave_up);
-      if (valid)
-        for (int p = 0; p < VPANELS; ++p)
-          if (any_element(do_tile + p * kPanelBytes + row * 128 + half * 64)) most = kUnknown;
+      if (valid && (quarter >> 1) < VPANELS &&
+          any_element(do_tile + (quarter >> 1) * kPanelBytes + row * 128 + (quarter & 1) * 64))
+        most = kUnknown;
     }
     put_most<T>(most, finite, sh.most);
   }
