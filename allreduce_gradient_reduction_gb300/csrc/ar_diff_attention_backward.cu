@@ -13,18 +13,21 @@
 // both dq (scores and dp are made by both kinds).  The last blocks of the launch
 // sum lambda's gradients.
 //
-// Tiles of 64 are walked, so that both maps' scores, dp in two places by turns
-// and all sums fit tensor memory.  Four threads have a row's 64 columns (two left
-// the issue slots empty more than half of the time, with two warps on each quarter
-// of the multiprocessor).  The
-// difference of probabilities takes the second map's scores' place and both ds
-// take dp's, as 16-bit pairs.  So the products of the next step are under way in
-// every phase of a worker's: the first map's scores are made while the second's
-// exponentials are taken, the second's while ds is made, dp a step ahead.
+// Tiles of 64 are walked, so that both maps' scores, dp and all sums fit tensor
+// memory.  Four threads have a row's 64 columns (424 us at the size below, two
+// 434).  The difference of probabilities has a place of its own, two by turns, so
+// the next scores are computed as soon as the current ones have been read; both ds
+// take dp's place, as 16-bit pairs.  A warp fetches the queries' statistics for
+// dk and dv's workers (who waited for them a third of a step before).
 //
 // What a product of 128 x 64 reads from shared memory takes half as long again as
 // the product; dq's blocks have their kept tiles, the left operands of scores and
 // dp, in tensor memory instead.
+//
+// Measured: 8192 tokens in 3 sequences, 16 heads of 2 x 64 over 4, bf16, 424 us a
+// call.  A step of dk and dv takes 1940 cycles, of which the tensor cores are busy
+// for 1500 (scores and dp wait for shared memory), one of dq 1290; starting and
+// ending a block takes 9000, a third of the time where sequences are short.
 //
 // lambda may differ from one by any factor, and f16 would lose what it makes
 // small: ds_1 is held without it in dq's blocks and relative to the group's
@@ -45,12 +48,13 @@ constexpr uint32_t kStageBytes = 2 * kPart;   // of a walked tile
 constexpr int kStages = 4;                    // tiles of q and of dout in flight, for dk and dv
 constexpr int kKStages = 4, kVStages = 4;     // of k and v, for dq
 constexpr int kCols = 16;                     // of a walked tile's columns that a worker has
+constexpr int kParts = kWalk / kCols;         // workers to a row
 constexpr int kStats = 4 * kWalk + 16;        // floats of a tile of queries: [lse 0, lse 1, delta 0, delta 1][query], lambda
 
 struct Form {
-  static constexpr int kWorkers = 512;  // threads: 128 rows, four quarters of the columns
-  static constexpr int kIssuer = 16, kLoader = 17, kFetcher = 18;  // warps
-  static constexpr int kThreads = 608;
+  static constexpr int kWorkers = kTile * kParts;  // threads
+  static constexpr int kIssuer = kWorkers / 32, kLoader = kIssuer + 1, kFetcher = kIssuer + 2;  // warps
+  static constexpr int kThreads = kWorkers + 96;
   static constexpr int kColumns = 512;
 };
 // shared memory of both kinds of block
@@ -202,7 +206,8 @@ __device__ __forceinline__ void probabilities(float (&p)[kCols], float c, L lse,
   }
 }
 
-__device__ __forceinline__ void tmem_store8(uint32_t at, const uint32_t (&r)[8]) {
+static_assert(kCols == 16, "what a worker loads at a time, and stores as pairs");
+__device__ __forceinline__ void store_pairs(uint32_t at, const uint32_t (&r)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(at), "r"(r[0]),
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
@@ -232,8 +237,8 @@ __device__ __forceinline__ float score_gradients(const float (&p)[kCols], const 
 // ---- dk and dv ---------------------------------------------------------------------
 
 struct SharedKV {
-  alignas(8) uint64_t kv_full, q_full[kStages], do_full[kStages], stats_full[kStages], empty[kStages], s_full[2], s_read,
-      dp_full[2], p_ready, ds_ready[2], done, own;
+  alignas(8) uint64_t kv_full, q_full[kStages], do_full[kStages], stats_full[kStages], empty[kStages], s_full, s_read,
+      dp_full, p_ready[2], ds_ready[2], done, own;
   uint32_t tmem;
   int gave_up;
   SeqUnit unit;
@@ -241,7 +246,7 @@ struct SharedKV {
 };
 
 __device__ __forceinline__ void init_barriers(SharedKV& sh) {
-  uint64_t* const one[] = {&sh.kv_full, &sh.s_full[0], &sh.s_full[1], &sh.dp_full[0], &sh.dp_full[1], &sh.done, &sh.own};
+  uint64_t* const one[] = {&sh.kv_full, &sh.s_full, &sh.dp_full, &sh.done, &sh.own};
   for (uint64_t* b : one) mbar_init(smem_addr(b), 1);
   for (int i = 0; i < kStages; ++i) {
     mbar_init(smem_addr(&sh.q_full[i]), 1);
@@ -249,7 +254,7 @@ __device__ __forceinline__ void init_barriers(SharedKV& sh) {
     mbar_init(smem_addr(&sh.stats_full[i]), 1);
     mbar_init(smem_addr(&sh.empty[i]), 1);
   }
-  uint64_t* const warps[] = {&sh.s_read, &sh.p_ready, &sh.ds_ready[0], &sh.ds_ready[1]};
+  uint64_t* const warps[] = {&sh.s_read, &sh.p_ready[0], &sh.p_ready[1], &sh.ds_ready[0], &sh.ds_ready[1]};
   for (uint64_t* b : warps) mbar_init(smem_addr(b), Form::kWorkers / 32);
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 }
@@ -279,14 +284,14 @@ __device__ __forceinline__ bool dkv_walk(const Maps& maps, const DiffArgs& a, in
     load_kept<2, true>(&maps.k, k_tile, kv_head, unit.begin + unit.index * kTile, bar);
     load_kept<VPANELS, false>(&maps.v, v_tile, kv_head, unit.begin + unit.index * kTile, bar);
   }
-  // Tensor memory: both maps' scores, dout v^T (in two places by turns), dv, both
-  // dk.  The difference of probabilities takes the second scores' place and both
-  // ds take dout v^T's, eight or twice eight of each quarter's 16 columns.  A
-  // warp may have made its ds of the next step before another has this one's,
-  // though not one more (the scores after it wait for every warp's difference):
-  // ds_ready is two barriers by turns.
-  const uint32_t tmem = sh.tmem, diff_at = tmem + 64, dv_at = tmem + 256, dk_at = tmem + 384;
-  auto dp_at = [&](int n) { return tmem + 128 + 64 * (n & 1); };
+  // Tensor memory: both maps' scores, their difference (two places by turns),
+  // dout v^T, dv, both dk.  Both ds take dout v^T's place, half of each part's
+  // columns each.  A warp may have made its difference or ds of the next
+  // step before another has this one's, though not one more (the scores after it
+  // wait for every warp's look at these): p_ready and ds_ready are two barriers
+  // by turns.
+  const uint32_t tmem = sh.tmem, dp_at = tmem + 192, dv_at = tmem + 256, dk_at = tmem + 384;
+  auto diff_at = [&](int n) { return tmem + 128 + (n & 1) * 32; };
 
   // The group's largest lambda; f16 holds probabilities times a power of two
   // that leaves their difference, at most 1 + |lambda| in size, below 2^15.
@@ -348,48 +353,46 @@ __device__ __forceinline__ bool dkv_walk(const Maps& maps, const DiffArgs& a, in
     if (elect_one()) {
       const uint32_t wide = mma_shape<T>(kWalk, false), keys = mma_shape<T>(dim16 * 16, true),
                      values = mma_shape<T>(value16 * 16, true);
-      auto scores = [&](int m, int n) {  // K_m Q_m^T
+      auto scores = [&](int n) {  // K_m Q_m^T
         if (!mbar_wait(smem_addr(&sh.q_full[n % kStages]), (n / kStages) & 1, gave_up)) return false;
-        product_ss<4>(tmem + m * 64, k_tile + m * kPanelBytes, maps_at(q_tile, n % kStages) + m * kPart, wide, dim16);
-        mma_commit(smem_addr(&sh.s_full[m]));
+        for (int m = 0; m < 2; ++m)
+          product_ss<4>(tmem + m * 64, k_tile + m * kPanelBytes, maps_at(q_tile, n % kStages) + m * kPart, wide, dim16);
+        mma_commit(smem_addr(&sh.s_full));
         return true;
       };
       auto dprob = [&](int n) {  // V dout^T
         if (!mbar_wait(smem_addr(&sh.do_full[n % kStages]), (n / kStages) & 1, gave_up)) return false;
-        product_ss<4 * VPANELS>(dp_at(n), v_tile, panels_at(do_tile, n % kStages), wide, value16);
-        mma_commit(smem_addr(&sh.dp_full[n & 1]));
+        product_ss<4 * VPANELS>(dp_at, v_tile, panels_at(do_tile, n % kStages), wide, value16);
+        mma_commit(smem_addr(&sh.dp_full));
         return true;
       };
-      bool ok = mbar_wait(smem_addr(&sh.kv_full), 0, gave_up) && scores(0, base) && scores(1, base) && dprob(base) &&
-                (base + 1 == end || dprob(base + 1));
+      bool ok = mbar_wait(smem_addr(&sh.kv_full), 0, gave_up) && scores(base) && dprob(base);
       for (int n = base; n < end && ok; ++n) {
         const bool more = n + 1 < end;
         // every warp's look at the scores is waited for in the last step too, so that phases keep in step
         if (!(ok = mbar_wait(smem_addr(&sh.s_read), n & 1, gave_up))) break;
         tc_fence_after();
-        if (more && !(ok = scores(0, n + 1))) break;
-        if (!(ok = mbar_wait(smem_addr(&sh.p_ready), n & 1, gave_up))) break;
+        if (more && !(ok = scores(n + 1))) break;
+        if (!(ok = mbar_wait(smem_addr(&sh.p_ready[n & 1]), (n >> 1) & 1, gave_up))) break;
         tc_fence_after();
-        for (int h = 0; h < 4; ++h)
-          product_ts<1>(dv_at, diff_at + h * kCols, panels_at(do_tile, n % kStages), h, values, n > base || h > 0);
-        if (more && !(ok = scores(1, n + 1))) break;
+        product_ts<4>(dv_at, diff_at(n), panels_at(do_tile, n % kStages), 0, values, n > base);
         if (!(ok = mbar_wait(smem_addr(&sh.ds_ready[n & 1]), (n >> 1) & 1, gave_up))) break;
         tc_fence_after();
         for (int m = 0; m < 2; ++m)
-          for (int h = 0; h < 4; ++h)
-            product_ts<1>(dk_at + m * 64, dp_at(n) + h * kCols + m * 8, maps_at(q_tile, n % kStages) + m * kPart, h, keys,
+          for (int h = 0; h < kParts; ++h)
+            product_ts<kCols / 16>(dk_at + m * 64, dp_at + h * kCols + m * kCols / 2, maps_at(q_tile, n % kStages) + m * kPart, h, keys,
                           n > base || h > 0);
         mma_commit(smem_addr(&sh.empty[n % kStages]));
-        if (n + 2 < end) ok = dprob(n + 2);
+        if (more) ok = dprob(n + 1);
       }
       if (ok) mma_commit(smem_addr(&sh.done));
     }
     __syncwarp();
   } else {
-    // thread: key row, queries [16 quarter, 16 quarter + 16) of each tile
-    const int quarter = warp >> 2, row = (warp & 3) * 32 + lane;
+    // thread: key row, a part of the queries of each tile
+    const int part = warp >> 2, row = (warp & 3) * 32 + lane;
     const int left = unit.length - unit.index * kTile;  // queries from the first key to the sequence's end
-    const uint32_t lane0 = (uint32_t)(warp & 3) << 21, s_at = tmem + lane0 + quarter * kCols;
+    const uint32_t lane0 = (uint32_t)(warp & 3) << 21, s_at = tmem + lane0 + part * kCols;
     const float c = a.scale * kLog2e;
     int tile = 0;
     bool ok = true, finite = true;
@@ -399,24 +402,21 @@ __device__ __forceinline__ bool dkv_walk(const Maps& maps, const DiffArgs& a, in
       const bool masked = from < kTile || from + kWalk > left;
       auto step = [&](auto mask) {
         constexpr bool kMasked = decltype(mask)::value;
-        auto seen = [&](int x) { return from + quarter * kCols + x >= row && from + quarter * kCols + x < left; };
-        const float* at = stats + n % kStages * kStats + quarter * kCols;
+        auto seen = [&](int x) { return from + part * kCols + x >= row && from + part * kCols + x < left; };
+        const float* at = stats + n % kStages * kStats + part * kCols;
         float p0[kCols], p1[kCols], d[kCols];
         uint32_t packed[kCols / 2];
         if (!mbar_wait(smem_addr(&sh.stats_full[n % kStages]), (n / kStages) & 1, gave_up)) return false;
         const float lambda = stats[n % kStages * kStats + 4 * kWalk];
-        if (!mbar_wait(smem_addr(&sh.s_full[0]), n & 1, gave_up)) return false;
+        if (!mbar_wait(smem_addr(&sh.s_full), n & 1, gave_up)) return false;
         tc_fence_after();
         tmem_load16(s_at, p0);
-        tmem_wait_load();
-        tmem_loaded(p0);
-        warp_arrive(smem_addr(&sh.s_read));
-        probabilities<kMasked>(p0, c, [&](int x) { return two_of(at, x); }, seen);
-        if (!mbar_wait(smem_addr(&sh.s_full[1]), n & 1, gave_up)) return false;
-        tc_fence_after();
         tmem_load16(s_at + 64, p1);
         tmem_wait_load();
+        tmem_loaded(p0);
         tmem_loaded(p1);
+        warp_arrive(smem_addr(&sh.s_read));
+        probabilities<kMasked>(p0, c, [&](int x) { return two_of(at, x); }, seen);
         probabilities<kMasked>(p1, c, [&](int x) { return two_of(at + kWalk, x); }, seen);
         const Two less = two(-lambda, -lambda);
 #pragma unroll
@@ -425,20 +425,21 @@ __device__ __forceinline__ bool dkv_walk(const Maps& maps, const DiffArgs& a, in
           split(fma2(two(p1[x], p1[x + 1]), less, two(p0[x], p0[x + 1])), lo, hi);
           packed[x / 2] = pack2<T>(lo, hi);
         }
-        tmem_store8(s_at + 64, packed);
+        // (dv's product of the step before last, which read this place, came before these scores)
+        store_pairs(lane0 + diff_at(n) + part * (kCols / 2), packed);
         tmem_wait_store();
-        warp_arrive(smem_addr(&sh.p_ready));
-        const uint32_t dp = lane0 + dp_at(n) + quarter * kCols;
-        if (!mbar_wait(smem_addr(&sh.dp_full[n & 1]), (n >> 1) & 1, gave_up)) return false;
+        warp_arrive(smem_addr(&sh.p_ready[n & 1]));
+        const uint32_t dp = lane0 + dp_at + part * kCols;
+        if (!mbar_wait(smem_addr(&sh.dp_full), n & 1, gave_up)) return false;
         tc_fence_after();
         tmem_load16(dp, d);
         tmem_wait_load();
         tmem_loaded(d);
         const float e0 = score_gradients<T, kMasked>(p0, d, packed, by_unshift, [&](int x) { return two_of(at + 2 * kWalk, x); });
-        tmem_store8(dp, packed);
+        store_pairs(dp, packed);
         const float e1 = score_gradients<T, kMasked>(p1, d, packed, by_unshift * (lambda * per_largest),
                                                      [&](int x) { return two_of(at + 3 * kWalk, x); });
-        tmem_store8(dp + 8, packed);
+        store_pairs(dp + kCols / 2, packed);
         tmem_wait_store();
         warp_arrive(smem_addr(&sh.ds_ready[n & 1]));
         if (kScaled<T>) most = fmaxf(most, fmaxf(fabsf(e0), fabsf(e1)));
@@ -449,20 +450,20 @@ __device__ __forceinline__ bool dkv_walk(const Maps& maps, const DiffArgs& a, in
     }
     if (ok && mbar_wait(smem_addr(&sh.done), FIRST ? 0 : state.walks & 1, gave_up)) {
       tc_fence_after();
-      // quarter: 64 columns of dv, or one of the dk
       const int key = unit.index * kTile + (warp & 3) * 32;
       const uint32_t stage = q_tile + warp * 4096;
       auto place = [&](const AttnTensor& to, int head) {
         return static_cast<T*>(const_cast<void*>(to.ptr)) + (int64_t)(unit.begin + key) * to.token_stride +
                head * to.head_stride;
       };
-      if (quarter < VPANELS) {
-        write_rows<T, 64>(lane0 + dv_at, stage, place(a.dv, kv_head), a.dv.token_stride, unit.length - key, quarter * 64,
-                          a.value_dim, unshift);
-      } else if (quarter >= 2) {
-        const int m = quarter - 2;
-        finite = write_rows<T, 64>(lane0 + dk_at + m * 64, stage, place(a.dk, 2 * kv_head + m), a.dk.token_stride,
-                                   unit.length - key, 0, a.dim, a.scale * unscale * (m ? largest : 1.f));
+      // both dk and the panels of dv
+      for (int i = part; i < 2 + VPANELS; i += kParts) {
+        if (i < 2)
+          finite &= write_rows<T, 64>(lane0 + dk_at + i * 64, stage, place(a.dk, 2 * kv_head + i), a.dk.token_stride,
+                                      unit.length - key, 0, a.dim, a.scale * unscale * (i ? largest : 1.f));
+        else
+          write_rows<T, 64>(lane0 + dv_at, stage, place(a.dv, kv_head), a.dv.token_stride, unit.length - key,
+                            (i - 2) * 64, a.value_dim, unshift);
       }
     }
     put_most<T>(most, finite, sh.most);
@@ -597,8 +598,8 @@ __device__ __forceinline__ bool dq_walk(const Maps& maps, const DiffArgs& a, int
         if (!(ok = mbar_wait(smem_addr(&sh.ds_ready[n & 1]), (n >> 1) & 1, gave_up))) break;
         tc_fence_after();
         for (int m = 0; m < 2; ++m)
-          for (int h = 0; h < 4; ++h)
-            product_ts<1>(dq_at + m * 64, dp_at(n) + h * kCols + m * 8, maps_at(k_tile, n % kKStages) + m * kPart, h, sums,
+          for (int h = 0; h < kParts; ++h)
+            product_ts<kCols / 16>(dq_at + m * 64, dp_at(n) + h * kCols + m * kCols / 2, maps_at(k_tile, n % kKStages) + m * kPart, h, sums,
                           n > base || h > 0);
         mma_commit(smem_addr(&sh.k_empty[n % kKStages]));
       }
@@ -606,20 +607,11 @@ __device__ __forceinline__ bool dq_walk(const Maps& maps, const DiffArgs& a, int
     }
     __syncwarp();
   } else if (warp < Form::kIssuer) {
-    // thread: query row, keys [16 quarter, 16 quarter + 16) of each tile
-    const int quarter = warp >> 2, row = (warp & 3) * 32 + lane;
+    // thread: query row, a part of the keys of each tile
+    const int part = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lane0 = (uint32_t)(warp & 3) << 21;
     const float c = a.scale * kLog2e;
     const bool valid = query + row < unit.length;
-    bool ok = true;
-    if (FIRST && (ok = mbar_wait(smem_addr(&sh.q_full), 0, gave_up))) {
-      // each quarter half a panel of both
-      const int panel = quarter >> 1;
-      keep_half(q_tile + panel * kPanelBytes, row, quarter & 1, lane0 + q_at + quarter * 16);
-      if (panel < VPANELS) keep_half(do_tile + panel * kPanelBytes, row, quarter & 1, lane0 + do_at + quarter * 16);
-      tmem_wait_store();
-      warp_arrive(smem_addr(&sh.kept));
-    }
     wait_for_delta();
     const int64_t at = (int64_t)2 * head * a.tokens + unit.begin + query + row;
     Two lse[2], delta[2];
@@ -629,6 +621,15 @@ __device__ __forceinline__ bool dq_walk(const Maps& maps, const DiffArgs& a, int
       lse[m] = two(l, l);
       delta[m] = two(dl, dl);
     }
+    bool ok = true;
+    if (FIRST && (ok = mbar_wait(smem_addr(&sh.q_full), 0, gave_up))) {
+      for (int i = part; i < 4; i += kParts) {  // half a panel of both
+        keep_half(q_tile + (i >> 1) * kPanelBytes, row, i & 1, lane0 + q_at + i * 16);
+        if (i < 2 * VPANELS) keep_half(do_tile + (i >> 1) * kPanelBytes, row, i & 1, lane0 + do_at + i * 16);
+      }
+      tmem_wait_store();
+      warp_arrive(smem_addr(&sh.kept));
+    }
     bool finite = true;
     float most = 0.f;
     for (int n = base; n < end && ok; ++n) {
@@ -636,29 +637,29 @@ __device__ __forceinline__ bool dq_walk(const Maps& maps, const DiffArgs& a, int
       const bool masked = key + kWalk > query;
       auto step = [&](auto mask) {
         constexpr bool kMasked = decltype(mask)::value;
-        auto seen = [&](int x) { return key + quarter * kCols + x <= query + row; };
+        auto seen = [&](int x) { return key + part * kCols + x <= query + row; };
         if (!mbar_wait(smem_addr(&sh.s_full), n & 1, gave_up)) return false;
         tc_fence_after();
         float p0[kCols], p1[kCols], d[kCols];
         uint32_t packed[kCols / 2];
-        tmem_load16(lane0 + tmem + quarter * kCols, p0);
-        tmem_load16(lane0 + tmem + 64 + quarter * kCols, p1);
+        tmem_load16(lane0 + tmem + part * kCols, p0);
+        tmem_load16(lane0 + tmem + 64 + part * kCols, p1);
         tmem_wait_load();
         tmem_loaded(p0);
         tmem_loaded(p1);
         warp_arrive(smem_addr(&sh.s_read));
         probabilities<kMasked>(p0, c, [&](int) { return lse[0]; }, seen);
         probabilities<kMasked>(p1, c, [&](int) { return lse[1]; }, seen);
-        const uint32_t dp = lane0 + dp_at(n) + quarter * kCols;
+        const uint32_t dp = lane0 + dp_at(n) + part * kCols;
         if (!mbar_wait(smem_addr(&sh.dp_full[n & 1]), (n >> 1) & 1, gave_up)) return false;
         tc_fence_after();
         tmem_load16(dp, d);
         tmem_wait_load();
         tmem_loaded(d);
         const float e0 = score_gradients<T, kMasked>(p0, d, packed, by, [&](int) { return delta[0]; });
-        tmem_store8(dp, packed);
+        store_pairs(dp, packed);
         const float e1 = score_gradients<T, kMasked>(p1, d, packed, by, [&](int) { return delta[1]; });
-        tmem_store8(dp + 8, packed);
+        store_pairs(dp + kCols / 2, packed);
         tmem_wait_store();
         warp_arrive(smem_addr(&sh.ds_ready[n & 1]));
         if (kScaled<T>) most = fmaxf(most, fmaxf(fabsf(e0), fabsf(e1)));
@@ -668,19 +669,21 @@ __device__ __forceinline__ bool dq_walk(const Maps& maps, const DiffArgs& a, int
     }
     if (ok && mbar_wait(smem_addr(&sh.done), FIRST ? 0 : state.walks & 1, gave_up)) {
       tc_fence_after();
-      // quarter: 32 columns of one map's
-      const int from = query + (warp & 3) * 32, m = quarter >> 1;
-      T* out = static_cast<T*>(const_cast<void*>(a.dq.ptr)) + (int64_t)(unit.begin + from) * a.dq.token_stride +
-               (2 * head + m) * a.dq.head_stride;
-      finite = write_rows<T, 32>(lane0 + dq_at + m * 64, k_tile + warp * 2048, out, a.dq.token_stride, unit.length - from,
-                                 (quarter & 1) * 32, a.dim, a.scale * (1.f / by) * (m ? -a.lambda[head] : 1.f));
+      const int from = query + (warp & 3) * 32;
+      for (int i = part; i < 4; i += kParts) {  // 32 columns of one map's
+        const int m = i >> 1;
+        T* out = static_cast<T*>(const_cast<void*>(a.dq.ptr)) + (int64_t)(unit.begin + from) * a.dq.token_stride +
+                 (2 * head + m) * a.dq.head_stride;
+        finite &= write_rows<T, 32>(lane0 + dq_at + m * 64, k_tile + warp * 2048, out, a.dq.token_stride,
+                                    unit.length - from, (i & 1) * 32, a.dim,
+                                    a.scale * (1.f / by) * (m ? -a.lambda[head] : 1.f));
+      }
     }
     if (kScaled<T> && FIRST && ok && !__any_sync(0xFFFFFFFFu, most > 0.f)) {
       // a prompt's queries often have no gradient at all, and need no other power
       ok = mbar_wait(smem_addr(&sh.q_full), 0, gave_up);
-      if (valid && (quarter >> 1) < VPANELS &&
-          any_element(do_tile + (quarter >> 1) * kPanelBytes + row * 128 + (quarter & 1) * 64))
-        most = kUnknown;
+      for (int i = part; valid && i < 2 * VPANELS; i += kParts)
+        if (any_element(do_tile + (i >> 1) * kPanelBytes + row * 128 + (i & 1) * 64)) most = kUnknown;
     }
     put_most<T>(most, finite, sh.most);
   }
