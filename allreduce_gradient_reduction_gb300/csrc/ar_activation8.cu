@@ -101,9 +101,10 @@ __device__ __forceinline__ Two activation(Two x) {
 }
 
 // The activation and its slope.  `one` is one, or a NaN for a block of those.
-// Beyond 10 (the exact gelu: 18) the slope is that at 10, within 2^-120 of 0 or
-// 1, and so is the activation's factor: what follows would multiply an infinity
-// by zero.
+// Beyond 10.035 (the exact gelu: 18) the slope is that there, 0 or 1, and so is
+// the activation's factor: e^-u is 2^127.1 or so, still a number, and its
+// reciprocal is flushed to zero.  Farther out an infinity would be multiplied by
+// zero.
 template <int KIND>
 __device__ __forceinline__ void activation_and_slope(Two x, float one, Two& y, Two& slope) {
   if constexpr (KIND == AR_ACT_IDENTITY) {
@@ -111,7 +112,7 @@ __device__ __forceinline__ void activation_and_slope(Two x, float one, Two& y, T
     slope = both(one);
     return;
   }
-  constexpr float kFar = KIND == AR_ACT_GELU ? 18.f : 10.f;
+  constexpr float kFar = KIND == AR_ACT_GELU ? 18.f : 10.035f;
   float x0, x1;
   split(x, x0, x1);
   x0 = fmaxf(x0, -kFar);

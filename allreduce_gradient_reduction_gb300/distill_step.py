@@ -9,9 +9,15 @@ the attention and the loss are the library's, matrix products and the rest
 PyTorch's), ar_bucketed_allreduce of all ranks' gradients, and the same plain
 update on every rank; the copies stay equal bit for bit.
 
-layer_norm, packed_attention and distill_loss are the operators as PyTorch
-functions with gradients, for use in other models as well.  The gradients have
-none of their own: asking for second derivatives raises.
+--block diff trains another kind of decoder: queries and keys are normalised for
+each head and turned by their positions (there is no table of positions),
+attention is the difference of two maps with a learned weight for each head, and
+the hidden layer's input is kept in 8 bits for the backward pass.
+
+layer_norm, packed_attention, distill_loss, qk_norm_rope, diff_attention and
+activation8_linear are the operators as PyTorch functions with gradients, for
+use in other models as well.  The gradients have none of their own: asking for
+second derivatives raises.
 """
 import argparse
 import functools
@@ -31,8 +37,8 @@ class _NoSecondDerivative(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, *grads):
-        raise RuntimeError("the gradients of layer_norm, packed_attention and distill_loss have no derivative: "
-                           "second derivatives through them are not available")
+        raise RuntimeError("the gradients of the library's operators have no derivative: second derivatives through "
+                           "them are not available")
 
 
 def _once(backward):
@@ -134,11 +140,109 @@ def distill_loss(logits, teacher_index, teacher_logits, temperature=1.0):
     return _DistillLoss.apply(logits, teacher_index, teacher_logits, temperature)
 
 
-def make_parameters(layers, width, vocab, positions, seed=0, device="cuda"):
-    """name: f32 tensor, GPT-2's names and shapes (weights as [in, out])."""
+class _QkNormRope(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, positions, how):
+        q_out, k_out = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k))
+        ar.check(ar.ar_qk_norm_rope(q, k, q_weight, k_weight, positions, q_out, k_out, **how), "ar_qk_norm_rope")
+        ctx.save_for_backward(q, k, q_weight, k_weight, positions)
+        ctx.how = how
+        return q_out, k_out
+
+    @staticmethod
+    @_once
+    def backward(ctx, dq_out, dk_out):
+        q, k, q_weight, k_weight, positions = ctx.saved_tensors
+        dq, dk = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k))
+        dq_weight, dk_weight = torch.empty_like(q_weight), torch.empty_like(k_weight)
+        workspace = torch.empty(ar.ar_qk_norm_rope_workspace_bytes(*q.shape[:2], k.shape[1], q.shape[2]),
+                                dtype=torch.uint8, device=q.device)
+        ar.check(ar.ar_qk_norm_rope_backward(dq_out.contiguous(), dk_out.contiguous(), q, k, q_weight, k_weight,
+                                             positions, dq, dk, dq_weight, dk_weight, workspace, **ctx.how),
+                 "ar_qk_norm_rope_backward")
+        return dq, dk, dq_weight, dk_weight, None, None
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, positions, **how):
+    """q [tokens, heads, dim] and k [tokens, kv_heads, dim], each head
+    normalised, weighted [dim] and turned by its token's position (i32); how:
+    ar_qk_norm_rope's rotary_dim, base, frequencies, interleaved and eps."""
+    return _QkNormRope.apply(q, k, q_weight, k_weight, positions, how)
+
+
+class _DiffAttention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, lam, cu_seqlens):
+        shape = (q.shape[0], lam.shape[0], v.shape[2])
+        out, second = (torch.empty(shape, dtype=q.dtype, device=q.device) for _ in range(2))
+        lse = torch.empty(q.shape[1], q.shape[0], dtype=torch.float32, device=q.device)
+        ar.check(ar.ar_diff_attention(q, k, v, lam, cu_seqlens, out, second, lse), "ar_diff_attention")
+        ctx.save_for_backward(q, k, v, lam, cu_seqlens, out, second, lse)
+        return out
+
+    @staticmethod
+    @_once
+    def backward(ctx, dout):
+        q, k, v, lam, cu_seqlens, out, second, lse = ctx.saved_tensors
+        dq, dk, dv, dlam = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v, lam))
+        workspace = torch.empty(ar.ar_diff_attention_workspace_bytes(q.shape[0], lam.shape[0], v.shape[1], q.shape[2],
+                                                                     v.shape[2]), dtype=torch.uint8, device=q.device)
+        ar.check(ar.ar_diff_attention_backward(dout.contiguous(), q, k, v, lam, out, second, lse, cu_seqlens, dq, dk,
+                                               dv, dlam, workspace), "ar_diff_attention_backward")
+        return dq, dk, dv, dlam, None
+
+
+def diff_attention(q, k, v, lam, cu_seqlens):
+    """q [tokens, 2 heads, dim], k [tokens, 2 kv_heads, dim], v [tokens,
+    kv_heads, value_dim], bf16 or f16; lam [heads] f32.  The sequences have to
+    cover every token."""
+    return _DiffAttention.apply(q, k, v, lam, cu_seqlens)
+
+
+class _Activation8Linear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, kind):
+        rows, cols = x.shape
+        blocks = -(-cols // ar.ACTIVATION8_BLOCK)
+        y = torch.empty_like(x)
+        codes = torch.empty(rows, blocks * ar.ACTIVATION8_BLOCK, dtype=torch.int8, device=x.device)
+        scales = torch.empty(rows, blocks, dtype=torch.float32, device=x.device)
+        ar.check(ar.ar_activation8(x, y, codes, scales, kind=kind), "ar_activation8")
+        ctx.save_for_backward(codes, scales, weight)
+        ctx.kind = kind
+        ctx.cols = cols
+        return torch.addmm(bias, y, weight)
+
+    @staticmethod
+    @_once
+    def backward(ctx, dout):
+        codes, scales, weight = ctx.saved_tensors
+        dy = dout @ weight.t()
+        y = torch.empty_like(dy)
+        ar.check(ar.ar_activation8_backward(codes, scales, dy, dy, y, kind=ctx.kind), "ar_activation8_backward")
+        return dy, y.t() @ dout, dout.sum(0), None
+
+
+def activation8_linear(x, weight, bias, kind="gelu_tanh"):
+    """activation(x) @ weight + bias, all of one type.  Neither x nor the
+    activation is kept for the backward pass, but x in 8 bits: gradients are
+    those at what the codes stand for, the weight's with the activation made
+    again from them."""
+    return _Activation8Linear.apply(x, weight, bias, kind)
+
+
+BLOCKS = ("gpt2", "diff")
+
+
+def make_parameters(layers, width, vocab, positions, seed=0, device="cuda", block="gpt2", heads=1):
+    """name: f32 tensor, GPT-2's names and shapes (weights as [in, out]).
+    block "diff", of `heads` heads: weights of the norms of queries and keys and
+    of the second maps in the place of a table of positions."""
     g = torch.Generator(device="cpu")
     g.manual_seed(seed)
     shapes = {"wte": (vocab, width), "wpe": (positions, width), "ln_f.weight": (width,), "ln_f.bias": (width,)}
+    if block == "diff":
+        del shapes["wpe"]
     for i in range(layers):
         for name, shape in (("ln_1.weight", (width,)), ("ln_1.bias", (width,)), ("c_attn.weight", (width, 3 * width)),
                             ("c_attn.bias", (3 * width,)), ("c_proj.weight", (width, width)), ("c_proj.bias", (width,)),
@@ -146,12 +250,18 @@ def make_parameters(layers, width, vocab, positions, seed=0, device="cuda"):
                             ("c_fc.bias", (4 * width,)), ("mlp.c_proj.weight", (4 * width, width)),
                             ("mlp.c_proj.bias", (width,))):
             shapes[f"h.{i}.{name}"] = shape
+        if block == "diff":
+            for name, n in (("q_norm.weight", width // heads // 2), ("k_norm.weight", width // heads // 2),
+                            ("lambda", heads)):
+                shapes[f"h.{i}.{name}"] = (n,)
     out = {}
     for name, shape in shapes.items():
         if name.endswith("bias"):
             t = torch.zeros(shape)
-        elif ".ln_" in name or name.startswith("ln_"):
+        elif ".ln_" in name or name.startswith("ln_") or "_norm." in name:
             t = torch.ones(shape)
+        elif name.endswith("lambda"):
+            t = torch.full(shape, 0.5)
         else:
             t = torch.randn(shape, generator=g) * 0.05
         out[name] = t.to(device)
@@ -167,6 +277,8 @@ def logits_of(p, tokens, positions, cu_seqlens, heads, dtype=torch.bfloat16, nor
     def linear(x, name):
         return x @ p[name + ".weight"].to(dtype) + p[name + ".bias"].to(dtype)
 
+    if "wpe" not in p:
+        return diff_logits_of(p, tokens, positions, cu_seqlens, heads, dtype, norm)
     x = (p["wte"][tokens] + p["wpe"][positions]).to(dtype)
     for i in range(layers):
         h = f"h.{i}."
@@ -175,6 +287,33 @@ def logits_of(p, tokens, positions, cu_seqlens, heads, dtype=torch.bfloat16, nor
         x = x + linear(attention(q, k, v, cu_seqlens).flatten(1), h + "c_proj")
         y = norm(x, p[h + "ln_2.weight"], p[h + "ln_2.bias"])
         x = x + linear(F.gelu(linear(y, h + "c_fc"), approximate="tanh"), h + "mlp.c_proj")
+    return norm(x, p["ln_f.weight"], p["ln_f.bias"]) @ p["wte"].to(dtype).t()
+
+
+def diff_logits_of(p, tokens, positions, cu_seqlens, heads, dtype=torch.bfloat16, norm=layer_norm,
+                   prepare=qk_norm_rope, attention=diff_attention, mlp=activation8_linear):
+    """The same for parameters of block "diff"; prepare, attention and mlp may
+    be other implementations of the same functions."""
+    layers = sum(name.endswith("ln_1.weight") for name in p)
+    width = p["wte"].shape[1]
+    positions = positions.to(torch.int32)
+
+    def weights(name):
+        return p[name + ".weight"].to(dtype), p[name + ".bias"].to(dtype)
+
+    def linear(x, name):
+        w, b = weights(name)
+        return x @ w + b
+
+    x = p["wte"][tokens].to(dtype)
+    for i in range(layers):
+        h = f"h.{i}."
+        qkv = linear(norm(x, p[h + "ln_1.weight"], p[h + "ln_1.bias"]), h + "c_attn")
+        q, k, v = (t.unflatten(1, (n, width // n)) for t, n in zip(qkv.split(width, 1), (2 * heads, 2 * heads, heads)))
+        q, k = prepare(q, k, p[h + "q_norm.weight"], p[h + "k_norm.weight"], positions)
+        x = x + linear(attention(q, k, v, p[h + "lambda"], cu_seqlens).flatten(1), h + "c_proj")
+        y = norm(x, p[h + "ln_2.weight"], p[h + "ln_2.bias"])
+        x = x + mlp(linear(y, h + "c_fc"), *weights(h + "mlp.c_proj"))
     return norm(x, p["ln_f.weight"], p["ln_f.bias"]) @ p["wte"].to(dtype).t()
 
 
@@ -213,9 +352,9 @@ def step(ranks, batches, heads, temperature, rate):
 
 
 def run(ranks=2, steps=5, layers=2, heads=4, width=256, vocab=5003, top=32, lengths=(100, 1, 155, 64),
-        temperature=2.0, rate=0.5):
+        temperature=2.0, rate=0.5, block="gpt2"):
     """The ranks' parameters after `steps` steps, and each step's losses."""
-    models = [make_parameters(layers, width, vocab, max(lengths)) for _ in range(ranks)]
+    models = [make_parameters(layers, width, vocab, max(lengths), block=block, heads=heads) for _ in range(ranks)]
     batches = [make_batch(lengths, vocab, top, 100 + r) for r in range(ranks)]
     losses = [step(models, batches, heads, temperature, rate) for _ in range(steps)]
     rc, status = ar.ar_device_status()
@@ -229,6 +368,7 @@ def main():
     for name, value in (("ranks", 2), ("steps", 5), ("layers", 2), ("heads", 4), ("width", 256), ("vocab", 5003),
                         ("top", 32)):
         parser.add_argument("--" + name, type=int, default=value)
+    parser.add_argument("--block", choices=BLOCKS, default=BLOCKS[0])
     models, losses = run(**vars(parser.parse_args()))
     for n, each in enumerate(losses):
         print(f"step {n}: mean loss of each rank " + " ".join(f"{x:.4f}" for x in each))
