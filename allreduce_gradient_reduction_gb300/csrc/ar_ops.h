@@ -138,7 +138,8 @@ struct QkArgs {
 // Blocks whose partial sums of the weights' gradients are kept, one row each.
 constexpr int kQkMaxBlocks = 456;
 
-cudaError_t launch_qk_norm_rope(int dtype, int wdtype, bool backward, bool interleaved, const QkArgs& a, cudaStream_t stream);
+cudaError_t launch_qk_norm_rope(int dtype, int wdtype, bool interleaved, const QkArgs& a, cudaStream_t stream);
+cudaError_t launch_qk_norm_rope_backward(int dtype, int wdtype, bool interleaved, const QkArgs& a, cudaStream_t stream);
 
 // ---- activation kept in 8 bits ------------------------------------------------------------
 

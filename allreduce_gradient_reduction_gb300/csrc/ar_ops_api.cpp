@@ -358,7 +358,8 @@ int qk_norm_rope(bool backward, const ar_attention_tensor* q_up, const ar_attent
   a.dim = (int32_t)dim;
   a.rotary = (int32_t)rotary;
   a.eps = eps;
-  return status_of(ar::launch_qk_norm_rope(dtype, wdtype, backward, interleaved, a, s));
+  return status_of(backward ? ar::launch_qk_norm_rope_backward(dtype, wdtype, interleaved, a, s)
+                            : ar::launch_qk_norm_rope(dtype, wdtype, interleaved, a, s));
 }
 
 // ---- activation kept in 8 bits

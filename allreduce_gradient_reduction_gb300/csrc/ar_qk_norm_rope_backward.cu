@@ -1,0 +1,10 @@
+// Norm and rotation of queries and keys, backward: ar_qk_norm_rope.cuh.
+#include "ar_qk_norm_rope.cuh"
+
+namespace ar {
+
+cudaError_t launch_qk_norm_rope_backward(int dtype, int wdtype, bool interleaved, const QkArgs& a, cudaStream_t s) {
+  return launch_qk<true>(dtype, wdtype, interleaved, a, s);
+}
+
+}  // namespace ar
