@@ -564,17 +564,18 @@ def ar_attention_backward(dout, q, k, v, out, lse, cu_seqlens, dq, dk, dv, works
                                      workspace.nbytes, _stream_of(stream, q))
 
 
-def _heads_of(dtype, dim, tensors):
-    """The operands as an array of ar_attention_tensor; None unless each is
-    [tokens, heads, dim] of this type with the head's elements side by side."""
+def _heads_of(dtype, groups):
+    """The operands as an array of ar_attention_tensor; None unless each is of
+    this type and its group's shape, with a head's elements side by side."""
     flat = []
-    for t, shape in tensors:
-        if t.dtype is not dtype or t.shape != shape:
-            return None
-        token, head, inner = t.stride()
-        if inner != 1 and dim > 1:
-            return None
-        flat += (t.data_ptr(), token, head)
+    for shape, tensors in groups:
+        for t in tensors:
+            if t.dtype is not dtype or t.shape != shape:
+                return None
+            token, head, inner = t.stride()
+            if inner != 1 and shape[2] > 1:
+                return None
+            flat += (t.data_ptr(), token, head)
     return array.array("q", flat)
 
 
@@ -585,23 +586,24 @@ def _qk(q, k, q_weight, k_weight, positions, queries, keys, weights, rotary_dim,
     types = _TORCH_DTYPE or _dtypes()
     bad = AR_ERR_INVALID_ARG, None, 0, 0, 0, 0, None
     shape, dtype = q.shape, q.dtype
-    if len(shape) != 3 or (k is None) != all(t is None for t in keys):
-        return bad
     wdtype = q_weight.dtype if q_weight is not None else k_weight.dtype if k_weight is not None else dtype
-    dt, wt = types.get(dtype), types.get(wdtype)
+    dt, wt, pdtype = types.get(dtype), types.get(wdtype), positions.dtype
+    if len(shape) != 3:
+        return bad
     if dt is None or wt is None:
         return AR_ERR_UNSUPPORTED, None, 0, 0, 0, 0, None
-    tokens, heads, dim = shape
-    tensors = [(q, shape), *((t, shape) for t in queries)]
-    kv_heads = 0
-    if k is not None:
+    tokens, _, dim = shape
+    if k is None:
+        if any(t is not None for t in keys):
+            return bad
+        kv_heads, groups = 0, ((shape, (q, *queries)),)
+    else:
         kshape = k.shape
         if len(kshape) != 3 or kshape[0] != tokens or kshape[2] != dim or any(t is None for t in keys):
             return bad
-        kv_heads = kshape[1]
-        tensors += [(k, kshape), *((t, kshape) for t in keys)]
-    operands = _heads_of(dtype, dim, tensors)
-    if operands is None or types.get(positions.dtype) != 2 or not _vector(positions, tokens, positions.dtype):
+        kv_heads, groups = kshape[1], ((shape, (q, *queries)), (kshape, (k, *keys)))
+    operands = _heads_of(dtype, groups)
+    if operands is None or types.get(pdtype) != 2 or not _vector(positions, tokens, pdtype):
         return bad
     for w in (q_weight, k_weight, *weights):
         if w is not None and not _vector(w, dim, wdtype):
@@ -682,9 +684,8 @@ def _diff_operands(q, k, v, lam, cu_seqlens, lse, queries, keys, values, outs):
     if dt is None:
         return AR_ERR_UNSUPPORTED, 0, 0, None
     oshape = (tokens, heads, vshape[2])
-    operands = _heads_of(dtype, 2, ((q, qshape), (k, kshape), (v, vshape), *((t, qshape) for t in queries),
-                                    *((t, kshape) for t in keys), *((t, vshape) for t in values),
-                                    *((t, oshape) for t in outs)))
+    operands = _heads_of(dtype, ((qshape, (q,)), (kshape, (k,)), (vshape, (v,)), (qshape, queries), (kshape, keys),
+                                 (vshape, values), (oshape, outs)))
     if operands is None:
         return bad
     if (types.get(cu_seqlens.dtype) != 2 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1
