@@ -340,64 +340,35 @@ __device__ __forceinline__ SeqUnit find_unit_in_order(const int32_t* cu_seqlens,
   return SeqUnit{begin, length, n - 1 - i, n};
 }
 
-// The `unit`-th unit with the most work first, by one warp.  There are
-// sum_s max(0, n_s - w) units with more work than w, n_s being the units of
-// sequence s.  The work of the one asked for is found by looking at 32 values
-// of w at a time, one to a lane; then the sequence, which is the next one in
-// order that has a unit of that work.  Entries of cu_seqlens are clamped, so
-// that no value in it leads outside the tensors.
+// The `unit`-th unit with the most work first, by one warp, a lane to a sequence.
+// There are sum_s max(0, n_s - w) units with more work than w, n_s being the units
+// of sequence s.  The work of the one asked for is found by halving, one sum over
+// the warp for every bit of the longest sequence's units; then the sequence, which
+// is the next one in order that has a unit of that work.  Entries of cu_seqlens are
+// clamped, so that no value in it leads outside the tensors.
 __device__ __forceinline__ SeqUnit find_unit(const int32_t* cu_seqlens, int seqs, int tokens, int size, int unit) {
   if (seqs > kFewSequences) return find_unit_in_order(cu_seqlens, seqs, tokens, size, unit);
   constexpr uint32_t kAll = 0xFFFFFFFFu;
   const int lane = threadIdx.x & 31;
-  int begin = 0, length = 0, first = -1;
-  auto look = [&](int s0) {  // this lane's sequence of the 32 from s0; its units
-    if (s0 != first) {
-      const int s = s0 + lane;
-      begin = length = 0;
-      if (s < seqs) {
-        begin = min(max(cu_seqlens[s], 0), tokens);
-        length = min(max(cu_seqlens[s + 1], begin), tokens) - begin;
-      }
-      first = s0;
-    }
-    return (length + size - 1) / size;
-  };
-  int w = 0, range = (tokens + size - 1) / size;  // the work less one is in [w, w + range)
-  int after;                                      // units with more work than that and one
-  for (;;) {
-    const int step = (range + 30) / 31;
-    const int mine = w + lane * step;
-    int above = 0;
-    for (int s0 = 0; s0 < seqs; s0 += 32) {
-      const int n = look(s0), here = min(32, seqs - s0);
-      for (int k = 0; k < here; k += 8)  // lanes without a sequence have no units
-#pragma unroll
-        for (int i = 0; i < 8; ++i) above += max(__shfl_sync(kAll, n, k + i) - mine, 0);
-    }
-    const uint32_t more = __ballot_sync(kAll, above > unit);
-    if (!more) return SeqUnit{0, 0, 0, 0};
-    const int last = 31 - __clz(more);
-    w += last * step;
-    if (step == 1) {
-      after = __shfl_sync(kAll, above, min(last + 1, 31));
-      break;
-    }
-    range = step;
+  int begin = 0, length = 0;
+  if (lane < seqs) {
+    begin = min(max(cu_seqlens[lane], 0), tokens);
+    length = min(max(cu_seqlens[lane + 1], begin), tokens) - begin;
   }
-  int place = unit - after;
-  for (int s0 = 0; s0 < seqs; s0 += 32) {
-    const int n = look(s0);
-    const uint32_t has = __ballot_sync(kAll, n > w);
-    const int here = __popc(has);
-    if (place < here) {
-      const bool it = n > w && __popc(has & ((1u << lane) - 1)) == place;
-      const int from = __ffs(__ballot_sync(kAll, it)) - 1;
-      return SeqUnit{__shfl_sync(kAll, begin, from), __shfl_sync(kAll, length, from), w, __shfl_sync(kAll, n, from)};
-    }
-    place -= here;
+  const int n = (length + size - 1) / size;
+  auto above = [&](int w) { return __reduce_add_sync(kAll, max(n - w, 0)); };
+  int w = 0, range = __reduce_max_sync(kAll, n);  // the last w with more than `unit` units from it on is in [w, w + range)
+  if (above(0) <= unit) return SeqUnit{0, 0, 0, 0};
+  while (range > 1) {
+    const int half = range / 2, more = above(w + half);
+    if (more <= unit) range = half;
+    else w += half, range -= half;
   }
-  return SeqUnit{0, 0, 0, 0};
+  const int after = above(w + 1);
+  const uint32_t has = __ballot_sync(kAll, n > w);
+  const bool it = n > w && __popc(has & ((1u << lane) - 1)) == unit - after;
+  const int from = __ffs(__ballot_sync(kAll, it)) - 1;
+  return SeqUnit{__shfl_sync(kAll, begin, from), __shfl_sync(kAll, length, from), w, __shfl_sync(kAll, n, from)};
 }
 
 // Host: at most this many units (or places), however the tokens are split.
