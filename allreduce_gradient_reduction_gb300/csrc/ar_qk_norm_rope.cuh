@@ -308,16 +308,23 @@ __global__ void __launch_bounds__(kThreads, kResident<VEC * CHUNKS, BACKWARD>)
   const float mean = 1.f / (float)a.dim;
   for (bool turned = true; left; --left) {
     if (turned) {
-      // another token: its angles, for all of its heads
+      // another token: its angles, for all of its heads.  The groups have the same
+      // pairs, so each takes a part of them and they exchange what they made.
+      constexpr int kEach = (kPairs + kGroups - 1) / kGroups;
+      float c[kEach], s[kEach];
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) {
+        const int i = min(group * kEach, kPairs - kEach) + j;
+        cos_sin(position, turns[min(H::pair_of(a, lane, i), kMaxPairs - 1)], c[j], s[j]);
+        if (BACKWARD) s[j] = -s[j];  // backward turns the other way
+      }
 #pragma unroll
       for (int i = 0; i < kPairs; i += 2) {
-        float c[2], s[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          cos_sin(position, turns[min(H::pair_of(a, lane, i + j), kMaxPairs - 1)], c[j], s[j]);
-        cs[i / 2] = two(c[0], c[1]);
-        // backward turns the other way
-        sn[i / 2] = BACKWARD ? two(-s[0], -s[1]) : two(s[0], s[1]);
+        auto of = [&](const float (&v)[kEach], int i) {
+          return kGroups == 1 ? v[i % kEach] : __shfl_sync(0xFFFFFFFFu, v[i % kEach], i / kEach * LANES + lane);
+        };
+        cs[i / 2] = two(of(c, i), of(c, i + 1));
+        sn[i / 2] = two(of(s, i), of(s, i + 1));
       }
       if (token + 1 < a.tokens) position = a.positions[token + 1];
     }
