@@ -613,6 +613,7 @@ __device__ __forceinline__ bool dq_walk(const Maps& maps, const DiffArgs& a, int
     const float c = a.scale * kLog2e;
     const bool valid = query + row < unit.length;
     wait_for_delta();
+    const float lambda = a.lambda[head];
     const int64_t at = (int64_t)2 * head * a.tokens + unit.begin + query + row;
     Two lse[2], delta[2];
     for (int m = 0; m < 2; ++m) {
@@ -676,7 +677,7 @@ __device__ __forceinline__ bool dq_walk(const Maps& maps, const DiffArgs& a, int
                  (2 * head + m) * a.dq.head_stride;
         finite &= write_rows<T, 32>(lane0 + dq_at + m * 64, k_tile + warp * 2048, out, a.dq.token_stride,
                                     unit.length - from, (i & 1) * 32, a.dim,
-                                    a.scale * (1.f / by) * (m ? -a.lambda[head] : 1.f));
+                                    a.scale * (1.f / by) * (m ? -lambda : 1.f));
       }
     }
     if (kScaled<T> && FIRST && ok && !__any_sync(0xFFFFFFFFu, most > 0.f)) {
