@@ -136,7 +136,7 @@ struct QkArgs {
 };
 
 // Blocks whose partial sums of the weights' gradients are kept, one row each.
-constexpr int kQkMaxBlocks = 456;
+constexpr int kQkMaxBlocks = 304;
 
 cudaError_t launch_qk_norm_rope(int dtype, int wdtype, bool interleaved, const QkArgs& a, cudaStream_t stream);
 cudaError_t launch_qk_norm_rope_backward(int dtype, int wdtype, bool interleaved, const QkArgs& a, cudaStream_t stream);

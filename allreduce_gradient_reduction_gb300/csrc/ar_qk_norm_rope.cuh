@@ -13,7 +13,7 @@
 // of a pair in the same lane, so that the rotation exchanges nothing; a warp has
 // as many heads at a time as it has groups (a round).  All rounds of all tokens,
 // of the queries by some blocks and of the keys by others, are dealt out to the
-// warps in equal runs.  A warp keeps the weights, the current token's angles and
+// warps evenly.  A warp keeps the weights, the current token's angles and
 // its part of the weights' gradients in registers and works in pairs of binary32
 // values.  The next rounds are copied into shared memory meanwhile, each lane's
 // own vectors into places of its own, so that nothing but its own copies is
@@ -37,10 +37,11 @@ namespace ar {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-// Blocks on a multiprocessor, by what a lane holds: eight pairs' gradients take
-// 128 registers.
-template <int PAIRS, bool BACKWARD>
-constexpr int kResident = BACKWARD ? 2 : 3;
+// Blocks on a multiprocessor: a lane's eight pairs of weights, angles and sums take
+// 128 registers backward; forward three were slower (61 us where two take 59).
+constexpr int kResident = 2;
+// Tokens to a warp from which on warps take whole ones, every `warps`-th.
+constexpr int kMany = 4;
 constexpr int kMaxPairs = kQkMaxDim / 2;
 
 __device__ __forceinline__ void cos_sin(int32_t position, uint64_t turn, float& c, float& s) {
@@ -224,7 +225,7 @@ struct Ring {
 
 // The first `q_blocks` blocks take the queries, the others the keys.
 template <class T, class W, int VEC, int LANES, int CHUNKS, bool INTERLEAVED, bool BACKWARD>
-__global__ void __launch_bounds__(kThreads, kResident<VEC * CHUNKS, BACKWARD>)
+__global__ void __launch_bounds__(kThreads, kResident)
     qk_kernel(const __grid_constant__ QkArgs a, int q_blocks) {
   using H = Head<T, VEC, LANES, CHUNKS, INTERLEAVED>;
   constexpr int kGroups = 32 / LANES, kPairs = H::kPairs, kTwos = kPairs / 2;
@@ -233,14 +234,22 @@ __global__ void __launch_bounds__(kThreads, kResident<VEC * CHUNKS, BACKWARD>)
   const int t = (int)blockIdx.x >= q_blocks;  // which tensor
   const int heads = a.heads[t], rounds = (heads + kGroups - 1) / kGroups;
 
-  // the warp's run of rounds
+  // The warp's rounds: a run of them, or those of every `warps`-th token, so that
+  // neighbouring warps read neighbouring rows at a time (16384 tokens, 32:8 heads
+  // of 128 bf16: forward 59 us and 62 in runs, backward 89 and 94).
   const int64_t all = a.tokens * rounds, warps = (int64_t)(t ? gridDim.x - q_blocks : q_blocks) * kWarps;
   const int64_t warp = (int64_t)(blockIdx.x - (t ? q_blocks : 0)) * kWarps + threadIdx.x / 32;
   const int64_t each = all / warps, over = all - each * warps;
   int left = (int)(each + (warp < over));  // (rows of two elements or more in memory: fewer than 2^31 to a warp)
   const int64_t begin = warp * each + min(warp, over);
-  int64_t token = begin / rounds;
+  int64_t token = begin / rounds, hop = 1;
   int head = (int)(begin - token * rounds) * kGroups + group;
+  if (a.tokens >= kMany * warps) {
+    token = warp;
+    hop = warps;
+    head = group;
+    left = (int)((a.tokens - warp + warps - 1) / warps) * rounds;
+  }
 
   // Rounds on their way: a ring of kAhead in shared memory, or one in registers
   // where a vector is too short for that.  A group without a head in a round
@@ -251,10 +260,10 @@ __global__ void __launch_bounds__(kThreads, kResident<VEC * CHUNKS, BACKWARD>)
   typename H::Raw x_next = {}, dy_next = {};
   int head_ahead = head, left_ahead = left, slot_ahead = 0, slot = 0;
   const int last = rounds * kGroups + group;  // one past the group's last
-  // From one round to the next, and from a token's last to the next token's first.
+  // From one round to the next, and from a token's last to its next token's first.
   auto place = [&](const QkTensor& of) { return token * of.token_stride + head * of.head_stride; };
   auto across = [&](const QkTensor& of) { return kGroups * of.head_stride; };
-  auto down = [&](const QkTensor& of) { return of.token_stride - (int64_t)(rounds - 1) * kGroups * of.head_stride; };
+  auto down = [&](const QkTensor& of) { return hop * of.token_stride - (int64_t)(rounds - 1) * kGroups * of.head_stride; };
   const T* from = static_cast<const T*>(a.x[t].ptr) + place(a.x[t]);
   const T* dfrom = static_cast<const T*>(a.dy[t].ptr) + (BACKWARD ? place(a.dy[t]) : 0);
   T* to_row = static_cast<T*>(const_cast<void*>(a.y[t].ptr)) + place(a.y[t]);
@@ -326,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, kResident<VEC * CHUNKS, BACKWARD>)
         cs[i / 2] = two(of(c, i), of(c, i + 1));
         sn[i / 2] = two(of(s, i), of(s, i + 1));
       }
-      if (token + 1 < a.tokens) position = a.positions[token + 1];
+      if (token + hop < a.tokens) position = a.positions[token + hop];
     }
     Two xa[kTwos], xb[kTwos], ga[kTwos], gb[kTwos];
     if constexpr (H::kCopied) {
@@ -344,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, kResident<VEC * CHUNKS, BACKWARD>)
     head += kGroups;
     turned = head >= last;
     if (turned) {
-      ++token;
+      token += hop;
       head = group;
     }
     to_row += turned ? y_down : y_across;
@@ -469,14 +478,21 @@ cudaError_t run(const QkArgs& a, cudaStream_t s) {
   constexpr int kGroups = 32 / LANES;
   // Blocks in proportion to the tensors' rounds, as many as are resident at a
   // time, or a warp to a round.  A token's angles cost about as much as a round.
-  constexpr int64_t kMost = 152 * kResident<VEC * CHUNKS, BACKWARD>;
+  // Where warps take whole tokens, as many warps as leave each the same number.
+  constexpr int64_t kMost = 152 * kResident;
   static_assert(!BACKWARD || kMost <= kQkMaxBlocks, "the workspace has a row for each block");
   int64_t rounds[2], blocks[2];
   for (int t = 0; t < 2; ++t) rounds[t] = (a.heads[t] + kGroups - 1) / kGroups;
   const int64_t cost[2] = {rounds[0] + 1, rounds[1] ? rounds[1] + 1 : 0};
   for (int t = 0; t < 2; ++t) {
-    const int64_t share = t ? kMost - blocks[0] : std::max<int64_t>(1, kMost * cost[0] / (cost[0] + cost[1]) - (cost[1] > 0));
-    blocks[t] = std::min(rounds[t] ? std::max<int64_t>(share, 1) : 0, (a.tokens * rounds[t] + kWarps - 1) / kWarps);
+    const int64_t share =
+        std::max<int64_t>(1, t ? kMost - blocks[0] : kMost * cost[0] / (cost[0] + cost[1]) - (cost[1] > 0));
+    blocks[t] = std::min(rounds[t] ? share : 0, (a.tokens * rounds[t] + kWarps - 1) / kWarps);
+    if (a.tokens < kMany * share * kWarps || !rounds[t]) continue;
+    // (up to 2% more than the queries' share is the keys' to lack)
+    const int64_t room = t ? share : std::min<int64_t>(share + share / 50, kMost - (rounds[1] > 0));
+    const int64_t each = (a.tokens + room * kWarps - 1) / (room * kWarps);
+    blocks[t] = (a.tokens + each * kWarps - 1) / (each * kWarps);
   }
   const int all = (int)(blocks[0] + blocks[1]);
   auto* kernel = qk_kernel<T, W, VEC, LANES, CHUNKS, INTERLEAVED, BACKWARD>;

@@ -171,6 +171,25 @@ def test_many_tokens_are_as_few(ar):
         assert all(torch.equal(x[a:a + 10], y) for x, y in zip(outs, few))
 
 
+@pytest.mark.parametrize("heads,kv", [(4, 0), (60, 1), (1, 60), (3, 3)])
+def test_whole_tokens_to_a_warp(ar, heads, kv):
+    """Enough tokens that warps take whole ones; keys that there are none of, or
+    few, and as many blocks as the workspace has rows.  (A weight's gradient is
+    summed over up to 60 x 10001 rows, in chains of at most 10001 * 60 / 2400 =
+    250: 512 units of 2^-24 with its terms'.)"""
+    global SUMS
+    xs, ups, ws = make(10001, heads, max(kv, 1), 16, "f16", 42), make(10001, heads, max(kv, 1), 16, "f16", 43), weights(16, "f32", 44)
+    if not kv:
+        xs[1] = ups[1] = ws[1] = None
+    pos = positions_of(10001)
+    check(ar, xs, ws, pos, "f16", "f32", rotary=0)
+    before, SUMS = SUMS, 2.0 ** -15
+    try:
+        check(ar, xs, ws, pos, "f16", "f32", ups, rotary=0)
+    finally:
+        SUMS = before
+
+
 @pytest.mark.parametrize("interleaved", [False, True])
 def test_far_positions(ar, interleaved):
     """Angles are as exact at 2^31 as at 0, below it and before it too."""
