@@ -419,9 +419,10 @@ int ar_plan_destroy(ar_plan* plan);
  *
  * The operators of a language model's training step that stand beside its
  * library matrix products and whose gradients the collectives above combine:
- * layer norm, causal attention over packed sequences and distillation from a
- * teacher's top logits, each with its gradient (additions with no counterpart
- * on the pages).
+ * layer norm, causal attention over packed sequences, distillation from a
+ * teacher's top logits, the norm and rotation of queries and keys,
+ * differential attention and activations kept in 8 bits, each with its gradient
+ * (additions with no counterpart on the pages).
  *
  * Conventions they share, beyond the common ones above:
  *   - Sums, softmax statistics and norms are held in binary32, and each
@@ -605,7 +606,8 @@ int64_t ar_attention_workspace_bytes(int64_t tokens, int64_t heads, int64_t kv_h
  *               2 i + 1
  *   eps         finite, >= 0
  * The angle is exact modulo one turn for the frequency in binary64, so far
- * positions are as exact as near ones.
+ * positions are as exact as near ones.  Squares are summed in binary32: f32 rows
+ * with elements beyond 2^60 or so in size overflow.
  */
 #define AR_QK_MAX_DIM 256
 int ar_qk_norm_rope(const ar_attention_tensor* q, const ar_attention_tensor* k, const void* q_weight,
@@ -677,7 +679,8 @@ int ar_diff_attention(const ar_attention_tensor* q, const ar_attention_tensor* k
  *   workspace   16-byte aligned device memory of at least
  *               ar_diff_attention_workspace_bytes bytes
  * p_0 - lambda p_1 and da are rounded to dtype for their products, f16 within
- * the same bounds as in ar_attention_backward.
+ * the same bounds as in ar_attention_backward, where da_1 counts without lambda
+ * for dq and relative to the largest lambda of its group for dk.
  */
 int ar_diff_attention_backward(const ar_attention_tensor* dout, const ar_attention_tensor* q,
                                const ar_attention_tensor* k, const ar_attention_tensor* v, const float* lambda,
