@@ -564,56 +564,64 @@ def ar_attention_backward(dout, q, k, v, out, lse, cu_seqlens, dq, dk, dv, works
                                      workspace.nbytes, _stream_of(stream, q))
 
 
-def _heads_of(dtype, groups):
-    """The operands as an array of ar_attention_tensor; None unless each is of
-    this type and its group's shape, with a head's elements side by side."""
-    flat = []
-    for shape, tensors in groups:
-        for t in tensors:
-            if t.dtype is not dtype or t.shape != shape:
-                return None
-            token, head, inner = t.stride()
-            if inner != 1 and shape[2] > 1:
-                return None
-            flat += (t.data_ptr(), token, head)
-    return array.array("q", flat)
+def _add_heads(flat, dtype, shape, tensors):
+    """Adds the tensors to an array of ar_attention_tensor; False unless each is
+    of this type and shape, with a head's elements side by side."""
+    for t in tensors:
+        if t.dtype is not dtype or t.shape != shape:
+            return False
+        token, head, inner = t.stride()
+        if inner != 1 and shape[2] > 1:
+            return False
+        flat += (t.data_ptr(), token, head)
+    return True
 
 
-def _qk(q, k, q_weight, k_weight, positions, queries, keys, weights, rotary_dim, frequencies):
-    """(status, the operands as an array of ar_attention_tensor: q and
-    `queries`, then k and `keys`; the number of key heads, element types, the
-    rotated size, host frequencies)."""
+def _qk(q, k, positions, queries, keys, weights, rotary_dim, frequencies):
+    """(status, the operands as an array of ar_attention_tensor: `queries`, of
+    which q is the first, then `keys`; the number of key heads, element types,
+    the rotated size, host frequencies).  `weights` are those and their
+    gradients."""
     types = _TORCH_DTYPE or _dtypes()
-    bad = AR_ERR_INVALID_ARG, None, 0, 0, 0, 0, None
-    shape, dtype = q.shape, q.dtype
-    wdtype = q_weight.dtype if q_weight is not None else k_weight.dtype if k_weight is not None else dtype
-    dt, wt, pdtype = types.get(dtype), types.get(wdtype), positions.dtype
+    shape, dtype, flat, kv_heads, wdtype = q.shape, q.dtype, [], 0, None
     if len(shape) != 3:
-        return bad
+        return AR_ERR_INVALID_ARG, None, 0, 0, 0, 0, None
+    tokens, _, dim = shape
+    fits = True
+    for w in weights:
+        if w is not None:
+            if wdtype is None:
+                wdtype = w.dtype
+            elif w.dtype is not wdtype:
+                fits = False
+            if w.dim() != 1 or w.numel() != dim or not w.is_contiguous():
+                fits = False
+    dt = types.get(dtype)
+    wt = dt if wdtype is None else types.get(wdtype)
     if dt is None or wt is None:
         return AR_ERR_UNSUPPORTED, None, 0, 0, 0, 0, None
-    tokens, _, dim = shape
-    if k is None:
-        if any(t is not None for t in keys):
-            return bad
-        kv_heads, groups = 0, ((shape, (q, *queries)),)
-    else:
+    pdtype = positions.dtype
+    if (not fits or types.get(pdtype) != 2 or not _vector(positions, tokens, pdtype)
+            or not _add_heads(flat, dtype, shape, queries)):
+        return AR_ERR_INVALID_ARG, None, 0, 0, 0, 0, None
+    if k is not None:
         kshape = k.shape
-        if len(kshape) != 3 or kshape[0] != tokens or kshape[2] != dim or any(t is None for t in keys):
-            return bad
-        kv_heads, groups = kshape[1], ((shape, (q, *queries)), (kshape, (k, *keys)))
-    operands = _heads_of(dtype, groups)
-    if operands is None or types.get(pdtype) != 2 or not _vector(positions, tokens, pdtype):
-        return bad
-    for w in (q_weight, k_weight, *weights):
-        if w is not None and not _vector(w, dim, wdtype):
-            return bad
+        for t in keys:
+            fits = fits and t is not None
+        if (not fits or len(kshape) != 3 or kshape[0] != tokens or kshape[2] != dim
+                or not _add_heads(flat, dtype, kshape, keys)):
+            return AR_ERR_INVALID_ARG, None, 0, 0, 0, 0, None
+        kv_heads = kshape[1]
+    else:
+        for t in keys:
+            if t is not None:
+                return AR_ERR_INVALID_ARG, None, 0, 0, 0, 0, None
     rotary = dim if rotary_dim is None else rotary_dim
     if frequencies is not None:
         frequencies = array.array("d", frequencies)
         if 2 * len(frequencies) != rotary:
-            return bad
-    return AR_OK, operands, kv_heads, dt, wt, rotary, frequencies
+            return AR_ERR_INVALID_ARG, None, 0, 0, 0, 0, None
+    return AR_OK, array.array("q", flat), kv_heads, dt, wt, rotary, frequencies
 
 
 def ar_qk_norm_rope(q, k, q_weight, k_weight, positions, q_out, k_out, rotary_dim=None, base=10000.0,
@@ -623,7 +631,7 @@ def ar_qk_norm_rope(q, k, q_weight, k_weight, positions, q_out, k_out, rotary_di
     position.  q_out may be q, k_out k; k, k_weight and k_out may be None, as may
     either weight.  rotary_dim None: dim.  frequencies: a sequence of rotary_dim / 2
     numbers, in the place of base."""
-    rc, operands, kv_heads, dt, wt, rotary, freq = _qk(q, k, q_weight, k_weight, positions, (q_out,), (k_out,), (),
+    rc, operands, kv_heads, dt, wt, rotary, freq = _qk(q, k, positions, (q, q_out), (k, k_out), (q_weight, k_weight),
                                                        rotary_dim, frequencies)
     if rc:
         return rc
@@ -633,7 +641,7 @@ def ar_qk_norm_rope(q, k, q_weight, k_weight, positions, q_out, k_out, rotary_di
     return lib.ar_qk_norm_rope(at, at + 2 * n if some else None, None if q_weight is None else q_weight.data_ptr(),
                                None if k_weight is None else k_weight.data_ptr(), positions.data_ptr(), at + n,
                                at + 3 * n if some else None, tokens, heads, kv_heads, dim, rotary, base,
-                               None if freq is None else freq.buffer_info()[0], int(interleaved), eps, dt, wt,
+                               None if freq is None else freq.buffer_info()[0], 1 if interleaved else 0, eps, dt, wt,
                                _stream_of(stream, q))
 
 
@@ -648,8 +656,9 @@ def ar_qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, positions
     None) for upstream dq_out and dk_out.  workspace: a tensor of at least
     ar_qk_norm_rope_workspace_bytes(tokens, heads, kv_heads, dim) bytes; None if
     no weight's gradient is wanted."""
-    rc, operands, kv_heads, dt, wt, rotary, freq = _qk(q, k, q_weight, k_weight, positions, (dq_out, dq),
-                                                       (dk_out, dk), (dq_weight, dk_weight), rotary_dim, frequencies)
+    rc, operands, kv_heads, dt, wt, rotary, freq = _qk(q, k, positions, (q, dq_out, dq), (k, dk_out, dk),
+                                                       (q_weight, k_weight, dq_weight, dk_weight), rotary_dim,
+                                                       frequencies)
     if rc:
         return rc
     if workspace is not None and not workspace.is_contiguous():
@@ -669,31 +678,31 @@ def ar_qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, positions
 
 def _diff_operands(q, k, v, lam, cu_seqlens, lse, queries, keys, values, outs):
     """(status, element type, heads, the operands as an array of
-    ar_attention_tensor: q, k, v, then `queries`, `keys`, `values` and `outs`,
-    which have the shapes of q, k, v and the result)."""
+    ar_attention_tensor: `queries`, `keys`, `values` and `outs`, which have the
+    shapes of q, k, v, the first of the first three, and of the result)."""
     types = _TORCH_DTYPE or _dtypes()
     bad = AR_ERR_INVALID_ARG, 0, 0, None
-    qshape, kshape, vshape, dtype = q.shape, k.shape, v.shape, q.dtype
-    if len(qshape) != 3 or len(kshape) != 3 or len(vshape) != 3 or lam.dim() != 1:
+    qshape, kshape, vshape, dtype, f32 = q.shape, k.shape, v.shape, q.dtype, _F32[0]
+    if len(qshape) != 3 or len(kshape) != 3 or len(vshape) != 3:
         return bad
-    heads, tokens = lam.numel(), qshape[0]
-    if (qshape[1] != 2 * heads or kshape[1] != 2 * vshape[1] or kshape[0] != tokens or vshape[0] != tokens
-            or kshape[2] != qshape[2] or qshape[2] < 1 or not _vector(lam, heads, _F32[0])):
+    tokens, heads2, dim = qshape
+    heads = heads2 // 2
+    if (heads2 % 2 or dim < 1 or kshape[1] != 2 * vshape[1] or kshape[0] != tokens or vshape[0] != tokens
+            or kshape[2] != dim or not _vector(lam, heads, f32)):
         return bad
     dt = types.get(dtype)
     if dt is None:
         return AR_ERR_UNSUPPORTED, 0, 0, None
-    oshape = (tokens, heads, vshape[2])
-    operands = _heads_of(dtype, ((qshape, (q,)), (kshape, (k,)), (vshape, (v,)), (qshape, queries), (kshape, keys),
-                                 (vshape, values), (oshape, outs)))
-    if operands is None:
+    flat = []
+    if not (_add_heads(flat, dtype, qshape, queries) and _add_heads(flat, dtype, kshape, keys)
+            and _add_heads(flat, dtype, vshape, values) and _add_heads(flat, dtype, (tokens, heads, vshape[2]), outs)):
         return bad
     if (types.get(cu_seqlens.dtype) != 2 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1
             or not cu_seqlens.is_contiguous()):
         return bad
-    if lse is not None and (lse.dtype is not _F32[0] or lse.shape != (2 * heads, tokens) or not lse.is_contiguous()):
+    if lse is not None and (lse.dtype is not f32 or lse.shape != (heads2, tokens) or not lse.is_contiguous()):
         return bad
-    return AR_OK, dt, heads, operands
+    return AR_OK, dt, heads, array.array("q", flat)
 
 
 def ar_diff_attention(q, k, v, lam, cu_seqlens, out, second=None, lse=None, scale=None, stream=None) -> int:
@@ -702,7 +711,7 @@ def ar_diff_attention(q, k, v, lam, cu_seqlens, out, second=None, lse=None, scal
     by cu_seqlens [seqs + 1] (i32, on the device), with lam [heads] (f32, the
     second map's weight).  scale None: dim ** -0.5.  second (as out) and lse
     [2 heads, tokens] are what the backward call needs."""
-    rc, dt, heads, operands = _diff_operands(q, k, v, lam, cu_seqlens, lse, (), (), (),
+    rc, dt, heads, operands = _diff_operands(q, k, v, lam, cu_seqlens, lse, (q,), (k,), (v,),
                                              (out,) if second is None else (out, second))
     if rc:
         return rc
@@ -724,15 +733,16 @@ def ar_diff_attention_backward(dout, q, k, v, lam, out, second, lse, cu_seqlens,
     forward call's out, second and lse.  workspace: a tensor of at least
     ar_diff_attention_workspace_bytes(tokens, heads, kv_heads, dim, value_dim)
     bytes."""
-    rc, dt, heads, operands = _diff_operands(q, k, v, lam, cu_seqlens, lse, (dq,), (dk,), (dv,), (out, second, dout))
+    rc, dt, heads, operands = _diff_operands(q, k, v, lam, cu_seqlens, lse, (q, dq), (k, dk), (v, dv),
+                                             (out, second, dout))
     if rc:
         return rc
     if lse is None or not workspace.is_contiguous() or (dlam is not None and not _vector(dlam, heads, _F32[0])):
         return AR_ERR_INVALID_ARG
     tokens, _, dim = q.shape
-    at, n = operands.buffer_info()[0], _TENSOR_BYTES  # q, k, v, dq, dk, dv, out, second, dout
-    return lib.ar_diff_attention_backward(at + 8 * n, at, at + n, at + 2 * n, lam.data_ptr(), at + 6 * n, at + 7 * n,
-                                          lse.data_ptr(), cu_seqlens.data_ptr(), at + 3 * n, at + 4 * n, at + 5 * n,
+    at, n = operands.buffer_info()[0], _TENSOR_BYTES  # q, dq, k, dk, v, dv, out, second, dout
+    return lib.ar_diff_attention_backward(at + 8 * n, at, at + 2 * n, at + 4 * n, lam.data_ptr(), at + 6 * n, at + 7 * n,
+                                          lse.data_ptr(), cu_seqlens.data_ptr(), at + n, at + 3 * n, at + 5 * n,
                                           None if dlam is None else dlam.data_ptr(), tokens, cu_seqlens.numel() - 1,
                                           heads, v.shape[1], dim, v.shape[2], dim ** -0.5 if scale is None else scale,
                                           dt, workspace.data_ptr(), workspace.nbytes, _stream_of(stream, q))
