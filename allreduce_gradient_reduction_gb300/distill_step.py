@@ -154,7 +154,7 @@ class _QkNormRope(torch.autograd.Function):
     def backward(ctx, dq_out, dk_out):
         q, k, q_weight, k_weight, positions = ctx.saved_tensors
         dq, dk = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k))
-        dq_weight, dk_weight = torch.empty_like(q_weight), torch.empty_like(k_weight)
+        dq_weight, dk_weight = (None if w is None else torch.empty_like(w) for w in (q_weight, k_weight))
         workspace = torch.empty(ar.ar_qk_norm_rope_workspace_bytes(*q.shape[:2], k.shape[1], q.shape[2]),
                                 dtype=torch.uint8, device=q.device)
         ar.check(ar.ar_qk_norm_rope_backward(dq_out.contiguous(), dk_out.contiguous(), q, k, q_weight, k_weight,
@@ -165,8 +165,9 @@ class _QkNormRope(torch.autograd.Function):
 
 def qk_norm_rope(q, k, q_weight, k_weight, positions, **how):
     """q [tokens, heads, dim] and k [tokens, kv_heads, dim], each head
-    normalised, weighted [dim] and turned by its token's position (i32); how:
-    ar_qk_norm_rope's rotary_dim, base, frequencies, interleaved and eps."""
+    normalised, weighted [dim] (None: not weighted) and turned by its token's
+    position (i32); how: ar_qk_norm_rope's rotary_dim, base, frequencies,
+    interleaved and eps."""
     return _QkNormRope.apply(q, k, q_weight, k_weight, positions, how)
 
 

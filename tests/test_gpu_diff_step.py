@@ -155,3 +155,19 @@ def test_a_step_in_a_graph(ex):
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("one", (False, True))
+def test_heads_without_a_weight_are_those_with_a_weight_of_one(ex, one):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+    q, k, uq, uk = (torch.randn(70, n, 64, device="cuda", generator=g).bfloat16() for n in (4, 2, 4, 2))
+    w, pos = torch.ones(64, device="cuda"), torch.arange(70, dtype=torch.int32, device="cuda")
+
+    def both(wq, wk):
+        of = [t.detach().requires_grad_() for t in (q, k)]
+        y = ex.qk_norm_rope(*of, wq, wk, pos)
+        return *y, *torch.autograd.grad(y, of, (uq, uk))
+
+    got, want = both(w if one else None, None), both(w, w)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
