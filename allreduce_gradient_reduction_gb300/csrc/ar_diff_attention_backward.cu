@@ -293,13 +293,14 @@ __device__ __forceinline__ bool dkv_walk(const Maps& maps, const DiffArgs& a, in
   const uint32_t tmem = sh.tmem, dp_at = tmem + 192, dv_at = tmem + 256, dk_at = tmem + 384;
   auto diff_at = [&](int n) { return tmem + 128 + (n & 1) * 32; };
 
-  // The group's largest lambda; f16 holds probabilities times a power of two
-  // that leaves their difference, at most 1 + |lambda| in size, below 2^15.
-  float largest = 0.f, shift = 0.f;
+  // The group's largest lambda, or 2^-100, whose reciprocal is a number; f16
+  // holds probabilities times a power of two that leaves their difference, at
+  // most 1 + |lambda| in size, below 2^15.
+  float largest = 0x1p-100f, shift = 0.f;
   for (int h = 0; h < group; ++h) largest = fmaxf(largest, fabsf(a.lambda[kv_head * group + h]));
   if (kScaled<T>) shift = 14.f - (float)max(0, min(100, (__float_as_int(0.5f * (1.f + largest)) >> 23) - 126));
-  const float unshift = exp2f(-shift), by_unshift = by * unshift, unscale = 1.f / by;
-  const float per_largest = largest > 0.f ? -1.f / largest : 0.f;
+  const float unshift = exp2f(-shift), by_unshift = by * unshift, unscale = 1.f / by,
+              per_largest = -1.f / largest;
   float* const stats = reinterpret_cast<float*>(tiles + kTilesKV);
 
   if (warp == Form::kFetcher) {

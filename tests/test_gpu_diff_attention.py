@@ -217,6 +217,24 @@ def test_lambda_of_zero_is_the_first_map(ar):
     assert (grads[0][:, 1::2] == 0).all() and (grads[1][:, 1::2] == 0).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("lam", [(1e-40,), (-1e-45, 0.0), (1.4e-39, -2.9e-39)])
+def test_a_lambda_whose_reciprocal_is_no_number(ar, dtype, lam):
+    """Gradients of the second map are below 1e-37, all others those without it.
+    (bf16 has multiples of 2^-133 there, 9e-41: nothing relative is asked.)"""
+    *x, no, dout = make(150, 4, 2, 64, 64, dtype, 24, (0.0,))
+    cu, few = packed([100, 50]), torch.tensor([lam[i % len(lam)] for i in range(4)], device="cuda")
+    *want, (dq, dk, dv), dlam = check(ar, *x, no, cu, dtype, dout)
+    got, g, got_dlam = [torch.empty_like(t) for t in want], [torch.empty_like(t) for t in x], torch.empty(4, device="cuda")
+    ws = torch.empty(ar.ar_diff_attention_workspace_bytes(150, 4, 2, 64, 64), dtype=torch.uint8, device="cuda")
+    ar.check(ar.ar_diff_attention(*x, few, cu, *got), "forward")
+    ar.check(ar.ar_diff_attention_backward(dout, *x, few, *got, cu, *g, got_dlam, ws), "backward")
+    for a, b in ((dq, g[0]), (dk, g[1])):
+        assert torch.equal(a[:, ::2], b[:, ::2]) and b[:, 1::2].abs().max() <= 1e-37
+    for a, b in zip((*want, dv, dlam), (*got, g[2], got_dlam)):
+        assert torch.equal(a, b)
+
+
 def test_many_sequences(ar):
     """More sequences than a warp looks at at once, empty ones among them."""
     g = np.random.Generator(np.random.PCG64(6))
