@@ -255,6 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (h == 0) tmem_loaded(s[2]);  // it has arrived with the others
+          tmem_wait_store();              // the first ones stand where these go
           part = 0.f;
 #pragma unroll
           for (int b = 2 * h; b < 2 * h + 2; ++b) part += powers(s[b], m, s_at + b * 16);
