@@ -132,7 +132,7 @@ struct QkArgs {
   int32_t heads[2];
   int32_t dim, rotary;
   float eps;
-  uint64_t turn[kQkMaxDim / 2];  // turns per position of each pair, times 2^64
+  const uint64_t* turn;  // host: turns per position of each of the rotary / 2 pairs, times 2^64
 };
 
 // Blocks whose partial sums of the weights' gradients are kept, one row each.

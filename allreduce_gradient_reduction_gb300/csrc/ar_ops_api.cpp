@@ -255,10 +255,11 @@ bool add_heads(Operands& o, ar::QkTensor& t, const ar_attention_tensor* p, int64
   return true;
 }
 
-// Turns per position of each pair, times 2^64.  A training loop asks for the
-// same ones in every call, and powers take longer than the rest of it, so a
-// thread has those of its last base at hand.
-bool fill_turns(uint64_t* turn, int64_t rotary, double base, const double* frequencies) {
+// Turns per position of each pair, times 2^64, or NULL.  A training loop asks for
+// the same ones in every call, and powers take longer than the rest of it, so a
+// thread has those of its last base at hand.  Those of frequencies are put into
+// `turn`.
+const uint64_t* turns_of(uint64_t* turn, int64_t rotary, double base, const double* frequencies) {
   constexpr double kTurn = 6.283185307179586476925;
   auto fraction = [](double frequency) {
     const double turns = frequency / kTurn, part = turns - std::floor(turns);
@@ -266,10 +267,10 @@ bool fill_turns(uint64_t* turn, int64_t rotary, double base, const double* frequ
   };
   if (frequencies) {
     for (int64_t i = 0; i < rotary / 2; ++i) {
-      if (!std::isfinite(frequencies[i])) return false;
+      if (!std::isfinite(frequencies[i])) return nullptr;
       turn[i] = fraction(frequencies[i]);
     }
-    return true;
+    return turn;
   }
   struct Last {
     double base = 0;
@@ -281,14 +282,13 @@ bool fill_turns(uint64_t* turn, int64_t rotary, double base, const double* frequ
     last.rotary = -1;
     for (int64_t i = 0; i < rotary / 2; ++i) {
       const double f = std::pow(base, -2.0 * (double)i / (double)rotary);
-      if (!std::isfinite(f)) return false;
+      if (!std::isfinite(f)) return nullptr;
       last.turn[i] = fraction(f);
     }
     last.base = base;
     last.rotary = rotary;
   }
-  std::memcpy(turn, last.turn, (size_t)(rotary / 2) * sizeof(uint64_t));
-  return true;
+  return last.turn;
 }
 
 int64_t qk_workspace(int64_t dim) { return (int64_t)ar::kQkMaxBlocks * dim * (int64_t)sizeof(float); }
@@ -308,7 +308,8 @@ int qk_norm_rope(bool backward, const ar_attention_tensor* q_up, const ar_attent
   if (rc) return rc;
   const int es = esize_of(dtype), ws = esize_of(wdtype);
   ar::QkArgs a{};
-  if (!fill_turns(a.turn, rotary, base, frequencies)) return AR_ERR_INVALID_ARG;
+  uint64_t turn[ar::kQkMaxDim / 2];
+  if (!(a.turn = turns_of(turn, rotary, base, frequencies))) return AR_ERR_INVALID_ARG;
   if (kv_heads == 0) k_weight = nullptr;
   Operands o;
   void* const dweight[2] = {dq_weight, dk_weight};

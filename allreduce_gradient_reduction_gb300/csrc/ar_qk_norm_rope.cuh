@@ -42,7 +42,6 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kResident = 2;
 // Tokens to a warp from which on warps take whole ones, every `warps`-th.
 constexpr int kMany = 4;
-constexpr int kMaxPairs = kQkMaxDim / 2;
 
 __device__ __forceinline__ void cos_sin(int32_t position, uint64_t turn, float& c, float& s) {
   const uint64_t angle = (uint64_t)(int64_t)position * turn;
@@ -223,12 +222,20 @@ struct Ring {
   static constexpr uint32_t kWarpBytes = kAhead * kBytes;
 };
 
+// The pairs' turns, no more than a kernel's heads have: with 1 KB of them a
+// call of 3 tokens takes the host 14.0 us, with 256 bytes 12.9.
+template <int PAIRS>
+struct Turns {
+  uint64_t of[PAIRS];
+};
+
 // The first `q_blocks` blocks take the queries, the others the keys.
 template <class T, class W, int VEC, int LANES, int CHUNKS, bool INTERLEAVED, bool BACKWARD>
 __global__ void __launch_bounds__(kThreads, kResident)
-    qk_kernel(const __grid_constant__ QkArgs a, int q_blocks) {
+    qk_kernel(const __grid_constant__ QkArgs a, const __grid_constant__ Turns<VEC * LANES * CHUNKS> turn, int q_blocks) {
   using H = Head<T, VEC, LANES, CHUNKS, INTERLEAVED>;
-  constexpr int kGroups = 32 / LANES, kPairs = H::kPairs, kTwos = kPairs / 2;
+  constexpr int kGroups = 32 / LANES, kPairs = H::kPairs, kTwos = kPairs / 2,
+                kMaxPairs = VEC * LANES * CHUNKS;
   __shared__ uint64_t turns[kMaxPairs];
   const int lane = threadIdx.x % LANES, group = threadIdx.x % 32 / LANES;
   const int t = (int)blockIdx.x >= q_blocks;  // which tensor
@@ -293,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, kResident)
   };
   for (int i = 0; i < (H::kCopied ? kAhead - 1 : 1); ++i) fetch();
   int32_t position = left ? a.positions[token] : 0;
-  for (int i = threadIdx.x; i < kMaxPairs; i += kThreads) turns[i] = i < a.rotary / 2 ? a.turn[i] : 0;
+  for (int i = threadIdx.x; i < kMaxPairs; i += kThreads) turns[i] = i < a.rotary / 2 ? turn.of[i] : 0;
   Two wa[kTwos], wb[kTwos];
   {
     const W* w = static_cast<const W*>(a.weight[t]);
@@ -500,7 +507,9 @@ cudaError_t run(const QkArgs& a, cudaStream_t s) {
   static std::atomic<unsigned long long> opened[256];
   cudaError_t e = open_kernel((const void*)kernel, smem, false, opened);
   if (e != cudaSuccess) return e;
-  kernel<<<all, kThreads, smem, s>>>(a, (int)blocks[0]);
+  Turns<VEC * LANES * CHUNKS> turn = {};
+  std::copy_n(a.turn, a.rotary / 2, turn.of);
+  kernel<<<all, kThreads, smem, s>>>(a, turn, (int)blocks[0]);
   note_launch();
   e = cudaGetLastError();
   return e != cudaSuccess || !BACKWARD || !a.partial ? e : sum_weights<W>(a, (int)blocks[0], all, s);
@@ -511,7 +520,7 @@ template <class T, class W, int VEC, bool INTERLEAVED, bool BACKWARD>
 cudaError_t by_lanes(const QkArgs& a, cudaStream_t s) {
   const int lanes = (a.dim / 2 + VEC - 1) / VEC;
   if constexpr (VEC == 1) {
-    return run<T, W, 1, 32, kMaxPairs / 32, INTERLEAVED, BACKWARD>(a, s);
+    return run<T, W, 1, 32, kQkMaxDim / 64, INTERLEAVED, BACKWARD>(a, s);
   } else {
     if (lanes <= 4) return run<T, W, VEC, 4, 1, INTERLEAVED, BACKWARD>(a, s);
     if (lanes <= 8) return run<T, W, VEC, 8, 1, INTERLEAVED, BACKWARD>(a, s);
