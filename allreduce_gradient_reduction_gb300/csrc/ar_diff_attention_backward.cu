@@ -125,9 +125,14 @@ __device__ __forceinline__ void dlambda_block(const DiffArgs& a, int head, float
 
 // ---- loads ------------------------------------------------------------------------
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
 // The kept tile of both maps (PANELS 2, a panel each), or of v or dout.
 template <int PANELS, bool BOTH_MAPS>
 __device__ __forceinline__ void load_kept(const CUtensorMap* map, uint32_t dst, int head, int token, uint32_t bar) {
+  mbar_expect(bar, PANELS * kPanelBytes);
   for (int p = 0; p < PANELS; ++p)
     for (int r = 0; r < kTile; r += kWalk)
       tma_load(dst + p * kPanelBytes + r * 128, map, BOTH_MAPS ? 0 : p * 64, BOTH_MAPS ? 2 * head + p : head, token + r, bar);
@@ -237,16 +242,17 @@ __device__ __forceinline__ float score_gradients(const float (&p)[kCols], const 
 // ---- dk and dv ---------------------------------------------------------------------
 
 struct SharedKV {
-  alignas(8) uint64_t kv_full, q_full[kStages], do_full[kStages], stats_full[kStages], empty[kStages], s_full, s_read,
+  alignas(8) uint64_t k_full, v_full, q_full[kStages], do_full[kStages], stats_full[kStages], empty[kStages], s_full, s_read,
       dp_full, p_ready[2], ds_ready[2], done, own;
   uint32_t tmem;
   int gave_up;
   SeqUnit unit;
   float most[Form::kWorkers / 32];  // what each worker warp has seen of the score gradients
+  float largest;                    // lambda of the group in size, or 2^-100, whose reciprocal is a number
 };
 
 __device__ __forceinline__ void init_barriers(SharedKV& sh) {
-  uint64_t* const one[] = {&sh.kv_full, &sh.s_full, &sh.dp_full, &sh.done, &sh.own};
+  uint64_t* const one[] = {&sh.k_full, &sh.v_full, &sh.s_full, &sh.dp_full, &sh.done, &sh.own};
   for (uint64_t* b : one) mbar_init(smem_addr(b), 1);
   for (int i = 0; i < kStages; ++i) {
     mbar_init(smem_addr(&sh.q_full[i]), 1);
@@ -278,11 +284,10 @@ __device__ __forceinline__ bool dkv_walk(const Maps& maps, const DiffArgs& a, in
   const int dim16 = (a.dim + 15) / 16, value16 = (a.value_dim + 15) / 16;
   const int base = FIRST ? 0 : state.walks * steps, end = base + steps;  // steps made before, and after
   const float by = FIRST ? 1.f : state.by;
-  if (FIRST && warp == Form::kLoader && lane == 0) {
-    const uint32_t bar = smem_addr(&sh.kv_full);
-    mbar_expect(bar, (2 + VPANELS) * kPanelBytes);
-    load_kept<2, true>(&maps.k, k_tile, kv_head, unit.begin + unit.index * kTile, bar);
-    load_kept<VPANELS, false>(&maps.v, v_tile, kv_head, unit.begin + unit.index * kTile, bar);
+  if (FIRST && warp == Form::kFetcher && lane == 0) {
+    // (by a warp other than the walked tiles': a copy takes 80 cycles to issue)
+    load_kept<2, true>(&maps.k, k_tile, kv_head, unit.begin + unit.index * kTile, smem_addr(&sh.k_full));
+    load_kept<VPANELS, false>(&maps.v, v_tile, kv_head, unit.begin + unit.index * kTile, smem_addr(&sh.v_full));
   }
   // Tensor memory: both maps' scores, their difference (two places by turns),
   // dout v^T, dv, both dk.  Both ds take dout v^T's place, half of each part's
@@ -293,11 +298,10 @@ __device__ __forceinline__ bool dkv_walk(const Maps& maps, const DiffArgs& a, in
   const uint32_t tmem = sh.tmem, dp_at = tmem + 192, dv_at = tmem + 256, dk_at = tmem + 384;
   auto diff_at = [&](int n) { return tmem + 128 + (n & 1) * 32; };
 
-  // The group's largest lambda, or 2^-100, whose reciprocal is a number; f16
-  // holds probabilities times a power of two that leaves their difference, at
-  // most 1 + |lambda| in size, below 2^15.
-  float largest = 0x1p-100f, shift = 0.f;
-  for (int h = 0; h < group; ++h) largest = fmaxf(largest, fabsf(a.lambda[kv_head * group + h]));
+  // f16 holds probabilities times a power of two that leaves their difference,
+  // at most 1 + |lambda| in size, below 2^15.
+  const float largest = sh.largest;
+  float shift = 0.f;
   if (kScaled<T>) shift = 14.f - (float)max(0, min(100, (__float_as_int(0.5f * (1.f + largest)) >> 23) - 126));
   const float unshift = exp2f(-shift), by_unshift = by * unshift, unscale = 1.f / by,
               per_largest = -1.f / largest;
@@ -367,7 +371,8 @@ __device__ __forceinline__ bool dkv_walk(const Maps& maps, const DiffArgs& a, in
         mma_commit(smem_addr(&sh.dp_full));
         return true;
       };
-      bool ok = mbar_wait(smem_addr(&sh.kv_full), 0, gave_up) && scores(base) && dprob(base);
+      bool ok = mbar_wait(smem_addr(&sh.k_full), 0, gave_up) && scores(base) &&
+                mbar_wait(smem_addr(&sh.v_full), 0, gave_up) && dprob(base);
       for (int n = base; n < end && ok; ++n) {
         const bool more = n + 1 < end;
         // every warp's look at the scores is waited for in the last step too, so that phases keep in step
@@ -486,6 +491,14 @@ __device__ __forceinline__ void dkv_block(const Maps& maps, const DiffArgs& a, i
     tmem_alloc(smem_addr(&sh.tmem), Form::kColumns);
   } else if (warp == Form::kLoader && lane == 0) {
     init_barriers(sh);
+    prefetch_map(&maps.k);
+    prefetch_map(&maps.q);
+  } else if (warp == Form::kFetcher) {
+    const int group = a.heads / a.kv_heads;
+    float largest = 0x1p-100f;
+    for (int h = lane; h < group; h += 32) largest = fmaxf(largest, fabsf(a.lambda[kv_head * group + h]));
+    largest = warp_max(largest);
+    if (lane == 0) sh.largest = largest;
   }
   tc_fence_before();
   __syncthreads();
@@ -505,7 +518,7 @@ __device__ __forceinline__ void dkv_block(const Maps& maps, const DiffArgs& a, i
 // ---- dq ---------------------------------------------------------------------------
 
 struct SharedQ {
-  alignas(8) uint64_t q_full, kept, k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages], s_full,
+  alignas(8) uint64_t q_full, do_full, kept, k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages], s_full,
       s_read, dp_full[2], ds_ready[2], done, own;
   uint32_t tmem;
   int gave_up;
@@ -514,7 +527,7 @@ struct SharedQ {
 };
 
 __device__ __forceinline__ void init_barriers(SharedQ& sh) {
-  uint64_t* const one[] = {&sh.q_full, &sh.s_full, &sh.dp_full[0], &sh.dp_full[1], &sh.done, &sh.own};
+  uint64_t* const one[] = {&sh.q_full, &sh.do_full, &sh.s_full, &sh.dp_full[0], &sh.dp_full[1], &sh.done, &sh.own};
   for (uint64_t* b : one) mbar_init(smem_addr(b), 1);
   for (int i = 0; i < kKStages; ++i) {
     mbar_init(smem_addr(&sh.k_full[i]), 1);
@@ -545,11 +558,9 @@ __device__ __forceinline__ bool dq_walk(const Maps& maps, const DiffArgs& a, int
   const int dim16 = (a.dim + 15) / 16, value16 = (a.value_dim + 15) / 16;
   const int base = FIRST ? 0 : state.walks * steps, end = base + steps;  // steps made before, and after
   const float by = FIRST ? 1.f : state.by;
-  if (FIRST && warp == Form::kLoader && lane == 0) {
-    const uint32_t bar = smem_addr(&sh.q_full);
-    mbar_expect(bar, (2 + VPANELS) * kPanelBytes);
-    load_kept<2, true>(&maps.q, q_tile, head, unit.begin + query, bar);
-    load_kept<VPANELS, false>(&maps.dout, do_tile, head, unit.begin + query, bar);
+  if (FIRST && warp == Form::kFetcher && lane == 0) {
+    load_kept<2, true>(&maps.q, q_tile, head, unit.begin + query, smem_addr(&sh.q_full));
+    load_kept<VPANELS, false>(&maps.dout, do_tile, head, unit.begin + query, smem_addr(&sh.do_full));
   }
   // Tensor memory: both maps' scores, dout v^T (in two places by turns), both
   // dq, then the kept tiles q_0, q_1 and dout as pairs.  The next tile's scores and dout v^T are under way while this one's ds
@@ -624,7 +635,7 @@ __device__ __forceinline__ bool dq_walk(const Maps& maps, const DiffArgs& a, int
       delta[m] = two(dl, dl);
     }
     bool ok = true;
-    if (FIRST && (ok = mbar_wait(smem_addr(&sh.q_full), 0, gave_up))) {
+    if (FIRST && (ok = mbar_wait(smem_addr(&sh.q_full), 0, gave_up) && mbar_wait(smem_addr(&sh.do_full), 0, gave_up))) {
       for (int i = part; i < 4; i += kParts) {  // half a panel of both
         keep_half(q_tile + (i >> 1) * kPanelBytes, row, i & 1, lane0 + q_at + i * 16);
         if (i < 2 * VPANELS) keep_half(do_tile + (i >> 1) * kPanelBytes, row, i & 1, lane0 + do_at + i * 16);
@@ -683,7 +694,7 @@ __device__ __forceinline__ bool dq_walk(const Maps& maps, const DiffArgs& a, int
     }
     if (kScaled<T> && FIRST && ok && !__any_sync(0xFFFFFFFFu, most > 0.f)) {
       // a prompt's queries often have no gradient at all, and need no other power
-      ok = mbar_wait(smem_addr(&sh.q_full), 0, gave_up);
+      ok = mbar_wait(smem_addr(&sh.do_full), 0, gave_up);
       for (int i = part; valid && i < 2 * VPANELS; i += kParts)
         if (any_element(do_tile + (i >> 1) * kPanelBytes + row * 128 + (i & 1) * 64)) most = kUnknown;
     }
@@ -706,6 +717,8 @@ __device__ __forceinline__ void dq_block(const Maps& maps, const DiffArgs& a, in
     tmem_alloc(smem_addr(&sh.tmem), Form::kColumns);
   } else if (warp == Form::kLoader && lane == 0) {
     init_barriers(sh);
+    prefetch_map(&maps.k);
+    prefetch_map(&maps.q);
   }
   tc_fence_before();
   __syncthreads();
