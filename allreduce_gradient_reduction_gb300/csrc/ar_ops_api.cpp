@@ -255,20 +255,49 @@ bool add_heads(Operands& o, ar::QkTensor& t, const ar_attention_tensor* p, int64
   return true;
 }
 
+// 1 / (2 pi), its bits after the point (by Machin's formula).
+constexpr uint64_t kInverseTurn[] = {
+    0x28be60db9391054aull, 0x7f09d5f47d4d3770ull, 0x36d8a5664f10e410ull, 0x7f9458eaf7aef158ull,
+    0x6dc91b8e909374b8ull, 0x01924bba82746487ull, 0x3f877ac72c4a69cfull, 0xba208d7d4baed121ull,
+    0x3a671c09ad17df90ull, 0x4e64758e60d4ce7dull, 0x272117e2ef7e4a0eull, 0xc7fe25fff7816603ull,
+    0xfbcbc462d6829b47ull, 0xdb4d9fb3c9f2c26dull, 0xd3d18fd9a797fa8bull, 0x5d49eeb1faf97c5eull,
+    0xcf41ce7de294a4baull, 0x9afed7ec47e35742ull, 0x1580cc11bf1edaeaull,
+};
+
+// A finite frequency in turns, its part below one times 2^64, to the nearest: the
+// binary64 is whole / 2^k, and of the constant's bits only those matter that give
+// neither whole turns nor less than is asked for (Payne and Hanek's reduction).
+// A quotient in binary64 loses as many bits as its turns have: at position 2^31 a
+// frequency of 10 was 2e-6 radians off, one of 1e9 anything.
+uint64_t fraction_of_turn(double frequency) {
+  int shift;
+  const double half = std::frexp(std::fabs(frequency), &shift);  // below one
+  const uint64_t whole = (uint64_t)std::ldexp(half, 53);
+  shift -= 53;  // the frequency is whole * 2^shift
+  // the constant's 64 bits after the first `skip`, which is at most 971 + 128
+  auto bits = [](int skip) -> uint64_t {
+    if (skip <= -64) return 0;
+    if (skip < 0) return kInverseTurn[0] >> -skip;
+    const uint64_t* at = kInverseTurn + skip / 64;
+    return skip % 64 ? at[0] << skip % 64 | at[1] >> (64 - skip % 64) : at[0];
+  };
+  // whole times 192 bits, modulo 2^192: what is cut off is below whole, 2^-139 turns
+  unsigned __int128 part = (unsigned __int128)whole * bits(shift + 128);
+  part = (unsigned __int128)whole * bits(shift + 64) + (uint64_t)(part >> 64);
+  const uint64_t round = (uint64_t)part >> 63;
+  const uint64_t turn = whole * bits(shift) + (uint64_t)(part >> 64) + round;
+  return std::signbit(frequency) ? 0 - turn : turn;
+}
+
 // Turns per position of each pair, times 2^64, or NULL.  A training loop asks for
 // the same ones in every call, and powers take longer than the rest of it, so a
 // thread has those of its last base at hand.  Those of frequencies are put into
 // `turn`.
 const uint64_t* turns_of(uint64_t* turn, int64_t rotary, double base, const double* frequencies) {
-  constexpr double kTurn = 6.283185307179586476925;
-  auto fraction = [](double frequency) {
-    const double turns = frequency / kTurn, part = turns - std::floor(turns);
-    return part < 1.0 ? (uint64_t)std::ldexp(part, 64) : 0;  // a small negative one may round to a whole turn
-  };
   if (frequencies) {
     for (int64_t i = 0; i < rotary / 2; ++i) {
       if (!std::isfinite(frequencies[i])) return nullptr;
-      turn[i] = fraction(frequencies[i]);
+      turn[i] = fraction_of_turn(frequencies[i]);
     }
     return turn;
   }
@@ -283,7 +312,7 @@ const uint64_t* turns_of(uint64_t* turn, int64_t rotary, double base, const doub
     for (int64_t i = 0; i < rotary / 2; ++i) {
       const double f = std::pow(base, -2.0 * (double)i / (double)rotary);
       if (!std::isfinite(f)) return nullptr;
-      last.turn[i] = fraction(f);
+      last.turn[i] = fraction_of_turn(f);
     }
     last.base = base;
     last.rotary = rotary;

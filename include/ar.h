@@ -605,8 +605,8 @@ int64_t ar_attention_workspace_bytes(int64_t tokens, int64_t heads, int64_t kv_h
  *   interleaved  0: pair i is elements i and i + rotary_dim / 2; else 2 i and
  *               2 i + 1
  *   eps         finite, >= 0
- * The angle is exact modulo one turn for the frequency in binary64, so far
- * positions are as exact as near ones.  Squares are summed in binary32: f32 rows
+ * An angle, modulo one turn, is that of the frequency in binary64 to 2^-33 turns,
+ * whatever the frequency and the position.  Squares are summed in binary32: f32 rows
  * with elements beyond 2^60 or so in size overflow.
  */
 #define AR_QK_MAX_DIM 256
