@@ -48,7 +48,7 @@ __device__ __forceinline__ void cos_sin(int32_t position, uint64_t turn, float& 
   const uint64_t round = angle + (1ull << 61);
   const uint32_t quarter = (uint32_t)(round >> 62);
   // what is left of the turn, in [-1/8, 1/8), to 34 bits after the point
-  const int32_t rest = (int32_t)(round >> 30 & 0xFFFFFFFFu) - (int32_t)0x80000000;
+  const int32_t rest = (int32_t)((uint32_t)(round >> 30) ^ 0x80000000u);
   const float x = (float)rest * (float)(6.283185307179586 / 17179869184.0);
   const float sq = x * x;
   float sn = fmaf(sq, 2.75573192e-6f, -1.98412698e-4f);  // 1/9!, 1/7!

@@ -88,3 +88,13 @@ def test_bases_below_one(ar):
     """Frequencies that grow from pair to pair, up to 1 / base."""
     for base in (1e-3, 1e-9, 0.5):
         check(ar, [base ** (-2 * i / 64) for i in range(32)], base=base, given=False)
+
+
+def test_a_whole_turn_in_steps(ar):
+    """Angles on both sides of every eighth of a turn, whose remainders from the
+    nearest quarter have either sign: the bits of the remainder are arithmetic
+    without overflow."""
+    check(ar, [math.ldexp(2 * math.pi, -e) * n for e, n in ((3, 1), (3, 3), (4, 1), (5, 7), (9, 1), (9, 255), (33, 1), (33, 3))])
+    steps = [2 * math.pi * (i + d) / 64 for i in range(64) for d in (-1e-7, 1e-7)]
+    check(ar, steps)
+    check(ar, [-f for f in steps])
