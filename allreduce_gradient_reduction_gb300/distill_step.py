@@ -60,6 +60,13 @@ def _once(backward):
     return wrapped
 
 
+def _rows(grad):
+    """An upstream gradient as the attention calls take it, which is on a 16-byte
+    boundary: a part of a concatenation's gradient begins anywhere."""
+    grad = grad.contiguous()
+    return grad if grad.data_ptr() % 16 == 0 else grad.clone()
+
+
 class _LayerNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, eps):
@@ -103,7 +110,7 @@ class _PackedAttention(torch.autograd.Function):
         dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))
         workspace = torch.empty(ar.ar_attention_workspace_bytes(*q.shape[:2], k.shape[1], q.shape[2]),
                                 dtype=torch.uint8, device=q.device)
-        ar.check(ar.ar_attention_backward(dout.contiguous(), q, k, v, out, lse, cu_seqlens, dq, dk, dv, workspace),
+        ar.check(ar.ar_attention_backward(_rows(dout), q, k, v, out, lse, cu_seqlens, dq, dk, dv, workspace),
                  "ar_attention_backward")
         return dq, dk, dv, None
 
@@ -188,7 +195,7 @@ class _DiffAttention(torch.autograd.Function):
         dq, dk, dv, dlam = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v, lam))
         workspace = torch.empty(ar.ar_diff_attention_workspace_bytes(q.shape[0], lam.shape[0], v.shape[1], q.shape[2],
                                                                      v.shape[2]), dtype=torch.uint8, device=q.device)
-        ar.check(ar.ar_diff_attention_backward(dout.contiguous(), q, k, v, lam, out, second, lse, cu_seqlens, dq, dk,
+        ar.check(ar.ar_diff_attention_backward(_rows(dout), q, k, v, lam, out, second, lse, cu_seqlens, dq, dk,
                                                dv, dlam, workspace), "ar_diff_attention_backward")
         return dq, dk, dv, dlam, None
 
