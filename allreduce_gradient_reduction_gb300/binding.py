@@ -672,8 +672,8 @@ def ar_qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, positions
         positions.data_ptr(), at + 2 * n, at + 5 * n if some else None,
         None if dq_weight is None else dq_weight.data_ptr(), None if dk_weight is None else dk_weight.data_ptr(),
         tokens, heads, kv_heads, dim, rotary, base, None if freq is None else freq.buffer_info()[0],
-        1 if interleaved else 0, eps, dt, wt, None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.nbytes,
-        _stream_of(stream, q))
+        1 if interleaved else 0, eps, dt, wt, None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.nbytes, _stream_of(stream, q))
 
 
 def _diff_operands(q, k, v, lam, cu_seqlens, lse, queries, keys, values, outs):

@@ -150,7 +150,7 @@ def distill_loss(logits, teacher_index, teacher_logits, temperature=1.0):
 class _QkNormRope(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, q_weight, k_weight, positions, how):
-        q_out, k_out = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k))
+        q_out, k_out = (None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k))
         ar.check(ar.ar_qk_norm_rope(q, k, q_weight, k_weight, positions, q_out, k_out, **how), "ar_qk_norm_rope")
         ctx.save_for_backward(q, k, q_weight, k_weight, positions)
         ctx.how = how
@@ -160,12 +160,14 @@ class _QkNormRope(torch.autograd.Function):
     @_once
     def backward(ctx, dq_out, dk_out):
         q, k, q_weight, k_weight, positions = ctx.saved_tensors
-        dq, dk = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k))
+        dq, dk = (None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k))
         dq_weight, dk_weight = (None if w is None else torch.empty_like(w) for w in (q_weight, k_weight))
-        workspace = torch.empty(ar.ar_qk_norm_rope_workspace_bytes(*q.shape[:2], k.shape[1], q.shape[2]),
+        kv_heads = 0 if k is None else k.shape[1]
+        workspace = torch.empty(ar.ar_qk_norm_rope_workspace_bytes(*q.shape[:2], kv_heads, q.shape[2]),
                                 dtype=torch.uint8, device=q.device)
-        ar.check(ar.ar_qk_norm_rope_backward(dq_out.contiguous(), dk_out.contiguous(), q, k, q_weight, k_weight,
-                                             positions, dq, dk, dq_weight, dk_weight, workspace, **ctx.how),
+        dq_out, dk_out = dq_out.contiguous(), None if k is None else dk_out.contiguous()
+        ar.check(ar.ar_qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, positions, dq, dk, dq_weight,
+                                             dk_weight, workspace, **ctx.how),
                  "ar_qk_norm_rope_backward")
         return dq, dk, dq_weight, dk_weight, None, None
 
@@ -173,8 +175,8 @@ class _QkNormRope(torch.autograd.Function):
 def qk_norm_rope(q, k, q_weight, k_weight, positions, **how):
     """q [tokens, heads, dim] and k [tokens, kv_heads, dim], each head
     normalised, weighted [dim] (None: not weighted) and turned by its token's
-    position (i32); how: ar_qk_norm_rope's rotary_dim, base, frequencies,
-    interleaved and eps."""
+    position (i32).  k may be None, as is its result then.  how:
+    ar_qk_norm_rope's rotary_dim, base, frequencies, interleaved and eps."""
     return _QkNormRope.apply(q, k, q_weight, k_weight, positions, how)
 
 

@@ -1,0 +1,46 @@
+"""The PyTorch functions of a decoder block's operators in forms that the calls
+below them have: queries without keys."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def ex():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    from allreduce_gradient_reduction_gb300 import build as b
+    b.build()
+    from allreduce_gradient_reduction_gb300 import distill_step
+    torch.cuda.set_device(0)
+    return distill_step
+
+
+def normal(g, *shape, dtype=torch.bfloat16):
+    return torch.randn(*shape, device="cuda", generator=g).to(dtype).requires_grad_()
+
+
+def generator():
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    return g
+
+
+@pytest.mark.parametrize("weighted", [False, True])
+def test_queries_without_keys(ex, weighted):
+    """The same bits as with keys beside them."""
+    g = generator()
+    q, k, up = normal(g, 70, 4, 64), normal(g, 70, 2, 64), normal(g, 70, 4, 64).detach()
+    w = normal(g, 64, dtype=torch.float32) if weighted else None
+    of = [t for t in (q, w) if t is not None]
+    pos = torch.arange(70, dtype=torch.int32, device="cuda")
+    alone, none = ex.qk_norm_rope(q, None, w, None, pos, base=500.0)
+    beside, _ = ex.qk_norm_rope(q, k, w, w, pos, base=500.0)
+    assert none is None and torch.equal(alone, beside)
+    got, want = torch.autograd.grad(alone, of, up), torch.autograd.grad(beside, of, up)
+    assert torch.equal(got[0], want[0])
+    if weighted:  # summed over as many blocks as there are queries for: 280 terms of 2^-24 in another order
+        terms = (up.float() * beside.detach().float()).abs().sum((0, 1)) / w.detach().abs()
+        assert ((got[1] - want[1]).abs() <= 280 * 2.0 ** -24 * 2 * terms.max()).all()
