@@ -220,8 +220,8 @@ class _Activation8Linear(torch.autograd.Function):
         ar.check(ar.ar_activation8(x, y, codes, scales, kind=kind), "ar_activation8")
         ctx.save_for_backward(codes, scales, weight)
         ctx.kind = kind
-        ctx.cols = cols
-        return torch.addmm(bias, y, weight)
+        ctx.has_bias = bias is not None
+        return y @ weight if bias is None else torch.addmm(bias, y, weight)
 
     @staticmethod
     @_once
@@ -230,11 +230,11 @@ class _Activation8Linear(torch.autograd.Function):
         dy = dout @ weight.t()
         y = torch.empty_like(dy)
         ar.check(ar.ar_activation8_backward(codes, scales, dy, dy, y, kind=ctx.kind), "ar_activation8_backward")
-        return dy, y.t() @ dout, dout.sum(0), None
+        return dy, y.t() @ dout, dout.sum(0) if ctx.has_bias else None, None
 
 
 def activation8_linear(x, weight, bias, kind="gelu_tanh"):
-    """activation(x) @ weight + bias, all of one type.  Neither x nor the
+    """activation(x) @ weight + bias, all of one type; bias may be None.  Neither x nor the
     activation is kept for the backward pass, but x in 8 bits: gradients are
     those at what the codes stand for, the weight's with the activation made
     again from them."""

@@ -1,5 +1,5 @@
 """The PyTorch functions of a decoder block's operators in forms that the calls
-below them have: queries without keys."""
+below them have: queries without keys, no bias."""
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -44,3 +44,16 @@ def test_queries_without_keys(ex, weighted):
     if weighted:  # summed over as many blocks as there are queries for: 280 terms of 2^-24 in another order
         terms = (up.float() * beside.detach().float()).abs().sum((0, 1)) / w.detach().abs()
         assert ((got[1] - want[1]).abs() <= 280 * 2.0 ** -24 * 2 * terms.max()).all()
+
+
+@pytest.mark.parametrize("kind", ["gelu_tanh", "gelu", "identity"])
+def test_activation_without_a_bias(ex, kind):
+    """A bias of zeros changes no gradient, and no result but by the rounding of
+    another order of 300 products in binary32, and that to bf16."""
+    g = generator()
+    x, w, up = normal(g, 41, 300), normal(g, 300, 64), normal(g, 41, 64).detach()
+    plain, zeros = (ex.activation8_linear(x, w, b, kind) for b in (None, torch.zeros(64, device="cuda").bfloat16()))
+    size = x.detach().double().abs() @ w.detach().double().abs()
+    assert ((plain - zeros).double().abs() <= 2.0 ** -8 * 2 * plain.detach().double().abs() + 300 * 2.0 ** -23 * size).all()
+    got, want = (torch.autograd.grad(y, (x, w), up) for y in (plain, zeros))
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and all(t.abs().max() > 0 for t in got)
