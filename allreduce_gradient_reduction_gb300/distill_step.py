@@ -182,12 +182,13 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, **how):
 
 class _DiffAttention(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, v, lam, cu_seqlens):
+    def forward(ctx, q, k, v, lam, cu_seqlens, how):
         shape = (q.shape[0], lam.shape[0], v.shape[2])
         out, second = (torch.empty(shape, dtype=q.dtype, device=q.device) for _ in range(2))
         lse = torch.empty(q.shape[1], q.shape[0], dtype=torch.float32, device=q.device)
-        ar.check(ar.ar_diff_attention(q, k, v, lam, cu_seqlens, out, second, lse), "ar_diff_attention")
+        ar.check(ar.ar_diff_attention(q, k, v, lam, cu_seqlens, out, second, lse, **how), "ar_diff_attention")
         ctx.save_for_backward(q, k, v, lam, cu_seqlens, out, second, lse)
+        ctx.how = how
         return out
 
     @staticmethod
@@ -198,15 +199,15 @@ class _DiffAttention(torch.autograd.Function):
         workspace = torch.empty(ar.ar_diff_attention_workspace_bytes(q.shape[0], lam.shape[0], v.shape[1], q.shape[2],
                                                                      v.shape[2]), dtype=torch.uint8, device=q.device)
         ar.check(ar.ar_diff_attention_backward(_rows(dout), q, k, v, lam, out, second, lse, cu_seqlens, dq, dk,
-                                               dv, dlam, workspace), "ar_diff_attention_backward")
-        return dq, dk, dv, dlam, None
+                                               dv, dlam, workspace, **ctx.how), "ar_diff_attention_backward")
+        return dq, dk, dv, dlam, None, None
 
 
-def diff_attention(q, k, v, lam, cu_seqlens):
+def diff_attention(q, k, v, lam, cu_seqlens, scale=None):
     """q [tokens, 2 heads, dim], k [tokens, 2 kv_heads, dim], v [tokens,
-    kv_heads, value_dim], bf16 or f16; lam [heads] f32.  The sequences have to
-    cover every token."""
-    return _DiffAttention.apply(q, k, v, lam, cu_seqlens)
+    kv_heads, value_dim], bf16 or f16; lam [heads] f32; scale None: dim ** -0.5.
+    The sequences have to cover every token."""
+    return _DiffAttention.apply(q, k, v, lam, cu_seqlens, {} if scale is None else {"scale": scale})
 
 
 class _Activation8Linear(torch.autograd.Function):

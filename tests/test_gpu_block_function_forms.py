@@ -1,5 +1,5 @@
 """The PyTorch functions of a decoder block's operators in forms that the calls
-below them have: queries without keys, no bias."""
+below them have: queries without keys, no bias, a scale."""
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -57,3 +57,19 @@ def test_activation_without_a_bias(ex, kind):
     assert ((plain - zeros).double().abs() <= 2.0 ** -8 * 2 * plain.detach().double().abs() + 300 * 2.0 ** -23 * size).all()
     got, want = (torch.autograd.grad(y, (x, w), up) for y in (plain, zeros))
     assert all(torch.equal(a, b) for a, b in zip(got, want)) and all(t.abs().max() > 0 for t in got)
+
+
+def test_differential_attention_with_a_scale(ex):
+    """A scale of 2^-3 over queries is one of 2^-2 over half of them, bit for bit,
+    and its gradient twice as large: powers of two round nowhere."""
+    g = generator()
+    q, k, v = (normal(g, 150, n, d) for n, d in ((4, 64), (4, 64), (2, 128)))
+    lam = torch.full((2,), 0.7, device="cuda").requires_grad_()
+    cu, up = torch.tensor([0, 90, 150], dtype=torch.int32, device="cuda"), normal(g, 150, 2, 128).detach()
+    half = (q.detach() / 2).requires_grad_()
+    own = ex.diff_attention(q, k, v, lam, cu)  # dim^-1/2 = 2^-3
+    given = ex.diff_attention(half, k, v, lam, cu, scale=0.25)
+    assert torch.equal(own, given)
+    a, b = torch.autograd.grad(own, (q, k, v, lam), up), torch.autograd.grad(given, (half, k, v, lam), up)
+    assert torch.equal(2 * a[0], b[0]) and all(torch.equal(x, y) for x, y in zip(a[1:], b[1:]))
+    assert not torch.equal(own, ex.diff_attention(q, k, v, lam, cu, scale=0.25))
