@@ -606,8 +606,9 @@ int64_t ar_attention_workspace_bytes(int64_t tokens, int64_t heads, int64_t kv_h
  *               2 i + 1
  *   eps         finite, >= 0
  * An angle, modulo one turn, is that of the frequency in binary64 to 2^-33 turns,
- * whatever the frequency and the position.  Squares are summed in binary32: f32 rows
- * with elements beyond 2^60 or so in size overflow.
+ * whatever the frequency and the position.  Squares are summed in binary32: f32
+ * and bf16 rows with elements beyond 2^60 or so in size overflow, and with eps 0
+ * rows whose elements are all below 2^-63 lose bits, or all of them.
  */
 #define AR_QK_MAX_DIM 256
 int ar_qk_norm_rope(const ar_attention_tensor* q, const ar_attention_tensor* k, const void* q_weight,
@@ -680,7 +681,10 @@ int ar_diff_attention(const ar_attention_tensor* q, const ar_attention_tensor* k
  *               ar_diff_attention_workspace_bytes bytes
  * p_0 - lambda p_1 and da are rounded to dtype for their products, f16 within
  * the same bounds as in ar_attention_backward, where da_1 counts without lambda
- * for dq and relative to the largest lambda of its group for dk.
+ * for dq and relative to the largest lambda of its group for dk.  out and second
+ * are rounded to dtype, so delta_0 is off by up to half a unit in the last place of
+ * |dout| . |out| + |lambda| |dout| . |second|: with |lambda| far above one that is
+ * much of dq and dk of the first map.
  */
 int ar_diff_attention_backward(const ar_attention_tensor* dout, const ar_attention_tensor* q,
                                const ar_attention_tensor* k, const ar_attention_tensor* v, const float* lambda,
