@@ -302,12 +302,13 @@ __device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.
 // Every sequence is split into ceil(length / size) units, the i-th of which
 // (from 0) stands for work in proportion to i + 1; where the first unit is the
 // longest, the caller counts from the end.  A launch takes the units of all
-// sequences with the most work first, so that no long one starts last.  Every
-// block looks at all sequences for that, so with more of them than a warp has
-// lanes it takes them in the sequences' order instead, each one's longest first
-// (gradient, 12 heads of 64, by work and in order: 24 sequences of 8179 tokens
-// 62.8 and 64.0 us, 48 of 8169 68.3 and 61.6, 192 of 8087 172 and 95, 8192 of
-// 9182 168 ms and 3.1 ms).
+// sequences with the most work first, so that no long one starts last.  For that
+// a warp has a lane to each sequence; more of them than lanes are taken in their
+// order instead, each one's longest first (12 heads of 64 bf16, by work and in
+// order, us a call: 3 sequences of 8191 tokens, forward 57.0 and 61.0, gradient
+// 146.0 and 147.5; 13 of 8185, 31.0 and 31.9, 76.2 and 77.3; 24 of 8179, 24.8 and
+// 27.9, 60.7 and 65.9; 32 of 8177, 26.9 and 27.0, 63.7 and 66.0.  One of 8192,
+// where the order is the same, 114.9 and 113.3, 314.3 and 312.0).
 constexpr int kFewSequences = 32;
 struct SeqUnit {
   int begin, length;  // the sequence
