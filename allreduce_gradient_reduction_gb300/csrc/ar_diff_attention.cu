@@ -17,8 +17,9 @@
 // 16-bit pairs: rounded to the type of v, half a unit in the last place of each;
 // the sums that divide them are of the unrounded.
 //
-// Measured: 8192 tokens of one sequence, 16 heads of 2 x 64 over 4, bf16, 303 us
-// (1.36 PFLOP/s, 72% of the rate of a plain matrix product on the same device).  A
+// Measured: 8192 tokens of one sequence, 16 heads of 2 x 64 over 4, bf16, 297
+// to 301 us a call (1.38 PFLOP/s, 73% of the measured rate of a plain matrix
+// product; 286 us on the device).  A
 // step of 128 keys takes 2260 cycles, of which the products take 1536: a map's
 // exponentials (1290) and products (800, with what announces them) follow one
 // another, as its scores have no second place in tensor memory, and the other
